@@ -481,6 +481,120 @@ zds_status zds_checkpoint_load(const char *path, const zds_checkpoint_meta *expe
 zds_status zds_consolidate_fp32(const char *const *paths, int32_t num_files, int32_t section, float *out,
                                 int64_t out_numel);
 
+/* ---------------------------------------------------------------------------
+ * Muon: the update of weight matrices by an orthogonalised momentum, next to
+ * AdamW for the other tensors. Three calls in this order on one stream:
+ *
+ *   zds_muon_momentum   momentum of the flat grads, and the update to
+ *                       orthogonalise (its grads unscaled and clipped by the
+ *                       step scalars, as zds_adam_step's are)
+ *   zds_newton_schulz   every matrix of the update orthogonalised
+ *   zds_muon_apply      decoupled decay, the update times the matrix's scale,
+ *                       and the cast back to 16 bits
+ *
+ * All three follow the step scalars' overflow flag: when it is set the step
+ * is skipped on the device and every array is left as it was. The
+ * orthogonalisation needs whole matrices, so a rank owns the matrices it
+ * updates this way as a whole (a partition by tensors, not by elements).
+ * ------------------------------------------------------------------------- */
+
+/* The factor of a matrix's update. */
+typedef enum zds_muon_scale {
+  ZDS_MUON_SCALE_NONE = 0,   /* 1 */
+  ZDS_MUON_SCALE_ASPECT = 1, /* sqrt(max(1, rows / cols)) */
+  ZDS_MUON_SCALE_RMS = 2,    /* 0.2 sqrt(max(rows, cols)): an orthogonal
+                                matrix's update then has an RMS of about 0.2
+                                per element, an AdamW step's usual size, so
+                                both kinds share lr and weight_decay */
+  ZDS_MUON_SCALE_RANGE_MIN_ = -2147483647 - 1,
+  ZDS_MUON_SCALE_RANGE_MAX_ = 2147483647
+} zds_muon_scale;
+
+/* Used as fp32 values. 20 bytes. */
+typedef struct zds_muon_hparams {
+  float lr;
+  float momentum;       /* mu, in [0, 1) */
+  float weight_decay;
+  int32_t nesterov;     /* 0 or 1 */
+  int32_t scale;        /* a zds_muon_scale */
+} zds_muon_hparams;
+
+/* The matrices of one flat buffer, kept on the device. */
+typedef struct zds_matrix_plan zds_matrix_plan;
+
+/* Matrix i is rows[i] x cols[i], row-major and contiguous, its first element
+ * at flat offset offset[i] (host arrays, num_matrices entries). Sizes of zero
+ * are allowed (an empty matrix); a size is below 2^17, a matrix holds fewer
+ * than 2^31 elements; matrices must not overlap. Allocates the plan's tables
+ * on the current device. Not called on the hot path. The plan is not changed
+ * by the calls that use it: any number of streams, threads and captured
+ * graphs may share it (not a workspace). Destroy it once the work that uses
+ * it has completed. */
+zds_status zds_matrix_plan_create(zds_matrix_plan **out, const int64_t *offset, const int32_t *rows,
+                                  const int32_t *cols, int32_t num_matrices);
+void zds_matrix_plan_destroy(zds_matrix_plan *plan);
+int32_t zds_matrix_plan_num_matrices(const zds_matrix_plan *plan);
+/* Elements a flat buffer of the plan holds at least: the largest end of a
+ * matrix (0 for an empty plan; -1 for NULL). */
+int64_t zds_matrix_plan_span(const zds_matrix_plan *plan);
+
+/* Muon's momentum on n elements of a flat buffer, in fp32 with one rounding
+ * per operation:
+ *   g = x * grad_scale; m = mu*m + (1-mu)*g;
+ *   u = nesterov ? mu*m + (1-mu)*g : m; update = round_nearest_even(u)
+ * with grad_scale from scalars_dev (zds_overflow_and_norm). Padding elements
+ * whose grad and momentum are zero stay zero.
+ *   grads     device, n elements of grad_dtype
+ *   momentum  device fp32, n elements, updated in place
+ *   update    device, n elements of update_dtype (BF16 or FP32), written. FP16
+ *             is refused: a momentum below its range would be lost.
+ * 6 B read + 4 B written per element and the update's size. */
+zds_status zds_muon_momentum(const zds_muon_hparams *hp, const void *grads, zds_dtype grad_dtype, float *momentum,
+                             void *update, zds_dtype update_dtype, int64_t n,
+                             const zds_step_scalars *scalars_dev, void *stream);
+
+/* Workspace zds_newton_schulz needs for the plan's matrices (0 for NULL or a
+ * dtype it does not take). */
+size_t zds_newton_schulz_workspace_bytes(const zds_matrix_plan *plan, zds_dtype dtype);
+
+/* Orthogonalisation of every matrix G of the plan by Newton-Schulz steps:
+ *   X_0 = G / (||G||_F + 1e-7)
+ *   X_{k+1} = a X_k + (b A + c A^2) X_k,  A = X_k X_k^T   (of the smaller size)
+ * which moves every singular value s of X to a s + b s^3 + c s^5, towards 1,
+ * and keeps the singular vectors.
+ *   src, dst  device, flat buffers of the plan, dtype BF16 or FP32. dst is
+ *             written inside the plan's matrices only; it may be src itself
+ *             but not overlap it otherwise.
+ *   coef      host, 3 * steps floats: (a, b, c) of each step; NULL: (3.4445,
+ *             -4.7750, 2.0315) in each. Steps whose singular values could pass
+ *             8 are refused (they diverge).
+ *   steps     1..16
+ *   scalars_dev  may be NULL; else nothing is done when its overflow flag is set
+ *   ws        device workspace, 256-byte aligned, zds_newton_schulz_workspace_bytes;
+ *             calls that may run at the same time need one each (so do two
+ *             captured graphs that may be replayed at the same time)
+ * BF16: the products take their operands in fp16 (11 bits, scaled by powers of
+ * two into its range) and sum in fp32; X is carried with 22 bits; the result
+ * is rounded once to bf16 and lies within about 1.3 bf16 roundings of the
+ * exact result (2-norm). FP32: operands are two fp16 numbers (22 bits) and
+ * three products replace one; the error is that of an fp32 evaluation.
+ * A matrix with an infinity or NaN becomes NaN; the others are not affected. A
+ * zero matrix stays zero. Entries of the result below 2^-24 may become zero. */
+zds_status zds_newton_schulz(const zds_matrix_plan *plan, const void *src, void *dst, zds_dtype dtype,
+                             const float *coef, int32_t steps, const zds_step_scalars *scalars_dev, void *ws,
+                             size_t ws_bytes, void *stream);
+
+/* Muon's step on the plan's matrices, fp32 with one rounding per operation:
+ *   p = p*(1-lr*wd); p = p - (lr*scale)*u; params_out = round_nearest_even(p)
+ * with 1-lr*wd and lr*scale formed in float64 and rounded once to fp32.
+ *   update      device, flat buffer of the plan, BF16 or FP32
+ *   master      device fp32, updated in place
+ *   params_out  device, FP16 or BF16, written; NULL skips the cast
+ * Elements outside the plan's matrices are not touched. */
+zds_status zds_muon_apply(const zds_muon_hparams *hp, const zds_matrix_plan *plan, const void *update,
+                          zds_dtype update_dtype, float *master, void *params_out, zds_dtype param_dtype,
+                          const zds_step_scalars *scalars_dev, void *stream);
+
 /* Row a3. Initialise the device step state from cfg with Adam step count t0
  * and powers beta1^t0, beta2^t0 (1, 1 for a fresh optimizer). */
 zds_status zds_step_state_init(zds_step_state *state_dev, const zds_scaler_config *cfg, int64_t t0,

@@ -1,0 +1,314 @@
+"""Muon's operators on the GPU against the plain definitions: the two element
+passes bit for bit, the orthogonalisation against float64.
+
+Tolerances of the orthogonalisation (2-norm of the difference over the 2-norm
+of the result). bf16: the result's rounding is at most 2^-8 per element, and
+the operands' fp16 roundings (at most 2^-11 each; X, A and B in 5 steps, so 15
+of them, independent) are carried to the result by slopes of the step's
+polynomial below 3.5 in a step and are contracted by later ones: together at
+most another 2^-8 or so. Hence 2^-7. fp32: operands of 22 bits (2^-23), fp32
+sums over up to K terms (sqrt(K) 2^-24), 15 of them, with the same slopes:
+15 * 3.5 * sqrt(1400) * 2^-24 is 1.2e-4 if all errors added up; as they are
+independent, sqrt(15) * 3.5 * sqrt(1400) * 2^-24 = 3e-5.
+"""
+
+import numpy as np
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+if not torch.cuda.is_available():
+    pytest.skip("no GPU", allow_module_level=True)
+
+from oracle import muon as M  # noqa: E402
+from oracle.zero_step import narrow, widen  # noqa: E402
+from tests.util import to_dev, to_host  # noqa: E402
+from zero_sharded_mixed_tensor_amd import zds  # noqa: E402
+
+TOL = {"bf16": 2.0 ** -7, "fp32": 3e-5}
+TDT = {"fp16": torch.float16, "bf16": torch.bfloat16, "fp32": torch.float32}
+
+
+def scalars(grad_scale=1.0, overflow=0):
+    t = zds.new_scalars()
+    zds.write_scalars(t, zds.StepScalars(overflow=overflow, accum_steps=1, clip_coef=1.0, grad_scale=grad_scale,
+                                         scale_used=1.0))
+    return t
+
+
+def bits(x, dtype):
+    """fp32 values -> the dtype's host form."""
+    return x.astype(np.float32) if dtype == "fp32" else narrow(x.astype(np.float32), dtype)
+
+
+# ------------------------------------------------------------------ momentum
+
+@pytest.mark.parametrize("gdt", ["fp16", "bf16", "fp32"])
+@pytest.mark.parametrize("udt", ["bf16", "fp32"])
+@pytest.mark.parametrize("n,shift", [(1, 0), (3, 0), (4, 0), (1021, 0), (1024, 1), (70003, 0), (70003, 3)])
+def test_momentum_bit_exact(gdt, udt, n, shift):
+    rng = np.random.default_rng(n * 10 + shift)
+    g = bits(rng.standard_normal(n + shift) * 8, gdt)
+    m = (rng.standard_normal(n + shift) * 1e-3).astype(np.float32)
+    for nesterov in (True, False):
+        hp = zds.muon_hparams(momentum=0.95, nesterov=nesterov)
+        dg, dm = to_dev(g, gdt), to_dev(m, "fp32")
+        du = torch.full((n + shift + 8,), 7.0, dtype=TDT[udt], device="cuda")
+        zds.zds_muon_momentum(hp, dg[shift:], dm[shift:], du[shift:shift + n], scalars(0.37))
+        wm, wu = M.muon_momentum(g[shift:], gdt, m[shift:], 0.37, 0.95, nesterov, udt)
+        assert np.array_equal(to_host(dm)[shift:].view(np.uint32), wm.view(np.uint32))
+        assert np.array_equal(to_host(du)[shift:shift + n], wu)
+        assert np.array_equal(to_host(dm)[:shift], m[:shift])  # nothing in front or behind is written
+        assert (du[:shift] == 7).all() and (du[shift + n:] == 7).all()
+
+
+def test_momentum_skips_on_overflow_and_takes_none():
+    n = 1000
+    g = torch.full((n,), float("inf"), device="cuda", dtype=torch.bfloat16)
+    m = torch.ones(n, device="cuda")
+    u = torch.full((n,), 3.0, device="cuda", dtype=torch.bfloat16)
+    zds.zds_muon_momentum(zds.muon_hparams(), g, m, u, scalars(0.0, overflow=1))
+    zds.zds_muon_momentum(zds.muon_hparams(), g, m, u, scalars(1.0), n=0)
+    assert (m == 1).all() and (u == 3).all()
+
+
+# ------------------------------------------------------------------ layouts
+
+def layout(shapes, gap=0, first=0):
+    """Matrices one after another, `gap` elements between them."""
+    out, pos = [], first
+    for r, c in shapes:
+        out.append((pos, r, c))
+        pos += r * c + gap
+    return out, pos
+
+
+def fill(mats, total, seed, dtype, kind="gauss"):
+    rng = np.random.default_rng(seed)
+    x = np.full(total, 5.0, np.float32)
+    for o, r, c in mats:
+        if kind == "gauss":
+            g = rng.standard_normal((r, c))
+        else:  # most of the weight in a few directions
+            k = max(1, min(r, c) // 16)
+            g = rng.standard_normal((r, k)) @ rng.standard_normal((k, c)) / np.sqrt(k) + 0.3 * rng.standard_normal((r, c))
+        x[o:o + r * c] = (g * 1e-3).reshape(-1)
+    return bits(x, dtype)
+
+
+# ------------------------------------------------------------------ apply
+
+@pytest.mark.parametrize("udt", ["bf16", "fp32"])
+@pytest.mark.parametrize("pdt", ["bf16", "fp16"])
+@pytest.mark.parametrize("mode", ["none", "aspect", "rms"])
+@pytest.mark.parametrize("gap,first", [(0, 0), (64, 0), (5, 3)])
+def test_apply_bit_exact(udt, pdt, mode, gap, first):
+    mats, total = layout([(16, 32), (1, 1), (7, 1), (0, 9), (65, 130), (130, 65), (1, 4099)], gap, first)
+    u = fill(mats, total, 3, udt)
+    rng = np.random.default_rng(4)
+    p = (rng.standard_normal(total) * 0.02).astype(np.float32)
+    du, dp = to_dev(u, udt), to_dev(p, "fp32")
+    do = torch.full((total,), 3.0, dtype=TDT[pdt], device="cuda")
+    want_p, want_o = p.copy(), to_host(do).copy()
+    for o, r, c in mats:
+        s = slice(o, o + r * c)
+        want_p[s], want_o[s] = M.muon_apply(u[s], udt, p[s], r, c, 2e-2, 0.1, mode, pdt)
+    plan = zds.zds_matrix_plan_create(mats)
+    hp = zds.muon_hparams(lr=2e-2, weight_decay=0.1, scale=mode)
+    zds.zds_muon_apply(hp, plan, du, dp, do, scalars(overflow=1))   # skipped
+    assert np.array_equal(to_host(dp), p) and (do == 3).all()
+    zds.zds_muon_apply(hp, plan, du, dp, do, scalars())
+    assert np.array_equal(to_host(dp).view(np.uint32), want_p.view(np.uint32))
+    assert np.array_equal(to_host(do), want_o)
+    zds.zds_muon_apply(hp, plan, du, dp, None, scalars())           # no cast
+    assert np.array_equal(to_host(do), want_o)
+    plan.close()
+
+
+# ------------------------------------------------------------------ orthogonalise
+
+SETS = {
+    "one": [(1, 1)],
+    "thin": [(1, 513), (513, 1), (2, 64), (63, 3)],
+    "small": [(16, 32), (64, 64), (65, 63), (63, 65), (128, 128), (129, 127)],
+    "middle": [(200, 333), (333, 200), (256, 256), (257, 511)],
+    "large": [(1024, 1024), (1025, 1090), (1400, 1030)],
+    "mixed": [(64, 64), (0, 5), (300, 1030), (1030, 1100), (5, 0), (1, 3)],
+}
+
+
+def check(mats, x, y, dtype, steps=5, coef=None, tol=None):
+    xs, ys = widen(x, dtype).astype(np.float64), widen(y, dtype).astype(np.float64)
+    for o, r, c in mats:
+        if r * c == 0:
+            continue
+        want = M.newton_schulz(xs[o:o + r * c].reshape(r, c), steps, coef)
+        got = ys[o:o + r * c].reshape(r, c)
+        rel = np.linalg.norm(got - want) / np.linalg.norm(want)
+        assert rel <= (tol or TOL[dtype]), (r, c, rel)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("name", list(SETS))
+@pytest.mark.parametrize("kind,gap,first", [("gauss", 0, 0), ("lowrank", 3, 1)])
+def test_orthogonalise(dtype, name, kind, gap, first):
+    mats, total = layout(SETS[name], gap, first)
+    total += 8
+    x = fill(mats, total, 11, dtype, kind)
+    plan = zds.zds_matrix_plan_create(mats)
+    assert plan.span == max(o + r * c for o, r, c in mats)
+    dx = to_dev(x, dtype)
+    ws = zds.new_newton_schulz_workspace(plan, TDT[dtype])
+    ws.fill_(0xFF)                                    # NaN patterns: nothing stale is read
+    dy = torch.full((total,), 9.0, dtype=TDT[dtype], device="cuda")
+    zds.zds_newton_schulz(plan, dx, dy, ws)
+    y = to_host(dy)
+    check(mats, x, y, dtype)
+    inside = np.zeros(total, bool)
+    for o, r, c in mats:
+        inside[o:o + r * c] = True
+    assert (widen(y, dtype)[~inside] == 9.0).all()
+    again = torch.full((total,), 9.0, dtype=TDT[dtype], device="cuda")
+    zds.zds_newton_schulz(plan, dx, again, ws)        # the same bits, on a used workspace
+    assert np.array_equal(to_host(again), y)
+    zds.zds_newton_schulz(plan, dx, dx, ws)           # in place
+    got = to_host(dx)
+    assert np.array_equal(got[inside], y[inside]) and np.array_equal(got[~inside], x[~inside])
+    plan.close()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("steps,coef", [(1, None), (2, None), (8, None), (3, [(1.875, -1.25, 0.375)] * 3),
+                                        (4, [(3.4, -4.7, 2.0), (3.0, -4.0, 1.8), (2.0, -1.5, 0.5), (1.5, -0.5, 0.0)])])
+def test_orthogonalise_steps_and_coefficients(dtype, steps, coef):
+    mats, total = layout([(40, 70), (300, 180)])
+    x = fill(mats, total, 5, dtype)
+    plan = zds.zds_matrix_plan_create(mats)
+    ws = zds.new_newton_schulz_workspace(plan, TDT[dtype])
+    dy = torch.zeros(total, dtype=TDT[dtype], device="cuda")
+    zds.zds_newton_schulz(plan, to_dev(x, dtype), dy, ws, steps=steps, coef=coef)
+    check(mats, x, to_host(dy), dtype, steps, coef)
+    plan.close()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_orthogonalise_extremes(dtype):
+    """Infinite, NaN, zero, tiny and huge matrices next to an ordinary one."""
+    shapes = [(40, 50)] * 6 + [(1050, 1100)] * 3
+    mats, total = layout(shapes)
+    x = widen(fill(mats, total, 6, dtype), dtype).copy()
+    part = [slice(o, o + r * c) for o, r, c in mats]
+    x[part[0]][7] = np.inf
+    x[part[1]][9] = np.nan
+    x[part[2]] = 0
+    x[part[3]] *= 2.0 ** 110
+    x[part[4]] *= 2.0 ** 60
+    x[part[6]][12345] = -np.inf
+    x[part[7]] = 0
+    xb = bits(x, dtype)
+    plan = zds.zds_matrix_plan_create(mats)
+    ws = zds.new_newton_schulz_workspace(plan, TDT[dtype])
+    dy = torch.full((total,), 9.0, dtype=TDT[dtype], device="cuda")
+    zds.zds_newton_schulz(plan, to_dev(xb, dtype), dy, ws)
+    y = to_host(dy)
+    yf = widen(y, dtype)
+    for k in (0, 1, 6):
+        assert np.isnan(yf[part[k]]).all()
+    for k in (2, 7):
+        assert (yf[part[k]] == 0).all()
+    check([mats[k] for k in (3, 4, 5, 8)], xb, y, dtype)
+    plan.close()
+
+
+def test_orthogonalise_small_norms_follow_the_floor():
+    """A norm next to the 1e-7 floor: the floor's share shows in the result."""
+    mats, total = layout([(48, 96)] * 3)
+    x = widen(fill(mats, total, 8, "fp32"), "fp32").copy()
+    for k, s in enumerate((1e-6, 1e-5, 1e-4)):
+        x[mats[k][0]:mats[k][0] + 48 * 96] *= s
+    plan = zds.zds_matrix_plan_create(mats)
+    ws = zds.new_newton_schulz_workspace(plan, torch.float32)
+    dy = torch.zeros(total, device="cuda")
+    zds.zds_newton_schulz(plan, to_dev(x, "fp32"), dy, ws)
+    check(mats, x, to_host(dy), "fp32")
+    plan.close()
+
+
+def test_orthogonalise_skips_on_overflow_and_takes_an_empty_plan():
+    mats, total = layout([(40, 50), (200, 200), (1024, 1030)])
+    plan = zds.zds_matrix_plan_create(mats)
+    ws = zds.new_newton_schulz_workspace(plan, torch.bfloat16)
+    src = torch.ones(total, dtype=torch.bfloat16, device="cuda")
+    dst = torch.full_like(src, 9.0)
+    zds.zds_newton_schulz(plan, src, dst, ws, scalars=scalars(overflow=1))
+    assert (dst == 9).all()
+    zds.zds_newton_schulz(plan, src, dst, ws, scalars=scalars())
+    assert (dst != 9).all()
+    plan.close()
+    for empty in ([], [(0, 0, 7), (0, 7, 0)]):
+        plan = zds.zds_matrix_plan_create(empty)
+        assert plan.span == 0 and zds.zds_newton_schulz_workspace_bytes(plan, torch.bfloat16) == 0
+        e = torch.empty(0, dtype=torch.bfloat16, device="cuda")
+        zds.zds_newton_schulz(plan, e, e, zds.new_newton_schulz_workspace(plan, torch.bfloat16))
+        zds.zds_muon_apply(zds.muon_hparams(), plan, e, torch.empty(0, device="cuda"), None, scalars())
+        plan.close()
+
+
+def test_refusals_with_a_plan():
+    mats, total = layout([(40, 50)])
+    plan = zds.zds_matrix_plan_create(mats)
+    x = torch.ones(total, dtype=torch.bfloat16, device="cuda")
+    ws = zds.new_newton_schulz_workspace(plan, torch.bfloat16)
+
+    def refused(text, fn):
+        with pytest.raises(zds.ZdsError) as e:
+            fn()
+        assert text in str(e.value), str(e.value)
+
+    refused("workspace of", lambda: zds.zds_newton_schulz(plan, x, x, ws[:-1]))
+    big = torch.empty(ws.numel() + 16, dtype=torch.uint8, device="cuda")
+    refused("256-byte aligned", lambda: zds.zds_newton_schulz(plan, x, x, big[16:]))
+    refused("src holds", lambda: zds.zds_newton_schulz(plan, x[:-1], x, ws))
+    refused("dst holds", lambda: zds.zds_newton_schulz(plan, x, x[:-1], ws))
+    refused("one dtype", lambda: zds.zds_newton_schulz(plan, x, x.float(), ws))
+    h = x.half()
+    refused("bf16 or fp32", lambda: zds.zds_newton_schulz(plan, h, h, ws))
+    refused("bf16 or fp32", lambda: zds.zds_muon_apply(zds.muon_hparams(), plan, h, x.float(), None, scalars()))
+    refused("fp16 or bf16", lambda: zds.zds_muon_apply(zds.muon_hparams(), plan, x, x.float(), x.float(), scalars()))
+    refused("device tensor", lambda: zds.zds_newton_schulz(plan, x.cpu(), x, ws))
+    torch.cuda.synchronize()
+    assert (x == 1).all()
+    plan.close()
+
+
+def test_streams_and_graph_replays():
+    """On a stream of the caller's; captured once and replayed with the grads
+    refilled in place, eager work in between, every replay against the eager
+    result."""
+    mats, total = layout([(48, 80), (300, 200), (1030, 1100)], gap=7)
+    plan = zds.zds_matrix_plan_create(mats)
+    ws, ws2 = (zds.new_newton_schulz_workspace(plan, torch.bfloat16) for _ in range(2))
+    src = to_dev(fill(mats, total, 1, "bf16"), "bf16")
+    want = torch.zeros_like(src)
+    zds.zds_newton_schulz(plan, src, want, ws)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    got = torch.zeros_like(src)
+    with torch.cuda.stream(side):
+        zds.zds_newton_schulz(plan, src, got, ws2)
+    zds.zds_newton_schulz(plan, src, want, ws)         # at the same time, its own workspace
+    torch.cuda.synchronize()
+    assert torch.equal(got, want)
+    out = torch.zeros_like(src)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        zds.zds_newton_schulz(plan, src, out, ws)
+    for seed in (2, 3, 4, 5):
+        src.copy_(to_dev(fill(mats, total, seed, "bf16"), "bf16"))
+        out.zero_()
+        graph.replay()
+        zds.zds_newton_schulz(plan, src, want.zero_(), ws2)
+        torch.cuda.synchronize()
+        assert torch.equal(out, want)
+    plan.close()

@@ -1,0 +1,77 @@
+// The matrix plan: host description and device tables of the matrices of one
+// flat buffer, shared by the Muon and Newton-Schulz translation units.
+#pragma once
+
+#include <vector>
+
+#include "zds_internal.h"
+
+namespace zds {
+
+// Padding of a matrix's two sizes in the Newton-Schulz workspace, and the
+// depth of a product's steps (elements of fp16).
+constexpr int kNsDepth = 64;
+
+// One matrix as the device code sees it. m <= n are its sizes with the
+// smaller first (tall: rows > cols, so X is the transpose), mp and np the
+// padded ones. Workspace offsets are in fp16 elements from the workspace's
+// start; a second plane (the low halves) follows each array of an FP32 plan.
+struct NsMatrix {
+  int64_t offset;   // flat offset
+  int32_t rows, cols;
+  int32_t m, n, mp, np;
+  int32_t tall;
+  int32_t part0, nparts;  // this matrix's partial sums of squares in the group's
+  int32_t pad_;
+  int64_t x;        // X, mp x np
+  int64_t xt[2];    // X^T, np x mp, of even and odd steps
+  int64_t lo;       // what X^T's fp16 values leave of X^T, np x mp
+  int64_t a, b;     // A and B, mp x mp
+};
+
+// A block's piece of work: tile (ti, tj) of matrix `mat`, or chunk ti of it.
+struct NsTile {
+  int32_t mat, ti, tj, pad_;
+};
+
+// Matrices that go through one sequence of launches. Tables: tile lists of
+// the triangular products (ti >= tj), the full product, the conversion
+// (64 x 64 tiles over the padded matrix) and the norm's chunks.
+struct NsGroup {
+  int32_t tile;                 // the products' tile size
+  int32_t mat0, nmat;           // matrices in the plan's device array
+  int32_t tri0, ntri, full0, nfull, conv0, nconv, chunk0, nchunk;  // in the plan's tile array
+};
+
+// A chunk of a matrix for zds_muon_apply: up to kApplyChunk elements from flat
+// offset `first`, and the matrix's two scale factors (zds_muon_scale 1 and 2).
+constexpr int kApplyChunk = 4096;
+struct ApplyChunk {
+  int64_t first;
+  int32_t len;
+  float aspect, rms;
+  int32_t pad_;
+};
+
+}  // namespace zds
+
+struct zds_matrix_plan {
+  int device = 0;
+  int32_t num = 0;
+  int64_t span = 0;
+  std::vector<zds::NsGroup> groups;
+  // workspace of one group (the largest of all): partial sums and scales in
+  // front, then the fp16 arrays
+  size_t ws_bytes[2] = {0, 0};      // [FP32]
+  int32_t max_parts = 0, max_mats = 0;
+  zds::NsMatrix *d_mats[2] = {nullptr, nullptr};  // [FP32]: workspace offsets differ
+  zds::NsTile *d_tiles = nullptr;
+  zds::ApplyChunk *d_chunks = nullptr;
+  int64_t num_chunks = 0;
+};
+
+namespace zds {
+// Tables of the Newton-Schulz groups into the plan (sizes already checked).
+zds_status build_newton_schulz(zds_matrix_plan *p, const int64_t *offset, const int32_t *rows, const int32_t *cols,
+                               int32_t num);
+}  // namespace zds

@@ -22,6 +22,7 @@ ZDS_OK, ZDS_EINVAL, ZDS_EALIGN, ZDS_ENOMEM, ZDS_EHIP, ZDS_EIO = 0, 1, 2, 3, 4, 5
 ZDS_FP16, ZDS_BF16, ZDS_FP32 = 0, 1, 2
 ZDS_COPY, ZDS_OVERWRITE, ZDS_ACCUMULATE = 0, 1, 2
 ZDS_ON_DEVICE, ZDS_ON_HOST = 0, 1
+ZDS_MUON_SCALE_NONE, ZDS_MUON_SCALE_ASPECT, ZDS_MUON_SCALE_RMS = 0, 1, 2
 
 STATE_BYTES = 64
 SCALARS_BYTES = 64
@@ -63,6 +64,11 @@ class StepScalars(ctypes.Structure):
                 ("beta1", ctypes.c_float), ("beta2", ctypes.c_float), ("eps", ctypes.c_float)]
 
 
+class MuonHparams(ctypes.Structure):
+    _fields_ = [("lr", ctypes.c_float), ("momentum", ctypes.c_float), ("weight_decay", ctypes.c_float),
+                ("nesterov", ctypes.c_int32), ("scale", ctypes.c_int32)]
+
+
 class CheckpointMeta(ctypes.Structure):
     _fields_ = [("world", ctypes.c_int32), ("rank", ctypes.c_int32), ("flat_align", ctypes.c_int32),
                 ("stage", ctypes.c_int32), ("offload", ctypes.c_int32), ("num_tensors", ctypes.c_int32),
@@ -73,7 +79,7 @@ class CheckpointMeta(ctypes.Structure):
 
 
 assert ctypes.sizeof(StepState) == STATE_BYTES and ctypes.sizeof(StepScalars) == SCALARS_BYTES
-assert ctypes.sizeof(CheckpointMeta) == 48
+assert ctypes.sizeof(CheckpointMeta) == 48 and ctypes.sizeof(MuonHparams) == 20
 
 _P = ctypes.c_void_p
 _I32, _I64, _U32 = ctypes.c_int32, ctypes.c_int64, ctypes.c_uint32
@@ -112,6 +118,14 @@ _SIGS = {
     "zds_checkpoint_load": (_I32, [ctypes.c_char_p, ctypes.POINTER(CheckpointMeta), _PI64, _P, _P, _P, _P,
                                    _I32, _P]),
     "zds_consolidate_fp32": (_I32, [ctypes.POINTER(ctypes.c_char_p), _I32, _I32, _P, _I64]),
+    "zds_matrix_plan_create": (_I32, [ctypes.POINTER(_P), _PI64, ctypes.POINTER(_I32), ctypes.POINTER(_I32), _I32]),
+    "zds_matrix_plan_destroy": (None, [_P]),
+    "zds_matrix_plan_num_matrices": (_I32, [_P]),
+    "zds_matrix_plan_span": (_I64, [_P]),
+    "zds_muon_momentum": (_I32, [ctypes.POINTER(MuonHparams), _P, _I32, _P, _P, _I32, _I64, _P, _P]),
+    "zds_newton_schulz_workspace_bytes": (ctypes.c_size_t, [_P, _I32]),
+    "zds_newton_schulz": (_I32, [_P, _P, _P, _I32, ctypes.POINTER(ctypes.c_float), _I32, _P, _P, ctypes.c_size_t, _P]),
+    "zds_muon_apply": (_I32, [ctypes.POINTER(MuonHparams), _P, _P, _I32, _P, _P, _I32, _P, _P]),
     "zds_step_state_init": (_I32, [_P, ctypes.POINTER(ScalerConfig), _I64, ctypes.c_double,
                                    ctypes.c_double, _P]),
     "zds_loss_scaler_update": (_I32, [_P, _P, ctypes.POINTER(AdamWHparams), _P]),
@@ -511,6 +525,108 @@ def zds_onebit_decompress(payloads, chunk, dst, mode=ZDS_OVERWRITE, stream=None,
     W = (_P * len(payloads))(*[_dev_ptr(w, "words") for w, _ in payloads])
     S = (_P * len(payloads))(*[_dev_ptr(s, "scales") for _, s in payloads])
     _check(lib.zds_onebit_decompress(W, S, len(payloads), n, chunk, _dev_ptr(dst, "dst"), mode, _stream(stream)))
+
+
+# ------------------------------------------------------------------ Muon
+
+_MUON_SCALES = {"none": ZDS_MUON_SCALE_NONE, "aspect": ZDS_MUON_SCALE_ASPECT, "rms": ZDS_MUON_SCALE_RMS}
+
+
+def muon_hparams(lr=2e-3, momentum=0.95, weight_decay=0.1, nesterov=True, scale="rms"):
+    """scale: "none", "aspect" or "rms" (see zds_muon_scale in include/zds.h)."""
+    if scale not in _MUON_SCALES:
+        raise ZdsError(ZDS_EINVAL, "scale must be one of %s" % ", ".join(sorted(_MUON_SCALES)))
+    return MuonHparams(lr, momentum, weight_decay, int(bool(nesterov)), _MUON_SCALES[scale])
+
+
+class MatrixPlan:
+    """Owning handle of a zds_matrix_plan (the matrices of one flat buffer)."""
+
+    def __init__(self, handle, matrices):
+        self.handle = handle
+        self.matrices = matrices  # [(offset, rows, cols)]
+        self.span = lib.zds_matrix_plan_span(handle)
+
+    def close(self):
+        if self.handle:
+            lib.zds_matrix_plan_destroy(self.handle)
+            self.handle = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+def zds_matrix_plan_create(matrices):
+    """matrices: [(flat offset, rows, cols)], row-major in one flat buffer."""
+    matrices = [(int(o), int(r), int(c)) for o, r, c in matrices]
+    k = len(matrices)
+    for o, r, c in matrices:
+        if not (abs(r) < 1 << 31 and abs(c) < 1 << 31 and abs(o) < 1 << 63):
+            raise ZdsError(ZDS_EINVAL, "matrix (%d, %d, %d) out of range" % (o, r, c))
+    i32 = ctypes.c_int32 * max(1, k)
+    h = ctypes.c_void_p()
+    _check(lib.zds_matrix_plan_create(ctypes.byref(h), _i64arr([m[0] for m in matrices]),
+                                      i32(*[m[1] for m in matrices]), i32(*[m[2] for m in matrices]), k))
+    return MatrixPlan(h, matrices)
+
+
+def zds_muon_momentum(hp, grads, momentum, update, scalars, stream=None, n=None):
+    n = momentum.numel() if n is None else n
+    if momentum.dtype != torch.float32:
+        raise ZdsError(ZDS_EINVAL, "momentum must be fp32")
+    for name, t in (("grads", grads), ("momentum", momentum), ("update", update)):
+        _need(t, n, name)
+    _need_bytes(scalars, SCALARS_BYTES, "scalars")
+    _check(lib.zds_muon_momentum(ctypes.byref(hp), _dev_ptr(grads, "grads"), dtype_code(grads),
+                                 _dev_ptr(momentum, "momentum"), _dev_ptr(update, "update"), dtype_code(update), n,
+                                 _dev_ptr(scalars, "scalars"), _stream(stream)))
+
+
+def zds_newton_schulz_workspace_bytes(plan, dtype):
+    """Bytes for a plan and a torch dtype (bfloat16 or float32)."""
+    if dtype not in (torch.bfloat16, torch.float32):
+        raise ZdsError(ZDS_EINVAL, "dtype must be bfloat16 or float32")
+    return lib.zds_newton_schulz_workspace_bytes(plan.handle, _DT[dtype])
+
+
+def new_newton_schulz_workspace(plan, dtype, device="cuda"):
+    return torch.empty(max(1, zds_newton_schulz_workspace_bytes(plan, dtype)), dtype=torch.uint8, device=device)
+
+
+def zds_newton_schulz(plan, src, dst, ws, steps=5, coef=None, scalars=None, stream=None):
+    """Every matrix of src orthogonalised into dst (flat buffers of the plan,
+    dst may be src). coef: None, or steps triples (a, b, c); scalars: the step
+    scalars whose overflow flag skips the call, or None."""
+    _need(src, plan.span, "src")
+    _need(dst, plan.span, "dst")
+    if src.dtype != dst.dtype:
+        raise ZdsError(ZDS_EINVAL, "src and dst must share one dtype")
+    if scalars is not None:
+        _need_bytes(scalars, SCALARS_BYTES, "scalars")
+    karr = None
+    if coef is not None:
+        flat = [float(x) for triple in coef for x in triple]
+        if len(flat) != 3 * steps:
+            raise ZdsError(ZDS_EINVAL, "coef holds %d numbers, %d steps need %d" % (len(flat), steps, 3 * steps))
+        karr = (ctypes.c_float * len(flat))(*flat)
+    _check(lib.zds_newton_schulz(plan.handle, _dev_ptr(src, "src"), _dev_ptr(dst, "dst"), dtype_code(src), karr, steps,
+                                 _dev_ptr(scalars, "scalars"), _dev_ptr(ws, "workspace"),
+                                 ws.numel() * ws.element_size(), _stream(stream)))
+
+
+def zds_muon_apply(hp, plan, update, master, params_out, scalars, stream=None):
+    if master.dtype != torch.float32:
+        raise ZdsError(ZDS_EINVAL, "master must be fp32")
+    for name, t in (("update", update), ("master", master), ("params_out", params_out)):
+        _need(t, plan.span, name)
+    _need_bytes(scalars, SCALARS_BYTES, "scalars")
+    pdt = dtype_code(params_out) if params_out is not None else ZDS_FP16
+    _check(lib.zds_muon_apply(ctypes.byref(hp), plan.handle, _dev_ptr(update, "update"), dtype_code(update),
+                              _dev_ptr(master, "master"), _dev_ptr(params_out, "params_out"), pdt,
+                              _dev_ptr(scalars, "scalars"), _stream(stream)))
 
 
 # ------------------------------------------------------------------ checkpoints
