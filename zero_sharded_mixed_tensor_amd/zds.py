@@ -577,7 +577,7 @@ def zds_muon_momentum(hp, grads, momentum, update, scalars, stream=None, n=None)
     n = momentum.numel() if n is None else n
     if momentum.dtype != torch.float32:
         raise ZdsError(ZDS_EINVAL, "momentum must be fp32")
-    for name, t in (("grads", grads), ("momentum", momentum), ("update", update)):
+    for name, t in (("momentum", momentum), ("grads", grads), ("update", update)):
         _need(t, n, name)
     _need_bytes(scalars, SCALARS_BYTES, "scalars")
     _check(lib.zds_muon_momentum(ctypes.byref(hp), _dev_ptr(grads, "grads"), dtype_code(grads),
