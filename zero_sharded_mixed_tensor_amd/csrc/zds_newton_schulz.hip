@@ -17,6 +17,7 @@
 // fp16 numbers (high and low) and a product runs its sum over three pieces,
 // high*high + high*low + low*high, into the same fp32 accumulators.
 #include <new>
+#include <type_traits>
 
 #include "zds_device.h"
 #include "zds_matrix.h"
@@ -165,10 +166,12 @@ struct NsArgs {
 
 template <int T>
 struct NsShape {
-  static constexpr int WM = 2, WN = T == 256 ? 4 : 2;
-  static constexpr int WAVES = WM * WN;
-  static constexpr int TM = T / WM, TN = T / WN;   // a wave's part of the tile
-  static constexpr int MI = TM / 16, NI = TN / 16;
+  static constexpr int WN = 2, WAVES = 4;
+  static constexpr int TM = T / 2, TN = T / 2;     // a wave's part of the tile
+  static constexpr int MT = T == 64 ? 16 : 32;     // the matrix instruction's tile, MT x MT x (512 / MT)
+  static constexpr int MI = TM / MT, NI = TN / MT;
+  static constexpr int KI = MT / 16;               // instructions deep in half a depth step
+  static constexpr int GROUPS = MT * MT / 256;     // a lane's runs of 4 rows in an instruction's tile
   static constexpr int LOADS = T / 8 / WAVES;      // 1 KiB loads of a wave per operand and depth step
 };
 
@@ -177,22 +180,8 @@ struct NsShape {
 // fall on all banks.
 __device__ __forceinline__ int ns_swizzle(int r, int c) { return c ^ ((r >> 1) & 7); }
 
-// One operand's T x 64 tile, global to LDS without passing through registers:
-// each load moves 8 rows of 128 bytes; the LDS side is linear, so the lane
-// takes the chunk that belongs at its position.
-template <int T>
-__device__ __forceinline__ void ns_load_tile(const half_t *base, uint32_t lane_off, uint32_t row_step, char *lds, int w) {
-  typedef NsShape<T> S;
-#pragma unroll
-  for (int g = 0; g < S::LOADS; ++g) {
-    const char *p = reinterpret_cast<const char *>(base) + static_cast<uint64_t>(g) * row_step;
-    __builtin_amdgcn_global_load_lds((global_cvoid *)(p + lane_off),
-                                     (lds_void *)(lds + (w + g * S::WAVES) * 1024), 16, 0, 0);
-  }
-}
-
 template <int T, int SEG, int KIND>
-__global__ void __launch_bounds__(NsShape<T>::WAVES * 64) ns_product_kernel(const NsArgs q) {
+__global__ void __launch_bounds__(NsShape<T>::WAVES * 64, T == 256 ? 1 : 2) ns_product_kernel(const NsArgs q) {
   typedef NsShape<T> S;
   constexpr int STAGE = T * 128;  // bytes of one operand's tile
   __shared__ __align__(1024) char smem[2][2][STAGE];
@@ -236,62 +225,116 @@ __global__ void __launch_bounds__(NsShape<T>::WAVES * 64) ns_product_kernel(cons
   const uint32_t row_step = static_cast<uint32_t>(8 * S::WAVES * ld * 2);
   const half_t *p0 = P + static_cast<int64_t>(t.ti) * T * ld;
   const half_t *q0 = Q + static_cast<int64_t>(t.tj) * T * ld;
-  f32x4 acc[S::MI][S::NI];
+  typedef float AccT __attribute__((ext_vector_type(4 * S::GROUPS)));
+  AccT acc[S::MI][S::NI];
 #pragma unroll
   for (int i = 0; i < S::MI; ++i)
 #pragma unroll
-    for (int j = 0; j < S::NI; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int j = 0; j < S::NI; ++j)
+#pragma unroll
+      for (int r = 0; r < 4 * S::GROUPS; ++r) acc[i][j][r] = 0.0f;
 
-  auto issue = [&](int k) {
+  // Load g of depth step k (T / 16 of them, P's before Q's): global to LDS
+  // without passing through registers; the LDS side is linear, so the lane
+  // takes the chunk that belongs at its position.
+  const half_t *pk = p0, *qk = q0;
+  auto aim = [&](int k) {
     int seg = 0, kk = k;
     if (SEG == 3) {
       seg = k / steps;
       kk = k - seg * steps;
     }
     // pieces: high*high, high*low, low*high
-    const half_t *pk = p0 + (seg == 2 ? pplane : 0) + static_cast<int64_t>(kk) * kNsDepth;
-    const half_t *qk = q0 + (seg == 1 ? qplane : 0) + static_cast<int64_t>(kk) * kNsDepth;
-    ns_load_tile<T>(pk, lane_off, row_step, smem[k & 1][0], w);
-    ns_load_tile<T>(qk, lane_off, row_step, smem[k & 1][1], w);
+    pk = p0 + (seg == 2 ? pplane : 0) + static_cast<int64_t>(kk) * kNsDepth;
+    qk = q0 + (seg == 1 ? qplane : 0) + static_cast<int64_t>(kk) * kNsDepth;
   };
-  const int fr = lane & 15, fc = lane >> 4;
-  issue(0);
-  for (int k = 0; k < total; ++k) {
-    if (k + 1 < total) {
-      issue(k + 1);
-      asm volatile("s_waitcnt vmcnt(%0)" ::"n"(2 * S::LOADS) : "memory");
-    } else {
-      asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+  auto load = [&](int buf, int g) {
+    const int o = g / S::LOADS, r = g % S::LOADS;
+    const char *p = reinterpret_cast<const char *>(o ? qk : pk) + static_cast<uint64_t>(r) * row_step;
+    __builtin_amdgcn_global_load_lds((global_cvoid *)(p + lane_off),
+                                     (lds_void *)(smem[buf][o] + (w + r * S::WAVES) * 1024), 16, 0, 0);
+  };
+  const int fr = lane % S::MT, fc = lane / S::MT;
+  // operand pieces of half h of a depth step: buffer h in registers
+  f16x8 fp[2][S::KI][S::MI], fq[2][S::KI][S::NI];
+  int off_p[2][S::KI], off_q[2][S::KI];
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+#pragma unroll
+    for (int c = 0; c < S::KI; ++c) {
+      const int rp = wi * S::TM + fr, rq = wj * S::TN + fr, chunk = h * 4 + c * (64 / S::MT) + fc;
+      off_p[h][c] = rp * 128 + ns_swizzle(rp, chunk) * 16;
+      off_q[h][c] = rq * 128 + ns_swizzle(rq, chunk) * 16;
     }
-    __builtin_amdgcn_s_barrier();
-    asm volatile("" ::: "memory");
-    const char *sp = smem[k & 1][0], *sq = smem[k & 1][1];
+  // read g of half h: for each instruction depth the MI pieces of P, then the
+  // NI of Q; MT rows on are 128 MT bytes on
+  auto read = [&](int buf, int h, int g) {
+    const int c = g / (S::MI + S::NI), r = g % (S::MI + S::NI);
+    if (r < S::MI) fp[h][c][r] = *reinterpret_cast<const f16x8 *>(smem[buf][0] + off_p[h][c] + r * 128 * S::MT);
+    else fq[h][c][r - S::MI] = *reinterpret_cast<const f16x8 *>(smem[buf][1] + off_q[h][c] + (r - S::MI) * 128 * S::MT);
+  };
+  constexpr int MFMAS = S::MI * S::NI * S::KI, READS = (S::MI + S::NI) * S::KI, ALL_LOADS = 2 * S::LOADS;
+  auto product = [&](int h, int e) {
+    const int c = e / (S::MI * S::NI), i = e / S::NI % S::MI, j = e % S::NI;
+    if constexpr (S::MT == 32)
+      asm volatile("v_mfma_f32_32x32x16_f16 %0, %1, %2, %0" : "+a"(acc[i][j]) : "v"(fp[h][c][i]), "v"(fq[h][c][j]));
+    else
+      acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(fp[h][c][i], fq[h][c][j], acc[i][j], 0, 0, 0);
+  };
+  // The products of half h. Between them the reads of half h ^ 1 (of tiles
+  // `buf`), as early as they can go but behind the first product, and for
+  // `reload` the loads into tiles `to`.
+  auto half_step = [&](int buf, int h, bool reload, int to) {
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      f16x8 fp[S::MI], fq[S::NI];
+    for (int e = 0; e < MFMAS; ++e) {
+      product(h, e);
+      constexpr int RATE = READS > MFMAS ? READS / MFMAS : 1;  // reads behind a product
 #pragma unroll
-      for (int i = 0; i < S::MI; ++i) {
-        const int r = wi * S::TM + i * 16 + fr;
-        fp[i] = *reinterpret_cast<const f16x8 *>(sp + r * 128 + ns_swizzle(r, h * 4 + fc) * 16);
+      for (int r = 0; r < RATE; ++r)
+        if (e * RATE + r < READS) read(buf, h ^ 1, e * RATE + r);
+      if (h == 1) {
+#pragma unroll
+        for (int g = e * ALL_LOADS / MFMAS; g < (e + 1) * ALL_LOADS / MFMAS; ++g)
+          if (reload) load(to, g);
       }
-#pragma unroll
-      for (int j = 0; j < S::NI; ++j) {
-        const int r = wj * S::TN + j * 16 + fr;
-        fq[j] = *reinterpret_cast<const f16x8 *>(sq + r * 128 + ns_swizzle(r, h * 4 + fc) * 16);
-      }
-#pragma unroll
-      for (int i = 0; i < S::MI; ++i)
-#pragma unroll
-        for (int j = 0; j < S::NI; ++j)
-          acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(fp[i], fq[j], acc[i][j], 0, 0, 0);
+      __builtin_amdgcn_sched_barrier(0);
     }
-    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-    __builtin_amdgcn_s_barrier();
-    asm volatile("" ::: "memory");
+  };
+  aim(0);
+#pragma unroll
+  for (int g = 0; g < ALL_LOADS; ++g) load(0, g);
+  if (total > 1) {
+    aim(1);
+#pragma unroll
+    for (int g = 0; g < ALL_LOADS; ++g) load(1, g);
+    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(ALL_LOADS) : "memory");
+  } else {
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
   }
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+#pragma unroll
+  for (int g = 0; g < READS; ++g) read(0, 0, g);
+  // One depth step. While the products of its first half run, the second
+  // half's operands are read; then one barrier (every wave has read the
+  // step's tiles, and the next step's have arrived), and while the second
+  // half's products run, the tiles just read are refilled with the step after
+  // next and the next step's first operands are read (after the last step:
+  // tiles that are there and not used).
+  for (int k = 0; k < total; ++k) {
+    const int buf = k & 1;
+    half_step(buf, 0, false, 0);
+    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+    const bool reload = k + 2 < total;
+    if (reload) aim(k + 2);
+    half_step(buf ^ 1, 1, reload, buf);
+  }
+  asm volatile("s_nop 15\n\ts_nop 15" ::: "memory");
 
-  // Epilogue. Lane: column j = lane & 15 of a 16 x 16 piece, rows 4 (lane >> 4)
-  // + 0..3: four consecutive values of a row of C^T.
+  // Epilogue. A lane holds column fr of an instruction's tile and, in run g, its
+  // rows 4 (64 / MT) g + 4 fc + 0..3: four consecutive values of a row of C^T.
   const float alpha = q.first ? q.scales[t.mat].alpha : 1.0f / q.sx;
   auto split = [](float v, half_t &h, half_t &l) {
     h = static_cast<half_t>(v);
@@ -300,9 +343,13 @@ __global__ void __launch_bounds__(NsShape<T>::WAVES * 64) ns_product_kernel(cons
 #pragma unroll
   for (int i = 0; i < S::MI; ++i)
 #pragma unroll
-    for (int j = 0; j < S::NI; ++j) {
-      const int64_t row = static_cast<int64_t>(t.ti) * T + wi * S::TM + i * 16 + fc * 4;
-      const int64_t col = static_cast<int64_t>(t.tj) * T + wj * S::TN + j * 16 + fr;
+    for (int jg = 0; jg < S::NI * S::GROUPS; ++jg) {
+      const int j = jg / S::GROUPS, gr = jg % S::GROUPS;
+      const int64_t row = static_cast<int64_t>(t.ti) * T + wi * S::TM + i * S::MT + gr * 8 + fc * 4;
+      const int64_t col = static_cast<int64_t>(t.tj) * T + wj * S::TN + j * S::MT + fr;
+      f32x4 cv;
+#pragma unroll
+      for (int r = 0; r < 4; ++r) cv[r] = acc[i][j][gr * 4 + r];
       f16x4 h, l;
       if constexpr (KIND == kGram || KIND == kPoly) {
         half_t *out = q.ws + (KIND == kGram ? mt.a : mt.b);
@@ -310,7 +357,7 @@ __global__ void __launch_bounds__(NsShape<T>::WAVES * 64) ns_product_kernel(cons
         if constexpr (KIND == kGram) {
           const float f = alpha * alpha * q.sa;
 #pragma unroll
-          for (int r = 0; r < 4; ++r) v[r] = acc[i][j][r] * f;
+          for (int r = 0; r < 4; ++r) v[r] = cv[r] * f;
         } else {
           // A is stored whole, so its value at (row, col) is that at (col, row)
           const f16x4 ah = *reinterpret_cast<const f16x4 *>(q.ws + mt.a + col * mp + row);
@@ -321,7 +368,7 @@ __global__ void __launch_bounds__(NsShape<T>::WAVES * 64) ns_product_kernel(cons
           for (int r = 0; r < 4; ++r) {
             float av = static_cast<float>(ah[r]);
             if (SEG == 3) av += static_cast<float>(al[r]);
-            v[r] = fb * av + fc2 * acc[i][j][r];
+            v[r] = fb * av + fc2 * cv[r];
           }
         }
 #pragma unroll
@@ -346,7 +393,7 @@ __global__ void __launch_bounds__(NsShape<T>::WAVES * 64) ns_product_kernel(cons
         float v[4];
 #pragma unroll
         for (int r = 0; r < 4; ++r)
-          v[r] = fa * (static_cast<float>(xh[r]) + q.carry * static_cast<float>(xl[r])) + fb * acc[i][j][r];
+          v[r] = fa * (static_cast<float>(xh[r]) + q.carry * static_cast<float>(xl[r])) + fb * cv[r];
         if constexpr (KIND == kUpdate) {
 #pragma unroll
           for (int r = 0; r < 4; ++r) { half_t hh, ll; split(v[r], hh, ll); h[r] = hh; l[r] = ll; }
