@@ -23,9 +23,8 @@ struct NsMatrix {
   int32_t tall;
   int32_t part0, nparts;  // this matrix's partial sums of squares in the group's
   int32_t pad_;
-  int64_t x;        // X, mp x np
-  int64_t xt[2];    // X^T, np x mp, of even and odd steps
-  int64_t lo;       // what X^T's fp16 values leave of X^T, np x mp
+  int64_t x[2];     // X of even and odd steps, mp x np
+  int64_t lo;       // what X's fp16 values leave of X, mp x np
   int64_t a, b;     // A and B, mp x mp
 };
 

@@ -2,12 +2,13 @@
 //   X_0 = G / (||G||_F + eps);  A = X X^T;  B = b A + c A^2;  X <- a X + B X
 // on the smaller side of each matrix (a tall G is worked on as its transpose).
 //
-// Every product is of the form C = P Q^T with both operands contiguous along
-// the summed axis: A = X X^T, A^2 = A A^T (A is symmetric) and B X = B (X^T)^T,
-// so one kernel serves all three and X is kept in both orientations. A and B
-// are symmetric: only tiles on and below the diagonal are computed, and each
-// is stored twice, which takes a step from 4 m^2 n + 2 m^3 operations to
-// 3 m^2 n + m^3.
+// Every product is a sum over the rows' elements of two operands. A = X X^T and
+// A^2 = A A^T (A is symmetric) take both operands as they lie; in B X the
+// summed axis runs down X's rows, and its pieces are turned on the way from
+// LDS to the registers (transposing LDS reads), so X is kept in one
+// orientation. A and B are symmetric: only tiles on and below the diagonal
+// are computed, and each is stored twice, which takes a step from
+// 4 m^2 n + 2 m^3 operations to 3 m^2 n + m^3.
 //
 // Numbers. The matrix instructions take fp16 operands and sum in fp32. X, A and
 // B have bounded spectra, so powers of two bring them into fp16's range,
@@ -81,11 +82,11 @@ __global__ void __launch_bounds__(256) ns_norm_kernel(const NsMatrix *mats, cons
   if (threadIdx.x == 0) partials[mt.part0 + t.ti] = b;
 }
 
-// Writes X and X^T (both padded with zeros) of the first step, scaled by the
-// power of two that brings the norm into [2^13, 2^14): exact for bf16 but for
-// elements below 2^-28 of the norm. Each block adds its matrix's partial sums
-// again, in index order (every block the same value); the matrix's first
-// block stores alpha.
+// Writes the first step's X (padded with zeros; the transpose of a tall
+// matrix), scaled by the power of two that brings the norm into [2^13, 2^14):
+// exact for bf16 but for elements below 2^-28 of the norm. Each block adds its
+// matrix's partial sums again, in index order (every block the same value);
+// the matrix's first block stores alpha.
 template <int D, int SEG>
 __global__ void __launch_bounds__(256) ns_convert_kernel(const NsMatrix *mats, const NsTile *tiles, const void *src,
                                                          const double *partials, NsScale *scales, half_t *ws,
@@ -120,32 +121,25 @@ __global__ void __launch_bounds__(256) ns_convert_kernel(const NsMatrix *mats, c
   }
   __syncthreads();
   const int64_t plane = static_cast<int64_t>(mt.mp) * mt.np;
-  half_t *straight = ws + (mt.tall ? mt.xt[0] : mt.x);   // rows x cols order
-  half_t *turned = ws + (mt.tall ? mt.x : mt.xt[0]);
-  const int64_t sld = mt.tall ? mt.mp : mt.np, tld = mt.tall ? mt.np : mt.mp;
+  half_t *x = ws + mt.x[0];
   for (int k = threadIdx.x; k < kConvTile * 8; k += 256) {
     const int r = k >> 3, c = (k & 7) * 8;
-    f16x8 h, l, th, tl;
+    f16x8 h, l;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      const float v = sh[r][c + j], w = sh[c + j][r];
+      const float v = mt.tall ? sh[c + j][r] : sh[r][c + j];
       h[j] = static_cast<half_t>(v);
-      th[j] = static_cast<half_t>(w);
       l[j] = static_cast<half_t>(v - static_cast<float>(h[j]));
-      tl[j] = static_cast<half_t>(w - static_cast<float>(th[j]));
     }
-    const int64_t s = (r0 + r) * sld + c0 + c, u = (c0 + r) * tld + r0 + c;
-    *reinterpret_cast<f16x8 *>(straight + s) = h;
-    *reinterpret_cast<f16x8 *>(turned + u) = th;
-    if (SEG == 3) {
-      *reinterpret_cast<f16x8 *>(straight + plane + s) = l;
-      *reinterpret_cast<f16x8 *>(turned + plane + u) = tl;
-    }
+    const int64_t e = mt.tall ? (c0 + r) * static_cast<int64_t>(mt.np) + r0 + c
+                              : (r0 + r) * static_cast<int64_t>(mt.np) + c0 + c;
+    *reinterpret_cast<f16x8 *>(x + e) = h;
+    if (SEG == 3) *reinterpret_cast<f16x8 *>(x + plane + e) = l;
   }
 }
 
 // ---------------------------------------------------------------------------
-// The product C = P Q^T
+// The products
 // ---------------------------------------------------------------------------
 
 enum NsKind { kGram = 0, kPoly = 1, kUpdate = 2, kLast = 3 };
@@ -161,121 +155,170 @@ struct NsArgs {
   float sa, sb, sx;    // powers of two: A, B and X (but the first) as stored
   float carry;         // factor of X's remainder in a X
   int32_t first;       // the first step: X is scaled by its own alpha
-  int32_t odd;         // which X^T is read
+  int32_t odd;         // which X is read
 };
 
+// A block of four waves computes a T x T tile, each wave a quarter.
 template <int T>
 struct NsShape {
-  static constexpr int WN = 2, WAVES = 4;
-  static constexpr int TM = T / 2, TN = T / 2;     // a wave's part of the tile
+  static constexpr int WAVES = 4;
+  static constexpr int TW = T / 2;                 // a wave's part of the tile, TW x TW
   static constexpr int MT = T == 64 ? 16 : 32;     // the matrix instruction's tile, MT x MT x (512 / MT)
-  static constexpr int MI = TM / MT, NI = TN / MT;
+  static constexpr int MI = TW / MT;
   static constexpr int KI = MT / 16;               // instructions deep in half a depth step
-  static constexpr int GROUPS = MT * MT / 256;     // a lane's runs of 4 rows in an instruction's tile
+  static constexpr int RUNS = MT * MT / 256;       // a lane's runs of 4 rows in an instruction's tile
   static constexpr int LOADS = T / 8 / WAVES;      // 1 KiB loads of a wave per operand and depth step
+  static constexpr int STAGE = T * 128;            // bytes of an operand's tile in LDS
+  // the epilogue's strip: MT rows of the wave's part, 16 bits an element
+  static constexpr int ROW = TW * 2, CHUNKS = TW / 8;
+  static constexpr int STRIP = MT * ROW;
+  static constexpr int MOVES = STRIP / 1024;       // 1 KiB accesses of a wave per strip
 };
 
-// Position of 16-byte chunk c of row r in an operand's LDS tile (128-byte
-// rows): the 16 rows that a matrix instruction's operand read covers at once
-// fall on all banks.
-__device__ __forceinline__ int ns_swizzle(int r, int c) { return c ^ ((r >> 1) & 7); }
+// Positions of the 16-byte chunks in LDS, so that one access of a wave falls on
+// all banks alike. An operand read as it lies: tile rows of 128 bytes, 16 (or
+// 32) rows read at one chunk.
+__device__ __forceinline__ int ns_swizzle(int row, int chunk) { return chunk ^ ((row >> 1) & 7); }
+// X in B X: 64 rows of 2 T bytes; a transposing read takes 4 + 4 rows at 32 or
+// 64 bytes.
+template <int T>
+__device__ __forceinline__ int ns_swizzle_x(int row, int chunk) {
+  if (T == 256) return chunk ^ (((row & 3) | ((row >> 1) & 4)) << 2);
+  if (T == 128) return chunk ^ ((row & 3) << 2);
+  return chunk ^ ((((row >> 1) & 1) | ((row >> 2) & 2)) << 1);
+}
+// A strip of the epilogue, written by columns and read by rows.
+template <int T>
+__device__ __forceinline__ int ns_swizzle_strip(int row, int chunk) { return chunk ^ (row & (NsShape<T>::CHUNKS - 1)); }
+
+// Four rows of 16-bit columns turned: within 16 lanes, lane i addresses 8 bytes
+// of row i / 4 and receives column i of the four rows.
+__device__ __forceinline__ f16x4 read_turned(const char *p) {
+  typedef short s16x4 __attribute__((ext_vector_type(4)));
+  typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+  return __builtin_bit_cast(f16x4, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(p)));
+}
+
+// 16 bytes a lane from global memory to LDS, 1 KiB from LDS address `lds` on in
+// lane order. Written out, because the compiler takes every transposing read
+// for a reader of what its own form of this load brings and waits for all
+// loads in front of each. It has no output register; the waits are this
+// file's own, and so is the wait state between the write of m0 and its use.
+__device__ __forceinline__ void to_lds(const void *global, uint32_t lds) {
+  asm volatile("s_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(global), "{m0}"(lds) : "memory");
+}
+__device__ __forceinline__ uint32_t lds_address(const void *p) {
+  return __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(reinterpret_cast<uintptr_t>((lds_void *)p)));
+}
+__device__ __forceinline__ void block_barrier() {
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
 
 template <int T, int SEG, int KIND>
-__global__ void __launch_bounds__(NsShape<T>::WAVES * 64, T == 256 ? 1 : 2) ns_product_kernel(const NsArgs q) {
+__global__ void __launch_bounds__(256, T == 256 ? 1 : 2) ns_product_kernel(const NsArgs q) {
   typedef NsShape<T> S;
-  constexpr int STAGE = T * 128;  // bytes of one operand's tile
-  __shared__ __align__(1024) char smem[2][2][STAGE];
+  constexpr bool TURN = KIND == kUpdate || KIND == kLast;  // P is X, read down its rows
+  __shared__ __align__(1024) char smem[2][2][S::STAGE];
   if (q.sc && q.sc->overflow) return;
   const NsTile t = q.tiles[blockIdx.x];
   const NsMatrix &mt = q.mats[t.mat];
   const int lane = threadIdx.x & 63;
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int wi = w / S::WN, wj = w % S::WN;
+  const int wi = w >> 1, wj = w & 1;
   const int64_t mp = mt.mp, np = mt.np;
   const int64_t xplane = mp * np, aplane = mp * mp;
-  const half_t *P, *Q;
-  int64_t pplane, qplane;
-  int depth;       // summed elements
-  int64_t ld;
-  if constexpr (KIND == kGram) {
-    P = Q = q.ws + mt.x;
-    pplane = qplane = xplane;
-    depth = mt.np;
-    ld = np;
-  } else if constexpr (KIND == kPoly) {
-    P = Q = q.ws + mt.a;
-    pplane = qplane = aplane;
-    depth = mt.mp;
-    ld = mp;
-  } else {
-    P = q.ws + mt.b;
-    Q = q.ws + mt.xt[q.odd];
-    pplane = aplane;
-    qplane = xplane;
-    depth = mt.mp;
-    ld = mp;
-  }
-  const int steps = depth / kNsDepth;
+  // C = P Q^T, tile (ti, tj): rows of P are columns of what is stored
+  half_t *const xin = q.ws + mt.x[q.odd];
+  const half_t *const P = KIND == kPoly ? q.ws + mt.a : xin;
+  const half_t *const Q = KIND == kGram ? xin : q.ws + (KIND == kPoly ? mt.a : mt.b);
+  const int64_t pld = KIND == kPoly ? mp : np, qld = KIND == kGram ? np : mp;
+  const int64_t pplane = KIND == kPoly ? aplane : xplane, qplane = KIND == kGram ? xplane : aplane;
+  const int steps = (KIND == kGram ? mt.np : mt.mp) / kNsDepth;
   const int total = steps * SEG;
-  // the lane's place in a load: row lane / 8 of the wave's 8 rows, chunk by
-  // the swizzle (the same for all of the wave's loads: their first rows are
-  // 8 WAVES apart, a multiple of 16)
-  const int lrow = w * 8 + (lane >> 3);
-  const uint32_t lane_off = static_cast<uint32_t>(lrow * ld * 2 + ns_swizzle(lrow, lane & 7) * 16);
-  const uint32_t row_step = static_cast<uint32_t>(8 * S::WAVES * ld * 2);
-  const half_t *p0 = P + static_cast<int64_t>(t.ti) * T * ld;
-  const half_t *q0 = Q + static_cast<int64_t>(t.tj) * T * ld;
-  typedef float AccT __attribute__((ext_vector_type(4 * S::GROUPS)));
-  AccT acc[S::MI][S::NI];
+
+  typedef float AccT __attribute__((ext_vector_type(4 * S::RUNS)));
+  AccT acc[S::MI][S::MI];
 #pragma unroll
   for (int i = 0; i < S::MI; ++i)
 #pragma unroll
-    for (int j = 0; j < S::NI; ++j)
+    for (int j = 0; j < S::MI; ++j)
 #pragma unroll
-      for (int r = 0; r < 4 * S::GROUPS; ++r) acc[i][j][r] = 0.0f;
+      for (int r = 0; r < 4 * S::RUNS; ++r) acc[i][j][r] = 0.0f;
 
-  // Load g of depth step k (T / 16 of them, P's before Q's): global to LDS
-  // without passing through registers; the LDS side is linear, so the lane
-  // takes the chunk that belongs at its position.
+  // Loads of a depth step: global to LDS without passing through registers.
+  // The LDS side of a load is linear (1 KiB), so the lane takes the chunk that
+  // belongs at its position. Load r of wave w is piece w + 4 r of the tile; the
+  // swizzle of its rows is the same for every r, but for X at T = 256, where
+  // it alternates.
+  const int lrow = w * 8 + (lane >> 3);
+  const uint32_t q_off = static_cast<uint32_t>(lrow * qld * 2 + ns_swizzle(lrow, lane & 7) * 16);
+  const uint64_t q_step = static_cast<uint64_t>(32 * qld * 2);
+  constexpr int XC = T / 8;  // chunks of a row of X's tile
+  const int xrow = w * (64 / XC) + lane / XC;
+  uint32_t p_off[2];
+#pragma unroll
+  for (int v = 0; v < 2; ++v)
+    p_off[v] = TURN ? static_cast<uint32_t>(xrow * pld * 2 + ns_swizzle_x<T>(xrow + v * 8 * (T == 256), lane % XC) * 16)
+                    : static_cast<uint32_t>(lrow * pld * 2 + ns_swizzle(lrow, lane & 7) * 16);
+  const uint64_t p_step = static_cast<uint64_t>((TURN ? 256 / XC : 32) * pld * 2);
+  const half_t *const p0 = P + (TURN ? static_cast<int64_t>(t.ti) * T : static_cast<int64_t>(t.ti) * T * pld);
+  const half_t *const q0 = Q + static_cast<int64_t>(t.tj) * T * qld;
   const half_t *pk = p0, *qk = q0;
   auto aim = [&](int k) {
     int seg = 0, kk = k;
-    if (SEG == 3) {
+    if (SEG == 3) {  // pieces: high*high, high*low, low*high
       seg = k / steps;
       kk = k - seg * steps;
     }
-    // pieces: high*high, high*low, low*high
-    pk = p0 + (seg == 2 ? pplane : 0) + static_cast<int64_t>(kk) * kNsDepth;
-    qk = q0 + (seg == 1 ? qplane : 0) + static_cast<int64_t>(kk) * kNsDepth;
+    pk = p0 + (seg == 1 ? pplane : 0) + static_cast<int64_t>(kk) * kNsDepth * (TURN ? pld : 1);
+    qk = q0 + (seg == 2 ? qplane : 0) + static_cast<int64_t>(kk) * kNsDepth;
   };
+  const uint32_t lds0 = lds_address(smem) + w * 1024;
   auto load = [&](int buf, int g) {
-    const int o = g / S::LOADS, r = g % S::LOADS;
-    const char *p = reinterpret_cast<const char *>(o ? qk : pk) + static_cast<uint64_t>(r) * row_step;
-    __builtin_amdgcn_global_load_lds((global_cvoid *)(p + lane_off),
-                                     (lds_void *)(smem[buf][o] + (w + r * S::WAVES) * 1024), 16, 0, 0);
+    const int r = g % S::LOADS;
+    const uint32_t at = lds0 + buf * 2 * S::STAGE + r * 4096;
+    if (g < S::LOADS) to_lds(reinterpret_cast<const char *>(pk) + r * p_step + p_off[r & 1], at);
+    else to_lds(reinterpret_cast<const char *>(qk) + r * q_step + q_off, at + S::STAGE);
   };
+
+  // Operand pieces of half h of a depth step: register buffer h.
   const int fr = lane % S::MT, fc = lane / S::MT;
-  // operand pieces of half h of a depth step: buffer h in registers
-  f16x8 fp[2][S::KI][S::MI], fq[2][S::KI][S::NI];
-  int off_p[2][S::KI], off_q[2][S::KI];
+  f16x8 fp[2][S::KI][S::MI], fq[2][S::KI][S::MI];
+  int off_p[2][S::KI], off_q[2][S::KI], off_x[S::MI];
 #pragma unroll
   for (int h = 0; h < 2; ++h)
 #pragma unroll
     for (int c = 0; c < S::KI; ++c) {
-      const int rp = wi * S::TM + fr, rq = wj * S::TN + fr, chunk = h * 4 + c * (64 / S::MT) + fc;
+      const int rp = wi * S::TW + fr, rq = wj * S::TW + fr, chunk = h * 4 + c * (64 / S::MT) + fc;
       off_p[h][c] = rp * 128 + ns_swizzle(rp, chunk) * 16;
       off_q[h][c] = rq * 128 + ns_swizzle(rq, chunk) * 16;
     }
-  // read g of half h: for each instruction depth the MI pieces of P, then the
-  // NI of Q; MT rows on are 128 MT bytes on
+#pragma unroll
+  for (int r = 0; r < S::MI; ++r) {
+    const int row = 8 * fc + ((lane & 15) >> 2);
+    const int col = wi * S::TW + r * S::MT + (S::MT == 32 ? lane & 16 : 0) + (lane & 3) * 4;
+    off_x[r] = row * 2 * T + ns_swizzle_x<T>(row, col >> 3) * 16 + (col & 4) * 2;
+  }
   auto read = [&](int buf, int h, int g) {
-    const int c = g / (S::MI + S::NI), r = g % (S::MI + S::NI);
-    if (r < S::MI) fp[h][c][r] = *reinterpret_cast<const f16x8 *>(smem[buf][0] + off_p[h][c] + r * 128 * S::MT);
-    else fq[h][c][r - S::MI] = *reinterpret_cast<const f16x8 *>(smem[buf][1] + off_q[h][c] + (r - S::MI) * 128 * S::MT);
+    const int c = g / (2 * S::MI), r = g % (2 * S::MI);
+    if (r >= S::MI) {
+      fq[h][c][r - S::MI] = *reinterpret_cast<const f16x8 *>(smem[buf][1] + off_q[h][c] + (r - S::MI) * 128 * S::MT);
+    } else if constexpr (TURN) {
+      const char *x = smem[buf][0] + off_x[r] + (h * 32 + c * 16) * 2 * T;
+      const f16x4 a = read_turned(x), b = read_turned(x + 4 * 2 * T);
+      fp[h][c][r] = __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
+    } else {
+      fp[h][c][r] = *reinterpret_cast<const f16x8 *>(smem[buf][0] + off_p[h][c] + r * 128 * S::MT);
+    }
   };
-  constexpr int MFMAS = S::MI * S::NI * S::KI, READS = (S::MI + S::NI) * S::KI, ALL_LOADS = 2 * S::LOADS;
+  constexpr int MFMAS = S::MI * S::MI * S::KI, READS = 2 * S::MI * S::KI, ALL_LOADS = 2 * S::LOADS;
+  // The accumulators are updated in place by an instruction written out: left
+  // to itself the compiler copies all 256 of them in every step. (It knows
+  // the registers but not the instruction's latency: nothing reads them
+  // before the wait behind the loop.)
   auto product = [&](int h, int e) {
-    const int c = e / (S::MI * S::NI), i = e / S::NI % S::MI, j = e % S::NI;
+    const int c = e / (S::MI * S::MI), i = e / S::MI % S::MI, j = e % S::MI;
     if constexpr (S::MT == 32)
       asm volatile("v_mfma_f32_32x32x16_f16 %0, %1, %2, %0" : "+a"(acc[i][j]) : "v"(fp[h][c][i]), "v"(fq[h][c][j]));
     else
@@ -311,8 +354,7 @@ __global__ void __launch_bounds__(NsShape<T>::WAVES * 64, T == 256 ? 1 : 2) ns_p
   } else {
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
   }
-  __builtin_amdgcn_s_barrier();
-  asm volatile("" ::: "memory");
+  block_barrier();
 #pragma unroll
   for (int g = 0; g < READS; ++g) read(0, 0, g);
   // One depth step. While the products of its first half run, the second
@@ -325,101 +367,191 @@ __global__ void __launch_bounds__(NsShape<T>::WAVES * 64, T == 256 ? 1 : 2) ns_p
     const int buf = k & 1;
     half_step(buf, 0, false, 0);
     asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
-    __builtin_amdgcn_s_barrier();
-    asm volatile("" ::: "memory");
+    block_barrier();
     const bool reload = k + 2 < total;
     if (reload) aim(k + 2);
     half_step(buf ^ 1, 1, reload, buf);
   }
-  asm volatile("s_nop 15\n\ts_nop 15" ::: "memory");
+  asm volatile("s_nop 15\n\ts_nop 15\n\ts_waitcnt lgkmcnt(0)" ::: "memory");
+  block_barrier();
 
-  // Epilogue. A lane holds column fr of an instruction's tile and, in run g, its
-  // rows 4 (64 / MT) g + 4 fc + 0..3: four consecutive values of a row of C^T.
+  // Epilogue, in strips of MT rows of what is stored, each wave on its own in
+  // its part of the LDS (two strips' room). A lane holds row fr of a strip and
+  // in it runs of 4 elements: run g of instruction tile i is at columns
+  // i MT + 8 g + 4 fc. The strip's inputs come in rows (high and low plane)
+  // and are overwritten by its outputs, which leave in rows, and for a
+  // symmetric result also turned.
   const float alpha = q.first ? q.scales[t.mat].alpha : 1.0f / q.sx;
-  auto split = [](float v, half_t &h, half_t &l) {
-    h = static_cast<half_t>(v);
-    l = static_cast<half_t>(v - static_cast<float>(h));
+  char *const room = smem[0][0] + w * 2 * 2 * S::STRIP;
+  const uint32_t room_lds = lds_address(room);
+  static_assert(4 * 2 * 2 * S::STRIP <= 4 * S::STAGE, "two strips of two planes for each wave");
+  const int64_t prow = static_cast<int64_t>(t.ti) * T + wi * S::TW;  // first column of the wave's part
+  const int64_t qrow = static_cast<int64_t>(t.tj) * T + wj * S::TW;  // first row
+  const int64_t old = TURN ? np : mp;
+  const int64_t here = qrow * old + prow;
+  const half_t *in_h = TURN ? xin : q.ws + mt.a;
+  const half_t *in_l = SEG == 3 ? in_h + (TURN ? xplane : aplane) : q.ws + mt.lo;
+  const bool low_in = SEG == 3 || (TURN && !q.first);
+  constexpr int RPI = 64 / S::CHUNKS;  // rows of a 1 KiB access
+  const int mrow = lane / S::CHUNKS, mchunk = lane % S::CHUNKS;
+  auto fetch = [&](int s) {
+    if (KIND == kGram) return;
+    const uint32_t at = room_lds + (s & 1) * 2 * S::STRIP;
+    const half_t *h = in_h + here + s * S::MT * old, *l = in_l + here + s * S::MT * old;
+#pragma unroll
+    for (int g = 0; g < S::MOVES; ++g) {
+      const int r = g * RPI + mrow;
+      to_lds(h + r * old + ns_swizzle_strip<T>(r, mchunk) * 8, at + g * 1024);
+    }
+    if (low_in) {
+#pragma unroll
+      for (int g = 0; g < S::MOVES; ++g) {
+        const int r = g * RPI + mrow;
+        to_lds(l + r * old + ns_swizzle_strip<T>(r, mchunk) * 8, at + S::STRIP + g * 1024);
+      }
+    }
   };
+  // rows of plane `at` to global memory
+  auto put_rows = [&](const char *at, half_t *out, int s) {
+    half_t *o = out + here + s * S::MT * old;
 #pragma unroll
-  for (int i = 0; i < S::MI; ++i)
+    for (int g = 0; g < S::MOVES; ++g) {
+      const int r = g * RPI + mrow;
+      const f16x8 v = *reinterpret_cast<const f16x8 *>(at + r * S::ROW + ns_swizzle_strip<T>(r, mchunk) * 16);
+      *reinterpret_cast<f16x8 *>(o + r * old + mchunk * 8) = v;
+    }
+  };
+  // eight rows of plane `at` from row r on, turned: column col of them
+  auto turned8 = [&](const char *at, int r, int col) {
+    // within the lane's group of 16: row (lane & 15) / 4, columns 4 (lane & 3) on
+    const int cc = (col & ~15) + (lane & 3) * 4, ra = r + ((lane & 15) >> 2), rb = ra + 4;
+    const f16x4 a = read_turned(at + ra * S::ROW + ns_swizzle_strip<T>(ra, cc >> 3) * 16 + (cc & 4) * 2);
+    const f16x4 b = read_turned(at + rb * S::ROW + ns_swizzle_strip<T>(rb, cc >> 3) * 16 + (cc & 4) * 2);
+    return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
+  };
+  constexpr int GR = S::MT / 8;        // groups of 8 rows in a strip
+  constexpr int PC = 64 / GR;          // columns that a wave's turned access covers
+  const int tgrp = (lane >> 4) % GR * 8, tcol = (lane >> 4) / GR * 16 + (lane & 15);
+  auto put_turned = [&](const char *at, half_t *out, int s) {
+    half_t *o = out + prow * old + qrow + s * S::MT;
 #pragma unroll
-    for (int jg = 0; jg < S::NI * S::GROUPS; ++jg) {
-      const int j = jg / S::GROUPS, gr = jg % S::GROUPS;
-      const int64_t row = static_cast<int64_t>(t.ti) * T + wi * S::TM + i * S::MT + gr * 8 + fc * 4;
-      const int64_t col = static_cast<int64_t>(t.tj) * T + wj * S::TN + j * S::MT + fr;
-      f32x4 cv;
+    for (int c = 0; c < S::TW; c += PC) {
+      const f16x8 v = turned8(at, tgrp, c + tcol);
+      *reinterpret_cast<f16x8 *>(o + (c + tcol) * old + tgrp) = v;
+    }
+  };
+  fetch(0);
+  if (S::MI > 1) fetch(1);
 #pragma unroll
-      for (int r = 0; r < 4; ++r) cv[r] = acc[i][j][gr * 4 + r];
-      f16x4 h, l;
-      if constexpr (KIND == kGram || KIND == kPoly) {
-        half_t *out = q.ws + (KIND == kGram ? mt.a : mt.b);
-        float v[4];
-        if constexpr (KIND == kGram) {
-          const float f = alpha * alpha * q.sa;
-#pragma unroll
-          for (int r = 0; r < 4; ++r) v[r] = cv[r] * f;
-        } else {
-          // A is stored whole, so its value at (row, col) is that at (col, row)
-          const f16x4 ah = *reinterpret_cast<const f16x4 *>(q.ws + mt.a + col * mp + row);
-          f16x4 al = {};
-          if (SEG == 3) al = *reinterpret_cast<const f16x4 *>(q.ws + mt.a + aplane + col * mp + row);
-          const float fb = q.b * (q.sb / q.sa), fc2 = q.c * (q.sb / (q.sa * q.sa));
-#pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            float av = static_cast<float>(ah[r]);
-            if (SEG == 3) av += static_cast<float>(al[r]);
-            v[r] = fb * av + fc2 * cv[r];
-          }
-        }
-#pragma unroll
-        for (int r = 0; r < 4; ++r) { half_t hh, ll; split(v[r], hh, ll); h[r] = hh; l[r] = ll; }
-        *reinterpret_cast<f16x4 *>(out + col * mp + row) = h;
-        if (SEG == 3) *reinterpret_cast<f16x4 *>(out + aplane + col * mp + row) = l;
-        if (t.ti != t.tj) {
-#pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            out[(row + r) * mp + col] = h[r];
-            if (SEG == 3) out[aplane + (row + r) * mp + col] = l[r];
-          }
-        }
+  for (int s = 0; s < S::MI; ++s) {
+    char *at = room + (s & 1) * 2 * S::STRIP;
+    if (KIND != kGram) {
+      // the next strip's loads may still be on their way; what was stored in between counts too
+      if (s + 1 < S::MI) {
+        if (low_in) asm volatile("s_waitcnt vmcnt(%0)" ::"n"(2 * S::MOVES) : "memory");
+        else asm volatile("s_waitcnt vmcnt(%0)" ::"n"(S::MOVES) : "memory");
       } else {
-        const half_t *xin = q.ws + mt.xt[q.odd];
-        const f16x4 xh = *reinterpret_cast<const f16x4 *>(xin + col * mp + row);
-        f16x4 xl = {};
-        if (SEG == 3) xl = *reinterpret_cast<const f16x4 *>(xin + xplane + col * mp + row);
-        else if (!q.first) xl = *reinterpret_cast<const f16x4 *>(q.ws + mt.lo + col * mp + row);
-        const float out_scale = KIND == kLast ? 1.0f : q.sx;
-        const float fa = q.a * alpha * out_scale, fb = alpha / q.sb * out_scale;
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+      }
+    }
+    const char *line = at + fr * S::ROW;
+    float f0 = 0.0f, f1;  // v = f0 (high + carry low) + f1 acc
+    if (KIND == kGram) {
+      f1 = alpha * alpha * q.sa;
+    } else if (KIND == kPoly) {
+      f0 = q.b * (q.sb / q.sa);
+      f1 = q.c * (q.sb / (q.sa * q.sa));
+    } else {
+      const float os = KIND == kLast ? 1.0f : q.sx;
+      f0 = q.a * alpha * os;
+      f1 = alpha / q.sb * os;
+    }
+    const float carry = TURN ? q.carry : 1.0f;
+#pragma unroll
+    for (int i = 0; i < S::MI; ++i)
+#pragma unroll
+      for (int g = 0; g < S::RUNS; ++g) {
+        const int col = i * S::MT + g * 8 + fc * 4;
+        char *p = const_cast<char *>(line) + ns_swizzle_strip<T>(fr, col >> 3) * 16 + (col & 4) * 2;
+        f16x4 h = {}, l = {};
+        if (KIND != kGram) h = *reinterpret_cast<const f16x4 *>(p);
+        if (KIND != kGram && low_in) l = *reinterpret_cast<const f16x4 *>(p + S::STRIP);
         float v[4];
 #pragma unroll
-        for (int r = 0; r < 4; ++r)
-          v[r] = fa * (static_cast<float>(xh[r]) + q.carry * static_cast<float>(xl[r])) + fb * cv[r];
-        if constexpr (KIND == kUpdate) {
+        for (int r = 0; r < 4; ++r) {
+          v[r] = f1 * acc[i][s][4 * g + r];
+          if (KIND != kGram) v[r] += f0 * (static_cast<float>(h[r]) + carry * static_cast<float>(l[r]));
+        }
+        if constexpr (KIND == kLast) {
+          if constexpr (SEG == 1) {
+            const u32x2 o = {pack2<ZDS_BF16>(v[0], v[1]), pack2<ZDS_BF16>(v[2], v[3])};
+            *reinterpret_cast<u32x2 *>(p) = o;
+          } else {
+            // fp32: straight from the registers
+            const int64_t i0 = qrow + s * S::MT + fr, j0 = prow + col;
+            if (i0 < mt.m) {
 #pragma unroll
-          for (int r = 0; r < 4; ++r) { half_t hh, ll; split(v[r], hh, ll); h[r] = hh; l[r] = ll; }
-          half_t *xout = q.ws + mt.xt[q.odd ^ 1];
-          *reinterpret_cast<f16x4 *>(xout + col * mp + row) = h;
-          *reinterpret_cast<f16x4 *>((SEG == 3 ? xout + xplane : q.ws + mt.lo) + col * mp + row) = l;
-          half_t *x = q.ws + mt.x;
-#pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            x[(row + r) * np + col] = h[r];
-            if (SEG == 3) x[xplane + (row + r) * np + col] = l[r];
-          }
-        } else {
-          if (col < mt.n) {
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-              if (row + r < mt.m) {
-                const int64_t e = mt.offset + (mt.tall ? col * mt.cols + row + r : (row + r) * mt.cols + col);
-                if (SEG == 3) static_cast<float *>(q.dst)[e] = v[r];
-                else static_cast<uint16_t *>(q.dst)[e] = narrow1<ZDS_BF16>(v[r]);
-              }
+              for (int r = 0; r < 4; ++r)
+                if (j0 + r < mt.n)
+                  static_cast<float *>(q.dst)[mt.offset + (mt.tall ? (j0 + r) * mt.cols + i0 : i0 * mt.cols + j0 + r)] = v[r];
             }
           }
+        } else {
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            h[r] = static_cast<half_t>(v[r]);
+            l[r] = static_cast<half_t>(v[r] - static_cast<float>(h[r]));
+          }
+          *reinterpret_cast<f16x4 *>(p) = h;
+          if (SEG == 3 || KIND == kUpdate) *reinterpret_cast<f16x4 *>(p + S::STRIP) = l;
+        }
+      }
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    if constexpr (KIND == kGram || KIND == kPoly) {
+      half_t *out = q.ws + (KIND == kGram ? mt.a : mt.b);
+      put_rows(at, out, s);
+      if (SEG == 3) put_rows(at + S::STRIP, out + aplane, s);
+      if (t.ti != t.tj) {
+        put_turned(at, out, s);
+        if (SEG == 3) put_turned(at + S::STRIP, out + aplane, s);
+      }
+    } else if constexpr (KIND == kUpdate) {
+      half_t *out = q.ws + mt.x[q.odd ^ 1];
+      put_rows(at, out, s);
+      put_rows(at + S::STRIP, SEG == 3 ? out + xplane : q.ws + mt.lo, s);
+    } else if constexpr (SEG == 1) {
+      // the result, in its own orientation and inside its bounds: 16-byte
+      // pieces where the rows lie on them, else element by element
+      uint16_t *dst = static_cast<uint16_t *>(q.dst) + mt.offset;
+      const bool vec = aligned(dst, 16) && (mt.cols & 7) == 0;
+      const int64_t i0 = qrow + s * S::MT, j0 = prow;
+      if (vec && !mt.tall) {
+#pragma unroll
+        for (int g = 0; g < S::MOVES; ++g) {
+          const int r = g * RPI + mrow;
+          const u32x4 v = *reinterpret_cast<const u32x4 *>(at + r * S::ROW + ns_swizzle_strip<T>(r, mchunk) * 16);
+          if (i0 + r < mt.m && j0 + mchunk * 8 < mt.n)
+            *reinterpret_cast<u32x4 *>(dst + (i0 + r) * mt.cols + j0 + mchunk * 8) = v;
+        }
+      } else if (vec) {
+#pragma unroll
+        for (int c = 0; c < S::TW; c += PC) {
+          const u32x4 v = __builtin_bit_cast(u32x4, turned8(at, tgrp, c + tcol));
+          if (j0 + c + tcol < mt.n && i0 + tgrp < mt.m)
+            *reinterpret_cast<u32x4 *>(dst + (j0 + c + tcol) * mt.cols + i0 + tgrp) = v;
+        }
+      } else {
+        for (int e = lane; e < S::MT * S::TW; e += 64) {
+          const int r = mt.tall ? e % S::MT : e / S::TW, c = mt.tall ? e / S::MT : e % S::TW;
+          const uint16_t v = *reinterpret_cast<const uint16_t *>(at + r * S::ROW + ns_swizzle_strip<T>(r, c >> 3) * 16 + (c & 7) * 2);
+          if (i0 + r < mt.m && j0 + c < mt.n)
+            dst[mt.tall ? (j0 + c) * mt.cols + i0 + r : (i0 + r) * mt.cols + j0 + c] = v;
         }
       }
     }
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    if (s + 2 < S::MI) fetch(s + 2);
+  }
 }
 
 // ---------------------------------------------------------------------------
@@ -540,9 +672,8 @@ zds_status build_newton_schulz(zds_matrix_plan *p, const int64_t *offset, const 
           const int64_t planes = f ? 2 : 1;
           NsMatrix d = m;
           auto take = [&](int64_t e) { const int64_t at = pos[f]; pos[f] += e; return at; };
-          d.x = take(xe * planes);
-          d.xt[0] = take(xe * planes);
-          d.xt[1] = take(xe * planes);
+          d.x[0] = take(xe * planes);
+          d.x[1] = take(xe * planes);
           d.lo = f ? 0 : take(xe);
           d.a = take(ae * planes);
           d.b = take(ae * planes);
@@ -571,7 +702,7 @@ zds_status build_newton_schulz(zds_matrix_plan *p, const int64_t *offset, const 
       spread_over_dies(tiles, static_cast<size_t>(g.tri0));
       g.ntri = static_cast<int32_t>(tiles.size()) - g.tri0;
       g.full0 = static_cast<int32_t>(tiles.size());
-      each([&](int32_t k, const NsMatrix &m) { add_tiles(tiles, k, m.mp / tile, m.np / tile, false); });
+      each([&](int32_t k, const NsMatrix &m) { add_tiles(tiles, k, m.np / tile, m.mp / tile, false); });
       spread_over_dies(tiles, static_cast<size_t>(g.full0));
       g.nfull = static_cast<int32_t>(tiles.size()) - g.full0;
       p->groups.push_back(g);
