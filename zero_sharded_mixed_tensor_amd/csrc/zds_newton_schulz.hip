@@ -207,6 +207,16 @@ __device__ __forceinline__ f16x4 read_turned(const char *p) {
 __device__ __forceinline__ void to_lds(const void *global, uint32_t lds) {
   asm volatile("s_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(global), "{m0}"(lds) : "memory");
 }
+// The same in the form that costs the wave no address arithmetic: a buffer
+// descriptor (base, size in bytes: an access behind it loads nothing), a
+// lane's offset and the load's.
+__device__ __forceinline__ u32x4 buffer_at(const void *p, uint32_t bytes) {
+  const uint64_t a = reinterpret_cast<uint64_t>(p);
+  return u32x4{static_cast<uint32_t>(a), static_cast<uint32_t>(a >> 32) & 0xffffu, bytes, 0x00027000u};
+}
+__device__ __forceinline__ void buffer_to_lds(u32x4 desc, uint32_t lane_off, uint32_t off, uint32_t lds) {
+  asm volatile("s_nop 0\n\tbuffer_load_dwordx4 %0, %1, %2 offen lds" ::"v"(lane_off), "s"(desc), "s"(off), "{m0}"(lds) : "memory");
+}
 __device__ __forceinline__ uint32_t lds_address(const void *p) {
   return __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(reinterpret_cast<uintptr_t>((lds_void *)p)));
 }
@@ -253,7 +263,7 @@ __global__ void __launch_bounds__(256, T == 256 ? 1 : 2) ns_product_kernel(const
   // it alternates.
   const int lrow = w * 8 + (lane >> 3);
   const uint32_t q_off = static_cast<uint32_t>(lrow * qld * 2 + ns_swizzle(lrow, lane & 7) * 16);
-  const uint64_t q_step = static_cast<uint64_t>(32 * qld * 2);
+  const uint32_t q_step = static_cast<uint32_t>(32 * qld * 2);
   constexpr int XC = T / 8;  // chunks of a row of X's tile
   const int xrow = w * (64 / XC) + lane / XC;
   uint32_t p_off[2];
@@ -261,27 +271,22 @@ __global__ void __launch_bounds__(256, T == 256 ? 1 : 2) ns_product_kernel(const
   for (int v = 0; v < 2; ++v)
     p_off[v] = TURN ? static_cast<uint32_t>(xrow * pld * 2 + ns_swizzle_x<T>(xrow + v * 8 * (T == 256), lane % XC) * 16)
                     : static_cast<uint32_t>(lrow * pld * 2 + ns_swizzle(lrow, lane & 7) * 16);
-  const uint64_t p_step = static_cast<uint64_t>((TURN ? 256 / XC : 32) * pld * 2);
+  const uint32_t p_step = static_cast<uint32_t>((TURN ? 256 / XC : 32) * pld * 2);
   const half_t *const p0 = P + (TURN ? static_cast<int64_t>(t.ti) * T : static_cast<int64_t>(t.ti) * T * pld);
   const half_t *const q0 = Q + static_cast<int64_t>(t.tj) * T * qld;
-  const half_t *pk = p0, *qk = q0;
+  // the operands of depth step k; behind the last step nothing is loaded
+  u32x4 pk, qk;
   auto aim = [&](int k) {
     int seg = 0, kk = k;
     if (SEG == 3) {  // pieces: high*high, high*low, low*high
       seg = k / steps;
       kk = k - seg * steps;
     }
-    pk = p0 + (seg == 1 ? pplane : 0) + static_cast<int64_t>(kk) * kNsDepth * (TURN ? pld : 1);
-    qk = q0 + (seg == 2 ? qplane : 0) + static_cast<int64_t>(kk) * kNsDepth;
+    const uint32_t bytes = k < total ? 0x80000000u : 0u;
+    pk = buffer_at(p0 + (seg == 1 ? pplane : 0) + static_cast<int64_t>(kk) * kNsDepth * (TURN ? pld : 1), bytes);
+    qk = buffer_at(q0 + (seg == 2 ? qplane : 0) + static_cast<int64_t>(kk) * kNsDepth, bytes);
   };
   const uint32_t lds0 = lds_address(smem) + w * 1024;
-  auto load = [&](int buf, int g) {
-    const int r = g % S::LOADS;
-    const uint32_t at = lds0 + buf * 2 * S::STAGE + r * 4096;
-    if (g < S::LOADS) to_lds(reinterpret_cast<const char *>(pk) + r * p_step + p_off[r & 1], at);
-    else to_lds(reinterpret_cast<const char *>(qk) + r * q_step + q_off, at + S::STAGE);
-  };
-
   // Operand pieces of half h of a depth step: register buffer h.
   const int fr = lane % S::MT, fc = lane / S::MT;
   f16x8 fp[2][S::KI][S::MI], fq[2][S::KI][S::MI];
@@ -313,6 +318,14 @@ __global__ void __launch_bounds__(256, T == 256 ? 1 : 2) ns_product_kernel(const
     }
   };
   constexpr int MFMAS = S::MI * S::MI * S::KI, READS = 2 * S::MI * S::KI, ALL_LOADS = 2 * S::LOADS;
+  auto load = [&](int buf, int g) {
+    const int r = g % S::LOADS;
+    const uint32_t at = lds0 + buf * 2 * S::STAGE + r * 4096;
+    if (g < S::LOADS) buffer_to_lds(pk, p_off[r & 1], r * p_step, at);
+    else buffer_to_lds(qk, q_off, r * q_step, at + S::STAGE);
+  };
+  // A product, and behind it in the same breath a load (LOAD): the product
+  // stands in for the wait state between the write of m0 and the load.
   // The accumulators are updated in place by an instruction written out: left
   // to itself the compiler copies all 256 of them in every step. (It knows
   // the registers but not the instruction's latency: nothing reads them
@@ -324,22 +337,34 @@ __global__ void __launch_bounds__(256, T == 256 ? 1 : 2) ns_product_kernel(const
     else
       acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(fp[h][c][i], fq[h][c][j], acc[i][j], 0, 0, 0);
   };
+  auto product_load = [&](int h, int e, int buf, int g) {
+    if constexpr (S::MT == 32) {
+      const int c = e / (S::MI * S::MI), i = e / S::MI % S::MI, j = e % S::MI, r = g % S::LOADS;
+      const bool isp = g < S::LOADS;
+      const uint32_t at = lds0 + buf * 2 * S::STAGE + r * 4096 + (isp ? 0 : S::STAGE);
+      asm volatile("v_mfma_f32_32x32x16_f16 %0, %1, %2, %0\n\tbuffer_load_dwordx4 %3, %4, %5 offen lds"
+                   : "+a"(acc[i][j])
+                   : "v"(fp[h][c][i]), "v"(fq[h][c][j]), "v"(isp ? p_off[r & 1] : q_off), "s"(isp ? pk : qk),
+                     "s"(static_cast<uint32_t>(r * (isp ? p_step : q_step))), "{m0}"(at)
+                   : "memory");
+    } else {
+      product(h, e);
+      load(buf, g);
+    }
+  };
   // The products of half h. Between them the reads of half h ^ 1 (of tiles
-  // `buf`), as early as they can go but behind the first product, and for
-  // `reload` the loads into tiles `to`.
-  auto half_step = [&](int buf, int h, bool reload, int to) {
+  // `buf`), done an eighth before the end, and in the second half the loads
+  // into tiles `to`.
+  auto half_step = [&](int buf, int h, int to) {
 #pragma unroll
     for (int e = 0; e < MFMAS; ++e) {
-      product(h, e);
-      constexpr int RATE = READS > MFMAS ? READS / MFMAS : 1;  // reads behind a product
+      constexpr int SPAN = MFMAS - MFMAS / 8, EVERY = MFMAS / ALL_LOADS;
+      static_assert(EVERY * ALL_LOADS == MFMAS, "loads spread over the products");
+      if (h == 1 && e % EVERY == EVERY - 1) product_load(h, e, to, e / EVERY);
+      else product(h, e);
 #pragma unroll
-      for (int r = 0; r < RATE; ++r)
-        if (e * RATE + r < READS) read(buf, h ^ 1, e * RATE + r);
-      if (h == 1) {
-#pragma unroll
-        for (int g = e * ALL_LOADS / MFMAS; g < (e + 1) * ALL_LOADS / MFMAS; ++g)
-          if (reload) load(to, g);
-      }
+      for (int r = 0; r < READS; ++r)
+        if (r * SPAN / READS == e) read(buf, h ^ 1, r);
       __builtin_amdgcn_sched_barrier(0);
     }
   };
@@ -365,14 +390,13 @@ __global__ void __launch_bounds__(256, T == 256 ? 1 : 2) ns_product_kernel(const
   // tiles that are there and not used).
   for (int k = 0; k < total; ++k) {
     const int buf = k & 1;
-    half_step(buf, 0, false, 0);
+    half_step(buf, 0, 0);
     asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
     block_barrier();
-    const bool reload = k + 2 < total;
-    if (reload) aim(k + 2);
-    half_step(buf ^ 1, 1, reload, buf);
+    aim(k + 2);
+    half_step(buf ^ 1, 1, buf);
   }
-  asm volatile("s_nop 15\n\ts_nop 15\n\ts_waitcnt lgkmcnt(0)" ::: "memory");
+  asm volatile("s_nop 15\n\ts_nop 15\n\ts_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
   block_barrier();
 
   // Epilogue, in strips of MT rows of what is stored, each wave on its own in
