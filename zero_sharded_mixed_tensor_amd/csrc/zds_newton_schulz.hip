@@ -287,9 +287,10 @@ __global__ void __launch_bounds__(256, T == 256 ? 1 : 2) ns_product_kernel(const
     qk = buffer_at(q0 + (seg == 2 ? qplane : 0) + static_cast<int64_t>(kk) * kNsDepth, bytes);
   };
   const uint32_t lds0 = lds_address(smem) + w * 1024;
-  // Operand pieces of half h of a depth step: register buffer h.
+  // Operand pieces in registers: P's of this half of a depth step and the next,
+  // Q's of this instruction depth and the next.
   const int fr = lane % S::MT, fc = lane / S::MT;
-  f16x8 fp[2][S::KI][S::MI], fq[2][S::KI][S::MI];
+  f16x8 fp[2][S::KI][S::MI], fq[2][S::MI];
   int off_p[2][S::KI], off_q[2][S::KI], off_x[S::MI];
 #pragma unroll
   for (int h = 0; h < 2; ++h)
@@ -305,11 +306,10 @@ __global__ void __launch_bounds__(256, T == 256 ? 1 : 2) ns_product_kernel(const
     const int col = wi * S::TW + r * S::MT + (S::MT == 32 ? lane & 16 : 0) + (lane & 3) * 4;
     off_x[r] = row * 2 * T + ns_swizzle_x<T>(row, col >> 3) * 16 + (col & 4) * 2;
   }
-  auto read = [&](int buf, int h, int g) {
-    const int c = g / (2 * S::MI), r = g % (2 * S::MI);
-    if (r >= S::MI) {
-      fq[h][c][r - S::MI] = *reinterpret_cast<const f16x8 *>(smem[buf][1] + off_q[h][c] + (r - S::MI) * 128 * S::MT);
-    } else if constexpr (TURN) {
+  // piece g of half h of P
+  auto read_p = [&](int buf, int h, int g) {
+    const int c = g / S::MI, r = g % S::MI;
+    if constexpr (TURN) {
       const char *x = smem[buf][0] + off_x[r] + (h * 32 + c * 16) * 2 * T;
       const f16x4 a = read_turned(x), b = read_turned(x + 4 * 2 * T);
       fp[h][c][r] = __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
@@ -317,84 +317,126 @@ __global__ void __launch_bounds__(256, T == 256 ? 1 : 2) ns_product_kernel(const
       fp[h][c][r] = *reinterpret_cast<const f16x8 *>(smem[buf][0] + off_p[h][c] + r * 128 * S::MT);
     }
   };
-  constexpr int MFMAS = S::MI * S::MI * S::KI, READS = 2 * S::MI * S::KI, ALL_LOADS = 2 * S::LOADS;
-  auto load = [&](int buf, int g) {
-    const int r = g % S::LOADS;
-    const uint32_t at = lds0 + buf * 2 * S::STAGE + r * 4096;
-    if (g < S::LOADS) buffer_to_lds(pk, p_off[r & 1], r * p_step, at);
-    else buffer_to_lds(qk, q_off, r * q_step, at + S::STAGE);
+  // piece r of instruction depth u (of the step's 2 KI) of Q
+  auto read_q = [&](int buf, int u, int r) {
+    fq[u & 1][r] = *reinterpret_cast<const f16x8 *>(smem[buf][1] + off_q[u / S::KI][u % S::KI] + r * 128 * S::MT);
   };
-  // A product, and behind it in the same breath a load (LOAD): the product
-  // stands in for the wait state between the write of m0 and the load.
-  // The accumulators are updated in place by an instruction written out: left
-  // to itself the compiler copies all 256 of them in every step. (It knows
-  // the registers but not the instruction's latency: nothing reads them
-  // before the wait behind the loop.)
-  auto product = [&](int h, int e) {
-    const int c = e / (S::MI * S::MI), i = e / S::MI % S::MI, j = e % S::MI;
+  constexpr int MFMAS = S::MI * S::MI * S::KI, PER = S::MI * S::MI, READS = S::MI * S::KI;
+  auto load_p = [&](int buf, int r) {
+    buffer_to_lds(pk, p_off[r & 1], r * p_step, lds0 + buf * 2 * S::STAGE + r * 4096);
+  };
+  auto load_q = [&](int buf, int r) {
+    buffer_to_lds(qk, q_off, r * q_step, lds0 + (buf * 2 + 1) * S::STAGE + r * 4096);
+  };
+  // A product, and right behind it a load, for which the product stands in as
+  // the wait state behind the write of m0. The accumulators are updated in
+  // place by an instruction written out: left to itself the compiler copies
+  // all 256 of them in every step. (It knows the registers but not the
+  // instruction's latency: nothing reads them before the wait behind the
+  // loop.)
+  auto product = [&](int u, int e) {
+    const int i = e / S::MI, j = e % S::MI, h = u / S::KI, c = u % S::KI;
     if constexpr (S::MT == 32)
-      asm volatile("v_mfma_f32_32x32x16_f16 %0, %1, %2, %0" : "+a"(acc[i][j]) : "v"(fp[h][c][i]), "v"(fq[h][c][j]));
+      asm volatile("v_mfma_f32_32x32x16_f16 %0, %1, %2, %0" : "+a"(acc[i][j]) : "v"(fp[h][c][i]), "v"(fq[u & 1][j]));
     else
-      acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(fp[h][c][i], fq[h][c][j], acc[i][j], 0, 0, 0);
+      acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(fp[h][c][i], fq[u & 1][j], acc[i][j], 0, 0, 0);
   };
-  auto product_load = [&](int h, int e, int buf, int g) {
+  auto product_load = [&](int u, int e, bool is_p, int buf, int r) {
     if constexpr (S::MT == 32) {
-      const int c = e / (S::MI * S::MI), i = e / S::MI % S::MI, j = e % S::MI, r = g % S::LOADS;
-      const bool isp = g < S::LOADS;
-      const uint32_t at = lds0 + buf * 2 * S::STAGE + r * 4096 + (isp ? 0 : S::STAGE);
+      const int i = e / S::MI, j = e % S::MI, h = u / S::KI, c = u % S::KI;
+      const uint32_t at = lds0 + (buf * 2 + !is_p) * S::STAGE + r * 4096;
       asm volatile("v_mfma_f32_32x32x16_f16 %0, %1, %2, %0\n\tbuffer_load_dwordx4 %3, %4, %5 offen lds"
                    : "+a"(acc[i][j])
-                   : "v"(fp[h][c][i]), "v"(fq[h][c][j]), "v"(isp ? p_off[r & 1] : q_off), "s"(isp ? pk : qk),
-                     "s"(static_cast<uint32_t>(r * (isp ? p_step : q_step))), "{m0}"(at)
+                   : "v"(fp[h][c][i]), "v"(fq[u & 1][j]), "v"(is_p ? p_off[r & 1] : q_off), "s"(is_p ? pk : qk),
+                     "s"(static_cast<uint32_t>(r * (is_p ? p_step : q_step))), "{m0}"(at)
                    : "memory");
     } else {
-      product(h, e);
-      load(buf, g);
+      product(u, e);
+      if (is_p) load_p(buf, r);
+      else load_q(buf, r);
     }
   };
-  // The products of half h. Between them the reads of half h ^ 1 (of tiles
-  // `buf`), done an eighth before the end, and in the second half the loads
-  // into tiles `to`.
-  auto half_step = [&](int buf, int h, int to) {
+  // A depth step is 2 KI instruction depths u, half of them (MFMAS products) in
+  // each of its halves. Between the products stand
+  // - the reads of P's next half and of Q's next depth, done an eighth before
+  //   the end of what they stand in;
+  // - the loads of step k + 2: P's behind the barrier in the middle of step k
+  //   (both halves of P have been read then), Q's behind the next (KI = 2:
+  //   one depth later), one load in 3 products, into the next step's first
+  //   half.
+  // A barrier waits for the loads that the reads behind it need: P's of step
+  // k + 1 in the middle (Q's are younger), Q's of step k + 1 one depth later
+  // (but for the first of P's of step k + 2 they are the youngest). Behind the
+  // last steps the reads find tiles that are there and not used.
+  constexpr int WINDOW = MFMAS * 3 / 4;  // products that an operand's loads are spread over
+  constexpr auto at_p = [](int i) { return i * WINDOW / S::LOADS; };
+  constexpr auto at_q = [](int i) { return WINDOW + i * WINDOW / S::LOADS; };
+  constexpr int YOUNGER = [] {  // P's loads in front of the second barrier
+    int n = 0;
+    for (int i = 0; i < S::LOADS; ++i) n += i * WINDOW / S::LOADS < S::MI * S::MI;
+    return n;
+  }();
+  auto depth = [&](int k, auto which) {
+    constexpr int u = decltype(which)::value, h = u / S::KI;
+    const int buf = k & 1;
 #pragma unroll
-    for (int e = 0; e < MFMAS; ++e) {
-      constexpr int SPAN = MFMAS - MFMAS / 8, EVERY = MFMAS / ALL_LOADS;
-      static_assert(EVERY * ALL_LOADS == MFMAS, "loads spread over the products");
-      if (h == 1 && e % EVERY == EVERY - 1) product_load(h, e, to, e / EVERY);
-      else product(h, e);
+    for (int e = 0; e < PER; ++e) {
+      constexpr int SPAN = PER - PER / 8;
+      const int x = (u % S::KI) * PER + e;  // place in the half
+      int is_p = -1, is_q = -1;
+#pragma unroll
+      for (int i = 0; i < S::LOADS; ++i) {
+        if (h == 1 && at_p(i) == x) is_p = i;
+        if (at_q(i) == x + (h == 1 ? 0 : MFMAS)) is_q = i;
+      }
+      if (is_p >= 0) product_load(u, e, true, buf, is_p);
+      else if (is_q >= 0) product_load(u, e, false, h == 1 ? buf : buf ^ 1, is_q);
+      else product(u, e);
+#pragma unroll
+      for (int r = 0; r < S::MI; ++r)
+        if (r * SPAN / S::MI == e) {
+          if (u + 1 < 2 * S::KI) read_q(buf, u + 1, r);
+          else read_q(buf ^ 1, 0, r);
+        }
 #pragma unroll
       for (int r = 0; r < READS; ++r)
-        if (r * SPAN / READS == e) read(buf, h ^ 1, r);
+        if (r * (MFMAS - MFMAS / 8) / READS == x) read_p(h ? buf ^ 1 : buf, h ^ 1, r);
       __builtin_amdgcn_sched_barrier(0);
     }
   };
   aim(0);
 #pragma unroll
-  for (int g = 0; g < ALL_LOADS; ++g) load(0, g);
-  if (total > 1) {
-    aim(1);
+  for (int g = 0; g < S::LOADS; ++g) load_p(0, g);
 #pragma unroll
-    for (int g = 0; g < ALL_LOADS; ++g) load(1, g);
-    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(ALL_LOADS) : "memory");
-  } else {
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-  }
+  for (int g = 0; g < S::LOADS; ++g) load_q(0, g);
+  aim(1);
+#pragma unroll
+  for (int g = 0; g < S::LOADS; ++g) load_p(1, g);
+  constexpr int EARLY = [] {  // Q's loads in front of a step's first half
+    int n = 0;
+    for (int i = 0; i < S::LOADS; ++i) n += WINDOW + i * WINDOW / S::LOADS < S::MI * S::MI * S::KI;
+    return n;
+  }();
+#pragma unroll
+  for (int g = 0; g < EARLY; ++g) load_q(1, g);
+  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(S::LOADS + EARLY) : "memory");
   block_barrier();
 #pragma unroll
-  for (int g = 0; g < READS; ++g) read(0, 0, g);
-  // One depth step. While the products of its first half run, the second
-  // half's operands are read; then one barrier (every wave has read the
-  // step's tiles, and the next step's have arrived), and while the second
-  // half's products run, the tiles just read are refilled with the step after
-  // next and the next step's first operands are read (after the last step:
-  // tiles that are there and not used).
+  for (int g = 0; g < READS; ++g) read_p(0, 0, g);
+#pragma unroll
+  for (int g = 0; g < S::MI; ++g) read_q(0, 0, g);
   for (int k = 0; k < total; ++k) {
-    const int buf = k & 1;
-    half_step(buf, 0, 0);
-    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+    depth(k, std::integral_constant<int, 0>{});
+    if constexpr (S::KI == 2) depth(k, std::integral_constant<int, 1>{});
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(S::KI == 2 ? S::LOADS : 0) : "memory");
     block_barrier();
     aim(k + 2);
-    half_step(buf ^ 1, 1, buf);
+    depth(k, std::integral_constant<int, S::KI>{});
+    if constexpr (S::KI == 2) {
+      asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(YOUNGER) : "memory");
+      block_barrier();
+      depth(k, std::integral_constant<int, 3>{});
+    }
   }
   asm volatile("s_nop 15\n\ts_nop 15\n\ts_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
   block_barrier();
