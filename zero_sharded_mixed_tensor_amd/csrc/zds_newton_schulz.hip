@@ -163,10 +163,8 @@ template <int T>
 struct NsShape {
   static constexpr int WAVES = 4;
   static constexpr int TW = T / 2;                 // a wave's part of the tile, TW x TW
-  static constexpr int MT = T == 64 ? 16 : 32;     // the matrix instruction's tile, MT x MT x (512 / MT)
+  static constexpr int MT = 16;                    // the matrix instruction's tile, 16 x 16 x 32
   static constexpr int MI = TW / MT;
-  static constexpr int KI = MT / 16;               // instructions deep in half a depth step
-  static constexpr int RUNS = MT * MT / 256;       // a lane's runs of 4 rows in an instruction's tile
   static constexpr int LOADS = T / 8 / WAVES;      // 1 KiB loads of a wave per operand and depth step
   static constexpr int STAGE = T * 128;            // bytes of an operand's tile in LDS
   // the epilogue's strip: MT rows of the wave's part, 16 bits an element
@@ -247,14 +245,11 @@ __global__ void __launch_bounds__(256, T == 256 ? 1 : 2) ns_product_kernel(const
   const int steps = (KIND == kGram ? mt.np : mt.mp) / kNsDepth;
   const int total = steps * SEG;
 
-  typedef float AccT __attribute__((ext_vector_type(4 * S::RUNS)));
-  AccT acc[S::MI][S::MI];
+  f32x4 acc[S::MI][S::MI];
 #pragma unroll
   for (int i = 0; i < S::MI; ++i)
 #pragma unroll
-    for (int j = 0; j < S::MI; ++j)
-#pragma unroll
-      for (int r = 0; r < 4 * S::RUNS; ++r) acc[i][j][r] = 0.0f;
+    for (int j = 0; j < S::MI; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
 
   // Loads of a depth step: global to LDS without passing through registers.
   // The LDS side of a load is linear (1 KiB), so the lane takes the chunk that
@@ -288,40 +283,37 @@ __global__ void __launch_bounds__(256, T == 256 ? 1 : 2) ns_product_kernel(const
   };
   const uint32_t lds0 = lds_address(smem) + w * 1024;
   // Operand pieces in registers: P's of this half of a depth step and the next,
-  // Q's of this instruction depth and the next.
-  const int fr = lane % S::MT, fc = lane / S::MT;
-  f16x8 fp[2][S::KI][S::MI], fq[2][S::MI];
-  int off_p[2][S::KI], off_q[2][S::KI], off_x[S::MI];
+  // half of Q's of a half step and the next half of them.
+  constexpr int NQ = S::MI / 2;
+  const int fr = lane & 15, fc = lane >> 4;
+  f16x8 fp[2][S::MI], fq[2][NQ];
+  int off_p[2], off_q[2], off_x[S::MI];
 #pragma unroll
-  for (int h = 0; h < 2; ++h)
-#pragma unroll
-    for (int c = 0; c < S::KI; ++c) {
-      const int rp = wi * S::TW + fr, rq = wj * S::TW + fr, chunk = h * 4 + c * (64 / S::MT) + fc;
-      off_p[h][c] = rp * 128 + ns_swizzle(rp, chunk) * 16;
-      off_q[h][c] = rq * 128 + ns_swizzle(rq, chunk) * 16;
-    }
+  for (int h = 0; h < 2; ++h) {
+    const int rp = wi * S::TW + fr, rq = wj * S::TW + fr;
+    off_p[h] = rp * 128 + ns_swizzle(rp, h * 4 + fc) * 16;
+    off_q[h] = rq * 128 + ns_swizzle(rq, h * 4 + fc) * 16;
+  }
 #pragma unroll
   for (int r = 0; r < S::MI; ++r) {
-    const int row = 8 * fc + ((lane & 15) >> 2);
-    const int col = wi * S::TW + r * S::MT + (S::MT == 32 ? lane & 16 : 0) + (lane & 3) * 4;
+    const int row = 8 * fc + (fr >> 2), col = wi * S::TW + r * S::MT + (lane & 3) * 4;
     off_x[r] = row * 2 * T + ns_swizzle_x<T>(row, col >> 3) * 16 + (col & 4) * 2;
   }
-  // piece g of half h of P
-  auto read_p = [&](int buf, int h, int g) {
-    const int c = g / S::MI, r = g % S::MI;
+  // piece r of half h of P
+  auto read_p = [&](int buf, int h, int r) {
     if constexpr (TURN) {
-      const char *x = smem[buf][0] + off_x[r] + (h * 32 + c * 16) * 2 * T;
+      const char *x = smem[buf][0] + off_x[r] + h * 32 * 2 * T;
       const f16x4 a = read_turned(x), b = read_turned(x + 4 * 2 * T);
-      fp[h][c][r] = __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
+      fp[h][r] = __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
     } else {
-      fp[h][c][r] = *reinterpret_cast<const f16x8 *>(smem[buf][0] + off_p[h][c] + r * 128 * S::MT);
+      fp[h][r] = *reinterpret_cast<const f16x8 *>(smem[buf][0] + off_p[h] + r * 128 * S::MT);
     }
   };
-  // piece r of instruction depth u (of the step's 2 KI) of Q
+  // piece r of quarter u of Q: the quarter's half u / 2, its pieces (u % 2) NQ on
   auto read_q = [&](int buf, int u, int r) {
-    fq[u & 1][r] = *reinterpret_cast<const f16x8 *>(smem[buf][1] + off_q[u / S::KI][u % S::KI] + r * 128 * S::MT);
+    fq[u & 1][r] = *reinterpret_cast<const f16x8 *>(smem[buf][1] + off_q[u >> 1] + ((u & 1) * NQ + r) * 128 * S::MT);
   };
-  constexpr int MFMAS = S::MI * S::MI * S::KI, PER = S::MI * S::MI, READS = S::MI * S::KI;
+  constexpr int PER = S::MI * NQ, HALF = 2 * PER;  // products of a quarter, of a half step
   auto load_p = [&](int buf, int r) {
     buffer_to_lds(pk, p_off[r & 1], r * p_step, lds0 + buf * 2 * S::STAGE + r * 4096);
   };
@@ -335,72 +327,62 @@ __global__ void __launch_bounds__(256, T == 256 ? 1 : 2) ns_product_kernel(const
   // instruction's latency: nothing reads them before the wait behind the
   // loop.)
   auto product = [&](int u, int e) {
-    const int i = e / S::MI, j = e % S::MI, h = u / S::KI, c = u % S::KI;
-    if constexpr (S::MT == 32)
-      asm volatile("v_mfma_f32_32x32x16_f16 %0, %1, %2, %0" : "+a"(acc[i][j]) : "v"(fp[h][c][i]), "v"(fq[u & 1][j]));
-    else
-      acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(fp[h][c][i], fq[u & 1][j], acc[i][j], 0, 0, 0);
+    const int i = e / NQ, j = e % NQ;
+    asm volatile("v_mfma_f32_16x16x32_f16 %0, %1, %2, %0"
+                 : "+a"(acc[i][(u & 1) * NQ + j])
+                 : "v"(fp[u >> 1][i]), "v"(fq[u & 1][j]));
   };
   auto product_load = [&](int u, int e, bool is_p, int buf, int r) {
-    if constexpr (S::MT == 32) {
-      const int i = e / S::MI, j = e % S::MI, h = u / S::KI, c = u % S::KI;
-      const uint32_t at = lds0 + (buf * 2 + !is_p) * S::STAGE + r * 4096;
-      asm volatile("v_mfma_f32_32x32x16_f16 %0, %1, %2, %0\n\tbuffer_load_dwordx4 %3, %4, %5 offen lds"
-                   : "+a"(acc[i][j])
-                   : "v"(fp[h][c][i]), "v"(fq[u & 1][j]), "v"(is_p ? p_off[r & 1] : q_off), "s"(is_p ? pk : qk),
-                     "s"(static_cast<uint32_t>(r * (is_p ? p_step : q_step))), "{m0}"(at)
-                   : "memory");
-    } else {
-      product(u, e);
-      if (is_p) load_p(buf, r);
-      else load_q(buf, r);
-    }
+    const int i = e / NQ, j = e % NQ;
+    const uint32_t at = lds0 + (buf * 2 + !is_p) * S::STAGE + r * 4096;
+    asm volatile("v_mfma_f32_16x16x32_f16 %0, %1, %2, %0\n\tbuffer_load_dwordx4 %3, %4, %5 offen lds"
+                 : "+a"(acc[i][(u & 1) * NQ + j])
+                 : "v"(fp[u >> 1][i]), "v"(fq[u & 1][j]), "v"(is_p ? p_off[r & 1] : q_off), "s"(is_p ? pk : qk),
+                   "s"(static_cast<uint32_t>(r * (is_p ? p_step : q_step))), "{m0}"(at)
+                 : "memory");
   };
-  // A depth step is 2 KI instruction depths u, half of them (MFMAS products) in
-  // each of its halves. Between the products stand
-  // - the reads of P's next half and of Q's next depth, done an eighth before
+  // A depth step is four quarters u: two halves in depth, and in each the two
+  // halves of Q's pieces. Between the products stand
+  // - the reads of P's next half and of Q's next quarter, done an eighth before
   //   the end of what they stand in;
   // - the loads of step k + 2: P's behind the barrier in the middle of step k
-  //   (both halves of P have been read then), Q's behind the next (KI = 2:
-  //   one depth later), one load in 3 products, into the next step's first
-  //   half.
+  //   (both halves of P have been read then), Q's behind the next, a quarter
+  //   later, into the next step's first half.
   // A barrier waits for the loads that the reads behind it need: P's of step
-  // k + 1 in the middle (Q's are younger), Q's of step k + 1 one depth later
+  // k + 1 in the middle (Q's are younger), Q's of step k + 1 a quarter later
   // (but for the first of P's of step k + 2 they are the youngest). Behind the
   // last steps the reads find tiles that are there and not used.
-  constexpr int WINDOW = MFMAS * 3 / 4;  // products that an operand's loads are spread over
+  constexpr int WINDOW = HALF * 3 / 4;  // products that an operand's loads are spread over
   constexpr auto at_p = [](int i) { return i * WINDOW / S::LOADS; };
   constexpr auto at_q = [](int i) { return WINDOW + i * WINDOW / S::LOADS; };
-  constexpr int YOUNGER = [] {  // P's loads in front of the second barrier
+  constexpr auto before = [](auto at, int x) {
     int n = 0;
-    for (int i = 0; i < S::LOADS; ++i) n += i * WINDOW / S::LOADS < S::MI * S::MI;
+    for (int i = 0; i < S::LOADS; ++i) n += at(i) < x;
     return n;
-  }();
-  auto depth = [&](int k, auto which) {
-    constexpr int u = decltype(which)::value, h = u / S::KI;
+  };
+  constexpr int YOUNGER = before(at_p, PER);  // P's loads in front of the second barrier
+  constexpr int EARLY = before(at_q, HALF);   // Q's loads in front of a step's first half
+  auto quarter = [&](int k, auto which) {
+    constexpr int u = decltype(which)::value, h = u >> 1;
     const int buf = k & 1;
 #pragma unroll
     for (int e = 0; e < PER; ++e) {
-      constexpr int SPAN = PER - PER / 8;
-      const int x = (u % S::KI) * PER + e;  // place in the half
+      const int x = (u & 1) * PER + e;  // place in the half
       int is_p = -1, is_q = -1;
 #pragma unroll
       for (int i = 0; i < S::LOADS; ++i) {
         if (h == 1 && at_p(i) == x) is_p = i;
-        if (at_q(i) == x + (h == 1 ? 0 : MFMAS)) is_q = i;
+        if (at_q(i) == x + (h == 1 ? 0 : HALF)) is_q = i;
       }
       if (is_p >= 0) product_load(u, e, true, buf, is_p);
       else if (is_q >= 0) product_load(u, e, false, h == 1 ? buf : buf ^ 1, is_q);
       else product(u, e);
 #pragma unroll
-      for (int r = 0; r < S::MI; ++r)
-        if (r * SPAN / S::MI == e) {
-          if (u + 1 < 2 * S::KI) read_q(buf, u + 1, r);
-          else read_q(buf ^ 1, 0, r);
-        }
+      for (int r = 0; r < NQ; ++r)
+        if (r * (PER - PER / 8) / NQ == e) read_q(u == 3 ? buf ^ 1 : buf, (u + 1) & 3, r);
 #pragma unroll
-      for (int r = 0; r < READS; ++r)
-        if (r * (MFMAS - MFMAS / 8) / READS == x) read_p(h ? buf ^ 1 : buf, h ^ 1, r);
+      for (int r = 0; r < S::MI; ++r)
+        if (r * (HALF - HALF / 8) / S::MI == x) read_p(h ? buf ^ 1 : buf, h ^ 1, r);
       __builtin_amdgcn_sched_barrier(0);
     }
   };
@@ -412,39 +394,31 @@ __global__ void __launch_bounds__(256, T == 256 ? 1 : 2) ns_product_kernel(const
   aim(1);
 #pragma unroll
   for (int g = 0; g < S::LOADS; ++g) load_p(1, g);
-  constexpr int EARLY = [] {  // Q's loads in front of a step's first half
-    int n = 0;
-    for (int i = 0; i < S::LOADS; ++i) n += WINDOW + i * WINDOW / S::LOADS < S::MI * S::MI * S::KI;
-    return n;
-  }();
 #pragma unroll
   for (int g = 0; g < EARLY; ++g) load_q(1, g);
   asm volatile("s_waitcnt vmcnt(%0)" ::"n"(S::LOADS + EARLY) : "memory");
   block_barrier();
 #pragma unroll
-  for (int g = 0; g < READS; ++g) read_p(0, 0, g);
+  for (int g = 0; g < S::MI; ++g) read_p(0, 0, g);
 #pragma unroll
-  for (int g = 0; g < S::MI; ++g) read_q(0, 0, g);
+  for (int g = 0; g < NQ; ++g) read_q(0, 0, g);
   for (int k = 0; k < total; ++k) {
-    depth(k, std::integral_constant<int, 0>{});
-    if constexpr (S::KI == 2) depth(k, std::integral_constant<int, 1>{});
-    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(S::KI == 2 ? S::LOADS : 0) : "memory");
+    quarter(k, std::integral_constant<int, 0>{});
+    quarter(k, std::integral_constant<int, 1>{});
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(S::LOADS) : "memory");
     block_barrier();
     aim(k + 2);
-    depth(k, std::integral_constant<int, S::KI>{});
-    if constexpr (S::KI == 2) {
-      asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(YOUNGER) : "memory");
-      block_barrier();
-      depth(k, std::integral_constant<int, 3>{});
-    }
+    quarter(k, std::integral_constant<int, 2>{});
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(YOUNGER) : "memory");
+    block_barrier();
+    quarter(k, std::integral_constant<int, 3>{});
   }
   asm volatile("s_nop 15\n\ts_nop 15\n\ts_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
   block_barrier();
 
   // Epilogue, in strips of MT rows of what is stored, each wave on its own in
-  // its part of the LDS (two strips' room). A lane holds row fr of a strip and
-  // in it runs of 4 elements: run g of instruction tile i is at columns
-  // i MT + 8 g + 4 fc. The strip's inputs come in rows (high and low plane)
+  // its part of the LDS (two strips' room). A lane holds row fr of a strip, of
+  // each instruction tile i four elements from column 16 i + 4 fc on. The strip's inputs come in rows (high and low plane)
   // and are overwritten by its outputs, which leave in rows, and for a
   // symmetric result also turned.
   const float alpha = q.first ? q.scales[t.mat].alpha : 1.0f / q.sx;
@@ -459,7 +433,19 @@ __global__ void __launch_bounds__(256, T == 256 ? 1 : 2) ns_product_kernel(const
   const half_t *in_l = SEG == 3 ? in_h + (TURN ? xplane : aplane) : q.ws + mt.lo;
   const bool low_in = SEG == 3 || (TURN && !q.first);
   constexpr int RPI = 64 / S::CHUNKS;  // rows of a 1 KiB access
-  const int mrow = lane / S::CHUNKS, mchunk = lane % S::CHUNKS;
+  constexpr int GR = S::MT / 8;        // groups of 8 rows in a strip
+  constexpr int PC = 64 / GR;          // columns that a wave's turned access covers
+  int sl, mrow, mchunk, tgrp, tcol;
+  // The lane's places, taken anew for every strip: kept for all of them the
+  // addresses cost registers that the accumulators need.
+  auto places = [&] {
+    sl = lane;
+    asm volatile("" : "+v"(sl));
+    mrow = sl / S::CHUNKS;
+    mchunk = sl % S::CHUNKS;
+    tgrp = (sl >> 4) % GR * 8;
+    tcol = (sl >> 4) / GR * 16 + (sl & 15);
+  };
   auto fetch = [&](int s) {
     if (KIND == kGram) return;
     const uint32_t at = room_lds + (s & 1) * 2 * S::STRIP;
@@ -490,14 +476,11 @@ __global__ void __launch_bounds__(256, T == 256 ? 1 : 2) ns_product_kernel(const
   // eight rows of plane `at` from row r on, turned: column col of them
   auto turned8 = [&](const char *at, int r, int col) {
     // within the lane's group of 16: row (lane & 15) / 4, columns 4 (lane & 3) on
-    const int cc = (col & ~15) + (lane & 3) * 4, ra = r + ((lane & 15) >> 2), rb = ra + 4;
+    const int cc = (col & ~15) + (sl & 3) * 4, ra = r + ((sl & 15) >> 2), rb = ra + 4;
     const f16x4 a = read_turned(at + ra * S::ROW + ns_swizzle_strip<T>(ra, cc >> 3) * 16 + (cc & 4) * 2);
     const f16x4 b = read_turned(at + rb * S::ROW + ns_swizzle_strip<T>(rb, cc >> 3) * 16 + (cc & 4) * 2);
     return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
   };
-  constexpr int GR = S::MT / 8;        // groups of 8 rows in a strip
-  constexpr int PC = 64 / GR;          // columns that a wave's turned access covers
-  const int tgrp = (lane >> 4) % GR * 8, tcol = (lane >> 4) / GR * 16 + (lane & 15);
   auto put_turned = [&](const char *at, half_t *out, int s) {
     half_t *o = out + prow * old + qrow + s * S::MT;
 #pragma unroll
@@ -506,11 +489,14 @@ __global__ void __launch_bounds__(256, T == 256 ? 1 : 2) ns_product_kernel(const
       *reinterpret_cast<f16x8 *>(o + (c + tcol) * old + tgrp) = v;
     }
   };
+  places();
   fetch(0);
-  if (S::MI > 1) fetch(1);
+  fetch(1);
 #pragma unroll
   for (int s = 0; s < S::MI; ++s) {
     char *at = room + (s & 1) * 2 * S::STRIP;
+    places();
+    const int fr = sl & 15, fc = sl >> 4;
     if (KIND != kGram) {
       // the next strip's loads may still be on their way; what was stored in between counts too
       if (s + 1 < S::MI) {
@@ -534,10 +520,8 @@ __global__ void __launch_bounds__(256, T == 256 ? 1 : 2) ns_product_kernel(const
     }
     const float carry = TURN ? q.carry : 1.0f;
 #pragma unroll
-    for (int i = 0; i < S::MI; ++i)
-#pragma unroll
-      for (int g = 0; g < S::RUNS; ++g) {
-        const int col = i * S::MT + g * 8 + fc * 4;
+    for (int i = 0; i < S::MI; ++i) {
+        const int col = i * S::MT + fc * 4;
         char *p = const_cast<char *>(line) + ns_swizzle_strip<T>(fr, col >> 3) * 16 + (col & 4) * 2;
         f16x4 h = {}, l = {};
         if (KIND != kGram) h = *reinterpret_cast<const f16x4 *>(p);
@@ -545,7 +529,7 @@ __global__ void __launch_bounds__(256, T == 256 ? 1 : 2) ns_product_kernel(const
         float v[4];
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-          v[r] = f1 * acc[i][s][4 * g + r];
+          v[r] = f1 * acc[i][s][r];
           if (KIND != kGram) v[r] += f0 * (static_cast<float>(h[r]) + carry * static_cast<float>(l[r]));
         }
         if constexpr (KIND == kLast) {
@@ -607,7 +591,7 @@ __global__ void __launch_bounds__(256, T == 256 ? 1 : 2) ns_product_kernel(const
             *reinterpret_cast<u32x4 *>(dst + (j0 + c + tcol) * mt.cols + i0 + tgrp) = v;
         }
       } else {
-        for (int e = lane; e < S::MT * S::TW; e += 64) {
+        for (int e = sl; e < S::MT * S::TW; e += 64) {
           const int r = mt.tall ? e % S::MT : e / S::TW, c = mt.tall ? e / S::MT : e % S::TW;
           const uint16_t v = *reinterpret_cast<const uint16_t *>(at + r * S::ROW + ns_swizzle_strip<T>(r, c >> 3) * 16 + (c & 7) * 2);
           if (i0 + r < mt.m && j0 + c < mt.n)
