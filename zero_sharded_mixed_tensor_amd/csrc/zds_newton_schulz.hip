@@ -171,6 +171,7 @@ struct NsShape {
   static constexpr int ROW = TW * 2, CHUNKS = TW / 8;
   static constexpr int STRIP = MT * ROW;
   static constexpr int MOVES = STRIP / 1024;       // 1 KiB accesses of a wave per strip
+  static constexpr int AHEAD = MI < 4 ? MI : 4;    // strips in LDS, two planes each
 };
 
 // Positions of the 16-byte chunks in LDS, so that one access of a wave falls on
@@ -218,6 +219,22 @@ __device__ __forceinline__ void buffer_to_lds(u32x4 desc, uint32_t lane_off, uin
 __device__ __forceinline__ uint32_t lds_address(const void *p) {
   return __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(reinterpret_cast<uintptr_t>((lds_void *)p)));
 }
+// Waits until at most n of the wave's memory accesses are under way (n is a
+// constant once the caller's loop is unrolled).
+__device__ __forceinline__ void wait_loads(int n) {
+  asm volatile("" ::: "memory");
+  // vmcnt in bits 3:0 and 15:14, the other counters at their maxima
+  switch (n < 63 ? n : 63) {
+#define ZDS_WAIT(k) case k: __builtin_amdgcn_s_waitcnt(0x0f70 | (k & 15) | (k >> 4) << 14); break;
+#define ZDS_WAIT4(k) ZDS_WAIT(k) ZDS_WAIT(k + 1) ZDS_WAIT(k + 2) ZDS_WAIT(k + 3)
+#define ZDS_WAIT16(k) ZDS_WAIT4(k) ZDS_WAIT4(k + 4) ZDS_WAIT4(k + 8) ZDS_WAIT4(k + 12)
+    ZDS_WAIT16(0) ZDS_WAIT16(16) ZDS_WAIT16(32) ZDS_WAIT16(48)
+#undef ZDS_WAIT16
+#undef ZDS_WAIT4
+#undef ZDS_WAIT
+  }
+  asm volatile("" ::: "memory");
+}
 __device__ __forceinline__ void block_barrier() {
   __builtin_amdgcn_s_barrier();
   asm volatile("" ::: "memory");
@@ -230,14 +247,16 @@ __global__ void __launch_bounds__(256, T == 256 ? 1 : 2) ns_product_kernel(const
   __shared__ __align__(1024) char smem[2][2][S::STAGE];
   if (q.sc && q.sc->overflow) return;
   const NsTile t = q.tiles[blockIdx.x];
-  const NsMatrix &mt = q.mats[t.mat];
+  const NsMatrix mt = q.mats[t.mat];  // all of it now: the waits below count every access
   const int lane = threadIdx.x & 63;
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wi = w >> 1, wj = w & 1;
+  const float alpha = q.first ? q.scales[t.mat].alpha : 1.0f / q.sx;
   const int64_t mp = mt.mp, np = mt.np;
   const int64_t xplane = mp * np, aplane = mp * mp;
   // C = P Q^T, tile (ti, tj): rows of P are columns of what is stored
-  half_t *const xin = q.ws + mt.x[q.odd];
+  half_t *const xin = q.ws + (q.odd ? mt.x[1] : mt.x[0]);
+  half_t *const xout = q.ws + (q.odd ? mt.x[0] : mt.x[1]);
   const half_t *const P = KIND == kPoly ? q.ws + mt.a : xin;
   const half_t *const Q = KIND == kGram ? xin : q.ws + (KIND == kPoly ? mt.a : mt.b);
   const int64_t pld = KIND == kPoly ? mp : np, qld = KIND == kGram ? np : mp;
@@ -421,10 +440,9 @@ __global__ void __launch_bounds__(256, T == 256 ? 1 : 2) ns_product_kernel(const
   // each instruction tile i four elements from column 16 i + 4 fc on. The strip's inputs come in rows (high and low plane)
   // and are overwritten by its outputs, which leave in rows, and for a
   // symmetric result also turned.
-  const float alpha = q.first ? q.scales[t.mat].alpha : 1.0f / q.sx;
-  char *const room = smem[0][0] + w * 2 * 2 * S::STRIP;
+  char *const room = smem[0][0] + w * S::AHEAD * 2 * S::STRIP;
   const uint32_t room_lds = lds_address(room);
-  static_assert(4 * 2 * 2 * S::STRIP <= 4 * S::STAGE, "two strips of two planes for each wave");
+  static_assert(4 * S::AHEAD * 2 * S::STRIP <= 4 * S::STAGE, "each wave's strips fit");
   const int64_t prow = static_cast<int64_t>(t.ti) * T + wi * S::TW;  // first column of the wave's part
   const int64_t qrow = static_cast<int64_t>(t.tj) * T + wj * S::TW;  // first row
   const int64_t old = TURN ? np : mp;
@@ -448,7 +466,7 @@ __global__ void __launch_bounds__(256, T == 256 ? 1 : 2) ns_product_kernel(const
   };
   auto fetch = [&](int s) {
     if (KIND == kGram) return;
-    const uint32_t at = room_lds + (s & 1) * 2 * S::STRIP;
+    const uint32_t at = room_lds + s % S::AHEAD * 2 * S::STRIP;
     const half_t *h = in_h + here + s * S::MT * old, *l = in_l + here + s * S::MT * old;
 #pragma unroll
     for (int g = 0; g < S::MOVES; ++g) {
@@ -490,21 +508,21 @@ __global__ void __launch_bounds__(256, T == 256 ? 1 : 2) ns_product_kernel(const
     }
   };
   places();
-  fetch(0);
-  fetch(1);
+#pragma unroll
+  for (int s = 0; s < S::AHEAD; ++s) fetch(s);
 #pragma unroll
   for (int s = 0; s < S::MI; ++s) {
-    char *at = room + (s & 1) * 2 * S::STRIP;
+    char *at = room + s % S::AHEAD * 2 * S::STRIP;
     places();
     const int fr = sl & 15, fc = sl >> 4;
     if (KIND != kGram) {
-      // the next strip's loads may still be on their way; what was stored in between counts too
-      if (s + 1 < S::MI) {
-        if (low_in) asm volatile("s_waitcnt vmcnt(%0)" ::"n"(2 * S::MOVES) : "memory");
-        else asm volatile("s_waitcnt vmcnt(%0)" ::"n"(S::MOVES) : "memory");
-      } else {
-        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-      }
+      // wait for the strip's loads only: behind them stand the loads of the
+      // AHEAD - 1 next strips and the stores of as many (at least STORES each)
+      constexpr int STORES = KIND == kUpdate ? 2 * S::MOVES : KIND == kPoly ? SEG * S::MOVES : 0;
+      const int left = S::MI - 1 - s < S::AHEAD - 1 ? S::MI - 1 - s : S::AHEAD - 1;
+      const int gone = s < S::AHEAD - 1 ? s : S::AHEAD - 1;
+      if (low_in) wait_loads(left * 2 * S::MOVES + gone * STORES);
+      else wait_loads(left * S::MOVES + gone * STORES);
     }
     const char *line = at + fr * S::ROW;
     float f0 = 0.0f, f1;  // v = f0 (high + carry low) + f1 acc
@@ -566,9 +584,8 @@ __global__ void __launch_bounds__(256, T == 256 ? 1 : 2) ns_product_kernel(const
         if (SEG == 3) put_turned(at + S::STRIP, out + aplane, s);
       }
     } else if constexpr (KIND == kUpdate) {
-      half_t *out = q.ws + mt.x[q.odd ^ 1];
-      put_rows(at, out, s);
-      put_rows(at + S::STRIP, SEG == 3 ? out + xplane : q.ws + mt.lo, s);
+      put_rows(at, xout, s);
+      put_rows(at + S::STRIP, SEG == 3 ? xout + xplane : q.ws + mt.lo, s);
     } else if constexpr (SEG == 1) {
       // the result, in its own orientation and inside its bounds: 16-byte
       // pieces where the rows lie on them, else element by element
@@ -600,7 +617,7 @@ __global__ void __launch_bounds__(256, T == 256 ? 1 : 2) ns_product_kernel(const
       }
     }
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-    if (s + 2 < S::MI) fetch(s + 2);
+    if (s + S::AHEAD < S::MI) fetch(s + S::AHEAD);
   }
 }
 
