@@ -22,24 +22,29 @@ struct NsMatrix {
   int32_t m, n, mp, np;
   int32_t tall;
   int32_t part0, nparts;  // this matrix's partial sums of squares in the group's
-  int32_t pad_;
+  int32_t chunk;          // elements of one
   int64_t x[2];     // X of even and odd steps, mp x np
   int64_t lo;       // what X's fp16 values leave of X, mp x np
   int64_t a, b;     // A and B, mp x mp
 };
 
 // A block's piece of work: tile (ti, tj) of matrix `mat`, or chunk ti of it.
+// Of a product's sum it takes part `part` of `parts` (1: all of it); `slot`
+// numbers the tiles of a launch whose sum is cut.
 struct NsTile {
-  int32_t mat, ti, tj, pad_;
+  int32_t mat, ti, tj;
+  uint8_t part, parts;
+  uint16_t slot;
 };
 
 // Matrices that go through one sequence of launches. Tables: tile lists of
-// the triangular products (ti >= tj), the full product, the conversion
+// the triangular products (ti >= tj; with cut tiles, if any, for the first of
+// them), the full product, the conversion
 // (64 x 64 tiles over the padded matrix) and the norm's chunks.
 struct NsGroup {
   int32_t tile;                 // the products' tile size
   int32_t mat0, nmat;           // matrices in the plan's device array
-  int32_t tri0, ntri, full0, nfull, conv0, nconv, chunk0, nchunk;  // in the plan's tile array
+  int32_t tri0, ntri, cut0, ncut, full0, nfull, conv0, nconv, chunk0, nchunk;  // in the plan's tile array
 };
 
 // A chunk of a matrix for zds_muon_apply: up to kApplyChunk elements from flat
@@ -63,6 +68,7 @@ struct zds_matrix_plan {
   // front, then the fp16 arrays
   size_t ws_bytes[2] = {0, 0};      // [FP32]
   int32_t max_parts = 0, max_mats = 0;
+  int32_t max_cut = 0;  // most pieces of cut tiles in a launch
   zds::NsMatrix *d_mats[2] = {nullptr, nullptr};  // [FP32]: workspace offsets differ
   zds::NsTile *d_tiles = nullptr;
   zds::ApplyChunk *d_chunks = nullptr;

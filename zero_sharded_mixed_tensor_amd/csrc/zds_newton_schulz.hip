@@ -17,6 +17,7 @@
 // read and written by the epilogue only). For FP32 every operand is a pair of
 // fp16 numbers (high and low) and a product runs its sum over three pieces,
 // high*high + high*low + low*high, into the same fp32 accumulators.
+#include <algorithm>
 #include <new>
 #include <type_traits>
 
@@ -33,8 +34,12 @@ typedef __attribute__((address_space(1))) const void global_cvoid;
 
 constexpr int kMaxSteps = 16;
 constexpr double kNormEps = 1e-7;
-// A partial sum of squares covers this many elements.
-constexpr int kNormChunk = 32768;
+// Most tiles of a launch whose sum is cut (see cut_tail).
+constexpr int kMaxSlots = 128;
+// A partial sum of squares covers this many elements or more; a matrix has at
+// most kMaxParts of them.
+constexpr int64_t kNormChunk = 32768;
+constexpr int kMaxParts = 1024;
 constexpr int kConvTile = 64;
 
 // A matrix's first X as stored and true: X_true = alpha * X_stored.
@@ -46,56 +51,100 @@ struct NsScale {
 // Norm and conversion
 // ---------------------------------------------------------------------------
 
+// Eight consecutive elements from an address aligned to 16 bytes.
+template <int D>
+__device__ __forceinline__ void load_eight(const char *p, float (&v)[8]) {
+  if constexpr (D == ZDS_FP32) {
+    const f32x4 a = reinterpret_cast<const f32x4 *>(p)[0], b = reinterpret_cast<const f32x4 *>(p)[1];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      v[j] = a[j];
+      v[4 + j] = b[j];
+    }
+  } else {
+    const u32x4 w = *reinterpret_cast<const u32x4 *>(p);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      v[2 * j] = lo_of<D>(w[j]);
+      v[2 * j + 1] = hi_of<D>(w[j]);
+    }
+  }
+}
+
+// Sum of squares of one chunk (mt.chunk elements) of a matrix, in a fixed order.
 template <int D>
 __global__ void __launch_bounds__(256) ns_norm_kernel(const NsMatrix *mats, const NsTile *chunks, const void *src,
                                                       double *partials, const zds_step_scalars *sc) {
   if (sc && sc->overflow) return;
   const NsTile t = chunks[blockIdx.x];
-  const NsMatrix &mt = mats[t.mat];
-  const int64_t total = static_cast<int64_t>(mt.rows) * mt.cols;
-  const int64_t lo = static_cast<int64_t>(t.ti) * kNormChunk;
-  const int64_t hi = lo + kNormChunk < total ? lo + kNormChunk : total;
+  const NsMatrix mt = mats[t.mat];
+  const int64_t all = static_cast<int64_t>(mt.rows) * mt.cols;
+  const int64_t lo = static_cast<int64_t>(t.ti) * mt.chunk;
+  const int64_t hi = lo + mt.chunk < all ? lo + mt.chunk : all;
   constexpr int ES = D == ZDS_FP32 ? 4 : 2;
-  constexpr int PER = 16 / ES;
-  const char *base = static_cast<const char *>(src) + mt.offset * ES;
-  double acc = 0.0;
-  int64_t e = lo;
-  if (aligned(base, 16)) {  // lo is a multiple of PER
-    const int64_t groups = (hi - lo) / PER;
-    for (int64_t g = threadIdx.x; g < groups; g += 256) {
-      float v[PER];
-      if constexpr (D == ZDS_FP32) {
-        const f32x4 w = reinterpret_cast<const f32x4 *>(base)[lo / PER + g];
-        v[0] = w.x; v[1] = w.y; v[2] = w.z; v[3] = w.w;
-      } else {
-        const u32x4 w = reinterpret_cast<const u32x4 *>(base)[lo / PER + g];
-        v[0] = lo_of<D>(w.x); v[1] = hi_of<D>(w.x); v[2] = lo_of<D>(w.y); v[3] = hi_of<D>(w.y);
-        v[4] = lo_of<D>(w.z); v[5] = hi_of<D>(w.z); v[6] = lo_of<D>(w.w); v[7] = hi_of<D>(w.w);
-      }
+  const char *base = static_cast<const char *>(src) + (mt.offset + lo) * ES;
+  double acc[2] = {0.0, 0.0};
+  int64_t e = 0;
+  if (aligned(base, 16)) {
+    const int64_t groups = (hi - lo) / 8;
+    auto add = [&](const float (&v)[8]) {
 #pragma unroll
-      for (int j = 0; j < PER; ++j) acc = sq_add(v[j], acc);
+      for (int j = 0; j < 8; ++j) acc[j & 1] = sq_add(v[j], acc[j & 1]);
+    };
+    int64_t g = threadIdx.x;
+    for (; g + 3 * 256 < groups; g += 4 * 256) {
+      float v[4][8];
+#pragma unroll
+      for (int r = 0; r < 4; ++r) load_eight<D>(base + (g + r * 256) * 8 * ES, v[r]);
+#pragma unroll
+      for (int r = 0; r < 4; ++r) add(v[r]);
     }
-    e = lo + groups * PER;
+    for (; g < groups; g += 256) {
+      float v[8];
+      load_eight<D>(base + g * 8 * ES, v);
+      add(v);
+    }
+    e = groups * 8;
   }
-  for (int64_t i = e + threadIdx.x; i < hi; i += 256) acc = sq_add(widen1<D>(base, i), acc);
-  const double b = block_sum<256>(acc);
+  for (int64_t i = e + threadIdx.x; i < hi - lo; i += 256) acc[0] = sq_add(widen1<D>(base, i), acc[0]);
+  const double b = block_sum<256>(acc[0] + acc[1]);
   if (threadIdx.x == 0) partials[mt.part0 + t.ti] = b;
 }
 
 // Writes the first step's X (padded with zeros; the transpose of a tall
 // matrix), scaled by the power of two that brings the norm into [2^13, 2^14):
-// exact for bf16 but for elements below 2^-28 of the norm. Each block adds its
-// matrix's partial sums again, in index order (every block the same value);
-// the matrix's first block stores alpha.
+// exact for bf16 but for elements below 2^-28 of the norm. A block turns one
+// 64 x 64 tile. Each block adds its matrix's partial sums again (at most
+// kMaxParts of them), in a fixed order, so every block has the same norm; the
+// matrix's first block stores alpha.
 template <int D, int SEG>
 __global__ void __launch_bounds__(256) ns_convert_kernel(const NsMatrix *mats, const NsTile *tiles, const void *src,
-                                                         const double *partials, NsScale *scales, half_t *ws,
-                                                         const zds_step_scalars *sc) {
+                                                         const double *partials, NsScale *scales, int32_t *arrived,
+                                                         half_t *ws, const zds_step_scalars *sc) {
   if (sc && sc->overflow) return;
   __shared__ float sh[kConvTile][kConvTile + 1];
   __shared__ double ssum;
   const NsTile t = tiles[blockIdx.x];
-  const NsMatrix &mt = mats[t.mat];
+  const NsMatrix mt = mats[t.mat];
+  constexpr int ES = D == ZDS_FP32 ? 4 : 2;
+  const char *base = static_cast<const char *>(src) + mt.offset * ES;
+  // tile (ti, tj) of the rows x cols matrix as it lies in src: two eights of a
+  // row for each thread, their loads under way while the norm is added up
+  const int r0 = t.ti * kConvTile, c0 = t.tj * kConvTile;
+  const int tr = threadIdx.x >> 3, tc = (threadIdx.x & 7) * 8;
+  const bool vec = aligned(base, 16) && (mt.cols & 7) == 0;
+  float v[2][8];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int r = r0 + tr + 32 * h, c = c0 + tc;
+    const int64_t e = static_cast<int64_t>(r) * mt.cols + c;
+    if (vec && r < mt.rows && c < mt.cols) {
+      load_eight<D>(base + e * ES, v[h]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[h][j] = !vec && r < mt.rows && c + j < mt.cols ? widen1<D>(base, e + j) : 0.0f;
+    }
+  }
   double acc = 0.0;
   for (int i = threadIdx.x; i < mt.nparts; i += 256) acc += partials[mt.part0 + i];
   const double tot = block_sum<256>(acc);
@@ -107,34 +156,40 @@ __global__ void __launch_bounds__(256) ns_convert_kernel(const NsMatrix *mats, c
   int p2 = norm > 0.0 && norm <= DBL_MAX ? 14 - ex : 0;
   p2 = p2 > 126 ? 126 : (p2 < -126 ? -126 : p2);
   const float up = ldexpf(1.0f, p2);
-  if (t.ti == 0 && t.tj == 0 && threadIdx.x == 0)
-    scales[t.mat].alpha = static_cast<float>(ldexp(1.0 / (norm + kNormEps), -p2));
-  constexpr int ES = D == ZDS_FP32 ? 4 : 2;
-  const char *base = static_cast<const char *>(src) + mt.offset * ES;
-  // tile (ti, tj) of the rows x cols matrix as it lies in src
-  const int r0 = t.ti * kConvTile, c0 = t.tj * kConvTile;
-  for (int k = threadIdx.x; k < kConvTile * kConvTile; k += 256) {
-    const int r = k >> 6, c = k & 63;
-    float v = 0.0f;
-    if (r0 + r < mt.rows && c0 + c < mt.cols) v = widen1<D>(base, static_cast<int64_t>(r0 + r) * mt.cols + c0 + c);
-    sh[r][c] = v * up;
+  if (threadIdx.x == 0) {
+    if (t.ti == 0 && t.tj == 0) scales[t.mat].alpha = static_cast<float>(ldexp(1.0 / (norm + kNormEps), -p2));
+    if (blockIdx.x == 0)
+      for (int i = 0; i < kMaxSlots; ++i) arrived[i] = 0;
   }
-  __syncthreads();
   const int64_t plane = static_cast<int64_t>(mt.mp) * mt.np;
   half_t *x = ws + mt.x[0];
-  for (int k = threadIdx.x; k < kConvTile * 8; k += 256) {
-    const int r = k >> 3, c = (k & 7) * 8;
+  auto put = [&](int64_t e, const float (&f)[8]) {
     f16x8 h, l;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      const float v = mt.tall ? sh[c + j][r] : sh[r][c + j];
-      h[j] = static_cast<half_t>(v);
-      l[j] = static_cast<half_t>(v - static_cast<float>(h[j]));
+      const float y = f[j] * up;
+      h[j] = static_cast<half_t>(y);
+      l[j] = static_cast<half_t>(y - static_cast<float>(h[j]));
     }
-    const int64_t e = mt.tall ? (c0 + r) * static_cast<int64_t>(mt.np) + r0 + c
-                              : (r0 + r) * static_cast<int64_t>(mt.np) + c0 + c;
     *reinterpret_cast<f16x8 *>(x + e) = h;
     if (SEG == 3) *reinterpret_cast<f16x8 *>(x + plane + e) = l;
+  };
+  if (!mt.tall) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) put(static_cast<int64_t>(r0 + tr + 32 * h) * mt.np + c0 + tc, v[h]);
+    return;
+  }
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) sh[tr + 32 * h][tc + j] = v[h][j];
+  __syncthreads();
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    float u[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) u[j] = sh[tc + j][tr + 32 * h];
+    put(static_cast<int64_t>(c0 + tr + 32 * h) * mt.np + r0 + tc, u);
   }
 }
 
@@ -142,7 +197,8 @@ __global__ void __launch_bounds__(256) ns_convert_kernel(const NsMatrix *mats, c
 // The products
 // ---------------------------------------------------------------------------
 
-enum NsKind { kGram = 0, kPoly = 1, kUpdate = 2, kLast = 3 };
+// kGramCut: X X^T in a launch with cut tiles.
+enum NsKind { kGram = 0, kPoly = 1, kUpdate = 2, kLast = 3, kGramCut = 4 };
 
 struct NsArgs {
   const NsMatrix *mats;
@@ -151,6 +207,8 @@ struct NsArgs {
   half_t *ws;
   void *dst;
   const zds_step_scalars *sc;
+  float *pieces;       // of cut tiles: accumulators as the threads hold them
+  int32_t *arrived;    // and how many of a tile's pieces are there
   float a, b, c;       // the step's coefficients
   float sa, sb, sx;    // powers of two: A, B and X (but the first) as stored
   float carry;         // factor of X's remainder in a X
@@ -240,9 +298,11 @@ __device__ __forceinline__ void block_barrier() {
   asm volatile("" ::: "memory");
 }
 
-template <int T, int SEG, int KIND>
+template <int T, int SEG, int WHAT>
 __global__ void __launch_bounds__(256, T == 256 ? 1 : 2) ns_product_kernel(const NsArgs q) {
   typedef NsShape<T> S;
+  constexpr bool CUT = WHAT == kGramCut;
+  constexpr int KIND = CUT ? kGram : WHAT;
   constexpr bool TURN = KIND == kUpdate || KIND == kLast;  // P is X, read down its rows
   __shared__ __align__(1024) char smem[2][2][S::STAGE];
   if (q.sc && q.sc->overflow) return;
@@ -262,7 +322,9 @@ __global__ void __launch_bounds__(256, T == 256 ? 1 : 2) ns_product_kernel(const
   const int64_t pld = KIND == kPoly ? mp : np, qld = KIND == kGram ? np : mp;
   const int64_t pplane = KIND == kPoly ? aplane : xplane, qplane = KIND == kGram ? xplane : aplane;
   const int steps = (KIND == kGram ? mt.np : mt.mp) / kNsDepth;
-  const int total = steps * SEG;
+  const int all = steps * SEG;
+  const int from = CUT ? t.part * all / t.parts : 0;  // depth steps of this piece
+  const int total = CUT ? (t.part + 1) * all / t.parts : all;
 
   f32x4 acc[S::MI][S::MI];
 #pragma unroll
@@ -405,23 +467,24 @@ __global__ void __launch_bounds__(256, T == 256 ? 1 : 2) ns_product_kernel(const
       __builtin_amdgcn_sched_barrier(0);
     }
   };
-  aim(0);
+  const int b0 = from & 1;
+  aim(from);
 #pragma unroll
-  for (int g = 0; g < S::LOADS; ++g) load_p(0, g);
+  for (int g = 0; g < S::LOADS; ++g) load_p(b0, g);
 #pragma unroll
-  for (int g = 0; g < S::LOADS; ++g) load_q(0, g);
-  aim(1);
+  for (int g = 0; g < S::LOADS; ++g) load_q(b0, g);
+  aim(from + 1);
 #pragma unroll
-  for (int g = 0; g < S::LOADS; ++g) load_p(1, g);
+  for (int g = 0; g < S::LOADS; ++g) load_p(b0 ^ 1, g);
 #pragma unroll
-  for (int g = 0; g < EARLY; ++g) load_q(1, g);
+  for (int g = 0; g < EARLY; ++g) load_q(b0 ^ 1, g);
   asm volatile("s_waitcnt vmcnt(%0)" ::"n"(S::LOADS + EARLY) : "memory");
   block_barrier();
 #pragma unroll
-  for (int g = 0; g < S::MI; ++g) read_p(0, 0, g);
+  for (int g = 0; g < S::MI; ++g) read_p(b0, 0, g);
 #pragma unroll
-  for (int g = 0; g < NQ; ++g) read_q(0, 0, g);
-  for (int k = 0; k < total; ++k) {
+  for (int g = 0; g < NQ; ++g) read_q(b0, 0, g);
+  auto depth_step = [&](int k) {
     quarter(k, std::integral_constant<int, 0>{});
     quarter(k, std::integral_constant<int, 1>{});
     asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(S::LOADS) : "memory");
@@ -431,9 +494,49 @@ __global__ void __launch_bounds__(256, T == 256 ? 1 : 2) ns_product_kernel(const
     asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(YOUNGER) : "memory");
     block_barrier();
     quarter(k, std::integral_constant<int, 3>{});
+  };
+  if constexpr (CUT) {
+    int k = from;  // every piece has a step: only long sums are cut
+    do depth_step(k);
+    while (++k < total);
+  } else {
+    for (int k = 0; k < total; ++k) depth_step(k);
   }
   asm volatile("s_nop 15\n\ts_nop 15\n\ts_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
   block_barrier();
+
+  // A cut tile: every piece leaves its sums in memory, and the block that
+  // arrives last adds them in the pieces' order, so that the result does not
+  // depend on which one that is. It also clears the count for the next launch.
+  if (CUT && t.parts > 1) {
+    f32x4 *const pieces = reinterpret_cast<f32x4 *>(q.pieces) + static_cast<int64_t>(t.slot) * t.parts * (T * T / 4);
+    f32x4 *mine = pieces + t.part * (T * T / 4) + threadIdx.x;
+#pragma unroll
+    for (int i = 0; i < S::MI; ++i)
+#pragma unroll
+      for (int j = 0; j < S::MI; ++j) mine[(i * S::MI + j) * 256] = acc[i][j];
+    __threadfence();
+    __syncthreads();
+    int32_t *const last = reinterpret_cast<int32_t *>(smem);
+    if (threadIdx.x == 0)
+      *last = __hip_atomic_fetch_add(q.arrived + t.slot, 1, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT) == t.parts - 1;
+    __syncthreads();
+    if (!*last) return;
+    __syncthreads();  // smem is written again below
+    if (threadIdx.x == 0) q.arrived[t.slot] = 0;
+    __threadfence();
+#pragma unroll
+    for (int i = 0; i < S::MI; ++i)
+#pragma unroll
+      for (int j = 0; j < S::MI; ++j) acc[i][j] = pieces[(i * S::MI + j) * 256 + threadIdx.x];
+    for (int p = 1; p < t.parts; ++p) {
+      const f32x4 *o = pieces + p * (T * T / 4) + threadIdx.x;
+#pragma unroll
+      for (int i = 0; i < S::MI; ++i)
+#pragma unroll
+        for (int j = 0; j < S::MI; ++j) acc[i][j] += o[(i * S::MI + j) * 256];
+    }
+  }
 
   // Epilogue, in strips of MT rows of what is stored, each wave on its own in
   // its part of the LDS (two strips' room). A lane holds row fr of a strip, of
@@ -650,6 +753,13 @@ static void launch_products(const NsGroup &g, const NsTile *tiles, NsArgs q, int
   const dim3 block(NsShape<T>::WAVES * 64);
   if (kind == kGram || kind == kPoly) {
     q.tiles = tiles + g.tri0;
+    if constexpr (T == 256) {
+      if (kind == kGram && g.ncut) {
+        q.tiles = tiles + g.cut0;
+        hipLaunchKernelGGL((ns_product_kernel<T, SEG, kGramCut>), dim3(g.ncut), block, 0, s, q);
+        return;
+      }
+    }
     if (kind == kGram) hipLaunchKernelGGL((ns_product_kernel<T, SEG, kGram>), dim3(g.ntri), block, 0, s, q);
     else hipLaunchKernelGGL((ns_product_kernel<T, SEG, kPoly>), dim3(g.ntri), block, 0, s, q);
   } else {
@@ -682,13 +792,40 @@ static void spread_over_dies(std::vector<NsTile> &v, size_t from) {
   }
 }
 
+// The last launch round of X X^T's tiles from v[from] on, where it would leave
+// more than half of the compute units idle (one block a unit at this tile
+// size) and its sums are long: they are cut into pieces, up to kMaxPieces of
+// them, that fill the round. At 8192 x 22016 528 tiles are two rounds and 16
+// tiles: 1.30 ms cut, 1.49 ms whole. Leaving and adding the pieces takes about
+// 60 us, which sums of 4096 or 8192 do not pay for: the same cut in A^2 (8192
+// deep) costs 0.62 ms, whole it is 0.57. The matrices come in falling depth, so
+// the last tiles' sums are the shortest.
+constexpr int kUnits = 256, kMaxPieces = 8, kCutDepth = 16384;
+static bool cut_tail(std::vector<NsTile> &v, size_t from, const NsMatrix *mats, zds_matrix_plan *p) {
+  const int tail = static_cast<int>((v.size() - from) % kUnits);
+  const int parts = tail ? std::min(kMaxPieces, kUnits / tail) : 1;
+  if (parts < 2 || mats[v.back().mat].np < kCutDepth) return false;
+  const std::vector<NsTile> last(v.end() - tail, v.end());
+  v.resize(v.size() - static_cast<size_t>(tail));
+  for (int part = 0; part < parts; ++part)
+    for (int k = 0; k < tail; ++k) {
+      NsTile t = last[static_cast<size_t>(k)];
+      t.part = static_cast<uint8_t>(part);
+      t.parts = static_cast<uint8_t>(parts);
+      t.slot = static_cast<uint16_t>(k);
+      v.push_back(t);
+    }
+  p->max_cut = std::max(p->max_cut, tail * parts);
+  return true;
+}
+
 // Tiles in patches of 8 x 4, so that a run of 32 reads 8 + 4 operand tiles.
 static void add_tiles(std::vector<NsTile> &v, int mat, int ni, int nj, bool triangle) {
   for (int pj = 0; pj < nj; pj += 4)
     for (int pi = 0; pi < ni; pi += 8)
       for (int j = pj; j < pj + 4 && j < nj; ++j)
         for (int i = pi; i < pi + 8 && i < ni; ++i)
-          if (!triangle || i >= j) v.push_back(NsTile{mat, i, j, 0});
+          if (!triangle || i >= j) v.push_back(NsTile{mat, i, j, 0, 1, 0});
 }
 
 static int64_t round_up(int64_t x, int64_t a) { return (x + a - 1) / a * a; }
@@ -705,21 +842,56 @@ static int tile_of(int m, int n) {
 // chip many times over.
 constexpr int64_t kGroupElements = int64_t(1) << 28;
 
+// The workspace: partial sums of squares, scales, counts, the pieces of cut
+// tiles, and the fp16 arrays; the front is the same for every group.
+struct NsWorkspace {
+  double *partials;
+  NsScale *scales;
+  int32_t *arrived;
+  float *pieces;
+  half_t *arrays;
+  size_t front;
+  NsWorkspace(const zds_matrix_plan &p, void *ws) {
+    size_t at = 0;
+    auto take = [&](size_t bytes) {
+      char *here = static_cast<char *>(ws) + at;
+      at += (bytes + 255) / 256 * 256;
+      return static_cast<void *>(here);
+    };
+    partials = static_cast<double *>(take(sizeof(double) * static_cast<size_t>(p.max_parts)));
+    scales = static_cast<NsScale *>(take(sizeof(NsScale) * static_cast<size_t>(p.max_mats)));
+    arrived = static_cast<int32_t *>(take(sizeof(int32_t) * kMaxSlots));
+    pieces = static_cast<float *>(take(sizeof(float) * 256 * 256 * static_cast<size_t>(p.max_cut)));
+    arrays = static_cast<half_t *>(take(0));
+    front = at;
+  }
+  size_t bytes(int64_t halves) const { return front + static_cast<size_t>(halves) * 2; }
+};
+
 zds_status build_newton_schulz(zds_matrix_plan *p, const int64_t *offset, const int32_t *rows, const int32_t *cols,
                                int32_t num) {
+  // the longest sums first
+  std::vector<int32_t> order(static_cast<size_t>(num));
+  for (int32_t i = 0; i < num; ++i) order[static_cast<size_t>(i)] = i;
+  std::stable_sort(order.begin(), order.end(), [&](int32_t a, int32_t b) {
+    const auto key = [&](int32_t i) {
+      return std::make_pair(std::max(rows[i], cols[i]), std::min(rows[i], cols[i]));
+    };
+    return key(a) > key(b);
+  });
   std::vector<NsMatrix> mats[2];
   std::vector<NsTile> tiles;
-  size_t head = 0;  // bytes in front of the fp16 arrays, the same for every group
   int64_t most[2] = {0, 0};
   for (int tile : {256, 128, 64}) {
-    int32_t i = 0;
-    while (i < num) {
+    int32_t at = 0;
+    while (at < num) {
       NsGroup g{};
       g.tile = tile;
       g.mat0 = static_cast<int32_t>(mats[0].size());
       int64_t elems = 0, pos[2] = {0, 0};
       int32_t parts = 0;
-      for (; i < num && elems < kGroupElements; ++i) {
+      for (; at < num && elems < kGroupElements; ++at) {
+        const int32_t i = order[static_cast<size_t>(at)];
         if (rows[i] == 0 || cols[i] == 0) continue;
         NsMatrix m{};
         m.offset = offset[i];
@@ -732,7 +904,9 @@ zds_status build_newton_schulz(zds_matrix_plan *p, const int64_t *offset, const 
         m.mp = static_cast<int32_t>(round_up(m.m, tile));
         m.np = static_cast<int32_t>(round_up(m.n, tile));
         m.part0 = parts;
-        m.nparts = static_cast<int32_t>((static_cast<int64_t>(m.rows) * m.cols + kNormChunk - 1) / kNormChunk);
+        const int64_t len = static_cast<int64_t>(m.rows) * m.cols;
+        m.chunk = static_cast<int32_t>(std::max(kNormChunk, round_up((len + kMaxParts - 1) / kMaxParts, 2048)));
+        m.nparts = static_cast<int32_t>((len + m.chunk - 1) / m.chunk);
         parts += m.nparts;
         const int64_t xe = static_cast<int64_t>(m.mp) * m.np, ae = static_cast<int64_t>(m.mp) * m.mp;
         for (int f = 0; f < 2; ++f) {
@@ -755,19 +929,27 @@ zds_status build_newton_schulz(zds_matrix_plan *p, const int64_t *offset, const 
       if (g.nmat > p->max_mats) p->max_mats = g.nmat;
       auto each = [&](auto &&fn) { for (int32_t k = 0; k < g.nmat; ++k) fn(k, mats[0][static_cast<size_t>(g.mat0 + k)]); };
       g.chunk0 = static_cast<int32_t>(tiles.size());
-      each([&](int32_t k, const NsMatrix &m) { for (int c = 0; c < m.nparts; ++c) tiles.push_back(NsTile{k, c, 0, 0}); });
+      each([&](int32_t k, const NsMatrix &m) { for (int c = 0; c < m.nparts; ++c) tiles.push_back(NsTile{k, c, 0, 0, 1, 0}); });
       g.nchunk = static_cast<int32_t>(tiles.size()) - g.chunk0;
       g.conv0 = static_cast<int32_t>(tiles.size());
       each([&](int32_t k, const NsMatrix &m) {
         const int rp = (m.tall ? m.np : m.mp) / kConvTile, cp = (m.tall ? m.mp : m.np) / kConvTile;
         for (int a = 0; a < rp; ++a)
-          for (int b = 0; b < cp; ++b) tiles.push_back(NsTile{k, a, b, 0});
+          for (int b = 0; b < cp; ++b) tiles.push_back(NsTile{k, a, b, 0, 1, 0});
       });
       g.nconv = static_cast<int32_t>(tiles.size()) - g.conv0;
       g.tri0 = static_cast<int32_t>(tiles.size());
       each([&](int32_t k, const NsMatrix &m) { add_tiles(tiles, k, m.mp / tile, m.mp / tile, true); });
+      const std::vector<NsTile> triangle(tiles.begin() + g.tri0, tiles.end());
       spread_over_dies(tiles, static_cast<size_t>(g.tri0));
       g.ntri = static_cast<int32_t>(tiles.size()) - g.tri0;
+      g.cut0 = static_cast<int32_t>(tiles.size());
+      tiles.insert(tiles.end(), triangle.begin(), triangle.end());
+      if (tile == 256 && cut_tail(tiles, static_cast<size_t>(g.cut0), &mats[0][static_cast<size_t>(g.mat0)], p))
+        spread_over_dies(tiles, static_cast<size_t>(g.cut0));
+      else
+        tiles.resize(static_cast<size_t>(g.cut0));
+      g.ncut = static_cast<int32_t>(tiles.size()) - g.cut0;
       g.full0 = static_cast<int32_t>(tiles.size());
       each([&](int32_t k, const NsMatrix &m) { add_tiles(tiles, k, m.np / tile, m.mp / tile, false); });
       spread_over_dies(tiles, static_cast<size_t>(g.full0));
@@ -775,8 +957,7 @@ zds_status build_newton_schulz(zds_matrix_plan *p, const int64_t *offset, const 
       p->groups.push_back(g);
     }
   }
-  head = static_cast<size_t>(round_up(p->max_parts * 8 + p->max_mats * static_cast<int64_t>(sizeof(NsScale)), 256));
-  for (int f = 0; f < 2; ++f) p->ws_bytes[f] = p->groups.empty() ? 0 : head + static_cast<size_t>(most[f]) * 2;
+  for (int f = 0; f < 2; ++f) p->ws_bytes[f] = p->groups.empty() ? 0 : NsWorkspace(*p, nullptr).bytes(most[f]);
   if (p->groups.empty()) return ZDS_OK;
   const char *what = "zds_matrix_plan_create";
   auto upload = [&](void **d, const void *h, size_t bytes) -> zds_status {
@@ -796,14 +977,12 @@ zds_status build_newton_schulz(zds_matrix_plan *p, const int64_t *offset, const 
 template <int D, int SEG>
 static zds_status run_newton_schulz(const zds_matrix_plan &p, const void *src, void *dst, const float *coef, int32_t steps,
                                     double xb, double bb, const zds_step_scalars *sc, void *ws, hipStream_t s) {
-  double *partials = static_cast<double *>(ws);
-  NsScale *scales = reinterpret_cast<NsScale *>(partials + p.max_parts);
-  const size_t head = static_cast<size_t>(
-      round_up(p.max_parts * 8 + p.max_mats * static_cast<int64_t>(sizeof(NsScale)), 256));
-  half_t *arrays = reinterpret_cast<half_t *>(static_cast<char *>(ws) + head);
+  const NsWorkspace w(p, ws);
   NsArgs q{};
-  q.scales = scales;
-  q.ws = arrays;
+  q.scales = w.scales;
+  q.ws = w.arrays;
+  q.pieces = w.pieces;
+  q.arrived = w.arrived;
   q.dst = dst;
   q.sc = sc;
   // fp16 holds up to 65504: X up to xb, A up to xb^2, B up to bb stay below half of that
@@ -812,9 +991,9 @@ static zds_status run_newton_schulz(const zds_matrix_plan &p, const void *src, v
   q.sb = pow2_under(32768.0, bb > 0.0 ? bb : 1.0);
   for (const NsGroup &g : p.groups) {
     q.mats = p.d_mats[SEG == 3] + g.mat0;
-    hipLaunchKernelGGL((ns_norm_kernel<D>), dim3(g.nchunk), dim3(256), 0, s, q.mats, p.d_tiles + g.chunk0, src, partials, sc);
+    hipLaunchKernelGGL((ns_norm_kernel<D>), dim3(g.nchunk), dim3(256), 0, s, q.mats, p.d_tiles + g.chunk0, src, w.partials, sc);
     hipLaunchKernelGGL((ns_convert_kernel<D, SEG>), dim3(g.nconv), dim3(256), 0, s, q.mats, p.d_tiles + g.conv0, src,
-                       partials, scales, arrays, sc);
+                       w.partials, w.scales, w.arrived, w.arrays, sc);
     zds_status st = check_launch("newton_schulz conversion");
     if (st != ZDS_OK) return st;
     for (int k = 0; k < steps; ++k) {
