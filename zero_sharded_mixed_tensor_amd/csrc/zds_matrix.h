@@ -42,7 +42,7 @@ struct NsTile {
 // them), the full product, the conversion
 // (64 x 64 tiles over the padded matrix) and the norm's chunks.
 struct NsGroup {
-  int32_t tile;                 // the products' tile size
+  int32_t tri_tile, full_tile;  // tile sizes of the triangular products and of the full one
   int32_t mat0, nmat;           // matrices in the plan's device array
   int32_t tri0, ntri, cut0, ncut, full0, nfull, conv0, nconv, chunk0, nchunk;  // in the plan's tile array
 };

@@ -40,6 +40,7 @@ constexpr int kMaxSlots = 128;
 // most kMaxParts of them.
 constexpr int64_t kNormChunk = 32768;
 constexpr int kMaxParts = 1024;
+constexpr int kUnits = 256;  // compute units
 constexpr int kConvTile = 64;
 
 // A matrix's first X as stored and true: X_true = alpha * X_stored.
@@ -771,8 +772,9 @@ static void launch_products(const NsGroup &g, const NsTile *tiles, NsArgs q, int
 
 template <int SEG>
 static void launch_products(const NsGroup &g, const NsTile *tiles, const NsArgs &q, int kind, hipStream_t s) {
-  if (g.tile == 256) launch_products<256, SEG>(g, tiles, q, kind, s);
-  else if (g.tile == 128) launch_products<128, SEG>(g, tiles, q, kind, s);
+  const int tile = kind == kGram || kind == kPoly ? g.tri_tile : g.full_tile;
+  if (tile == 256) launch_products<256, SEG>(g, tiles, q, kind, s);
+  else if (tile == 128) launch_products<128, SEG>(g, tiles, q, kind, s);
   else launch_products<64, SEG>(g, tiles, q, kind, s);
 }
 
@@ -800,7 +802,7 @@ static void spread_over_dies(std::vector<NsTile> &v, size_t from) {
 // 60 us, which sums of 4096 or 8192 do not pay for: the same cut in A^2 (8192
 // deep) costs 0.62 ms, whole it is 0.57. The matrices come in falling depth, so
 // the last tiles' sums are the shortest.
-constexpr int kUnits = 256, kMaxPieces = 8, kCutDepth = 16384;
+constexpr int kMaxPieces = 8, kCutDepth = 16384;
 static bool cut_tail(std::vector<NsTile> &v, size_t from, const NsMatrix *mats, zds_matrix_plan *p) {
   const int tail = static_cast<int>((v.size() - from) % kUnits);
   const int parts = tail ? std::min(kMaxPieces, kUnits / tail) : 1;
@@ -830,14 +832,65 @@ static void add_tiles(std::vector<NsTile> &v, int mat, int ni, int nj, bool tria
 
 static int64_t round_up(int64_t x, int64_t a) { return (x + a - 1) / a * a; }
 
-// The product tile of a matrix by its smaller size.
-static int tile_of(int m, int n) {
-  if (m >= 1024) return 256;
-  if (m > 128) return 128;
+// Sizes are padded to a multiple of 256, 128 or 64: the largest that costs at
+// most 15 % more of the full product than 64 does, since a larger tile reads
+// its operands less often.
+static int padding_of(int64_t m, int64_t n) {
+  const auto work = [&](int64_t t) { return static_cast<double>(round_up(m, t)) * round_up(m, t) * round_up(n, t); };
+  for (int t : {256, 128})
+    if (work(t) <= 1.15 * work(64)) return t;
   return 64;
 }
 
-// A group's matrices share a tile size; it is closed when its elements reach
+// What a launch of `tiles` T x T tiles of `steps` depth steps on average takes,
+// in us, fitted to measured launches (1 to 2048 tiles of 16 to 172 steps): a
+// block's fixed part, and a step's time by how many blocks share a unit. At
+// 1024 x 1024 x 64 steps (10, 36, 136 tiles) 71, 35 and 27 us; at
+// 4096 x 4096 x 64 steps (256, 1024, 4096 tiles) 119, 131 and 244 us.
+static double launch_cost(int t, int64_t tiles, double steps) {
+  static const struct { int tile, blocks; double fixed[4], step[4]; } kinds[3] = {
+      {256, 1, {12.0}, {1.25}},
+      {128, 2, {5.0, 8.0}, {0.5, 0.95}},
+      {64, 4, {4.0, 5.0, 6.0, 7.5}, {0.37, 0.5, 0.67, 0.85}},
+  };
+  for (const auto &k : kinds) {
+    if (k.tile != t) continue;
+    const int64_t slots = static_cast<int64_t>(kUnits) * k.blocks;
+    const auto round = [&](int64_t n) {  // n tiles at once
+      const int64_t share = (n + kUnits - 1) / kUnits - 1;
+      return k.fixed[share] + steps * k.step[share];
+    };
+    return static_cast<double>(tiles / slots) * round(slots) + (tiles % slots ? round(tiles % slots) : 0.0);
+  }
+  return 0.0;
+}
+
+// The tile size, at most `most`, of a launch over a group's matrices; *cost: of
+// its launches in a step.
+static int tile_for(const NsMatrix *mats, int n, int most, bool triangle, double *cost) {
+  int best = most;
+  double least = -1.0;
+  for (int t = most; t >= 64; t /= 2) {
+    int64_t tiles = 0;
+    double steps = 0.0;
+    for (int i = 0; i < n; ++i) {
+      const int64_t a = mats[i].mp / t, b = mats[i].np / t;
+      const int64_t k = triangle ? a * (a + 1) / 2 : a * b;
+      tiles += k;
+      // the triangle is launched for X X^T, np deep, and for A A, mp deep
+      steps += static_cast<double>(k) * (triangle ? 0.5 * (mats[i].np + mats[i].mp) : mats[i].mp) / kNsDepth;
+    }
+    const double c = launch_cost(t, tiles, steps / static_cast<double>(tiles)) * (triangle ? 2 : 1);
+    if (least < 0.0 || c < least) {
+      least = c;
+      best = t;
+    }
+  }
+  *cost = least;
+  return best;
+}
+
+// A group's matrices share a padding; it is closed when its elements reach
 // this many (the workspace is about 9 bytes an element): enough to fill the
 // chip many times over.
 constexpr int64_t kGroupElements = int64_t(1) << 28;
@@ -879,19 +932,21 @@ zds_status build_newton_schulz(zds_matrix_plan *p, const int64_t *offset, const 
     };
     return key(a) > key(b);
   });
-  std::vector<NsMatrix> mats[2];
-  std::vector<NsTile> tiles;
-  int64_t most[2] = {0, 0};
-  for (int tile : {256, 128, 64}) {
-    int32_t at = 0;
-    while (at < num) {
-      NsGroup g{};
-      g.tile = tile;
-      g.mat0 = static_cast<int32_t>(mats[0].size());
-      int64_t elems = 0, pos[2] = {0, 0};
-      int32_t parts = 0;
-      for (; at < num && elems < kGroupElements; ++at) {
-        const int32_t i = order[static_cast<size_t>(at)];
+  // Groups, each of one padding: every matrix with the padding that suits it,
+  // or, where that makes several short sequences of launches, all with one.
+  struct Draft {
+    int padding;
+    std::vector<NsMatrix> mats;
+  };
+  std::vector<Draft> drafts;
+  double least = -1.0;
+  for (int only : {0, 256, 128, 64}) {
+    std::vector<Draft> d;
+    double cost = 0.0;
+    for (int padding : {256, 128, 64}) {
+      int64_t elems = kGroupElements;
+      const size_t before = d.size();
+      for (int32_t i : order) {
         if (rows[i] == 0 || cols[i] == 0) continue;
         NsMatrix m{};
         m.offset = offset[i];
@@ -900,62 +955,90 @@ zds_status build_newton_schulz(zds_matrix_plan *p, const int64_t *offset, const 
         m.tall = rows[i] > cols[i];
         m.m = m.tall ? cols[i] : rows[i];
         m.n = m.tall ? rows[i] : cols[i];
-        if (tile_of(m.m, m.n) != tile) continue;
-        m.mp = static_cast<int32_t>(round_up(m.m, tile));
-        m.np = static_cast<int32_t>(round_up(m.n, tile));
-        m.part0 = parts;
-        const int64_t len = static_cast<int64_t>(m.rows) * m.cols;
-        m.chunk = static_cast<int32_t>(std::max(kNormChunk, round_up((len + kMaxParts - 1) / kMaxParts, 2048)));
-        m.nparts = static_cast<int32_t>((len + m.chunk - 1) / m.chunk);
-        parts += m.nparts;
-        const int64_t xe = static_cast<int64_t>(m.mp) * m.np, ae = static_cast<int64_t>(m.mp) * m.mp;
-        for (int f = 0; f < 2; ++f) {
-          const int64_t planes = f ? 2 : 1;
-          NsMatrix d = m;
-          auto take = [&](int64_t e) { const int64_t at = pos[f]; pos[f] += e; return at; };
-          d.x[0] = take(xe * planes);
-          d.x[1] = take(xe * planes);
-          d.lo = f ? 0 : take(xe);
-          d.a = take(ae * planes);
-          d.b = take(ae * planes);
-          mats[f].push_back(d);
+        if ((only ? only : padding_of(m.m, m.n)) != padding) continue;
+        m.mp = static_cast<int32_t>(round_up(m.m, padding));
+        m.np = static_cast<int32_t>(round_up(m.n, padding));
+        if (elems >= kGroupElements) {
+          d.push_back(Draft{padding, {}});
+          elems = 0;
         }
-        elems += xe;
+        elems += static_cast<int64_t>(m.mp) * m.np;
+        d.back().mats.push_back(m);
       }
-      g.nmat = static_cast<int32_t>(mats[0].size()) - g.mat0;
-      if (g.nmat == 0) continue;
-      for (int f = 0; f < 2; ++f) most[f] = pos[f] > most[f] ? pos[f] : most[f];
-      if (parts > p->max_parts) p->max_parts = parts;
-      if (g.nmat > p->max_mats) p->max_mats = g.nmat;
-      auto each = [&](auto &&fn) { for (int32_t k = 0; k < g.nmat; ++k) fn(k, mats[0][static_cast<size_t>(g.mat0 + k)]); };
-      g.chunk0 = static_cast<int32_t>(tiles.size());
-      each([&](int32_t k, const NsMatrix &m) { for (int c = 0; c < m.nparts; ++c) tiles.push_back(NsTile{k, c, 0, 0, 1, 0}); });
-      g.nchunk = static_cast<int32_t>(tiles.size()) - g.chunk0;
-      g.conv0 = static_cast<int32_t>(tiles.size());
-      each([&](int32_t k, const NsMatrix &m) {
-        const int rp = (m.tall ? m.np : m.mp) / kConvTile, cp = (m.tall ? m.mp : m.np) / kConvTile;
-        for (int a = 0; a < rp; ++a)
-          for (int b = 0; b < cp; ++b) tiles.push_back(NsTile{k, a, b, 0, 1, 0});
-      });
-      g.nconv = static_cast<int32_t>(tiles.size()) - g.conv0;
-      g.tri0 = static_cast<int32_t>(tiles.size());
-      each([&](int32_t k, const NsMatrix &m) { add_tiles(tiles, k, m.mp / tile, m.mp / tile, true); });
-      const std::vector<NsTile> triangle(tiles.begin() + g.tri0, tiles.end());
-      spread_over_dies(tiles, static_cast<size_t>(g.tri0));
-      g.ntri = static_cast<int32_t>(tiles.size()) - g.tri0;
-      g.cut0 = static_cast<int32_t>(tiles.size());
-      tiles.insert(tiles.end(), triangle.begin(), triangle.end());
-      if (tile == 256 && cut_tail(tiles, static_cast<size_t>(g.cut0), &mats[0][static_cast<size_t>(g.mat0)], p))
-        spread_over_dies(tiles, static_cast<size_t>(g.cut0));
-      else
-        tiles.resize(static_cast<size_t>(g.cut0));
-      g.ncut = static_cast<int32_t>(tiles.size()) - g.cut0;
-      g.full0 = static_cast<int32_t>(tiles.size());
-      each([&](int32_t k, const NsMatrix &m) { add_tiles(tiles, k, m.np / tile, m.mp / tile, false); });
-      spread_over_dies(tiles, static_cast<size_t>(g.full0));
-      g.nfull = static_cast<int32_t>(tiles.size()) - g.full0;
-      p->groups.push_back(g);
+      for (size_t k = before; k < d.size(); ++k)
+        for (bool triangle : {true, false}) {
+          double c = 0.0;
+          (void)tile_for(d[k].mats.data(), static_cast<int>(d[k].mats.size()), padding, triangle, &c);
+          cost += c;
+        }
     }
+    if (least < 0.0 || cost < least) {
+      least = cost;
+      drafts = std::move(d);
+    }
+  }
+  std::vector<NsMatrix> mats[2];
+  std::vector<NsTile> tiles;
+  int64_t most[2] = {0, 0};
+  for (const Draft &draft : drafts) {
+    NsGroup g{};
+    g.mat0 = static_cast<int32_t>(mats[0].size());
+    int64_t pos[2] = {0, 0};
+    int32_t parts = 0;
+    for (NsMatrix m : draft.mats) {
+      m.part0 = parts;
+      const int64_t len = static_cast<int64_t>(m.rows) * m.cols;
+      m.chunk = static_cast<int32_t>(std::max(kNormChunk, round_up((len + kMaxParts - 1) / kMaxParts, 2048)));
+      m.nparts = static_cast<int32_t>((len + m.chunk - 1) / m.chunk);
+      parts += m.nparts;
+      const int64_t xe = static_cast<int64_t>(m.mp) * m.np, ae = static_cast<int64_t>(m.mp) * m.mp;
+      for (int f = 0; f < 2; ++f) {
+        const int64_t planes = f ? 2 : 1;
+        NsMatrix d = m;
+        auto take = [&](int64_t e) { const int64_t at = pos[f]; pos[f] += e; return at; };
+        d.x[0] = take(xe * planes);
+        d.x[1] = take(xe * planes);
+        d.lo = f ? 0 : take(xe);
+        d.a = take(ae * planes);
+        d.b = take(ae * planes);
+        mats[f].push_back(d);
+      }
+    }
+    g.nmat = static_cast<int32_t>(mats[0].size()) - g.mat0;
+    for (int f = 0; f < 2; ++f) most[f] = pos[f] > most[f] ? pos[f] : most[f];
+    if (parts > p->max_parts) p->max_parts = parts;
+    if (g.nmat > p->max_mats) p->max_mats = g.nmat;
+    auto each = [&](auto &&fn) { for (int32_t k = 0; k < g.nmat; ++k) fn(k, mats[0][static_cast<size_t>(g.mat0 + k)]); };
+    g.chunk0 = static_cast<int32_t>(tiles.size());
+    each([&](int32_t k, const NsMatrix &m) { for (int c = 0; c < m.nparts; ++c) tiles.push_back(NsTile{k, c, 0, 0, 1, 0}); });
+    g.nchunk = static_cast<int32_t>(tiles.size()) - g.chunk0;
+    g.conv0 = static_cast<int32_t>(tiles.size());
+    each([&](int32_t k, const NsMatrix &m) {
+      const int rp = (m.tall ? m.np : m.mp) / kConvTile, cp = (m.tall ? m.mp : m.np) / kConvTile;
+      for (int a = 0; a < rp; ++a)
+        for (int b = 0; b < cp; ++b) tiles.push_back(NsTile{k, a, b, 0, 1, 0});
+    });
+    g.nconv = static_cast<int32_t>(tiles.size()) - g.conv0;
+    double cost;
+    g.tri_tile = tile_for(draft.mats.data(), g.nmat, draft.padding, true, &cost);
+    g.full_tile = tile_for(draft.mats.data(), g.nmat, draft.padding, false, &cost);
+    g.tri0 = static_cast<int32_t>(tiles.size());
+    each([&](int32_t k, const NsMatrix &m) { add_tiles(tiles, k, m.mp / g.tri_tile, m.mp / g.tri_tile, true); });
+    const std::vector<NsTile> triangle(tiles.begin() + g.tri0, tiles.end());
+    spread_over_dies(tiles, static_cast<size_t>(g.tri0));
+    g.ntri = static_cast<int32_t>(tiles.size()) - g.tri0;
+    g.cut0 = static_cast<int32_t>(tiles.size());
+    tiles.insert(tiles.end(), triangle.begin(), triangle.end());
+    if (g.tri_tile == 256 && cut_tail(tiles, static_cast<size_t>(g.cut0), &mats[0][static_cast<size_t>(g.mat0)], p))
+      spread_over_dies(tiles, static_cast<size_t>(g.cut0));
+    else
+      tiles.resize(static_cast<size_t>(g.cut0));
+    g.ncut = static_cast<int32_t>(tiles.size()) - g.cut0;
+    g.full0 = static_cast<int32_t>(tiles.size());
+    each([&](int32_t k, const NsMatrix &m) { add_tiles(tiles, k, m.np / g.full_tile, m.mp / g.full_tile, false); });
+    spread_over_dies(tiles, static_cast<size_t>(g.full0));
+    g.nfull = static_cast<int32_t>(tiles.size()) - g.full0;
+    p->groups.push_back(g);
   }
   for (int f = 0; f < 2; ++f) p->ws_bytes[f] = p->groups.empty() ? 0 : NsWorkspace(*p, nullptr).bytes(most[f]);
   if (p->groups.empty()) return ZDS_OK;
