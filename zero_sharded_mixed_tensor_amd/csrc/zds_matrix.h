@@ -49,7 +49,7 @@ struct NsGroup {
 
 // A chunk of a matrix for zds_muon_apply: up to kApplyChunk elements from flat
 // offset `first`, and the matrix's two scale factors (zds_muon_scale 1 and 2).
-constexpr int kApplyChunk = 4096;
+constexpr int kApplyChunk = 2048;
 struct ApplyChunk {
   int64_t first;
   int32_t len;
