@@ -312,3 +312,109 @@ def test_streams_and_graph_replays():
         torch.cuda.synchronize()
         assert torch.equal(out, want)
     plan.close()
+
+
+# ------------------------------------------------------------------ the whole step
+
+def _oracle_step(O, x, master, mom, m, v, st, hp, mats, split, cfg):
+    """One MuonStep in plain NumPy: (the new arrays, or None when skipped; the step scalars)."""
+    sc = O.overflow_and_norm(x, "fp16", st.scale, cfg["K"], cfg["max_norm"])
+    if sc["overflow"]:
+        return None, sc
+    gs = sc["grad_scale"]
+    mom, u = M.muon_momentum(x[:split], "fp16", mom, gs, 0.95, True, "bf16")
+    master = master.copy()
+    for o, r, c in mats:
+        s = slice(o, o + r * c)
+        q = narrow(M.newton_schulz(widen(u[s], "bf16").astype(np.float64).reshape(r, c)).reshape(-1).astype(np.float32), "bf16")
+        master[s], _ = M.muon_apply(q, "bf16", master[s], r, c, cfg["lr"], cfg["wd"], "rms", "fp16")
+    con = O.adamw_constants(hp, st.beta1_pow, st.beta2_pow)
+    p, m, v = O.adamw_update(x[split:], "fp16", gs, master[split:], m, v, con)
+    master[split:] = p
+    return (master, mom, m, v), sc
+
+
+def test_muon_step_follows_the_definition():
+    """Three steps and one with an overflow between them, matrices and other
+    tensors together, eager and from a captured graph. The momentum and
+    AdamW's arrays are bit-exact; the matrices' weights are off by at most
+    lr * scale * (the orthogonalisation's error) in each step."""
+    import oracle as O
+    from zero_sharded_mixed_tensor_amd.step import MuonStep
+    mats, split = layout([(96, 160), (200, 72), (64, 64), (300, 300)], gap=64)
+    split = -(-split // 64) * 64
+    n = split + 5000
+    rng = np.random.default_rng(17)
+    master = (rng.standard_normal(n) * 0.02).astype(np.float32)
+    pad = np.ones(split, bool)
+    for o, r, c in mats:
+        pad[o:o + r * c] = False
+    master[:split][pad] = 0
+    xs = [(rng.standard_normal(n) * 1e-2 * 2.0 ** 10).astype(np.float16).view(np.uint16) for _ in range(4)]
+    for x in xs:
+        x[:split][pad] = 0
+    xs[2][7] = 0x7C00  # an infinity
+    cfg = dict(K=2, max_norm=1.0, lr=2e-2, wd=0.1)
+    muon = zds.muon_hparams(lr=cfg["lr"], momentum=0.95, weight_decay=cfg["wd"], scale="rms")
+
+    def fresh():
+        st = MuonStep(n, split, mats, zds.hparams(), muon, zds.scaler_config(initial_scale_power=10), 1.0, 2)
+        dev = [torch.from_numpy(master.copy()).cuda(), torch.zeros(split, device="cuda"),
+               torch.zeros(n - split, device="cuda"), torch.zeros(n - split, device="cuda"),
+               torch.zeros(n, dtype=torch.float16, device="cuda")]
+        return st, dev
+
+    st, dev = fresh()
+    want = [master.copy(), np.zeros(split, np.float32), np.zeros(n - split, np.float32), np.zeros(n - split, np.float32)]
+    ost = O.scaler_init(initial_scale_power=10)
+    hp = O.AdamW()
+    norms = {k: 0.2 * np.sqrt(max(r, c)) * np.sqrt(min(r, c)) * 1.3 for k, (_, r, c) in enumerate(mats)}
+    eager, steps = [], 0
+    for x in xs:
+        st.step(to_dev(x, "fp16"), dev[0], dev[1], dev[2], dev[3], dev[4])
+        new, sc = _oracle_step(O, x, want[0], want[1], want[2], want[3], ost, hp, mats, split, cfg)
+        ost = O.scaler_update(ost, sc["overflow"], hp.beta1, hp.beta2)
+        s = st.read_state()
+        assert (s.t, s.scale, s.steps_skipped) == (ost.t, ost.scale, int(x is xs[2] or x is xs[3]))
+        if new is not None:
+            want, steps = list(new), steps + 1
+        got = [to_host(t) for t in dev]
+        assert np.array_equal(got[1], want[1])
+        assert np.array_equal(got[0][split:], want[0][split:])
+        assert np.array_equal(got[2], want[2]) and np.array_equal(got[3], want[3])
+        assert (got[0][:split][pad] == 0).all()
+        for k, (o, r, c) in enumerate(mats):
+            a, b = got[0][o:o + r * c].astype(np.float64), want[0][o:o + r * c].astype(np.float64)
+            assert np.linalg.norm(a - b) <= steps * cfg["lr"] * norms[k] * TOL["bf16"] + 1e-6 * np.linalg.norm(b)
+            assert np.array_equal(got[4][o:o + r * c], narrow(got[0][o:o + r * c], "fp16"))
+        eager.append([t.clone() for t in dev])
+    # the same steps replayed from a graph
+    st, dev = fresh()
+    g = to_dev(xs[0], "fp16")
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        st.step(g, dev[0], dev[1], dev[2], dev[3], dev[4])
+    for x, e in zip(xs, eager):
+        g.copy_(to_dev(x, "fp16"))
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(dev, e):
+            assert torch.equal(a, b)
+
+
+def test_muon_step_from_config_and_refusals():
+    from zero_sharded_mixed_tensor_amd.config import from_ds_config
+    from zero_sharded_mixed_tensor_amd.step import MuonStep
+    cfg = from_ds_config({"optimizer": {"type": "Muon", "params": {"lr": 1e-2, "ns_steps": 3}}, "bf16": {"enabled": True}})
+    st = MuonStep.from_config(64 * 64, 64 * 64, [(0, 64, 64)], cfg)
+    assert st.ns_steps == 3 and st.split == 4096
+    g = torch.randn(4096, device="cuda").bfloat16()
+    w, m = torch.randn(4096, device="cuda"), torch.zeros(4096, device="cuda")
+    e = torch.empty(0, device="cuda")
+    before = w.clone()
+    st.step(g, w, m, e, e, None)                 # nothing but matrices, no 16-bit copy
+    assert not torch.equal(w, before) and torch.isfinite(w).all()
+    for split in (4095, -1, 4097):
+        with pytest.raises(zds.ZdsError):
+            MuonStep(4096, split, [(0, 64, 64)])

@@ -134,3 +134,26 @@ def test_newton_schulz_moves_singular_values_only():
 def test_apply_scales():
     assert M.muon_scale(400, 100, "aspect") == np.float32(2.0) and M.muon_scale(100, 400, "aspect") == np.float32(1.0)
     assert M.muon_scale(100, 400, "rms") == np.float32(0.2 * 20.0) and M.muon_scale(3, 7, "none") == 1.0
+
+
+def test_config_maps_muon():
+    from zero_sharded_mixed_tensor_amd.config import ConfigError, from_ds_config
+    c = from_ds_config({"optimizer": {"type": "Muon", "params": {"lr": 2e-2, "weight_decay": 0.1}},
+                        "bf16": {"enabled": True}, "gradient_clipping": 1.0})
+    assert (c.muon.lr, c.muon.momentum, c.muon.nesterov, c.muon.ns_steps, c.muon.scale) == (2e-2, 0.95, True, 5, "aspect")
+    assert c.lr == 2e-2 and c.param_dtype == "bf16"
+    hp = c.muon_hparams()
+    assert abs(hp.lr - 2e-2) < 1e-8 and hp.scale == zds.ZDS_MUON_SCALE_ASPECT and abs(hp.weight_decay - 0.1) < 1e-8
+    c = from_ds_config({"optimizer": {"type": "muon", "params": {
+        "lr": 1e-3, "muon_lr": 5e-3, "adam_lr": 3e-4, "momentum": 0.9, "nesterov": False, "ns_steps": 6, "scale": "rms",
+        "betas": [0.8, 0.95]}}})
+    assert (c.muon.lr, c.lr, c.beta1, c.beta2) == (5e-3, 3e-4, 0.8, 0.95)
+    assert (c.muon.momentum, c.muon.nesterov, c.muon.ns_steps, c.muon.scale) == (0.9, False, 6, "rms")
+    assert from_ds_config({}).muon is None
+    with pytest.raises(ConfigError):
+        from_ds_config({}).muon_hparams()
+    for bad in ({"momentum": 1.0}, {"ns_steps": 0}, {"ns_steps": 17}, {"scale": "fan"}, {"nesterov": 1}, {"momentum": "x"}):
+        with pytest.raises(ConfigError):
+            from_ds_config({"optimizer": {"type": "Muon", "params": bad}})
+    with pytest.raises(ConfigError):
+        from_ds_config({"optimizer": {"type": "Muon"}, "zero_optimization": {"offload_optimizer": {"device": "cpu"}}})

@@ -7,6 +7,10 @@ The fields that decide one rank's optimizer step are read here; the others
 
   optimizer.type / params   AdamW (or Adam in its decoupled-decay form):
                             lr, betas, eps, weight_decay -> zds_adamw_hparams
+  optimizer.type Muon       momentum, weight_decay, nesterov, ns_steps, scale
+                            ("aspect", "rms" or "none") -> zds_muon_hparams for
+                            the matrices; betas, eps, weight_decay for the other
+                            tensors' AdamW; lr for both, or muon_lr and adam_lr
   fp16.enabled + loss_scale 0 -> dynamic scaler with loss_scale_window,
                             initial_scale_power, hysteresis, min_loss_scale;
                             > 0 -> that static scale; fp16 params
@@ -24,8 +28,9 @@ The fields that decide one rank's optimizer step are read here; the others
 Readings where the pages are silent: an absent fp16 field takes the value of
 the tutorial's example block (window 1000, power 16, hysteresis 2, floor 1);
 an absent or "auto" optimizer parameter takes the library default (lr 1e-3,
-betas 0.9 / 0.999, eps 1e-8, weight decay 0.01); fp16 and bf16 both enabled,
-an optimizer other than AdamW, and batch sizes that do not multiply out are
+betas 0.9 / 0.999, eps 1e-8, weight decay 0.01; Muon: momentum 0.95, Nesterov,
+5 steps, scale "aspect"); fp16 and bf16 both enabled,
+an optimizer other than AdamW and Muon, and batch sizes that do not multiply out are
 refused (the chapter's §1.4 remarks that the fields constrain each other).
 The parsing needs no GPU and no built library; `hparams()` and
 `scaler_config()` build the C structs.
@@ -46,6 +51,18 @@ FP16_DEFAULTS = dict(loss_scale=0, loss_scale_window=1000, initial_scale_power=1
 ADAMW_DEFAULTS = dict(lr=1e-3, betas=(0.9, 0.999), eps=1e-8, weight_decay=0.01)
 
 
+MUON_DEFAULTS = dict(momentum=0.95, nesterov=True, ns_steps=5, scale="aspect")
+
+
+@dataclass(frozen=True)
+class MuonConfig:
+    lr: float
+    momentum: float
+    nesterov: bool
+    ns_steps: int
+    scale: str
+
+
 @dataclass(frozen=True)
 class StepConfig:
     lr: float
@@ -64,6 +81,14 @@ class StepConfig:
     param_dtype: Optional[str]  # "fp16", "bf16", or None (fp32 training: no 16-bit copy)
     stage: int
     offload: bool
+    muon: Optional[MuonConfig] = None  # optimizer.type Muon: the matrices' settings
+
+    def muon_hparams(self):
+        from . import zds
+        if self.muon is None:
+            raise ConfigError("the configuration's optimizer is not Muon")
+        m = self.muon
+        return zds.muon_hparams(m.lr, m.momentum, self.weight_decay, m.nesterov, m.scale)
 
     def hparams(self):
         from . import zds
@@ -120,6 +145,22 @@ def _accum_steps(cfg, world):
     return 1
 
 
+def _muon(p, lr):
+    momentum = _num(p, "momentum", MUON_DEFAULTS["momentum"])
+    if not 0.0 <= momentum < 1.0:
+        raise ConfigError("momentum must lie in [0, 1)")
+    nesterov = p.get("nesterov", MUON_DEFAULTS["nesterov"])
+    if not isinstance(nesterov, bool):
+        raise ConfigError("nesterov: expected true or false, got %r" % (nesterov,))
+    steps = _num(p, "ns_steps", MUON_DEFAULTS["ns_steps"], int)
+    if not 1 <= steps <= 16:
+        raise ConfigError("ns_steps must lie in [1, 16]")
+    scale = p.get("scale", MUON_DEFAULTS["scale"])
+    if scale not in ("none", "aspect", "rms"):
+        raise ConfigError("scale must be none, aspect or rms, got %r" % (scale,))
+    return MuonConfig(_num(p, "muon_lr", lr), momentum, nesterov, steps, scale)
+
+
 def from_ds_config(cfg, world=1):
     """StepConfig of a parsed JSON object (dict) for a job of `world` ranks."""
     if not isinstance(cfg, dict):
@@ -132,8 +173,8 @@ def from_ds_config(cfg, world=1):
     p = opt.get("params") or {}
     if typ.lower() == "adam" and p.get("adam_w_mode", True) is False and p.get("weight_decay", 0) not in (0, 0.0):
         raise ConfigError("Adam with L2-coupled weight decay is not this step's update (AdamW)")
-    if typ.lower() not in ("adamw", "adam"):
-        raise ConfigError("optimizer %r: the step implements AdamW" % typ)
+    if typ.lower() not in ("adamw", "adam", "muon"):
+        raise ConfigError("optimizer %r: the step implements AdamW and Muon" % typ)
     betas = p.get("betas", ADAMW_DEFAULTS["betas"])
     if _is_auto(betas):
         betas = ADAMW_DEFAULTS["betas"]
@@ -145,6 +186,10 @@ def from_ds_config(cfg, world=1):
     lr = _num(p, "lr", ADAMW_DEFAULTS["lr"])
     eps = _num(p, "eps", ADAMW_DEFAULTS["eps"])
     wd = _num(p, "weight_decay", ADAMW_DEFAULTS["weight_decay"])
+    muon = None
+    if typ.lower() == "muon":
+        muon = _muon(p, lr)
+        lr = _num(p, "adam_lr", lr)
     # precision and loss scaling
     fp16, f = _enabled(cfg, "fp16")
     bf16, _ = _enabled(cfg, "bf16")
@@ -178,10 +223,12 @@ def from_ds_config(cfg, world=1):
         raise ConfigError("zero_optimization.stage must be 0..3")
     off = z.get("offload_optimizer") or {}
     offload = str(off.get("device", "none")).lower() == "cpu"
+    if offload and muon is not None:
+        raise ConfigError("Muon's matrices are updated on the device: offload_optimizer is for AdamW")
     return StepConfig(lr=lr, beta1=b1, beta2=b2, eps=eps, weight_decay=wd, dynamic=dynamic,
                       initial_scale_power=power, window=window, hysteresis=hyst, min_scale=floor,
                       static_scale=static, max_norm=max_norm, accum_steps=k, param_dtype=pdt, stage=stage,
-                      offload=offload)
+                      offload=offload, muon=muon)
 
 
 def load_ds_config(path, world=1):

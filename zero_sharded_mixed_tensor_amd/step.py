@@ -1,7 +1,8 @@
 """Sequencing of one rank's optimizer step over the C ABI.
 
 engine.backward's gradient handling -> zds_grad_accumulate per micro-batch;
-engine.step -> zds_overflow_and_norm, zds_adam_step, zds_loss_scaler_update,
+engine.step -> zds_overflow_and_norm, zds_adam_step (MuonStep: Muon's three
+calls for the matrices and zds_adam_step for the rest), zds_loss_scaler_update,
 all on one stream with no host synchronisation (devpress.csdn.net DeepSpeed
 tutorial §3.3: the engine's backward and step replace the plain ones).
 """
@@ -88,6 +89,63 @@ class ShardStep:
 
     def read_scalars(self):
         return zds.read_scalars(self.scalars)
+
+
+class MuonStep:
+    """A rank that updates whole matrices with Muon and its other tensors with
+    AdamW. Its flat buffers hold the matrices in [0, split) and the rest in
+    [split, n): one overflow/norm/clip pass and one loss scale for all of
+    them. As every matrix is orthogonalised as a whole, the rank owns its
+    tensors whole (dealt out by tensors, not by elements).
+
+    matrices: [(flat offset, rows, cols)], all inside [0, split); elements of
+    that range outside them (padding) are not updated. A split at a multiple
+    of 64 keeps every slice aligned."""
+
+    def __init__(self, n, split, matrices, hp=None, muon=None, scaler=None, max_norm=1.0, accum_steps=1, ns_steps=5,
+                 t0=0, beta1_pow0=1.0, beta2_pow0=1.0, update_dtype=None, device="cuda", stream=None):
+        import torch
+        if not 0 <= split <= n:
+            raise zds.ZdsError(zds.ZDS_EINVAL, "split %d outside [0, %d]" % (split, n))
+        self.plan = zds.zds_matrix_plan_create(matrices)
+        if self.plan.span > split:
+            raise zds.ZdsError(zds.ZDS_EINVAL, "the matrices reach to %d, past the split at %d" % (self.plan.span, split))
+        self.n, self.split, self.ns_steps = n, split, ns_steps
+        self.muon = muon if muon is not None else zds.muon_hparams()
+        self.base = ShardStep(n, hp, scaler, max_norm, accum_steps, t0, beta1_pow0, beta2_pow0, device, stream)
+        dtype = torch.bfloat16 if update_dtype is None else update_dtype
+        self.update = torch.zeros(split, dtype=dtype, device=device)
+        self.ws = zds.new_newton_schulz_workspace(self.plan, dtype, device)
+
+    @classmethod
+    def from_config(cls, n, split, matrices, cfg, t0=0, beta1_pow0=1.0, beta2_pow0=1.0, device="cuda", stream=None):
+        """A step with the settings of a config.StepConfig whose optimizer is
+        Muon."""
+        return cls(n, split, matrices, cfg.hparams(), cfg.muon_hparams(), cfg.scaler_config(), cfg.max_norm,
+                   cfg.accum_steps, cfg.muon.ns_steps, t0, beta1_pow0, beta2_pow0, None, device, stream)
+
+    def apply(self, grads, master, momentum, exp_avg, exp_avg_sq, params_out, stream=None):
+        """The update under the step scalars that a norm pass has left.
+        grads, master, params_out (or None): n elements; momentum: split;
+        exp_avg, exp_avg_sq: n - split."""
+        b, k = self.base, self.split
+        zds.zds_muon_momentum(self.muon, grads, momentum, self.update, b.scalars, stream, n=k)
+        zds.zds_newton_schulz(self.plan, self.update, self.update, self.ws, self.ns_steps, None, b.scalars, stream)
+        zds.zds_muon_apply(self.muon, self.plan, self.update, master, params_out, b.scalars, stream)
+        zds.zds_adam_step(b.hp, grads[k:], master[k:], exp_avg, exp_avg_sq,
+                          None if params_out is None else params_out[k:], b.scalars, b.state, stream, n=self.n - k)
+
+    def step(self, grads, master, momentum, exp_avg, exp_avg_sq, params_out, stream=None):
+        """The whole step; kernels only, so it can be captured into a graph."""
+        self.base.norm(grads, stream)
+        self.apply(grads, master, momentum, exp_avg, exp_avg_sq, params_out, stream)
+        self.base.scaler(stream)
+
+    def read_state(self):
+        return self.base.read_state()
+
+    def read_scalars(self):
+        return self.base.read_scalars()
 
 
 class OffloadStep:
