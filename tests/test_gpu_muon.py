@@ -178,6 +178,32 @@ def test_orthogonalise(dtype, name, kind, gap, first):
     plan.close()
 
 
+@pytest.mark.parametrize("dtype,shapes", [
+    ("bf16", [(2000, 4090)]), ("fp32", [(2000, 2040)]),     # a few tiles of 256 with long sums
+    ("bf16", [(128, 4096), (250, 2000), (256, 256), (100, 120)]),   # tiles of 128, deep and shallow ones
+    ("fp32", [(128, 4096), (250, 2000), (256, 256), (100, 120)]),
+    ("bf16", [(128, 5000)] * 3), ("fp32", [(8000, 130)]),
+])
+def test_orthogonalise_sums_in_pieces(dtype, shapes):
+    """Sums long enough, and tiles few enough, to be cut into pieces: right, and
+    the same bits in every call."""
+    mats, total = layout(shapes, 3, 1)
+    x = fill(mats, total, 17, dtype)
+    plan = zds.zds_matrix_plan_create(mats)
+    ws = zds.new_newton_schulz_workspace(plan, TDT[dtype])
+    ws.fill_(0xFF)
+    dx = to_dev(x, dtype)
+    dy = torch.full((total,), 9.0, dtype=TDT[dtype], device="cuda")
+    zds.zds_newton_schulz(plan, dx, dy, ws)
+    y = to_host(dy)
+    check(mats, x, y, dtype)
+    for _ in range(2):
+        again = torch.full((total,), 9.0, dtype=TDT[dtype], device="cuda")
+        zds.zds_newton_schulz(plan, dx, again, ws)
+        assert np.array_equal(to_host(again), y)
+    plan.close()
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
 @pytest.mark.parametrize("steps,coef", [(1, None), (2, None), (8, None), (3, [(1.875, -1.25, 0.375)] * 3),
                                         (4, [(3.4, -4.7, 2.0), (3.0, -4.0, 1.8), (2.0, -1.5, 0.5), (1.5, -0.5, 0.0)])])

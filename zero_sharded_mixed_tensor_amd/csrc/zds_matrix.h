@@ -30,21 +30,26 @@ struct NsMatrix {
 
 // A block's piece of work: tile (ti, tj) of matrix `mat`, or chunk ti of it.
 // Of a product's sum it takes part `part` of `parts` (1: all of it); `slot`
-// numbers the tiles of a launch whose sum is cut.
+// numbers a launch's cut tiles.
 struct NsTile {
   int32_t mat, ti, tj;
   uint8_t part, parts;
   uint16_t slot;
 };
 
-// Matrices that go through one sequence of launches. Tables: tile lists of
-// the triangular products (ti >= tj; with cut tiles, if any, for the first of
-// them), the full product, the conversion
-// (64 x 64 tiles over the padded matrix) and the norm's chunks.
+// The launch of one product: blocks first..first + count of the plan's tile
+// array. `cut` more tiles, listed from `join` on, are summed in `parts` pieces
+// (cut * parts blocks from `pieces` on).
+struct NsList {
+  int32_t tile, first, count, join, cut, parts, pieces;
+};
+
+// Matrices that go through one sequence of launches: X X^T, A A and B X; the
+// conversion's 64 x 64 tiles over the padded matrices and the norm's chunks.
 struct NsGroup {
-  int32_t tri_tile, full_tile;  // tile sizes of the triangular products and of the full one
   int32_t mat0, nmat;           // matrices in the plan's device array
-  int32_t tri0, ntri, cut0, ncut, full0, nfull, conv0, nconv, chunk0, nchunk;  // in the plan's tile array
+  int32_t conv0, nconv, chunk0, nchunk;
+  NsList gram, poly, full;
 };
 
 // A chunk of a matrix for zds_muon_apply: up to kApplyChunk elements from flat
@@ -63,12 +68,13 @@ struct zds_matrix_plan {
   int device = 0;
   int32_t num = 0;
   int64_t span = 0;
-  std::vector<zds::NsGroup> groups;
+  std::vector<zds::NsGroup> groups[2];  // [FP32]
   // workspace of one group (the largest of all): partial sums and scales in
   // front, then the fp16 arrays
   size_t ws_bytes[2] = {0, 0};      // [FP32]
   int32_t max_parts = 0, max_mats = 0;
-  int32_t max_cut = 0;  // most pieces of cut tiles in a launch
+  int64_t piece_elems[2] = {0, 0};  // fp32 elements of cut tiles' pieces, the most of a launch
+  int64_t arrays[2] = {0, 0};       // fp16 elements
   zds::NsMatrix *d_mats[2] = {nullptr, nullptr};  // [FP32]: workspace offsets differ
   zds::NsTile *d_tiles = nullptr;
   zds::ApplyChunk *d_chunks = nullptr;

@@ -34,8 +34,6 @@ typedef __attribute__((address_space(1))) const void global_cvoid;
 
 constexpr int kMaxSteps = 16;
 constexpr double kNormEps = 1e-7;
-// Most tiles of a launch whose sum is cut (see cut_tail).
-constexpr int kMaxSlots = 128;
 // A partial sum of squares covers this many elements or more; a matrix has at
 // most kMaxParts of them.
 constexpr int64_t kNormChunk = 32768;
@@ -52,18 +50,23 @@ struct NsScale {
 // Norm and conversion
 // ---------------------------------------------------------------------------
 
-// Eight consecutive elements from an address aligned to 16 bytes.
+// 16-byte accesses at an element's address: a matrix may begin at any element
+// and have rows of any length.
+typedef f32x4 f32x4_any __attribute__((aligned(4)));
+typedef u32x4 u32x4_any __attribute__((aligned(2)));
+
+// Eight consecutive elements.
 template <int D>
 __device__ __forceinline__ void load_eight(const char *p, float (&v)[8]) {
   if constexpr (D == ZDS_FP32) {
-    const f32x4 a = reinterpret_cast<const f32x4 *>(p)[0], b = reinterpret_cast<const f32x4 *>(p)[1];
+    const f32x4 a = reinterpret_cast<const f32x4_any *>(p)[0], b = reinterpret_cast<const f32x4_any *>(p)[1];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       v[j] = a[j];
       v[4 + j] = b[j];
     }
   } else {
-    const u32x4 w = *reinterpret_cast<const u32x4 *>(p);
+    const u32x4 w = *reinterpret_cast<const u32x4_any *>(p);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       v[2 * j] = lo_of<D>(w[j]);
@@ -85,29 +88,25 @@ __global__ void __launch_bounds__(256) ns_norm_kernel(const NsMatrix *mats, cons
   constexpr int ES = D == ZDS_FP32 ? 4 : 2;
   const char *base = static_cast<const char *>(src) + (mt.offset + lo) * ES;
   double acc[2] = {0.0, 0.0};
-  int64_t e = 0;
-  if (aligned(base, 16)) {
-    const int64_t groups = (hi - lo) / 8;
-    auto add = [&](const float (&v)[8]) {
+  const int64_t groups = (hi - lo) / 8;
+  auto add = [&](const float (&v)[8]) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) acc[j & 1] = sq_add(v[j], acc[j & 1]);
-    };
-    int64_t g = threadIdx.x;
-    for (; g + 3 * 256 < groups; g += 4 * 256) {
-      float v[4][8];
+    for (int j = 0; j < 8; ++j) acc[j & 1] = sq_add(v[j], acc[j & 1]);
+  };
+  int64_t g = threadIdx.x;
+  for (; g + 3 * 256 < groups; g += 4 * 256) {
+    float v[4][8];
 #pragma unroll
-      for (int r = 0; r < 4; ++r) load_eight<D>(base + (g + r * 256) * 8 * ES, v[r]);
+    for (int r = 0; r < 4; ++r) load_eight<D>(base + (g + r * 256) * 8 * ES, v[r]);
 #pragma unroll
-      for (int r = 0; r < 4; ++r) add(v[r]);
-    }
-    for (; g < groups; g += 256) {
-      float v[8];
-      load_eight<D>(base + g * 8 * ES, v);
-      add(v);
-    }
-    e = groups * 8;
+    for (int r = 0; r < 4; ++r) add(v[r]);
   }
-  for (int64_t i = e + threadIdx.x; i < hi - lo; i += 256) acc[0] = sq_add(widen1<D>(base, i), acc[0]);
+  for (; g < groups; g += 256) {
+    float v[8];
+    load_eight<D>(base + g * 8 * ES, v);
+    add(v);
+  }
+  for (int64_t i = groups * 8 + threadIdx.x; i < hi - lo; i += 256) acc[0] = sq_add(widen1<D>(base, i), acc[0]);
   const double b = block_sum<256>(acc[0] + acc[1]);
   if (threadIdx.x == 0) partials[mt.part0 + t.ti] = b;
 }
@@ -120,7 +119,7 @@ __global__ void __launch_bounds__(256) ns_norm_kernel(const NsMatrix *mats, cons
 // matrix's first block stores alpha.
 template <int D, int SEG>
 __global__ void __launch_bounds__(256) ns_convert_kernel(const NsMatrix *mats, const NsTile *tiles, const void *src,
-                                                         const double *partials, NsScale *scales, int32_t *arrived,
+                                                         const double *partials, NsScale *scales,
                                                          half_t *ws, const zds_step_scalars *sc) {
   if (sc && sc->overflow) return;
   __shared__ float sh[kConvTile][kConvTile + 1];
@@ -133,17 +132,16 @@ __global__ void __launch_bounds__(256) ns_convert_kernel(const NsMatrix *mats, c
   // row for each thread, their loads under way while the norm is added up
   const int r0 = t.ti * kConvTile, c0 = t.tj * kConvTile;
   const int tr = threadIdx.x >> 3, tc = (threadIdx.x & 7) * 8;
-  const bool vec = aligned(base, 16) && (mt.cols & 7) == 0;
   float v[2][8];
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     const int r = r0 + tr + 32 * h, c = c0 + tc;
     const int64_t e = static_cast<int64_t>(r) * mt.cols + c;
-    if (vec && r < mt.rows && c < mt.cols) {
+    if (r < mt.rows && c + 8 <= mt.cols) {
       load_eight<D>(base + e * ES, v[h]);
     } else {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[h][j] = !vec && r < mt.rows && c + j < mt.cols ? widen1<D>(base, e + j) : 0.0f;
+      for (int j = 0; j < 8; ++j) v[h][j] = r < mt.rows && c + j < mt.cols ? widen1<D>(base, e + j) : 0.0f;
     }
   }
   double acc = 0.0;
@@ -157,11 +155,8 @@ __global__ void __launch_bounds__(256) ns_convert_kernel(const NsMatrix *mats, c
   int p2 = norm > 0.0 && norm <= DBL_MAX ? 14 - ex : 0;
   p2 = p2 > 126 ? 126 : (p2 < -126 ? -126 : p2);
   const float up = ldexpf(1.0f, p2);
-  if (threadIdx.x == 0) {
-    if (t.ti == 0 && t.tj == 0) scales[t.mat].alpha = static_cast<float>(ldexp(1.0 / (norm + kNormEps), -p2));
-    if (blockIdx.x == 0)
-      for (int i = 0; i < kMaxSlots; ++i) arrived[i] = 0;
-  }
+  if (t.ti == 0 && t.tj == 0 && threadIdx.x == 0)
+    scales[t.mat].alpha = static_cast<float>(ldexp(1.0 / (norm + kNormEps), -p2));
   const int64_t plane = static_cast<int64_t>(mt.mp) * mt.np;
   half_t *x = ws + mt.x[0];
   auto put = [&](int64_t e, const float (&f)[8]) {
@@ -198,8 +193,8 @@ __global__ void __launch_bounds__(256) ns_convert_kernel(const NsMatrix *mats, c
 // The products
 // ---------------------------------------------------------------------------
 
-// kGramCut: X X^T in a launch with cut tiles.
-enum NsKind { kGram = 0, kPoly = 1, kUpdate = 2, kLast = 3, kGramCut = 4 };
+// kGramPiece, kPolyPiece: pieces of cut tiles.
+enum NsKind { kGram = 0, kPoly = 1, kUpdate = 2, kLast = 3, kGramPiece = 4, kPolyPiece = 5 };
 
 struct NsArgs {
   const NsMatrix *mats;
@@ -209,7 +204,6 @@ struct NsArgs {
   void *dst;
   const zds_step_scalars *sc;
   float *pieces;       // of cut tiles: accumulators as the threads hold them
-  int32_t *arrived;    // and how many of a tile's pieces are there
   float a, b, c;       // the step's coefficients
   float sa, sb, sx;    // powers of two: A, B and X (but the first) as stored
   float carry;         // factor of X's remainder in a X
@@ -284,7 +278,7 @@ __device__ __forceinline__ void wait_loads(int n) {
   asm volatile("" ::: "memory");
   // vmcnt in bits 3:0 and 15:14, the other counters at their maxima
   switch (n < 63 ? n : 63) {
-#define ZDS_WAIT(k) case k: __builtin_amdgcn_s_waitcnt(0x0f70 | (k & 15) | (k >> 4) << 14); break;
+#define ZDS_WAIT(k) case k: __builtin_amdgcn_s_waitcnt(0x0f70 | ((k) & 15) | ((k) >> 4) << 14); break;
 #define ZDS_WAIT4(k) ZDS_WAIT(k) ZDS_WAIT(k + 1) ZDS_WAIT(k + 2) ZDS_WAIT(k + 3)
 #define ZDS_WAIT16(k) ZDS_WAIT4(k) ZDS_WAIT4(k + 4) ZDS_WAIT4(k + 8) ZDS_WAIT4(k + 12)
     ZDS_WAIT16(0) ZDS_WAIT16(16) ZDS_WAIT16(32) ZDS_WAIT16(48)
@@ -302,8 +296,8 @@ __device__ __forceinline__ void block_barrier() {
 template <int T, int SEG, int WHAT>
 __global__ void __launch_bounds__(256, T == 256 ? 1 : 2) ns_product_kernel(const NsArgs q) {
   typedef NsShape<T> S;
-  constexpr bool CUT = WHAT == kGramCut;
-  constexpr int KIND = CUT ? kGram : WHAT;
+  constexpr bool CUT = WHAT == kGramPiece || WHAT == kPolyPiece;
+  constexpr int KIND = WHAT == kGramPiece ? kGram : WHAT == kPolyPiece ? kPoly : WHAT;
   constexpr bool TURN = KIND == kUpdate || KIND == kLast;  // P is X, read down its rows
   __shared__ __align__(1024) char smem[2][2][S::STAGE];
   if (q.sc && q.sc->overflow) return;
@@ -497,7 +491,7 @@ __global__ void __launch_bounds__(256, T == 256 ? 1 : 2) ns_product_kernel(const
     quarter(k, std::integral_constant<int, 3>{});
   };
   if constexpr (CUT) {
-    int k = from;  // every piece has a step: only long sums are cut
+    int k = from;  // every piece has a step
     do depth_step(k);
     while (++k < total);
   } else {
@@ -506,44 +500,20 @@ __global__ void __launch_bounds__(256, T == 256 ? 1 : 2) ns_product_kernel(const
   asm volatile("s_nop 15\n\ts_nop 15\n\ts_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
   block_barrier();
 
-  // A cut tile: every piece leaves its sums in memory, and the block that
-  // arrives last adds them in the pieces' order, so that the result does not
-  // depend on which one that is. It also clears the count for the next launch.
-  if (CUT && t.parts > 1) {
-    f32x4 *const pieces = reinterpret_cast<f32x4 *>(q.pieces) + static_cast<int64_t>(t.slot) * t.parts * (T * T / 4);
-    f32x4 *mine = pieces + t.part * (T * T / 4) + threadIdx.x;
+  // A piece of a cut tile leaves its sums in memory, for ns_join_kernel.
+  if constexpr (CUT) {
+    f32x4 *mine = reinterpret_cast<f32x4 *>(q.pieces) + (static_cast<int64_t>(t.slot) * t.parts + t.part) * (T * T / 4) + threadIdx.x;
 #pragma unroll
     for (int i = 0; i < S::MI; ++i)
 #pragma unroll
       for (int j = 0; j < S::MI; ++j) mine[(i * S::MI + j) * 256] = acc[i][j];
-    __threadfence();
-    __syncthreads();
-    int32_t *const last = reinterpret_cast<int32_t *>(smem);
-    if (threadIdx.x == 0)
-      *last = __hip_atomic_fetch_add(q.arrived + t.slot, 1, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT) == t.parts - 1;
-    __syncthreads();
-    if (!*last) return;
-    __syncthreads();  // smem is written again below
-    if (threadIdx.x == 0) q.arrived[t.slot] = 0;
-    __threadfence();
-#pragma unroll
-    for (int i = 0; i < S::MI; ++i)
-#pragma unroll
-      for (int j = 0; j < S::MI; ++j) acc[i][j] = pieces[(i * S::MI + j) * 256 + threadIdx.x];
-    for (int p = 1; p < t.parts; ++p) {
-      const f32x4 *o = pieces + p * (T * T / 4) + threadIdx.x;
-#pragma unroll
-      for (int i = 0; i < S::MI; ++i)
-#pragma unroll
-        for (int j = 0; j < S::MI; ++j) acc[i][j] += o[(i * S::MI + j) * 256];
-    }
-  }
+  } else {
 
   // Epilogue, in strips of MT rows of what is stored, each wave on its own in
-  // its part of the LDS (two strips' room). A lane holds row fr of a strip, of
-  // each instruction tile i four elements from column 16 i + 4 fc on. The strip's inputs come in rows (high and low plane)
-  // and are overwritten by its outputs, which leave in rows, and for a
-  // symmetric result also turned.
+  // its part of the LDS (room for AHEAD strips). A lane holds row fr of a strip,
+  // of each instruction tile i four elements from column 16 i + 4 fc on. The
+  // strip's inputs come in rows (high and low plane) and are overwritten by its
+  // outputs, which leave in rows, and for a symmetric result also turned.
   char *const room = smem[0][0] + w * S::AHEAD * 2 * S::STRIP;
   const uint32_t room_lds = lds_address(room);
   static_assert(4 * S::AHEAD * 2 * S::STRIP <= 4 * S::STAGE, "each wave's strips fit");
@@ -691,37 +661,86 @@ __global__ void __launch_bounds__(256, T == 256 ? 1 : 2) ns_product_kernel(const
       put_rows(at, xout, s);
       put_rows(at + S::STRIP, SEG == 3 ? xout + xplane : q.ws + mt.lo, s);
     } else if constexpr (SEG == 1) {
-      // the result, in its own orientation and inside its bounds: 16-byte
-      // pieces where the rows lie on them, else element by element
+      // the result, in its own orientation and inside its bounds
       uint16_t *dst = static_cast<uint16_t *>(q.dst) + mt.offset;
-      const bool vec = aligned(dst, 16) && (mt.cols & 7) == 0;
       const int64_t i0 = qrow + s * S::MT, j0 = prow;
-      if (vec && !mt.tall) {
+      auto put = [&](int64_t row, int64_t col, u32x4 v) {
+        if (row >= mt.rows || col >= mt.cols) return;
+        uint16_t *o = dst + row * mt.cols + col;
+        if (col + 8 <= mt.cols) {
+          *reinterpret_cast<u32x4_any *>(o) = v;
+        } else {
+#pragma unroll
+          for (int j = 0; j < 7; ++j)
+            if (col + j < mt.cols) o[j] = static_cast<uint16_t>(v[j / 2] >> (j & 1) * 16);
+        }
+      };
+      if (!mt.tall) {
 #pragma unroll
         for (int g = 0; g < S::MOVES; ++g) {
           const int r = g * RPI + mrow;
-          const u32x4 v = *reinterpret_cast<const u32x4 *>(at + r * S::ROW + ns_swizzle_strip<T>(r, mchunk) * 16);
-          if (i0 + r < mt.m && j0 + mchunk * 8 < mt.n)
-            *reinterpret_cast<u32x4 *>(dst + (i0 + r) * mt.cols + j0 + mchunk * 8) = v;
-        }
-      } else if (vec) {
-#pragma unroll
-        for (int c = 0; c < S::TW; c += PC) {
-          const u32x4 v = __builtin_bit_cast(u32x4, turned8(at, tgrp, c + tcol));
-          if (j0 + c + tcol < mt.n && i0 + tgrp < mt.m)
-            *reinterpret_cast<u32x4 *>(dst + (j0 + c + tcol) * mt.cols + i0 + tgrp) = v;
+          put(i0 + r, j0 + mchunk * 8,
+              *reinterpret_cast<const u32x4 *>(at + r * S::ROW + ns_swizzle_strip<T>(r, mchunk) * 16));
         }
       } else {
-        for (int e = sl; e < S::MT * S::TW; e += 64) {
-          const int r = mt.tall ? e % S::MT : e / S::TW, c = mt.tall ? e / S::MT : e % S::TW;
-          const uint16_t v = *reinterpret_cast<const uint16_t *>(at + r * S::ROW + ns_swizzle_strip<T>(r, c >> 3) * 16 + (c & 7) * 2);
-          if (i0 + r < mt.m && j0 + c < mt.n)
-            dst[mt.tall ? (j0 + c) * mt.cols + i0 + r : (i0 + r) * mt.cols + j0 + c] = v;
-        }
+#pragma unroll
+        for (int c = 0; c < S::TW; c += PC)
+          put(j0 + c + tcol, i0 + tgrp, __builtin_bit_cast(u32x4, turned8(at, tgrp, c + tcol)));
       }
     }
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
     if (s + S::AHEAD < S::MI) fetch(s + S::AHEAD);
+  }
+  }
+}
+
+// The sums of cut tiles: block (k, j) adds, in the pieces' order, column j of
+// the instruction tiles of each wave's part of tile k, and stores it and its
+// mirror image. POLY: b A + c A^2, else A.
+template <int T, int SEG, bool POLY>
+__global__ void __launch_bounds__(256) ns_join_kernel(const NsArgs q, int parts) {
+  typedef NsShape<T> S;
+  if (q.sc && q.sc->overflow) return;
+  const NsTile t = q.tiles[blockIdx.x];
+  const NsMatrix mt = q.mats[t.mat];
+  const int j = blockIdx.y, lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+  const int64_t mp = mt.mp, aplane = mp * mp;
+  const f32x4 *o = reinterpret_cast<const f32x4 *>(q.pieces) + static_cast<int64_t>(t.slot) * parts * (T * T / 4) + threadIdx.x;
+  f32x4 v[S::MI];
+#pragma unroll
+  for (int i = 0; i < S::MI; ++i) v[i] = o[(i * S::MI + j) * 256];
+  for (int p = 1; p < parts; ++p) {
+    o += T * T / 4;
+#pragma unroll
+    for (int i = 0; i < S::MI; ++i) v[i] += o[(i * S::MI + j) * 256];
+  }
+  const float alpha = q.first ? q.scales[t.mat].alpha : 1.0f / q.sx;
+  const float f1 = POLY ? q.c * (q.sb / (q.sa * q.sa)) : alpha * alpha * q.sa;
+  half_t *const out = q.ws + (POLY ? mt.b : mt.a);
+  const int64_t row = static_cast<int64_t>(t.tj) * T + (w & 1) * S::TW + j * S::MT + (lane & 15);
+#pragma unroll
+  for (int i = 0; i < S::MI; ++i) {
+    const int64_t col = static_cast<int64_t>(t.ti) * T + (w >> 1) * S::TW + i * S::MT + (lane >> 4) * 4;
+    const half_t *a = q.ws + mt.a + row * mp + col;
+    f16x4 ah = {}, al = {}, h, l;
+    if (POLY) ah = *reinterpret_cast<const f16x4 *>(a);
+    if (POLY && SEG == 3) al = *reinterpret_cast<const f16x4 *>(a + aplane);
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      float x = f1 * v[i][r];
+      if (POLY) x += q.b * (q.sb / q.sa) * (static_cast<float>(ah[r]) + static_cast<float>(al[r]));
+      h[r] = static_cast<half_t>(x);
+      l[r] = static_cast<half_t>(x - static_cast<float>(h[r]));
+    }
+    *reinterpret_cast<f16x4 *>(out + row * mp + col) = h;
+    if (SEG == 3) *reinterpret_cast<f16x4 *>(out + aplane + row * mp + col) = l;
+    if (t.ti != t.tj) {
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        out[(col + r) * mp + row] = h[r];
+        if (SEG == 3) out[aplane + (col + r) * mp + row] = l[r];
+      }
+    }
   }
 }
 
@@ -750,32 +769,35 @@ static float pow2_under(double limit, double value) {  // largest power of two w
 }
 
 template <int T, int SEG>
-static void launch_products(const NsGroup &g, const NsTile *tiles, NsArgs q, int kind, hipStream_t s) {
-  const dim3 block(NsShape<T>::WAVES * 64);
-  if (kind == kGram || kind == kPoly) {
-    q.tiles = tiles + g.tri0;
-    if constexpr (T == 256) {
-      if (kind == kGram && g.ncut) {
-        q.tiles = tiles + g.cut0;
-        hipLaunchKernelGGL((ns_product_kernel<T, SEG, kGramCut>), dim3(g.ncut), block, 0, s, q);
-        return;
-      }
+static void launch_products(const NsList &l, const NsTile *tiles, NsArgs q, int kind, hipStream_t s) {
+  const dim3 block(NsShape<T>::WAVES * 64), grid(static_cast<uint32_t>(l.count));
+  if constexpr (T >= 128) {
+    if (l.cut) {
+      const dim3 pgrid(static_cast<uint32_t>(l.cut * l.parts)), jgrid(static_cast<uint32_t>(l.cut), NsShape<T>::MI);
+      q.tiles = tiles + l.pieces;
+      if (kind == kGram) hipLaunchKernelGGL((ns_product_kernel<T, SEG, kGramPiece>), pgrid, block, 0, s, q);
+      else hipLaunchKernelGGL((ns_product_kernel<T, SEG, kPolyPiece>), pgrid, block, 0, s, q);
+      q.tiles = tiles + l.join;
+      if (kind == kGram) hipLaunchKernelGGL((ns_join_kernel<T, SEG, false>), jgrid, dim3(256), 0, s, q, l.parts);
+      else hipLaunchKernelGGL((ns_join_kernel<T, SEG, true>), jgrid, dim3(256), 0, s, q, l.parts);
+      if (!l.count) return;
     }
-    if (kind == kGram) hipLaunchKernelGGL((ns_product_kernel<T, SEG, kGram>), dim3(g.ntri), block, 0, s, q);
-    else hipLaunchKernelGGL((ns_product_kernel<T, SEG, kPoly>), dim3(g.ntri), block, 0, s, q);
-  } else {
-    q.tiles = tiles + g.full0;
-    if (kind == kUpdate) hipLaunchKernelGGL((ns_product_kernel<T, SEG, kUpdate>), dim3(g.nfull), block, 0, s, q);
-    else hipLaunchKernelGGL((ns_product_kernel<T, SEG, kLast>), dim3(g.nfull), block, 0, s, q);
+  }
+  q.tiles = tiles + l.first;
+  switch (kind) {
+    case kGram: hipLaunchKernelGGL((ns_product_kernel<T, SEG, kGram>), grid, block, 0, s, q); break;
+    case kPoly: hipLaunchKernelGGL((ns_product_kernel<T, SEG, kPoly>), grid, block, 0, s, q); break;
+    case kUpdate: hipLaunchKernelGGL((ns_product_kernel<T, SEG, kUpdate>), grid, block, 0, s, q); break;
+    default: hipLaunchKernelGGL((ns_product_kernel<T, SEG, kLast>), grid, block, 0, s, q); break;
   }
 }
 
 template <int SEG>
 static void launch_products(const NsGroup &g, const NsTile *tiles, const NsArgs &q, int kind, hipStream_t s) {
-  const int tile = kind == kGram || kind == kPoly ? g.tri_tile : g.full_tile;
-  if (tile == 256) launch_products<256, SEG>(g, tiles, q, kind, s);
-  else if (tile == 128) launch_products<128, SEG>(g, tiles, q, kind, s);
-  else launch_products<64, SEG>(g, tiles, q, kind, s);
+  const NsList &l = kind == kGram ? g.gram : kind == kPoly ? g.poly : g.full;
+  if (l.tile == 256) launch_products<256, SEG>(l, tiles, q, kind, s);
+  else if (l.tile == 128) launch_products<128, SEG>(l, tiles, q, kind, s);
+  else launch_products<64, SEG>(l, tiles, q, kind, s);
 }
 
 // Rounds `n` tiles (already in an order whose neighbours share operands) so
@@ -792,33 +814,6 @@ static void spread_over_dies(std::vector<NsTile> &v, size_t from) {
         if (lo + k < hi) v.push_back(in[r + lo + k]);
       }
   }
-}
-
-// The last launch round of X X^T's tiles from v[from] on, where it would leave
-// more than half of the compute units idle (one block a unit at this tile
-// size) and its sums are long: they are cut into pieces, up to kMaxPieces of
-// them, that fill the round. At 8192 x 22016 528 tiles are two rounds and 16
-// tiles: 1.30 ms cut, 1.49 ms whole. Leaving and adding the pieces takes about
-// 60 us, which sums of 4096 or 8192 do not pay for: the same cut in A^2 (8192
-// deep) costs 0.62 ms, whole it is 0.57. The matrices come in falling depth, so
-// the last tiles' sums are the shortest.
-constexpr int kMaxPieces = 8, kCutDepth = 16384;
-static bool cut_tail(std::vector<NsTile> &v, size_t from, const NsMatrix *mats, zds_matrix_plan *p) {
-  const int tail = static_cast<int>((v.size() - from) % kUnits);
-  const int parts = tail ? std::min(kMaxPieces, kUnits / tail) : 1;
-  if (parts < 2 || mats[v.back().mat].np < kCutDepth) return false;
-  const std::vector<NsTile> last(v.end() - tail, v.end());
-  v.resize(v.size() - static_cast<size_t>(tail));
-  for (int part = 0; part < parts; ++part)
-    for (int k = 0; k < tail; ++k) {
-      NsTile t = last[static_cast<size_t>(k)];
-      t.part = static_cast<uint8_t>(part);
-      t.parts = static_cast<uint8_t>(parts);
-      t.slot = static_cast<uint16_t>(k);
-      v.push_back(t);
-    }
-  p->max_cut = std::max(p->max_cut, tail * parts);
-  return true;
 }
 
 // Tiles in patches of 8 x 4, so that a run of 32 reads 8 + 4 operand tiles.
@@ -842,52 +837,99 @@ static int padding_of(int64_t m, int64_t n) {
   return 64;
 }
 
-// What a launch of `tiles` T x T tiles of `steps` depth steps on average takes,
-// in us, fitted to measured launches (1 to 2048 tiles of 16 to 172 steps): a
-// block's fixed part, and a step's time by how many blocks share a unit. At
-// 1024 x 1024 x 64 steps (10, 36, 136 tiles) 71, 35 and 27 us; at
-// 4096 x 4096 x 64 steps (256, 1024, 4096 tiles) 119, 131 and 244 us.
-static double launch_cost(int t, int64_t tiles, double steps) {
-  static const struct { int tile, blocks; double fixed[4], step[4]; } kinds[3] = {
-      {256, 1, {12.0}, {1.25}},
-      {128, 2, {5.0, 8.0}, {0.5, 0.95}},
-      {64, 4, {4.0, 5.0, 6.0, 7.5}, {0.37, 0.5, 0.67, 0.85}},
-  };
-  for (const auto &k : kinds) {
-    if (k.tile != t) continue;
-    const int64_t slots = static_cast<int64_t>(kUnits) * k.blocks;
-    const auto round = [&](int64_t n) {  // n tiles at once
-      const int64_t share = (n + kUnits - 1) / kUnits - 1;
-      return k.fixed[share] + steps * k.step[share];
-    };
-    return static_cast<double>(tiles / slots) * round(slots) + (tiles % slots ? round(tiles % slots) : 0.0);
-  }
-  return 0.0;
+// What launches of T x T tiles take, in us, fitted to measured ones (1 to 2048
+// tiles of 16 to 172 depth steps): a block's fixed part (a full product's
+// epilogue also reads and writes X's low halves), and a step's time by how
+// many blocks share a unit. X X^T at 1024 x 4096 (64 steps; 10, 36, 136 tiles)
+// takes 71, 35 and 27 us, B X at 4096 x 4096 (64 steps; 256, 1024, 4096 tiles)
+// 119, 131 and 244 us.
+struct LaunchCost {
+  int tile, blocks;  // blocks of a unit at once
+  double fixed[4], full[4], step[4];
+};
+static const LaunchCost kCosts[3] = {
+    {256, 1, {12.0}, {22.0}, {1.25}},
+    {128, 2, {5.0, 8.0}, {7.0, 11.0}, {0.5, 0.95}},
+    {64, 4, {4.0, 5.0, 6.0, 7.5}, {5.5, 6.5, 8.0, 9.5}, {0.37, 0.5, 0.67, 0.85}},
+};
+static double round_cost(const LaunchCost &k, bool full, int64_t tiles, double steps) {
+  const int64_t share = (tiles + kUnits - 1) / kUnits - 1;
+  return (full ? k.full : k.fixed)[share] + steps * k.step[share];
 }
+// Storing the pieces of cut tiles and joining them.
+constexpr double kJoinCost = 14.0;
+constexpr int kMaxPieces = 8;
 
-// The tile size, at most `most`, of a launch over a group's matrices; *cost: of
-// its launches in a step.
-static int tile_for(const NsMatrix *mats, int n, int most, bool triangle, double *cost) {
-  int best = most;
+// The tiles of a product over a group's matrices (which come in falling depth).
+// Where the last round of blocks would leave units idle, its tiles' sums may be
+// cut into pieces that fill it (of A and B; at 8192 x 22016, X X^T has 528
+// tiles of 256: two rounds and 16 tiles). Returns the cost, and with `tiles`
+// adds the list to it.
+static double make_list(int kind, const std::vector<NsMatrix> &mats, int padding, int seg, NsList *l, std::vector<NsTile> *tiles) {
+  const bool full = kind == kUpdate;
   double least = -1.0;
-  for (int t = most; t >= 64; t /= 2) {
-    int64_t tiles = 0;
-    double steps = 0.0;
-    for (int i = 0; i < n; ++i) {
-      const int64_t a = mats[i].mp / t, b = mats[i].np / t;
-      const int64_t k = triangle ? a * (a + 1) / 2 : a * b;
-      tiles += k;
-      // the triangle is launched for X X^T, np deep, and for A A, mp deep
-      steps += static_cast<double>(k) * (triangle ? 0.5 * (mats[i].np + mats[i].mp) : mats[i].mp) / kNsDepth;
+  for (const LaunchCost &k : kCosts) {
+    if (k.tile > padding) continue;
+    std::vector<std::pair<int64_t, double>> runs;  // tiles, steps
+    int64_t n = 0;
+    for (const NsMatrix &m : mats) {
+      const int64_t a = m.mp / k.tile, b = m.np / k.tile;
+      const double steps = static_cast<double>(seg) * (kind == kGram ? m.np : m.mp) / kNsDepth;
+      runs.emplace_back(full ? a * b : a * (a + 1) / 2, steps);
+      n += runs.back().first;
     }
-    const double c = launch_cost(t, tiles, steps / static_cast<double>(tiles)) * (triangle ? 2 : 1);
-    if (least < 0.0 || c < least) {
-      least = c;
-      best = t;
+    // average depth of the last `tail` tiles, and of the ones in front
+    const int64_t slots = static_cast<int64_t>(kUnits) * k.blocks, tail = n % slots, front = n - tail;
+    double all = 0.0, behind = 0.0, least_steps = HUGE_VAL;
+    int64_t left = tail;
+    for (size_t i = runs.size(); i-- > 0;) {
+      const int64_t c = std::min(left, runs[i].first);
+      behind += static_cast<double>(c) * runs[i].second;
+      if (c) least_steps = std::min(least_steps, runs[i].second);
+      left -= c;
+      all += static_cast<double>(runs[i].first) * runs[i].second;
+    }
+    const double whole = front ? static_cast<double>(front / slots) * round_cost(k, full, slots, (all - behind) / static_cast<double>(front)) : 0.0;
+    const double deep = tail ? behind / static_cast<double>(tail) : 0.0;
+    const int most = full || k.tile < 128 ? 1 : kMaxPieces;
+    for (int parts = 1; parts <= most; ++parts) {
+      // every piece has a step of its own
+      if (parts > 1 && (tail == 0 || tail * parts > slots || least_steps < parts)) break;
+      const double c = whole + (tail ? round_cost(k, full, tail * parts, deep / parts) : 0.0) + (parts > 1 ? kJoinCost : 0.0);
+      if (least < 0.0 || c < least) {
+        least = c;
+        *l = NsList{};
+        l->tile = k.tile;
+        l->parts = parts;
+        l->cut = parts > 1 ? static_cast<int32_t>(tail) : 0;
+      }
     }
   }
-  *cost = least;
-  return best;
+  if (!tiles) return least;
+  std::vector<NsTile> v;
+  for (size_t i = 0; i < mats.size(); ++i)
+    add_tiles(v, static_cast<int>(i), (full ? mats[i].np : mats[i].mp) / l->tile, mats[i].mp / l->tile, !full);
+  l->join = static_cast<int32_t>(tiles->size());
+  for (int32_t k = 0; k < l->cut; ++k) {
+    NsTile t = v[v.size() - static_cast<size_t>(l->cut - k)];
+    t.slot = static_cast<uint16_t>(k);
+    tiles->push_back(t);
+  }
+  l->pieces = static_cast<int32_t>(tiles->size());
+  for (int part = 0; part < l->parts && l->cut; ++part)
+    for (int32_t k = 0; k < l->cut; ++k) {
+      NsTile t = (*tiles)[static_cast<size_t>(l->join + k)];
+      t.part = static_cast<uint8_t>(part);
+      t.parts = static_cast<uint8_t>(l->parts);
+      tiles->push_back(t);
+    }
+  spread_over_dies(*tiles, static_cast<size_t>(l->pieces));
+  v.resize(v.size() - static_cast<size_t>(l->cut));
+  l->first = static_cast<int32_t>(tiles->size());
+  tiles->insert(tiles->end(), v.begin(), v.end());
+  spread_over_dies(*tiles, static_cast<size_t>(l->first));
+  l->count = static_cast<int32_t>(tiles->size()) - l->first;
+  return least;
 }
 
 // A group's matrices share a padding; it is closed when its elements reach
@@ -895,16 +937,15 @@ static int tile_for(const NsMatrix *mats, int n, int most, bool triangle, double
 // chip many times over.
 constexpr int64_t kGroupElements = int64_t(1) << 28;
 
-// The workspace: partial sums of squares, scales, counts, the pieces of cut
-// tiles, and the fp16 arrays; the front is the same for every group.
+// The workspace: partial sums of squares, scales, the pieces of cut tiles,
+// and the fp16 arrays; the front is the same for every group.
 struct NsWorkspace {
   double *partials;
   NsScale *scales;
-  int32_t *arrived;
   float *pieces;
   half_t *arrays;
   size_t front;
-  NsWorkspace(const zds_matrix_plan &p, void *ws) {
+  NsWorkspace(const zds_matrix_plan &p, bool f, void *ws) {
     size_t at = 0;
     auto take = [&](size_t bytes) {
       char *here = static_cast<char *>(ws) + at;
@@ -913,8 +954,7 @@ struct NsWorkspace {
     };
     partials = static_cast<double *>(take(sizeof(double) * static_cast<size_t>(p.max_parts)));
     scales = static_cast<NsScale *>(take(sizeof(NsScale) * static_cast<size_t>(p.max_mats)));
-    arrived = static_cast<int32_t *>(take(sizeof(int32_t) * kMaxSlots));
-    pieces = static_cast<float *>(take(sizeof(float) * 256 * 256 * static_cast<size_t>(p.max_cut)));
+    pieces = static_cast<float *>(take(sizeof(float) * static_cast<size_t>(p.piece_elems[f])));
     arrays = static_cast<half_t *>(take(0));
     front = at;
   }
@@ -924,124 +964,110 @@ struct NsWorkspace {
 zds_status build_newton_schulz(zds_matrix_plan *p, const int64_t *offset, const int32_t *rows, const int32_t *cols,
                                int32_t num) {
   // the longest sums first
-  std::vector<int32_t> order(static_cast<size_t>(num));
-  for (int32_t i = 0; i < num; ++i) order[static_cast<size_t>(i)] = i;
+  std::vector<int32_t> order;
+  for (int32_t i = 0; i < num; ++i)
+    if (rows[i] > 0 && cols[i] > 0) order.push_back(i);
   std::stable_sort(order.begin(), order.end(), [&](int32_t a, int32_t b) {
-    const auto key = [&](int32_t i) {
-      return std::make_pair(std::max(rows[i], cols[i]), std::min(rows[i], cols[i]));
-    };
+    const auto key = [&](int32_t i) { return std::make_pair(std::max(rows[i], cols[i]), std::min(rows[i], cols[i])); };
     return key(a) > key(b);
   });
-  // Groups, each of one padding: every matrix with the padding that suits it,
-  // or, where that makes several short sequences of launches, all with one.
-  struct Draft {
-    int padding;
-    std::vector<NsMatrix> mats;
-  };
-  std::vector<Draft> drafts;
-  double least = -1.0;
-  for (int only : {0, 256, 128, 64}) {
-    std::vector<Draft> d;
-    double cost = 0.0;
-    for (int padding : {256, 128, 64}) {
-      int64_t elems = kGroupElements;
-      const size_t before = d.size();
-      for (int32_t i : order) {
-        if (rows[i] == 0 || cols[i] == 0) continue;
-        NsMatrix m{};
-        m.offset = offset[i];
-        m.rows = rows[i];
-        m.cols = cols[i];
-        m.tall = rows[i] > cols[i];
-        m.m = m.tall ? cols[i] : rows[i];
-        m.n = m.tall ? rows[i] : cols[i];
-        if ((only ? only : padding_of(m.m, m.n)) != padding) continue;
-        m.mp = static_cast<int32_t>(round_up(m.m, padding));
-        m.np = static_cast<int32_t>(round_up(m.n, padding));
-        if (elems >= kGroupElements) {
-          d.push_back(Draft{padding, {}});
-          elems = 0;
-        }
-        elems += static_cast<int64_t>(m.mp) * m.np;
-        d.back().mats.push_back(m);
-      }
-      for (size_t k = before; k < d.size(); ++k)
-        for (bool triangle : {true, false}) {
-          double c = 0.0;
-          (void)tile_for(d[k].mats.data(), static_cast<int>(d[k].mats.size()), padding, triangle, &c);
-          cost += c;
-        }
-    }
-    if (least < 0.0 || cost < least) {
-      least = cost;
-      drafts = std::move(d);
-    }
-  }
-  std::vector<NsMatrix> mats[2];
   std::vector<NsTile> tiles;
-  int64_t most[2] = {0, 0};
-  for (const Draft &draft : drafts) {
-    NsGroup g{};
-    g.mat0 = static_cast<int32_t>(mats[0].size());
-    int64_t pos[2] = {0, 0};
-    int32_t parts = 0;
-    for (NsMatrix m : draft.mats) {
-      m.part0 = parts;
-      const int64_t len = static_cast<int64_t>(m.rows) * m.cols;
-      m.chunk = static_cast<int32_t>(std::max(kNormChunk, round_up((len + kMaxParts - 1) / kMaxParts, 2048)));
-      m.nparts = static_cast<int32_t>((len + m.chunk - 1) / m.chunk);
-      parts += m.nparts;
-      const int64_t xe = static_cast<int64_t>(m.mp) * m.np, ae = static_cast<int64_t>(m.mp) * m.mp;
-      for (int f = 0; f < 2; ++f) {
-        const int64_t planes = f ? 2 : 1;
-        NsMatrix d = m;
-        auto take = [&](int64_t e) { const int64_t at = pos[f]; pos[f] += e; return at; };
-        d.x[0] = take(xe * planes);
-        d.x[1] = take(xe * planes);
-        d.lo = f ? 0 : take(xe);
-        d.a = take(ae * planes);
-        d.b = take(ae * planes);
-        mats[f].push_back(d);
+  std::vector<NsMatrix> mats[2];
+  for (int f = 0; f < 2; ++f) {
+    const int seg = f ? 3 : 1;
+    // Groups, each of one padding: every matrix with the padding that suits it,
+    // or, where that makes several short sequences of launches, all with one.
+    struct Draft {
+      int padding;
+      std::vector<NsMatrix> mats;
+    };
+    std::vector<Draft> drafts;
+    double least = -1.0;
+    for (int only : {0, 256, 128, 64}) {
+      std::vector<Draft> d;
+      for (int padding : {256, 128, 64}) {
+        int64_t elems = kGroupElements;
+        for (int32_t i : order) {
+          NsMatrix m{};
+          m.offset = offset[i];
+          m.rows = rows[i];
+          m.cols = cols[i];
+          m.tall = rows[i] > cols[i];
+          m.m = m.tall ? cols[i] : rows[i];
+          m.n = m.tall ? rows[i] : cols[i];
+          if ((only ? only : padding_of(m.m, m.n)) != padding) continue;
+          m.mp = static_cast<int32_t>(round_up(m.m, padding));
+          m.np = static_cast<int32_t>(round_up(m.n, padding));
+          if (elems >= kGroupElements) {
+            d.push_back(Draft{padding, {}});
+            elems = 0;
+          }
+          elems += static_cast<int64_t>(m.mp) * m.np;
+          d.back().mats.push_back(m);
+        }
+      }
+      double cost = 0.0;
+      NsList l;
+      for (const Draft &k : d)
+        for (int kind : {kGram, kPoly, kUpdate}) cost += make_list(kind, k.mats, k.padding, seg, &l, nullptr);
+      if (least < 0.0 || cost < least) {
+        least = cost;
+        drafts = std::move(d);
       }
     }
-    g.nmat = static_cast<int32_t>(mats[0].size()) - g.mat0;
-    for (int f = 0; f < 2; ++f) most[f] = pos[f] > most[f] ? pos[f] : most[f];
-    if (parts > p->max_parts) p->max_parts = parts;
-    if (g.nmat > p->max_mats) p->max_mats = g.nmat;
-    auto each = [&](auto &&fn) { for (int32_t k = 0; k < g.nmat; ++k) fn(k, mats[0][static_cast<size_t>(g.mat0 + k)]); };
-    g.chunk0 = static_cast<int32_t>(tiles.size());
-    each([&](int32_t k, const NsMatrix &m) { for (int c = 0; c < m.nparts; ++c) tiles.push_back(NsTile{k, c, 0, 0, 1, 0}); });
-    g.nchunk = static_cast<int32_t>(tiles.size()) - g.chunk0;
-    g.conv0 = static_cast<int32_t>(tiles.size());
-    each([&](int32_t k, const NsMatrix &m) {
-      const int rp = (m.tall ? m.np : m.mp) / kConvTile, cp = (m.tall ? m.mp : m.np) / kConvTile;
-      for (int a = 0; a < rp; ++a)
-        for (int b = 0; b < cp; ++b) tiles.push_back(NsTile{k, a, b, 0, 1, 0});
-    });
-    g.nconv = static_cast<int32_t>(tiles.size()) - g.conv0;
-    double cost;
-    g.tri_tile = tile_for(draft.mats.data(), g.nmat, draft.padding, true, &cost);
-    g.full_tile = tile_for(draft.mats.data(), g.nmat, draft.padding, false, &cost);
-    g.tri0 = static_cast<int32_t>(tiles.size());
-    each([&](int32_t k, const NsMatrix &m) { add_tiles(tiles, k, m.mp / g.tri_tile, m.mp / g.tri_tile, true); });
-    const std::vector<NsTile> triangle(tiles.begin() + g.tri0, tiles.end());
-    spread_over_dies(tiles, static_cast<size_t>(g.tri0));
-    g.ntri = static_cast<int32_t>(tiles.size()) - g.tri0;
-    g.cut0 = static_cast<int32_t>(tiles.size());
-    tiles.insert(tiles.end(), triangle.begin(), triangle.end());
-    if (g.tri_tile == 256 && cut_tail(tiles, static_cast<size_t>(g.cut0), &mats[0][static_cast<size_t>(g.mat0)], p))
-      spread_over_dies(tiles, static_cast<size_t>(g.cut0));
-    else
-      tiles.resize(static_cast<size_t>(g.cut0));
-    g.ncut = static_cast<int32_t>(tiles.size()) - g.cut0;
-    g.full0 = static_cast<int32_t>(tiles.size());
-    each([&](int32_t k, const NsMatrix &m) { add_tiles(tiles, k, m.np / g.full_tile, m.mp / g.full_tile, false); });
-    spread_over_dies(tiles, static_cast<size_t>(g.full0));
-    g.nfull = static_cast<int32_t>(tiles.size()) - g.full0;
-    p->groups.push_back(g);
+    int64_t most = 0;
+    for (Draft &draft : drafts) {
+      NsGroup g{};
+      g.mat0 = static_cast<int32_t>(mats[f].size());
+      g.nmat = static_cast<int32_t>(draft.mats.size());
+      int64_t pos = 0;
+      int32_t parts = 0;
+      const int64_t planes = f ? 2 : 1;
+      for (NsMatrix &m : draft.mats) {
+        const int64_t len = static_cast<int64_t>(m.rows) * m.cols;
+        m.part0 = parts;
+        m.chunk = static_cast<int32_t>(std::max(kNormChunk, round_up((len + kMaxParts - 1) / kMaxParts, 2048)));
+        m.nparts = static_cast<int32_t>((len + m.chunk - 1) / m.chunk);
+        parts += m.nparts;
+        const int64_t xe = static_cast<int64_t>(m.mp) * m.np, ae = static_cast<int64_t>(m.mp) * m.mp;
+        const auto take = [&](int64_t e) {
+          const int64_t at = pos;
+          pos += e;
+          return at;
+        };
+        m.x[0] = take(xe * planes);
+        m.x[1] = take(xe * planes);
+        m.lo = f ? 0 : take(xe);
+        m.a = take(ae * planes);
+        m.b = take(ae * planes);
+        mats[f].push_back(m);
+      }
+      most = std::max(most, pos);
+      p->max_parts = std::max(p->max_parts, parts);
+      p->max_mats = std::max(p->max_mats, g.nmat);
+      g.chunk0 = static_cast<int32_t>(tiles.size());
+      for (int32_t k = 0; k < g.nmat; ++k)
+        for (int c = 0; c < draft.mats[static_cast<size_t>(k)].nparts; ++c) tiles.push_back(NsTile{k, c, 0, 0, 1, 0});
+      g.nchunk = static_cast<int32_t>(tiles.size()) - g.chunk0;
+      g.conv0 = static_cast<int32_t>(tiles.size());
+      for (int32_t k = 0; k < g.nmat; ++k) {
+        const NsMatrix &m = draft.mats[static_cast<size_t>(k)];
+        const int rp = (m.tall ? m.np : m.mp) / kConvTile, cp = (m.tall ? m.mp : m.np) / kConvTile;
+        for (int a = 0; a < rp; ++a)
+          for (int b = 0; b < cp; ++b) tiles.push_back(NsTile{k, a, b, 0, 1, 0});
+      }
+      g.nconv = static_cast<int32_t>(tiles.size()) - g.conv0;
+      (void)make_list(kGram, draft.mats, draft.padding, seg, &g.gram, &tiles);
+      (void)make_list(kPoly, draft.mats, draft.padding, seg, &g.poly, &tiles);
+      (void)make_list(kUpdate, draft.mats, draft.padding, seg, &g.full, &tiles);
+      for (const NsList &l : {g.gram, g.poly})
+        p->piece_elems[f] = std::max(p->piece_elems[f], static_cast<int64_t>(l.cut) * l.parts * l.tile * l.tile);
+      p->groups[f].push_back(g);
+    }
+    p->arrays[f] = most;
   }
-  for (int f = 0; f < 2; ++f) p->ws_bytes[f] = p->groups.empty() ? 0 : NsWorkspace(*p, nullptr).bytes(most[f]);
-  if (p->groups.empty()) return ZDS_OK;
+  if (order.empty()) return ZDS_OK;
+  for (int f = 0; f < 2; ++f) p->ws_bytes[f] = NsWorkspace(*p, f, nullptr).bytes(p->arrays[f]);
   const char *what = "zds_matrix_plan_create";
   auto upload = [&](void **d, const void *h, size_t bytes) -> zds_status {
     hipError_t e = hipMalloc(d, bytes);
@@ -1060,23 +1086,22 @@ zds_status build_newton_schulz(zds_matrix_plan *p, const int64_t *offset, const 
 template <int D, int SEG>
 static zds_status run_newton_schulz(const zds_matrix_plan &p, const void *src, void *dst, const float *coef, int32_t steps,
                                     double xb, double bb, const zds_step_scalars *sc, void *ws, hipStream_t s) {
-  const NsWorkspace w(p, ws);
+  const NsWorkspace w(p, SEG == 3, ws);
   NsArgs q{};
   q.scales = w.scales;
   q.ws = w.arrays;
   q.pieces = w.pieces;
-  q.arrived = w.arrived;
   q.dst = dst;
   q.sc = sc;
   // fp16 holds up to 65504: X up to xb, A up to xb^2, B up to bb stay below half of that
   q.sx = pow2_under(32768.0, xb);
   q.sa = pow2_under(32768.0, xb * xb);
   q.sb = pow2_under(32768.0, bb > 0.0 ? bb : 1.0);
-  for (const NsGroup &g : p.groups) {
+  for (const NsGroup &g : p.groups[SEG == 3]) {
     q.mats = p.d_mats[SEG == 3] + g.mat0;
     hipLaunchKernelGGL((ns_norm_kernel<D>), dim3(g.nchunk), dim3(256), 0, s, q.mats, p.d_tiles + g.chunk0, src, w.partials, sc);
     hipLaunchKernelGGL((ns_convert_kernel<D, SEG>), dim3(g.nconv), dim3(256), 0, s, q.mats, p.d_tiles + g.conv0, src,
-                       w.partials, w.scales, w.arrived, w.arrays, sc);
+                       w.partials, w.scales, w.arrays, sc);
     zds_status st = check_launch("newton_schulz conversion");
     if (st != ZDS_OK) return st;
     for (int k = 0; k < steps; ++k) {
@@ -1129,7 +1154,7 @@ extern "C" zds_status zds_newton_schulz(const zds_matrix_plan *plan, const void 
     bb = nb > bb ? nb : bb;
   }
   if (!plan) return fail(ZDS_EINVAL, "%s: null plan", fn);
-  if (plan->groups.empty()) return ZDS_OK;
+  if (plan->groups[0].empty()) return ZDS_OK;
   if (!src || !dst) return fail(ZDS_EINVAL, "%s: null src or dst", fn);
   const uintptr_t es = static_cast<uintptr_t>(dtype_size(dtype));
   if (!aligned(src, es) || !aligned(dst, es) || (scalars_dev && !aligned(scalars_dev, 8)))
