@@ -204,6 +204,50 @@ def test_orthogonalise_sums_in_pieces(dtype, shapes):
     plan.close()
 
 
+def newton_schulz_64(x):
+    """The default steps in 64 bits on the GPU."""
+    tall = x.shape[0] > x.shape[1]
+    x = x.T.contiguous() if tall else x
+    x = x / (x.norm() + 1e-7)
+    for _ in range(5):
+        a = x @ x.T.contiguous()
+        x = 3.4445 * x + (-4.7750 * a + 2.0315 * (a @ a)) @ x
+    return x.T.contiguous() if tall else x
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("shapes", [
+    [(4000, 4090)],                     # tiles of 192, over a padded 4096
+    [(4090, 4001)],
+    [(2000, 2040)] * 8,                 # 288 tiles of 256: the last 32 in pieces
+    [(1100, 1110)] * 12,                # 540 tiles of 128, in FP32 the last 28 in pieces
+    [(2430, 2432)] * 3,                 # 570 tiles of 128: the last 58 in pieces
+    [(1000, 1000)] * 2,                 # in FP32 all of 72 tiles in pieces
+    [(700, 700)] * 21,                  # 441 tiles of 128, two to a unit
+], ids=lambda s: f"{len(s)}x{s[0][0]}x{s[0][1]}")
+def test_orthogonalise_tilings(dtype, shapes):
+    """Sets that the tilings differ for; the first and last matrix against 64 bits."""
+    mats, total = layout(shapes, 3, 1)
+    dx = torch.randn(total, generator=torch.Generator().manual_seed(19)).to(TDT[dtype]).cuda()
+    plan = zds.zds_matrix_plan_create(mats)
+    ws = zds.new_newton_schulz_workspace(plan, TDT[dtype])
+    ws.fill_(0xFF)
+    dy = torch.full((total,), 9.0, dtype=TDT[dtype], device="cuda")
+    zds.zds_newton_schulz(plan, dx, dy, ws)
+    inside = torch.zeros(total, dtype=torch.bool, device="cuda")
+    for o, r, c in mats:
+        inside[o:o + r * c] = True
+    assert (dy[~inside] == 9).all()
+    for o, r, c in (mats[0], mats[-1]):
+        want = newton_schulz_64(dx[o:o + r * c].double().view(r, c))
+        rel = ((dy[o:o + r * c].double().view(r, c) - want).norm() / want.norm()).item()
+        assert rel <= TOL[dtype], (r, c, rel)
+    again = torch.full((total,), 9.0, dtype=TDT[dtype], device="cuda")
+    zds.zds_newton_schulz(plan, dx, again, ws)
+    assert torch.equal(again, dy)
+    plan.close()
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
 @pytest.mark.parametrize("steps,coef", [(1, None), (2, None), (8, None), (3, [(1.875, -1.25, 0.375)] * 3),
                                         (4, [(3.4, -4.7, 2.0), (3.0, -4.0, 1.8), (2.0, -1.5, 0.5), (1.5, -0.5, 0.0)])])

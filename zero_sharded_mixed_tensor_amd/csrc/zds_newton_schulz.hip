@@ -211,8 +211,9 @@ struct NsArgs {
   int32_t odd;         // which X is read
 };
 
-// A block of four waves computes a T x T tile, each wave a quarter.
-template <int T>
+// A block of four waves computes a T x T tile, each wave a quarter. STAGES
+// depth steps lie in LDS at once.
+template <int T, int STAGES_ = T == 192 ? 3 : 2>
 struct NsShape {
   static constexpr int WAVES = 4;
   static constexpr int TW = T / 2;                 // a wave's part of the tile, TW x TW
@@ -220,11 +221,15 @@ struct NsShape {
   static constexpr int MI = TW / MT;
   static constexpr int LOADS = T / 8 / WAVES;      // 1 KiB loads of a wave per operand and depth step
   static constexpr int STAGE = T * 128;            // bytes of an operand's tile in LDS
-  // the epilogue's strip: MT rows of the wave's part, 16 bits an element
-  static constexpr int ROW = TW * 2, CHUNKS = TW / 8;
+  static constexpr int STAGES = STAGES_;
+  // tiles of 192 may hang over the padded sizes
+  static constexpr bool OVER = T == 192;
+  // the epilogue's strip: MT rows of the wave's part, 16 bits an element, in
+  // LDS rows of a power of two
+  static constexpr int CHUNKS = T == 192 ? 16 : TW / 8, ROW = CHUNKS * 16;
   static constexpr int STRIP = MT * ROW;
   static constexpr int MOVES = STRIP / 1024;       // 1 KiB accesses of a wave per strip
-  static constexpr int AHEAD = MI < 4 ? MI : 4;    // strips in LDS, two planes each
+  static constexpr int AHEAD = OVER ? 3 : MI < 4 ? MI : 4;  // strips in LDS, two planes each
 };
 
 // Positions of the 16-byte chunks in LDS, so that one access of a wave falls on
@@ -293,13 +298,13 @@ __device__ __forceinline__ void block_barrier() {
   asm volatile("" ::: "memory");
 }
 
-template <int T, int SEG, int WHAT>
-__global__ void __launch_bounds__(256, T == 256 ? 1 : 2) ns_product_kernel(const NsArgs q) {
-  typedef NsShape<T> S;
+template <int T, int SEG, int WHAT, int STAGES = NsShape<T>::STAGES>
+__global__ void __launch_bounds__(256, T >= 192 || STAGES > 2 ? 1 : 2) ns_product_kernel(const NsArgs q) {
+  typedef NsShape<T, STAGES> S;
   constexpr bool CUT = WHAT == kGramPiece || WHAT == kPolyPiece;
   constexpr int KIND = WHAT == kGramPiece ? kGram : WHAT == kPolyPiece ? kPoly : WHAT;
   constexpr bool TURN = KIND == kUpdate || KIND == kLast;  // P is X, read down its rows
-  __shared__ __align__(1024) char smem[2][2][S::STAGE];
+  __shared__ __align__(1024) char smem[S::STAGES][2][S::STAGE];
   if (q.sc && q.sc->overflow) return;
   const NsTile t = q.tiles[blockIdx.x];
   const NsMatrix mt = q.mats[t.mat];  // all of it now: the waits below count every access
@@ -343,15 +348,27 @@ __global__ void __launch_bounds__(256, T == 256 ? 1 : 2) ns_product_kernel(const
     p_off[v] = TURN ? static_cast<uint32_t>(xrow * pld * 2 + ns_swizzle_x<T>(xrow + v * 8 * (T == 256), lane % XC) * 16)
                     : static_cast<uint32_t>(lrow * pld * 2 + ns_swizzle(lrow, lane & 7) * 16);
   const uint32_t p_step = static_cast<uint32_t>((TURN ? 256 / XC : 32) * pld * 2);
+  // a tile that hangs over: load r's offsets, with the last row in place of rows
+  // that are not there
+  uint32_t p_over[S::LOADS], q_over[S::LOADS];
+#pragma unroll
+  for (int r = 0; S::OVER && r < S::LOADS; ++r) {
+    const int row = lrow + 32 * r, pl = mt.mp - t.ti * T - 1, ql = mt.mp - t.tj * T - 1;
+    p_over[r] = static_cast<uint32_t>((row < pl ? row : pl) * pld * 2 + ns_swizzle(lrow, lane & 7) * 16);
+    q_over[r] = static_cast<uint32_t>((row < ql ? row : ql) * qld * 2 + ns_swizzle(lrow, lane & 7) * 16);
+  }
+  const auto lane_p = [&](int r) { return S::OVER ? p_over[r] : p_off[r & 1]; };
+  const auto lane_q = [&](int r) { return S::OVER ? q_over[r] : q_off; };
+  const auto load_at = [&](int r, uint32_t step) { return S::OVER ? 0u : static_cast<uint32_t>(r * step); };
   const half_t *const p0 = P + (TURN ? static_cast<int64_t>(t.ti) * T : static_cast<int64_t>(t.ti) * T * pld);
   const half_t *const q0 = Q + static_cast<int64_t>(t.tj) * T * qld;
   // the operands of depth step k; behind the last step nothing is loaded
   u32x4 pk, qk;
   auto aim = [&](int k) {
-    int seg = 0, kk = k;
+    int seg = 0, kk = k < total ? k : total - 1;
     if (SEG == 3) {  // pieces: high*high, high*low, low*high
-      seg = k / steps;
-      kk = k - seg * steps;
+      seg = kk / steps;
+      kk -= seg * steps;
     }
     const uint32_t bytes = k < total ? 0x80000000u : 0u;
     pk = buffer_at(p0 + (seg == 1 ? pplane : 0) + static_cast<int64_t>(kk) * kNsDepth * (TURN ? pld : 1), bytes);
@@ -391,10 +408,10 @@ __global__ void __launch_bounds__(256, T == 256 ? 1 : 2) ns_product_kernel(const
   };
   constexpr int PER = S::MI * NQ, HALF = 2 * PER;  // products of a quarter, of a half step
   auto load_p = [&](int buf, int r) {
-    buffer_to_lds(pk, p_off[r & 1], r * p_step, lds0 + buf * 2 * S::STAGE + r * 4096);
+    buffer_to_lds(pk, lane_p(r), load_at(r, p_step), lds0 + buf * 2 * S::STAGE + r * 4096);
   };
   auto load_q = [&](int buf, int r) {
-    buffer_to_lds(qk, q_off, r * q_step, lds0 + (buf * 2 + 1) * S::STAGE + r * 4096);
+    buffer_to_lds(qk, lane_q(r), load_at(r, q_step), lds0 + (buf * 2 + 1) * S::STAGE + r * 4096);
   };
   // A product, and right behind it a load, for which the product stands in as
   // the wait state behind the write of m0. The accumulators are updated in
@@ -413,8 +430,8 @@ __global__ void __launch_bounds__(256, T == 256 ? 1 : 2) ns_product_kernel(const
     const uint32_t at = lds0 + (buf * 2 + !is_p) * S::STAGE + r * 4096;
     asm volatile("v_mfma_f32_16x16x32_f16 %0, %1, %2, %0\n\tbuffer_load_dwordx4 %3, %4, %5 offen lds"
                  : "+a"(acc[i][(u & 1) * NQ + j])
-                 : "v"(fp[u >> 1][i]), "v"(fq[u & 1][j]), "v"(is_p ? p_off[r & 1] : q_off), "s"(is_p ? pk : qk),
-                   "s"(static_cast<uint32_t>(r * (is_p ? p_step : q_step))), "{m0}"(at)
+                 : "v"(fp[u >> 1][i]), "v"(fq[u & 1][j]), "v"(is_p ? lane_p(r) : lane_q(r)), "s"(is_p ? pk : qk),
+                   "s"(load_at(r, is_p ? p_step : q_step)), "{m0}"(at)
                  : "memory");
   };
   // A depth step is four quarters u: two halves in depth, and in each the two
@@ -438,9 +455,15 @@ __global__ void __launch_bounds__(256, T == 256 ? 1 : 2) ns_product_kernel(const
   };
   constexpr int YOUNGER = before(at_p, PER);  // P's loads in front of the second barrier
   constexpr int EARLY = before(at_q, HALF);   // Q's loads in front of a step's first half
+  // the place in LDS of step k + d
+  int turn = from % S::STAGES;
+  auto stage = [&](int k, int d) {
+    if ((S::STAGES & (S::STAGES - 1)) == 0) return (k + d) & (S::STAGES - 1);
+    return turn + d < S::STAGES ? turn + d : turn + d - S::STAGES;
+  };
   auto quarter = [&](int k, auto which) {
     constexpr int u = decltype(which)::value, h = u >> 1;
-    const int buf = k & 1;
+    const int buf = stage(k, 0), next = stage(k, 1), last = stage(k, S::STAGES - 1);
 #pragma unroll
     for (int e = 0; e < PER; ++e) {
       const int x = (u & 1) * PER + e;  // place in the half
@@ -451,44 +474,43 @@ __global__ void __launch_bounds__(256, T == 256 ? 1 : 2) ns_product_kernel(const
         if (at_q(i) == x + (h == 1 ? 0 : HALF)) is_q = i;
       }
       if (is_p >= 0) product_load(u, e, true, buf, is_p);
-      else if (is_q >= 0) product_load(u, e, false, h == 1 ? buf : buf ^ 1, is_q);
+      else if (is_q >= 0) product_load(u, e, false, h == 1 ? buf : last, is_q);
       else product(u, e);
 #pragma unroll
       for (int r = 0; r < NQ; ++r)
-        if (r * (PER - PER / 8) / NQ == e) read_q(u == 3 ? buf ^ 1 : buf, (u + 1) & 3, r);
+        if (r * (PER - PER / 8) / NQ == e) read_q(u == 3 ? next : buf, (u + 1) & 3, r);
 #pragma unroll
       for (int r = 0; r < S::MI; ++r)
-        if (r * (HALF - HALF / 8) / S::MI == x) read_p(h ? buf ^ 1 : buf, h ^ 1, r);
+        if (r * (HALF - HALF / 8) / S::MI == x) read_p(h ? next : buf, h ^ 1, r);
       __builtin_amdgcn_sched_barrier(0);
     }
   };
-  const int b0 = from & 1;
-  aim(from);
 #pragma unroll
-  for (int g = 0; g < S::LOADS; ++g) load_p(b0, g);
+  for (int d = 0; d < S::STAGES; ++d) {
+    aim(from + d);
 #pragma unroll
-  for (int g = 0; g < S::LOADS; ++g) load_q(b0, g);
-  aim(from + 1);
+    for (int g = 0; g < S::LOADS; ++g) load_p(stage(from, d), g);
 #pragma unroll
-  for (int g = 0; g < S::LOADS; ++g) load_p(b0 ^ 1, g);
-#pragma unroll
-  for (int g = 0; g < EARLY; ++g) load_q(b0 ^ 1, g);
-  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(S::LOADS + EARLY) : "memory");
+    for (int g = 0; g < (d + 1 < S::STAGES ? S::LOADS : EARLY); ++g) load_q(stage(from, d), g);
+  }
+  constexpr int BEHIND = 2 * S::LOADS * (S::STAGES - 2);  // loads of whole steps behind the next
+  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(BEHIND + S::LOADS + EARLY) : "memory");
   block_barrier();
 #pragma unroll
-  for (int g = 0; g < S::MI; ++g) read_p(b0, 0, g);
+  for (int g = 0; g < S::MI; ++g) read_p(stage(from, 0), 0, g);
 #pragma unroll
-  for (int g = 0; g < NQ; ++g) read_q(b0, 0, g);
+  for (int g = 0; g < NQ; ++g) read_q(stage(from, 0), 0, g);
   auto depth_step = [&](int k) {
     quarter(k, std::integral_constant<int, 0>{});
     quarter(k, std::integral_constant<int, 1>{});
-    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(S::LOADS) : "memory");
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(BEHIND + S::LOADS) : "memory");
     block_barrier();
-    aim(k + 2);
+    aim(k + S::STAGES);
     quarter(k, std::integral_constant<int, 2>{});
-    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(YOUNGER) : "memory");
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(BEHIND + YOUNGER) : "memory");
     block_barrier();
     quarter(k, std::integral_constant<int, 3>{});
+    turn = stage(k, 1);
   };
   if constexpr (CUT) {
     int k = from;  // every piece has a step
@@ -538,21 +560,23 @@ __global__ void __launch_bounds__(256, T == 256 ? 1 : 2) ns_product_kernel(const
     tgrp = (sl >> 4) % GR * 8;
     tcol = (sl >> 4) / GR * 16 + (sl & 15);
   };
+  // what the lane loads of strip s in access g; where nothing is, from a place
+  // that is there
+  auto source = [&](int s, int g) {
+    const int r = g * RPI + mrow, c = ns_swizzle_strip<T>(r, mchunk);
+    if (!S::OVER) return r * old + c * 8;
+    const int64_t last = mp - 1 - (qrow + s * S::MT);
+    return (r < last ? r : last) * old + (c < S::TW / 8 && prow + c * 8 < mp ? c * 8 : 0);
+  };
   auto fetch = [&](int s) {
     if (KIND == kGram) return;
     const uint32_t at = room_lds + s % S::AHEAD * 2 * S::STRIP;
     const half_t *h = in_h + here + s * S::MT * old, *l = in_l + here + s * S::MT * old;
 #pragma unroll
-    for (int g = 0; g < S::MOVES; ++g) {
-      const int r = g * RPI + mrow;
-      to_lds(h + r * old + ns_swizzle_strip<T>(r, mchunk) * 8, at + g * 1024);
-    }
+    for (int g = 0; g < S::MOVES; ++g) to_lds(h + source(s, g), at + g * 1024);
     if (low_in) {
 #pragma unroll
-      for (int g = 0; g < S::MOVES; ++g) {
-        const int r = g * RPI + mrow;
-        to_lds(l + r * old + ns_swizzle_strip<T>(r, mchunk) * 8, at + S::STRIP + g * 1024);
-      }
+      for (int g = 0; g < S::MOVES; ++g) to_lds(l + source(s, g), at + S::STRIP + g * 1024);
     }
   };
   // rows of plane `at` to global memory
@@ -562,7 +586,8 @@ __global__ void __launch_bounds__(256, T == 256 ? 1 : 2) ns_product_kernel(const
     for (int g = 0; g < S::MOVES; ++g) {
       const int r = g * RPI + mrow;
       const f16x8 v = *reinterpret_cast<const f16x8 *>(at + r * S::ROW + ns_swizzle_strip<T>(r, mchunk) * 16);
-      *reinterpret_cast<f16x8 *>(o + r * old + mchunk * 8) = v;
+      if (!S::OVER || (mchunk < S::TW / 8 && prow + mchunk * 8 < mp && qrow + s * S::MT < mp))
+        *reinterpret_cast<f16x8 *>(o + r * old + mchunk * 8) = v;
     }
   };
   // eight rows of plane `at` from row r on, turned: column col of them
@@ -578,7 +603,8 @@ __global__ void __launch_bounds__(256, T == 256 ? 1 : 2) ns_product_kernel(const
 #pragma unroll
     for (int c = 0; c < S::TW; c += PC) {
       const f16x8 v = turned8(at, tgrp, c + tcol);
-      *reinterpret_cast<f16x8 *>(o + (c + tcol) * old + tgrp) = v;
+      if (!S::OVER || (prow + c + tcol < mp && qrow + s * S::MT < mp))
+        *reinterpret_cast<f16x8 *>(o + (c + tcol) * old + tgrp) = v;
     }
   };
   places();
@@ -592,7 +618,8 @@ __global__ void __launch_bounds__(256, T == 256 ? 1 : 2) ns_product_kernel(const
     if (KIND != kGram) {
       // wait for the strip's loads only: behind them stand the loads of the
       // AHEAD - 1 next strips and the stores of as many (at least STORES each)
-      constexpr int STORES = KIND == kUpdate ? 2 * S::MOVES : KIND == kPoly ? SEG * S::MOVES : 0;
+      // (a wave whose tile hangs over may skip its stores)
+      constexpr int STORES = S::OVER ? 0 : KIND == kUpdate ? 2 * S::MOVES : KIND == kPoly ? SEG * S::MOVES : 0;
       const int left = S::MI - 1 - s < S::AHEAD - 1 ? S::MI - 1 - s : S::AHEAD - 1;
       const int gone = s < S::AHEAD - 1 ? s : S::AHEAD - 1;
       if (low_in) wait_loads(left * 2 * S::MOVES + gone * STORES);
@@ -768,10 +795,15 @@ static float pow2_under(double limit, double value) {  // largest power of two w
   return ldexpf(1.0f, e - 1);
 }
 
+// Tiles of 128 that have a unit each to themselves: four depth steps in LDS
+// (2048 x 2048: X X^T 22.4 -> 19.4 us). Where two blocks share a unit two steps
+// leave room for both (16 of 1100 x 1100: 42 us against 45).
+constexpr int kAlone = 4;
+
 template <int T, int SEG>
 static void launch_products(const NsList &l, const NsTile *tiles, NsArgs q, int kind, hipStream_t s) {
   const dim3 block(NsShape<T>::WAVES * 64), grid(static_cast<uint32_t>(l.count));
-  if constexpr (T >= 128) {
+  if constexpr (T == 256 || T == 128) {
     if (l.cut) {
       const dim3 pgrid(static_cast<uint32_t>(l.cut * l.parts)), jgrid(static_cast<uint32_t>(l.cut), NsShape<T>::MI);
       q.tiles = tiles + l.pieces;
@@ -784,11 +816,23 @@ static void launch_products(const NsList &l, const NsTile *tiles, NsArgs q, int 
     }
   }
   q.tiles = tiles + l.first;
-  switch (kind) {
-    case kGram: hipLaunchKernelGGL((ns_product_kernel<T, SEG, kGram>), grid, block, 0, s, q); break;
-    case kPoly: hipLaunchKernelGGL((ns_product_kernel<T, SEG, kPoly>), grid, block, 0, s, q); break;
-    case kUpdate: hipLaunchKernelGGL((ns_product_kernel<T, SEG, kUpdate>), grid, block, 0, s, q); break;
-    default: hipLaunchKernelGGL((ns_product_kernel<T, SEG, kLast>), grid, block, 0, s, q); break;
+  if constexpr (T == 128) {
+    if (l.count <= kUnits) {
+      switch (kind) {
+        case kGram: hipLaunchKernelGGL((ns_product_kernel<T, SEG, kGram, kAlone>), grid, block, 0, s, q); return;
+        case kPoly: hipLaunchKernelGGL((ns_product_kernel<T, SEG, kPoly, kAlone>), grid, block, 0, s, q); return;
+        case kUpdate: hipLaunchKernelGGL((ns_product_kernel<T, SEG, kUpdate, kAlone>), grid, block, 0, s, q); return;
+        default: hipLaunchKernelGGL((ns_product_kernel<T, SEG, kLast, kAlone>), grid, block, 0, s, q); return;
+      }
+    }
+  }
+  if (kind == kGram) {
+    hipLaunchKernelGGL((ns_product_kernel<T, SEG, kGram>), grid, block, 0, s, q);
+  } else if (kind == kPoly) {
+    hipLaunchKernelGGL((ns_product_kernel<T, SEG, kPoly>), grid, block, 0, s, q);
+  } else if constexpr (T != 192) {
+    if (kind == kUpdate) hipLaunchKernelGGL((ns_product_kernel<T, SEG, kUpdate>), grid, block, 0, s, q);
+    else hipLaunchKernelGGL((ns_product_kernel<T, SEG, kLast>), grid, block, 0, s, q);
   }
 }
 
@@ -796,6 +840,7 @@ template <int SEG>
 static void launch_products(const NsGroup &g, const NsTile *tiles, const NsArgs &q, int kind, hipStream_t s) {
   const NsList &l = kind == kGram ? g.gram : kind == kPoly ? g.poly : g.full;
   if (l.tile == 256) launch_products<256, SEG>(l, tiles, q, kind, s);
+  else if (l.tile == 192) launch_products<192, SEG>(l, tiles, q, kind, s);
   else if (l.tile == 128) launch_products<128, SEG>(l, tiles, q, kind, s);
   else launch_products<64, SEG>(l, tiles, q, kind, s);
 }
@@ -847,17 +892,20 @@ struct LaunchCost {
   int tile, blocks;  // blocks of a unit at once
   double fixed[4], full[4], step[4];
 };
-static const LaunchCost kCosts[3] = {
+static const LaunchCost kCosts[4] = {
     {256, 1, {12.0}, {22.0}, {1.25}},
-    {128, 2, {5.0, 8.0}, {7.0, 11.0}, {0.5, 0.95}},
+    {192, 1, {10.0}, {}, {0.95}},
+    {128, 2, {5.0, 8.0}, {7.0, 11.0}, {0.45, 0.95}},
     {64, 4, {4.0, 5.0, 6.0, 7.5}, {5.5, 6.5, 8.0, 9.5}, {0.37, 0.5, 0.67, 0.85}},
 };
 static double round_cost(const LaunchCost &k, bool full, int64_t tiles, double steps) {
   const int64_t share = (tiles + kUnits - 1) / kUnits - 1;
   return (full ? k.full : k.fixed)[share] + steps * k.step[share];
 }
-// Storing the pieces of cut tiles and joining them.
-constexpr double kJoinCost = 14.0;
+// Storing and joining the pieces of cut tiles (4 MB of them take 7 us, 63 MB 20).
+static double join_cost(int tile, int64_t pieces) {
+  return 6.0 + 0.25e-6 * 4.0 * static_cast<double>(pieces) * tile * tile;
+}
 constexpr int kMaxPieces = 8;
 
 // The tiles of a product over a group's matrices (which come in falling depth).
@@ -869,11 +917,11 @@ static double make_list(int kind, const std::vector<NsMatrix> &mats, int padding
   const bool full = kind == kUpdate;
   double least = -1.0;
   for (const LaunchCost &k : kCosts) {
-    if (k.tile > padding) continue;
+    if (k.tile > padding || (full && k.tile == 192)) continue;
     std::vector<std::pair<int64_t, double>> runs;  // tiles, steps
     int64_t n = 0;
     for (const NsMatrix &m : mats) {
-      const int64_t a = m.mp / k.tile, b = m.np / k.tile;
+      const int64_t a = (m.mp + k.tile - 1) / k.tile, b = m.np / k.tile;
       const double steps = static_cast<double>(seg) * (kind == kGram ? m.np : m.mp) / kNsDepth;
       runs.emplace_back(full ? a * b : a * (a + 1) / 2, steps);
       n += runs.back().first;
@@ -891,11 +939,11 @@ static double make_list(int kind, const std::vector<NsMatrix> &mats, int padding
     }
     const double whole = front ? static_cast<double>(front / slots) * round_cost(k, full, slots, (all - behind) / static_cast<double>(front)) : 0.0;
     const double deep = tail ? behind / static_cast<double>(tail) : 0.0;
-    const int most = full || k.tile < 128 ? 1 : kMaxPieces;
+    const int most = full || k.tile == 192 || k.tile == 64 ? 1 : kMaxPieces;
     for (int parts = 1; parts <= most; ++parts) {
       // every piece has a step of its own
       if (parts > 1 && (tail == 0 || tail * parts > slots || least_steps < parts)) break;
-      const double c = whole + (tail ? round_cost(k, full, tail * parts, deep / parts) : 0.0) + (parts > 1 ? kJoinCost : 0.0);
+      const double c = whole + (tail ? round_cost(k, full, tail * parts, deep / parts) : 0.0) + (parts > 1 ? join_cost(k.tile, tail * parts) : 0.0);
       if (least < 0.0 || c < least) {
         least = c;
         *l = NsList{};
@@ -908,7 +956,8 @@ static double make_list(int kind, const std::vector<NsMatrix> &mats, int padding
   if (!tiles) return least;
   std::vector<NsTile> v;
   for (size_t i = 0; i < mats.size(); ++i)
-    add_tiles(v, static_cast<int>(i), (full ? mats[i].np : mats[i].mp) / l->tile, mats[i].mp / l->tile, !full);
+    add_tiles(v, static_cast<int>(i), ((full ? mats[i].np : mats[i].mp) + l->tile - 1) / l->tile,
+              (mats[i].mp + l->tile - 1) / l->tile, !full);
   l->join = static_cast<int32_t>(tiles->size());
   for (int32_t k = 0; k < l->cut; ++k) {
     NsTile t = v[v.size() - static_cast<size_t>(l->cut - k)];
