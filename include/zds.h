@@ -548,6 +548,8 @@ int64_t zds_matrix_plan_span(const zds_matrix_plan *plan);
  *   momentum  device fp32, n elements, updated in place
  *   update    device, n elements of update_dtype (BF16 or FP32), written. FP16
  *             is refused: a momentum below its range would be lost.
+ * The arrays must not overlap, but update may be grads if both have one dtype
+ * size.
  * 6 B read + 4 B written per element and the update's size. */
 zds_status zds_muon_momentum(const zds_muon_hparams *hp, const void *grads, zds_dtype grad_dtype, float *momentum,
                              void *update, zds_dtype update_dtype, int64_t n,
@@ -590,6 +592,7 @@ zds_status zds_newton_schulz(const zds_matrix_plan *plan, const void *src, void 
  *   update      device, flat buffer of the plan, BF16 or FP32
  *   master      device fp32, updated in place
  *   params_out  device, FP16 or BF16, written; NULL skips the cast
+ * The arrays must not overlap, but params_out may be a BF16 update.
  * Elements outside the plan's matrices are not touched. */
 zds_status zds_muon_apply(const zds_muon_hparams *hp, const zds_matrix_plan *plan, const void *update,
                           zds_dtype update_dtype, float *master, void *params_out, zds_dtype param_dtype,

@@ -352,6 +352,60 @@ def test_refusals_with_a_plan():
     plan.close()
 
 
+def test_overlaps_are_refused():
+    mats, total = layout([(40, 50), (3, 7)])
+    plan = zds.zds_matrix_plan_create(mats)
+    x = torch.ones(total, dtype=torch.bfloat16, device="cuda")
+    ws = zds.new_newton_schulz_workspace(plan, torch.bfloat16)
+
+    def refused(text, fn):
+        with pytest.raises(zds.ZdsError) as e:
+            fn()
+        assert text in str(e.value), str(e.value)
+
+    two = torch.ones(2 * total + 64, dtype=torch.bfloat16, device="cuda")
+    refused("overlaps src", lambda: zds.zds_newton_schulz(plan, two[:total], two[total - 1:], ws))
+    refused("overlaps src", lambda: zds.zds_newton_schulz(plan, two[8:], two, ws))
+    flat = ws.view(torch.bfloat16)
+    assert flat.numel() > total
+    refused("workspace overlaps", lambda: zds.zds_newton_schulz(plan, flat[flat.numel() - total:], x, ws))
+    refused("workspace overlaps", lambda: zds.zds_newton_schulz(plan, x, flat, ws))
+    p = torch.ones(total, device="cuda")
+    hp = zds.muon_hparams()
+    refused("overlap", lambda: zds.zds_muon_apply(hp, plan, p, p, None, scalars()))
+    refused("overlap", lambda: zds.zds_muon_apply(hp, plan, x, p, p.view(torch.bfloat16), scalars()))
+    refused("overlap", lambda: zds.zds_muon_apply(hp, plan, two, p, two[1:], scalars()))
+    torch.cuda.synchronize()
+    assert (x == 1).all() and (two == 1).all() and (p == 1).all()
+    two[:total].normal_()                             # side by side in one buffer is fine
+    zds.zds_newton_schulz(plan, two[:total], two[total:], ws)
+    zds.zds_newton_schulz(plan, two[:total], x, ws)
+    assert torch.equal(two[total:2 * total], x)
+    plan.close()
+
+
+@pytest.mark.parametrize("dtype,shapes", [("fp32", [(1000, 1000)] * 2), ("bf16", [(4000, 4090)])])
+def test_graph_replays_of_large_sets(dtype, shapes):
+    """Captured once, replayed with refilled grads: sums in pieces, and tiles
+    that hang over."""
+    mats, total = layout(shapes)
+    plan = zds.zds_matrix_plan_create(mats)
+    ws, ws2 = (zds.new_newton_schulz_workspace(plan, TDT[dtype]) for _ in range(2))
+    src = torch.randn(total, device="cuda").to(TDT[dtype])
+    out, want = torch.zeros_like(src), torch.zeros_like(src)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        zds.zds_newton_schulz(plan, src, out, ws)
+    for _ in range(4):
+        src.normal_()
+        out.zero_()
+        graph.replay()
+        zds.zds_newton_schulz(plan, src, want.zero_(), ws2)
+        torch.cuda.synchronize()
+        assert torch.equal(out, want) and out.abs().max() > 0
+    plan.close()
+
+
 def test_streams_and_graph_replays():
     """On a stream of the caller's; captured once and replayed with the grads
     refilled in place, eager work in between, every replay against the eager

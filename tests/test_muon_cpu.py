@@ -85,6 +85,17 @@ def test_momentum_refusals():
     assert f(hp, None, zds.ZDS_BF16, None, None, zds.ZDS_BF16, 0, None, None) == zds.ZDS_OK
 
 
+def test_momentum_overlaps_are_refused():
+    hp = ctypes.byref(zds.muon_hparams())
+    f = zds.lib.zds_muon_momentum
+    at = lambda k: ctypes.c_void_p(1 << 20 | k)
+    sc = ctypes.c_void_p(1 << 24)
+    for g, m, u, gdt in ((0, 1996, 65536, zds.ZDS_BF16), (0, 65536, 1998, zds.ZDS_BF16), (0, 65536, 0, zds.ZDS_FP32),
+                         (0, 65536, 2, zds.ZDS_BF16), (65536, 0, 3998, zds.ZDS_BF16), (3998, 0, 65536, zds.ZDS_BF16)):
+        assert f(hp, at(g), gdt, at(m), at(u), zds.ZDS_BF16, 1000, sc, None) == zds.ZDS_EINVAL, (g, m, u)
+        assert "overlap" in zds.zds_last_error()
+
+
 def test_momentum_binding_lengths():
     hp, sc = zds.muon_hparams(), torch.zeros(64, dtype=torch.uint8)
     g, m, u = torch.zeros(100, dtype=torch.bfloat16), torch.zeros(100), torch.zeros(100, dtype=torch.bfloat16)

@@ -187,6 +187,7 @@ static zds_status build_matrix_plan(zds_matrix_plan *p, const int64_t *offset, c
     const int64_t len = static_cast<int64_t>(rows[i]) * cols[i];
     if (offset[i] + len > p->span) p->span = offset[i] + len;
     if (len == 0) continue;
+    if (chunks.empty() || offset[i] < p->first) p->first = offset[i];
     const double r = rows[i], c = cols[i];
     const float aspect = static_cast<float>(sqrt(r > c ? r / c : 1.0));
     const float rms = static_cast<float>(0.2 * sqrt(r > c ? r : c));
@@ -266,6 +267,10 @@ extern "C" zds_status zds_muon_momentum(const zds_muon_hparams *hp, const void *
   if (!aligned(grads, static_cast<uintptr_t>(dtype_size(grad_dtype))) || !aligned(momentum, 4) ||
       !aligned(update, static_cast<uintptr_t>(dtype_size(update_dtype))) || !aligned(scalars_dev, 8))
     return fail(ZDS_EALIGN, "%s: pointer not aligned to its element size", fn);
+  const int64_t gb = n * dtype_size(grad_dtype), ub = n * dtype_size(update_dtype);
+  if (ranges_meet(momentum, n * 4, grads, gb) || ranges_meet(momentum, n * 4, update, ub) ||
+      (ranges_meet(grads, gb, update, ub) && !(grads == update && gb == ub)))
+    return fail(ZDS_EINVAL, "%s: grads, momentum and update overlap", fn);
   const MomentumArgs a{scalars_dev, grads, momentum, update, n, hp->momentum, 1.0f - hp->momentum, hp->nesterov};
   const bool vec = aligned(grads, grad_dtype == ZDS_FP32 ? 16 : 8) && aligned(momentum, 16) &&
                    aligned(update, update_dtype == ZDS_FP32 ? 16 : 8);
@@ -299,6 +304,14 @@ extern "C" zds_status zds_muon_apply(const zds_muon_hparams *hp, const zds_matri
   const hipError_t he = hipGetDevice(&dev);
   if (he != hipSuccess) return hip_fail(he, "hipGetDevice");
   if (dev != plan->device) return fail(ZDS_EINVAL, "%s: plan belongs to device %d, current is %d", fn, plan->device, dev);
+  // what the plan covers of each array
+  const auto from = [&](const void *p, int64_t es) { return static_cast<const char *>(p) + plan->first * es; };
+  const int64_t len = plan->span - plan->first, ue = dtype_size(update_dtype);
+  if (ranges_meet(from(master, 4), len * 4, from(update, ue), len * ue) ||
+      (params_out && ranges_meet(from(master, 4), len * 4, from(params_out, 2), len * 2)) ||
+      (params_out && ranges_meet(from(update, ue), len * ue, from(params_out, 2), len * 2) &&
+       !(params_out == update && ue == 2)))
+    return fail(ZDS_EINVAL, "%s: update, master and params_out overlap", fn);
   const double lr = hp->lr;
   const ApplyArgs a{scalars_dev, plan->d_chunks, update, master, params_out, lr,
                     static_cast<float>(1.0 - lr * static_cast<double>(hp->weight_decay)), hp->scale, plan->num_chunks};

@@ -1211,6 +1211,12 @@ extern "C" zds_status zds_newton_schulz(const zds_matrix_plan *plan, const void 
   const size_t need = zds_newton_schulz_workspace_bytes(plan, dtype);
   if (!ws || ws_bytes < need || !aligned(ws, 256))
     return fail(ZDS_EINVAL, "%s: workspace of %zu bytes needed (256-byte aligned)", fn, need);
+  const int64_t len = (plan->span - plan->first) * static_cast<int64_t>(es);
+  const char *from = static_cast<const char *>(src) + plan->first * static_cast<int64_t>(es);
+  const char *to = static_cast<const char *>(dst) + plan->first * static_cast<int64_t>(es);
+  if (src != dst && ranges_meet(from, len, to, len)) return fail(ZDS_EINVAL, "%s: dst overlaps src and is not src", fn);
+  if (ranges_meet(ws, static_cast<int64_t>(need), from, len) || ranges_meet(ws, static_cast<int64_t>(need), to, len))
+    return fail(ZDS_EINVAL, "%s: the workspace overlaps src or dst", fn);
   int dev = 0;
   const hipError_t he = hipGetDevice(&dev);
   if (he != hipSuccess) return hip_fail(he, "hipGetDevice");
