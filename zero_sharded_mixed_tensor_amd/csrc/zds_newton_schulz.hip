@@ -192,6 +192,25 @@ __global__ void __launch_bounds__(256) ns_convert_kernel(const NsMatrix *mats, c
 // ---------------------------------------------------------------------------
 // The products
 // ---------------------------------------------------------------------------
+//
+// One kernel for the three: C = P Q^T in tiles of T x T, a block of four waves
+// a tile, the operands' tiles of 64 deep through LDS. What bounds it is the
+// card's power: with the matrix units 68 to 80 % busy the clock falls to 1.6 -
+// 1.75 GHz of 2.4 (B X at 8192 x 22016: 2.31 ms, 1.28 PFLOP/s; a library
+// product of two large fp16 matrices reaches 1.4 - 1.5 on the same card). So
+// the shape is the one that moves the fewest bytes per product:
+// - T = 256, a wave 128 x 128 of it in 256 accumulator registers: an operand
+//   element read from LDS serves 128 products. 16 x 16 x 32 instructions
+//   (32 x 32 x 16 ones: 23.2 ms instead of 22.2 for the MLP of a 65B layer).
+// - Loads go from global memory straight to LDS, each placed right behind a
+//   product, P's and Q's in turn, so that two barriers a step are enough and
+//   neither waits for a load that was just issued.
+// - X lies in one orientation only (transposing LDS reads for B X).
+// - The epilogue reads and writes whole 16-byte rows through strips in LDS,
+//   the inputs of four strips under way at once.
+// Smaller tiles where there are too few of 256 to fill the units; which, the
+// cost of the launches decides (kCosts). Small matrices are bound by the
+// launches' latency (about 5 us each, 17 in a call of five steps).
 
 // kGramPiece, kPolyPiece: pieces of cut tiles.
 enum NsKind { kGram = 0, kPoly = 1, kUpdate = 2, kLast = 3, kGramPiece = 4, kPolyPiece = 5 };
@@ -212,7 +231,8 @@ struct NsArgs {
 };
 
 // A block of four waves computes a T x T tile, each wave a quarter. STAGES
-// depth steps lie in LDS at once.
+// depth steps lie in LDS at once: as many as fit for T = 192 (three against
+// two: 1307 and 1330 us for a 4096 x 4096 matrix).
 template <int T, int STAGES_ = T == 192 ? 3 : 2>
 struct NsShape {
   static constexpr int WAVES = 4;
@@ -236,12 +256,12 @@ struct NsShape {
 // all banks alike. An operand read as it lies: tile rows of 128 bytes, 16 (or
 // 32) rows read at one chunk.
 __device__ __forceinline__ int ns_swizzle(int row, int chunk) { return chunk ^ ((row >> 1) & 7); }
-// X in B X: 64 rows of 2 T bytes; a transposing read takes 4 + 4 rows at 32 or
-// 64 bytes.
+// X in B X: 64 rows of 2 T bytes; half a wave's transposing read takes 32 bytes
+// of each of 8 rows (r..r+3, r+8..r+11), here from all 64 banks (with the rows
+// 64 bytes apart instead, conflicts held the LDS for 10 % of the time).
 template <int T>
 __device__ __forceinline__ int ns_swizzle_x(int row, int chunk) {
-  if (T == 256) return chunk ^ (((row & 3) | ((row >> 1) & 4)) << 2);
-  if (T == 128) return chunk ^ ((row & 3) << 2);
+  if (T > 64) return chunk ^ (((row & 3) | ((row >> 1) & 4)) << 1);
   return chunk ^ ((((row >> 1) & 1) | ((row >> 2) & 2)) << 1);
 }
 // A strip of the epilogue, written by columns and read by rows.
@@ -885,9 +905,11 @@ static int padding_of(int64_t m, int64_t n) {
 // What launches of T x T tiles take, in us, fitted to measured ones (1 to 2048
 // tiles of 16 to 172 depth steps): a block's fixed part (a full product's
 // epilogue also reads and writes X's low halves), and a step's time by how
-// many blocks share a unit. X X^T at 1024 x 4096 (64 steps; 10, 36, 136 tiles)
-// takes 71, 35 and 27 us, B X at 4096 x 4096 (64 steps; 256, 1024, 4096 tiles)
-// 119, 131 and 244 us.
+// many blocks share a unit. X X^T at 1024 x 4096 (64 steps; 10 tiles of 256, 36
+// of 128, 136 of 64) takes 71, 35 and 27 us, B X at 4096 x 4096 (64 steps; 256,
+// 1024, 4096 tiles) 119, 131 and 244 us. Tiles of 192 are for X X^T and A A
+// only: at 4096 x 4096 there are 253, one a unit (78 us), against 136 of 256 or
+// 528 of 128 (94 us, the last 16 in pieces).
 struct LaunchCost {
   int tile, blocks;  // blocks of a unit at once
   double fixed[4], full[4], step[4];
