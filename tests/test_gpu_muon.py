@@ -248,6 +248,28 @@ def test_orthogonalise_tilings(dtype, shapes):
     plan.close()
 
 
+@pytest.mark.parametrize("rows,cols", [(16, 16), (16, 24), (90, 20), (32, 1000), (24, 3000), (64, 64), (64, 2000),
+                                       (96, 160), (333, 200), (700, 1000)])
+def test_orthogonalise_bf16_is_about_one_rounding(rows, cols):
+    """The error's 2-norm against that of rounding the exact result to bf16:
+    with that rounding and as much again of everything before it (independent
+    of it) it is sqrt(2) of it; a margin of 5 % for the draw."""
+    k = max(1, 200_000 // (rows * cols))
+    mats, total = layout([(rows, cols)] * k)
+    dx = torch.randn(total, generator=torch.Generator().manual_seed(20)).to(torch.bfloat16).cuda()
+    plan = zds.zds_matrix_plan_create(mats)
+    ws = zds.new_newton_schulz_workspace(plan, torch.bfloat16)
+    dy = torch.zeros_like(dx)
+    zds.zds_newton_schulz(plan, dx, dy, ws)
+    err = rounding = 0.0
+    for o, r, c in mats:
+        want = newton_schulz_64(dx[o:o + r * c].double().view(r, c))
+        err += (dy[o:o + r * c].double().view(r, c) - want).square().sum().item()
+        rounding += (want.bfloat16().double() - want).square().sum().item()
+    assert (err / rounding) ** 0.5 <= 1.05 * 2 ** 0.5, (err / rounding) ** 0.5
+    plan.close()
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
 @pytest.mark.parametrize("steps,coef", [(1, None), (2, None), (8, None), (3, [(1.875, -1.25, 0.375)] * 3),
                                         (4, [(3.4, -4.7, 2.0), (3.0, -4.0, 1.8), (2.0, -1.5, 0.5), (1.5, -0.5, 0.0)])])

@@ -21,6 +21,7 @@ struct NsMatrix {
   int32_t rows, cols;
   int32_t m, n, mp, np;
   int32_t tall;
+  int32_t pair;           // of a BF16 plan: A and B have a plane of low halves, too
   int32_t part0, nparts;  // this matrix's partial sums of squares in the group's
   int32_t chunk;          // elements of one
   int64_t x[2];     // X of even and odd steps, mp x np

@@ -14,7 +14,10 @@
 // B have bounded spectra, so powers of two bring them into fp16's range,
 // where they keep 11 bits (bf16 would keep 8 at the same speed). For BF16
 // results X is carried with what its fp16 value leaves (a second fp16 array,
-// read and written by the epilogue only). For FP32 every operand is a pair of
+// read and written by the epilogue only); matrices of up to 64 rows, whose
+// error it would leave at 1.5 roundings of the result, carry A and B as pairs,
+// too, and multiply them as FP32's do (three steps of one: their launches take
+// as long). For FP32 every operand is a pair of
 // fp16 numbers (high and low) and a product runs its sum over three pieces,
 // high*high + high*low + low*high, into the same fp32 accumulators.
 #include <algorithm>
@@ -223,9 +226,10 @@ struct NsArgs {
   void *dst;
   const zds_step_scalars *sc;
   float *pieces;       // of cut tiles: accumulators as the threads hold them
-  float a, b, c;       // the step's coefficients
+  float a, b, c;       // the step's coefficients (a: with B's shift)
+  float al;            // factor of X's remainder in a X
+  float shift;         // subtracted from B's diagonal, as stored
   float sa, sb, sx;    // powers of two: A, B and X (but the first) as stored
-  float carry;         // factor of X's remainder in a X
   int32_t first;       // the first step: X is scaled by its own alpha
   int32_t odd;         // which X is read
 };
@@ -242,6 +246,7 @@ struct NsShape {
   static constexpr int LOADS = T / 8 / WAVES;      // 1 KiB loads of a wave per operand and depth step
   static constexpr int STAGE = T * 128;            // bytes of an operand's tile in LDS
   static constexpr int STAGES = STAGES_;
+  static constexpr bool PAIRS = T == 64;           // matrices whose A and B are pairs, too (NsMatrix::pair)
   // tiles of 192 may hang over the padded sizes
   static constexpr bool OVER = T == 192;
   // the epilogue's strip: MT rows of the wave's part, 16 bits an element, in
@@ -342,7 +347,8 @@ __global__ void __launch_bounds__(256, T >= 192 || STAGES > 2 ? 1 : 2) ns_produc
   const int64_t pld = KIND == kPoly ? mp : np, qld = KIND == kGram ? np : mp;
   const int64_t pplane = KIND == kPoly ? aplane : xplane, qplane = KIND == kGram ? xplane : aplane;
   const int steps = (KIND == kGram ? mt.np : mt.mp) / kNsDepth;
-  const int all = steps * SEG;
+  const bool pair = S::PAIRS && SEG == 1 && mt.pair;
+  const int all = steps * (!pair || KIND == kGram ? SEG : TURN && q.first ? 2 : 3);
   const int from = CUT ? t.part * all / t.parts : 0;  // depth steps of this piece
   const int total = CUT ? (t.part + 1) * all / t.parts : all;
 
@@ -382,16 +388,18 @@ __global__ void __launch_bounds__(256, T >= 192 || STAGES > 2 ? 1 : 2) ns_produc
   const auto load_at = [&](int r, uint32_t step) { return S::OVER ? 0u : static_cast<uint32_t>(r * step); };
   const half_t *const p0 = P + (TURN ? static_cast<int64_t>(t.ti) * T : static_cast<int64_t>(t.ti) * T * pld);
   const half_t *const q0 = Q + static_cast<int64_t>(t.tj) * T * qld;
+  const int64_t plow = pair && TURN ? q.ws + mt.lo - P : pplane;  // P's low half
   // the operands of depth step k; behind the last step nothing is loaded
   u32x4 pk, qk;
   auto aim = [&](int k) {
     int seg = 0, kk = k < total ? k : total - 1;
-    if (SEG == 3) {  // pieces: high*high, high*low, low*high
-      seg = kk / steps;
+    if (SEG == 3 || pair) {  // pieces: high*high, P's low*high, high*Q's low
+      seg = (kk >= steps) + (kk >= 2 * steps);
       kk -= seg * steps;
+      if (pair && TURN && q.first && seg) seg = 2;  // the first X has no low half
     }
     const uint32_t bytes = k < total ? 0x80000000u : 0u;
-    pk = buffer_at(p0 + (seg == 1 ? pplane : 0) + static_cast<int64_t>(kk) * kNsDepth * (TURN ? pld : 1), bytes);
+    pk = buffer_at(p0 + (seg == 1 ? plow : 0) + static_cast<int64_t>(kk) * kNsDepth * (TURN ? pld : 1), bytes);
     qk = buffer_at(q0 + (seg == 2 ? qplane : 0) + static_cast<int64_t>(kk) * kNsDepth, bytes);
   };
   const uint32_t lds0 = lds_address(smem) + w * 1024;
@@ -564,8 +572,8 @@ __global__ void __launch_bounds__(256, T >= 192 || STAGES > 2 ? 1 : 2) ns_produc
   const int64_t old = TURN ? np : mp;
   const int64_t here = qrow * old + prow;
   const half_t *in_h = TURN ? xin : q.ws + mt.a;
-  const half_t *in_l = SEG == 3 ? in_h + (TURN ? xplane : aplane) : q.ws + mt.lo;
-  const bool low_in = SEG == 3 || (TURN && !q.first);
+  const half_t *in_l = SEG == 3 || (pair && !TURN) ? in_h + (TURN ? xplane : aplane) : q.ws + mt.lo;
+  const bool low_in = SEG == 3 || (TURN ? !q.first : pair);
   constexpr int RPI = 64 / S::CHUNKS;  // rows of a 1 KiB access
   constexpr int GR = S::MT / 8;        // groups of 8 rows in a strip
   constexpr int PC = 64 / GR;          // columns that a wave's turned access covers
@@ -646,18 +654,18 @@ __global__ void __launch_bounds__(256, T >= 192 || STAGES > 2 ? 1 : 2) ns_produc
       else wait_loads(left * S::MOVES + gone * STORES);
     }
     const char *line = at + fr * S::ROW;
-    float f0 = 0.0f, f1;  // v = f0 (high + carry low) + f1 acc
+    float f0 = 0.0f, f1, f2 = 0.0f;  // v = f0 high + f2 low + f1 acc
     if (KIND == kGram) {
       f1 = alpha * alpha * q.sa;
     } else if (KIND == kPoly) {
-      f0 = q.b * (q.sb / q.sa);
+      f0 = f2 = q.b * (q.sb / q.sa);
       f1 = q.c * (q.sb / (q.sa * q.sa));
     } else {
       const float os = KIND == kLast ? 1.0f : q.sx;
       f0 = q.a * alpha * os;
+      f2 = pair ? f0 : q.al * alpha * os;
       f1 = alpha / q.sb * os;
     }
-    const float carry = TURN ? q.carry : 1.0f;
 #pragma unroll
     for (int i = 0; i < S::MI; ++i) {
         const int col = i * S::MT + fc * 4;
@@ -669,7 +677,8 @@ __global__ void __launch_bounds__(256, T >= 192 || STAGES > 2 ? 1 : 2) ns_produc
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
           v[r] = f1 * acc[i][s][r];
-          if (KIND != kGram) v[r] += f0 * (static_cast<float>(h[r]) + carry * static_cast<float>(l[r]));
+          if (KIND != kGram) v[r] += f0 * static_cast<float>(h[r]) + f2 * static_cast<float>(l[r]);
+          if (KIND == kPoly && SEG == 1 && qrow + s * S::MT + fr == prow + col + r) v[r] -= q.shift;
         }
         if constexpr (KIND == kLast) {
           if constexpr (SEG == 1) {
@@ -692,17 +701,17 @@ __global__ void __launch_bounds__(256, T >= 192 || STAGES > 2 ? 1 : 2) ns_produc
             l[r] = static_cast<half_t>(v[r] - static_cast<float>(h[r]));
           }
           *reinterpret_cast<f16x4 *>(p) = h;
-          if (SEG == 3 || KIND == kUpdate) *reinterpret_cast<f16x4 *>(p + S::STRIP) = l;
+          if (SEG == 3 || KIND == kUpdate || pair) *reinterpret_cast<f16x4 *>(p + S::STRIP) = l;
         }
       }
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
     if constexpr (KIND == kGram || KIND == kPoly) {
       half_t *out = q.ws + (KIND == kGram ? mt.a : mt.b);
       put_rows(at, out, s);
-      if (SEG == 3) put_rows(at + S::STRIP, out + aplane, s);
+      if (SEG == 3 || pair) put_rows(at + S::STRIP, out + aplane, s);
       if (t.ti != t.tj) {
         put_turned(at, out, s);
-        if (SEG == 3) put_turned(at + S::STRIP, out + aplane, s);
+        if (SEG == 3 || pair) put_turned(at + S::STRIP, out + aplane, s);
       }
     } else if constexpr (KIND == kUpdate) {
       put_rows(at, xout, s);
@@ -776,6 +785,7 @@ __global__ void __launch_bounds__(256) ns_join_kernel(const NsArgs q, int parts)
     for (int r = 0; r < 4; ++r) {
       float x = f1 * v[i][r];
       if (POLY) x += q.b * (q.sb / q.sa) * (static_cast<float>(ah[r]) + static_cast<float>(al[r]));
+      if (POLY && SEG == 1 && row == col + r) x -= q.shift;
       h[r] = static_cast<half_t>(x);
       l[r] = static_cast<half_t>(x - static_cast<float>(h[r]));
     }
@@ -807,6 +817,19 @@ static void poly_bound(const float *k, double top, double *x, double *bx) {
   }
   *x = mx;
   *bx = mb;
+}
+
+// What is subtracted from B's diagonal as it is stored, and given back to X as
+// (a + shift) X, which takes no rounding. In the last steps most singular
+// values are near 1 and B near (b + c) I, so the rounding of its diagonal to
+// fp16 would be the largest of all. The remainder of X that B X leaves out
+// counts in a X only; its factors in the last two steps stand for (a + B) X.
+// Against 64 bits, the worst of Gaussian, low-rank and decaying spectra of 16 to
+// 200 rows: 2.3e-3, without the shift 2.65e-3 (a bf16 rounding is 1.7e-3).
+static float shift_of(const float *coef, int step, int steps) {
+  if (step + 3 < steps) return 0.0f;
+  const float d = coef[3 * step + 1] + coef[3 * step + 2];
+  return step + 1 < steps ? d : 0.5f * d;
 }
 
 static float pow2_under(double limit, double value) {  // largest power of two with p * value <= limit
@@ -944,7 +967,8 @@ static double make_list(int kind, const std::vector<NsMatrix> &mats, int padding
     int64_t n = 0;
     for (const NsMatrix &m : mats) {
       const int64_t a = (m.mp + k.tile - 1) / k.tile, b = m.np / k.tile;
-      const double steps = static_cast<double>(seg) * (kind == kGram ? m.np : m.mp) / kNsDepth;
+      const int pieces = m.pair && kind != kGram ? 3 : seg;
+      const double steps = static_cast<double>(pieces) * (kind == kGram ? m.np : m.mp) / kNsDepth;
       runs.emplace_back(full ? a * b : a * (a + 1) / 2, steps);
       n += runs.back().first;
     }
@@ -1054,7 +1078,10 @@ zds_status build_newton_schulz(zds_matrix_plan *p, const int64_t *offset, const 
     };
     std::vector<Draft> drafts;
     double least = -1.0;
-    for (int only : {0, 256, 128, 64}) {
+    // (matrices of up to 64 rows alone keep the padding that carries pairs)
+    const bool small = std::all_of(order.begin(), order.end(), [&](int32_t i) { return std::min(rows[i], cols[i]) <= 64; });
+    for (int only : {64, 0, 256, 128}) {
+      if (small && only != 64) break;
       std::vector<Draft> d;
       for (int padding : {256, 128, 64}) {
         int64_t elems = kGroupElements;
@@ -1069,6 +1096,7 @@ zds_status build_newton_schulz(zds_matrix_plan *p, const int64_t *offset, const 
           if ((only ? only : padding_of(m.m, m.n)) != padding) continue;
           m.mp = static_cast<int32_t>(round_up(m.m, padding));
           m.np = static_cast<int32_t>(round_up(m.n, padding));
+          m.pair = f == 0 && padding == 64 && m.m <= 64;
           if (elems >= kGroupElements) {
             d.push_back(Draft{padding, {}});
             elems = 0;
@@ -1109,8 +1137,8 @@ zds_status build_newton_schulz(zds_matrix_plan *p, const int64_t *offset, const 
         m.x[0] = take(xe * planes);
         m.x[1] = take(xe * planes);
         m.lo = f ? 0 : take(xe);
-        m.a = take(ae * planes);
-        m.b = take(ae * planes);
+        m.a = take(m.pair ? ae * 2 : ae * planes);
+        m.b = take(m.pair ? ae * 2 : ae * planes);
         mats[f].push_back(m);
       }
       most = std::max(most, pos);
@@ -1155,8 +1183,8 @@ zds_status build_newton_schulz(zds_matrix_plan *p, const int64_t *offset, const 
 }
 
 template <int D, int SEG>
-static zds_status run_newton_schulz(const zds_matrix_plan &p, const void *src, void *dst, const float *coef, int32_t steps,
-                                    double xb, double bb, const zds_step_scalars *sc, void *ws, hipStream_t s) {
+static zds_status run_newton_schulz(const zds_matrix_plan &p, const void *src, void *dst, const float *coef, const float *shift,
+                                    int32_t steps, double xb, double bb, const zds_step_scalars *sc, void *ws, hipStream_t s) {
   const NsWorkspace w(p, SEG == 3, ws);
   NsArgs q{};
   q.scales = w.scales;
@@ -1181,7 +1209,9 @@ static zds_status run_newton_schulz(const zds_matrix_plan &p, const void *src, v
       q.c = coef[3 * k + 2];
       q.first = k == 0;
       q.odd = k & 1;
-      q.carry = SEG == 3 || k + 2 < steps ? 1.0f : (k + 1 < steps ? 0.5f : 0.25f);
+      q.a += shift[k];
+      q.al = coef[3 * k] * (SEG == 3 || k + 2 < steps ? 1.0f : k + 1 < steps ? 0.75f : 0.25f);
+      q.shift = shift[k] * q.sb;
       launch_products<SEG>(g, p.d_tiles, q, kGram, s);
       launch_products<SEG>(g, p.d_tiles, q, kPoly, s);
       launch_products<SEG>(g, p.d_tiles, q, k + 1 == steps ? kLast : kUpdate, s);
@@ -1215,11 +1245,15 @@ extern "C" zds_status zds_newton_schulz(const zds_matrix_plan *plan, const void 
   }
   // the largest singular value any step can leave (2 % over for rounding)
   double x = 1.0, xb = 1.0, bb = 0.0;
+  float shift[kMaxSteps];
   for (int i = 0; i < steps; ++i) {
     double nx = 0.0, nb = 0.0;
     poly_bound(k + 3 * i, x * 1.02, &nx, &nb);
     if (!(nx <= 8.0) || !(nb <= 1e4))
       return fail(ZDS_EINVAL, "%s: step %d's coefficients can take a singular value past 8", fn, i);
+    // (a value at s = 1 that B does not reach is no use)
+    shift[i] = dtype == ZDS_BF16 && fabs(shift_of(k, i, steps)) <= nb ? shift_of(k, i, steps) : 0.0f;
+    nb += fabs(static_cast<double>(shift[i]));
     x = nx;
     xb = x > xb ? x : xb;
     bb = nb > bb ? nb : bb;
@@ -1244,6 +1278,6 @@ extern "C" zds_status zds_newton_schulz(const zds_matrix_plan *plan, const void 
   if (he != hipSuccess) return hip_fail(he, "hipGetDevice");
   if (dev != plan->device) return fail(ZDS_EINVAL, "%s: plan belongs to device %d, current is %d", fn, plan->device, dev);
   hipStream_t s = static_cast<hipStream_t>(stream);
-  return dtype == ZDS_BF16 ? run_newton_schulz<ZDS_BF16, 1>(*plan, src, dst, k, steps, xb, bb, scalars_dev, ws, s)
-                           : run_newton_schulz<ZDS_FP32, 3>(*plan, src, dst, k, steps, xb, bb, scalars_dev, ws, s);
+  return dtype == ZDS_BF16 ? run_newton_schulz<ZDS_BF16, 1>(*plan, src, dst, k, shift, steps, xb, bb, scalars_dev, ws, s)
+                           : run_newton_schulz<ZDS_FP32, 3>(*plan, src, dst, k, shift, steps, xb, bb, scalars_dev, ws, s);
 }
