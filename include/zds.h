@@ -576,9 +576,11 @@ size_t zds_newton_schulz_workspace_bytes(const zds_matrix_plan *plan, zds_dtype 
  *             calls that may run at the same time need one each (so do two
  *             captured graphs that may be replayed at the same time)
  * BF16: the products take their operands in fp16 (11 bits, scaled by powers of
- * two into its range) and sum in fp32; X is carried with 22 bits; the result
- * is rounded once to bf16 and lies within about 1.3 bf16 roundings of the
- * exact result (2-norm). FP32: operands are two fp16 numbers (22 bits) and
+ * two into its range) and sum in fp32; X is carried with 22 bits, and with up
+ * to 64 rows so are A and B (unless the plan also holds larger matrices and
+ * does all of them in one sequence of launches). The result is rounded once to
+ * bf16; the whole error (2-norm) is 1.1 to 1.4 times that rounding's, up to
+ * about 1.7 times for the exception. FP32: operands are two fp16 numbers (22 bits) and
  * three products replace one; the error is that of an fp32 evaluation.
  * A matrix with an infinity or NaN becomes NaN; the others are not affected. A
  * zero matrix stays zero. Entries of the result below 2^-24 may become zero. */
