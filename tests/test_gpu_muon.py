@@ -270,6 +270,21 @@ def test_orthogonalise_bf16_is_about_one_rounding(rows, cols):
     plan.close()
 
 
+@pytest.mark.parametrize("rows,cols", [(64, 64), (96, 160), (333, 200), (700, 1000), (1500, 2000)])
+def test_orthogonalise_fp32_is_an_fp32_evaluation(rows, cols):
+    """Operands of 22 bits or more and fp32 sums: at most the error of the steps
+    in plain fp32 and half as much again, for sums of 64 or more."""
+    x = torch.randn(rows, cols, generator=torch.Generator().manual_seed(21)).cuda()
+    plan = zds.zds_matrix_plan_create([(0, rows, cols)])
+    ws = zds.new_newton_schulz_workspace(plan, torch.float32)
+    y = torch.zeros_like(x)
+    zds.zds_newton_schulz(plan, x.view(-1), y.view(-1), ws)
+    want = newton_schulz_64(x.double())
+    err, plain = ((a.double() - want).norm().item() for a in (y, newton_schulz_64(x)))
+    assert err <= 1.5 * plain, (err, plain)
+    plan.close()
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
 @pytest.mark.parametrize("steps,coef", [(1, None), (2, None), (8, None), (3, [(1.875, -1.25, 0.375)] * 3),
                                         (4, [(3.4, -4.7, 2.0), (3.0, -4.0, 1.8), (2.0, -1.5, 0.5), (1.5, -0.5, 0.0)])])

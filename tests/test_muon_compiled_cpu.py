@@ -16,7 +16,8 @@ INSTR = re.compile(r"^\s+([a-z][a-z0-9_]+)(\s.*)?$")
 
 def early_accesses(lines):
     """Instructions (one function's, in the order they lie) that read or write
-    an accumulator behind a matrix instruction and before the wait."""
+    an accumulator behind a matrix instruction and before the wait; but for
+    the zeros it starts from, whose block may lie anywhere."""
     bad, pending = [], False
     for line in lines:
         m = INSTR.match(line.split(";")[0])
@@ -28,7 +29,7 @@ def early_accesses(lines):
             pending = True
         elif op == "s_nop" and args.strip() == "15":
             pending = False
-        elif pending and acc:
+        elif pending and acc and not re.match(r"v_accvgpr_write_b32 a\d+, 0$", (op + args).strip()):
             bad.append(line.strip())
     return bad
 

@@ -16,7 +16,7 @@
 // results X is carried with what its fp16 value leaves (a second fp16 array,
 // read and written by the epilogue only). For FP32 every operand is a pair of
 // fp16 numbers (high and low) and a product runs its sum over three pieces,
-// high*high + high*low + low*high, into the same fp32 accumulators. So do A A
+// low*high + high*low + high*high, into the same fp32 accumulators. So do A A
 // and B X of a BF16 result with up to 64 rows, where little averages out
 // (NsMatrix::pair; the error over that of the last rounding alone: 16 x 32
 // 1.60 -> 1.10, 32 x 1000 1.96 -> 1.03; 64 small matrices 92 -> 97 us).
@@ -227,7 +227,7 @@ struct NsArgs {
   const zds_step_scalars *sc;
   float *pieces;       // of cut tiles: accumulators as the threads hold them
   float a, b, c;       // the step's coefficients (a: with B's shift)
-  float al;            // factor of X's remainder in a X
+  float al;            // factor of X's remainder in a X, where B X leaves it out
   float shift;         // subtracted from B's diagonal, as stored
   float sa, sb, sx;    // powers of two: A, B and X (but the first) as stored
   int32_t first;       // the first step: X is scaled by its own alpha
@@ -392,15 +392,15 @@ __global__ void __launch_bounds__(256, T >= 192 || STAGES > 2 ? 1 : 2) ns_produc
   // the operands of depth step k; behind the last step nothing is loaded
   u32x4 pk, qk;
   auto aim = [&](int k) {
-    int seg = 0, kk = k < total ? k : total - 1;
-    if (SEG == 3 || pair) {  // pieces: high*high, P's low*high, high*Q's low
+    int seg = 2, kk = k < total ? k : total - 1;
+    if (SEG == 3 || (pair && KIND != kGram)) {  // P's low*high, high*Q's low, high*high: the small sums first
       seg = (kk >= steps) + (kk >= 2 * steps);
       kk -= seg * steps;
-      if (pair && TURN && q.first && seg) seg = 2;  // the first X has no low half
+      if (pair && TURN && q.first) ++seg;  // the first X has no low half
     }
     const uint32_t bytes = k < total ? 0x80000000u : 0u;
-    pk = buffer_at(p0 + (seg == 1 ? plow : 0) + static_cast<int64_t>(kk) * kNsDepth * (TURN ? pld : 1), bytes);
-    qk = buffer_at(q0 + (seg == 2 ? qplane : 0) + static_cast<int64_t>(kk) * kNsDepth, bytes);
+    pk = buffer_at(p0 + (seg == 0 ? plow : 0) + static_cast<int64_t>(kk) * kNsDepth * (TURN ? pld : 1), bytes);
+    qk = buffer_at(q0 + (seg == 1 ? qplane : 0) + static_cast<int64_t>(kk) * kNsDepth, bytes);
   };
   const uint32_t lds0 = lds_address(smem) + w * 1024;
   // Operand pieces in registers: P's of this half of a depth step and the next,
@@ -663,7 +663,7 @@ __global__ void __launch_bounds__(256, T >= 192 || STAGES > 2 ? 1 : 2) ns_produc
     } else {
       const float os = KIND == kLast ? 1.0f : q.sx;
       f0 = q.a * alpha * os;
-      f2 = pair ? f0 : q.al * alpha * os;
+      f2 = SEG == 3 || pair ? f0 : q.al * alpha * os;
       f1 = alpha / q.sb * os;
     }
 #pragma unroll
@@ -678,7 +678,7 @@ __global__ void __launch_bounds__(256, T >= 192 || STAGES > 2 ? 1 : 2) ns_produc
         for (int r = 0; r < 4; ++r) {
           v[r] = f1 * acc[i][s][r];
           if (KIND != kGram) v[r] += f0 * static_cast<float>(h[r]) + f2 * static_cast<float>(l[r]);
-          if (KIND == kPoly && SEG == 1 && qrow + s * S::MT + fr == prow + col + r) v[r] -= q.shift;
+          if (KIND == kPoly && qrow + s * S::MT + fr == prow + col + r) v[r] -= q.shift;
         }
         if constexpr (KIND == kLast) {
           if constexpr (SEG == 1) {
@@ -785,7 +785,7 @@ __global__ void __launch_bounds__(256) ns_join_kernel(const NsArgs q, int parts)
     for (int r = 0; r < 4; ++r) {
       float x = f1 * v[i][r];
       if (POLY) x += q.b * (q.sb / q.sa) * (static_cast<float>(ah[r]) + static_cast<float>(al[r]));
-      if (POLY && SEG == 1 && row == col + r) x -= q.shift;
+      if (POLY && row == col + r) x -= q.shift;
       h[r] = static_cast<half_t>(x);
       l[r] = static_cast<half_t>(x - static_cast<float>(h[r]));
     }
@@ -824,8 +824,9 @@ static void poly_bound(const float *k, double top, double *x, double *bx) {
 // values are near 1 and B near (b + c) I, so the rounding of its diagonal to
 // fp16 would be the largest of all. The remainder of X that B X leaves out
 // counts in a X only; its factors in the last two steps stand for (a + B) X.
-// The error over that of rounding the exact result: 96 x 160 1.43 -> 1.26,
-// 512 x 1024 1.29 -> 1.18.
+// The error of a BF16 result over that of rounding the exact one: 96 x 160
+// 1.43 -> 1.26, 512 x 1024 1.29 -> 1.18; of an FP32 one: 0.9e-6 -> 0.7e-6 and
+// 1.5e-6 -> 1.4e-6.
 static float shift_of(const float *coef, int step, int steps) {
   if (step + 3 < steps) return 0.0f;
   const float d = coef[3 * step + 1] + coef[3 * step + 2];
@@ -1210,7 +1211,7 @@ static zds_status run_newton_schulz(const zds_matrix_plan &p, const void *src, v
       q.first = k == 0;
       q.odd = k & 1;
       q.a += shift[k];
-      q.al = coef[3 * k] * (SEG == 3 || k + 2 < steps ? 1.0f : k + 1 < steps ? 0.75f : 0.25f);
+      q.al = coef[3 * k] * (k + 2 < steps ? 1.0f : k + 1 < steps ? 0.75f : 0.25f);
       q.shift = shift[k] * q.sb;
       launch_products<SEG>(g, p.d_tiles, q, kGram, s);
       launch_products<SEG>(g, p.d_tiles, q, kPoly, s);
@@ -1252,7 +1253,7 @@ extern "C" zds_status zds_newton_schulz(const zds_matrix_plan *plan, const void 
     if (!(nx <= 8.0) || !(nb <= 1e4))
       return fail(ZDS_EINVAL, "%s: step %d's coefficients can take a singular value past 8", fn, i);
     // (a value at s = 1 that B does not reach is no use)
-    shift[i] = dtype == ZDS_BF16 && fabs(shift_of(k, i, steps)) <= nb ? shift_of(k, i, steps) : 0.0f;
+    shift[i] = fabs(shift_of(k, i, steps)) <= nb ? shift_of(k, i, steps) : 0.0f;
     nb += fabs(static_cast<double>(shift[i]));
     x = nx;
     xb = x > xb ? x : xb;
