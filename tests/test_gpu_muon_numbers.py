@@ -1,0 +1,70 @@
+"""The accuracy of the orthogonalisation against 64 bits, next to that of the
+same steps in plain fp32 (FP32 results) or of one rounding (BF16 results)."""
+
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+if not torch.cuda.is_available():
+    pytest.skip("no GPU", allow_module_level=True)
+
+from zero_sharded_mixed_tensor_amd import zds  # noqa: E402
+
+QUINTIC = (3.4445, -4.7750, 2.0315)
+
+
+def steps_of(x, coef):
+    """The steps in x's type; in 64 bits with the coefficients the call gets."""
+    tall = x.shape[0] > x.shape[1]
+    x = x.T.contiguous() if tall else x
+    x = x / (x.norm() + 1e-7)
+    for a, b, c in torch.tensor(coef, dtype=torch.float32).double().tolist():
+        g = x @ x.T.contiguous()
+        x = a * x + (b * g + c * (g @ g)) @ x
+    return x.T.contiguous() if tall else x
+
+
+def orthogonalise(shapes, dtype, coef=None, seed=1):
+    """{(rows, cols): (err, ref)}: squared errors summed over a shape's
+    matrices, the library's and the reference's (plain fp32, or the exact
+    result rounded to bf16)."""
+    mats, pos = [], 0
+    for r, c in shapes:
+        mats.append((pos, r, c))
+        pos += r * c
+    x = torch.randn(pos, generator=torch.Generator().manual_seed(seed)).to(dtype).cuda()
+    plan = zds.zds_matrix_plan_create(mats)
+    ws = zds.new_newton_schulz_workspace(plan, dtype)
+    y = torch.zeros_like(x)
+    coef = [QUINTIC] * 5 if coef is None else coef
+    zds.zds_newton_schulz(plan, x, y, ws, steps=len(coef), coef=coef)
+    out = {}
+    for o, r, c in mats:
+        g = x[o:o + r * c].view(r, c)
+        want = steps_of(g.double(), coef)
+        ref = steps_of(g, coef) if dtype == torch.float32 else want.bfloat16()
+        e, f = out.get((r, c), (0.0, 0.0))
+        out[r, c] = (e + (y[o:o + r * c].view(r, c).double() - want).square().sum().item(),
+                     f + (ref.double() - want).square().sum().item())
+    plan.close()
+    return out
+
+
+@pytest.mark.parametrize("rows,cols", [(2, 2), (2, 64), (4, 5), (8, 8), (8, 9), (16, 16), (16, 17), (17, 16), (16, 300),
+                                       (24, 3000), (31, 31), (32, 32), (1000, 32), (48, 48), (64, 64), (64, 2000)])
+def test_fp32_results_of_few_rows(rows, cols):
+    """A pair of fp16 numbers holds a value to half a step of fp32 (11 bits,
+    then 11 bits of a remainder of at most 2^-12), and the product of two low
+    halves, which is left out, is at most as large again. So each operation is
+    off by at most twice what plain fp32's is. Many matrices together, as few
+    roundings decide about one of them."""
+    n = max(4, min(400, 20000 // (rows * cols)))
+    err, plain = orthogonalise([(rows, cols)] * n, torch.float32)[rows, cols]
+    assert err <= 4 * plain, (err / plain) ** 0.5
+
+
+def test_fp32_results_of_a_mixed_set():
+    shapes = [(16, 32)] * 24 + [(64, 64)] * 16 + [(96, 160)] * 12 + [(256, 128)] * 8 + [(200, 333)] * 4
+    for shape, (err, plain) in orthogonalise(shapes, torch.float32).items():
+        assert err <= 4 * plain, (shape, (err / plain) ** 0.5)

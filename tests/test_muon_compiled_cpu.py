@@ -57,3 +57,19 @@ def test_products_wait_before_their_accumulators_are_read(tmp_path):
     # and they keep everything in registers
     sizes = re.findall(r"\.name:\s+(_ZN3zds17ns_product_kernel\w+).*?\.private_segment_fixed_size:\s+(\d+)", text, re.S)
     assert len(sizes) == len(found) and all(int(n) == 0 for _, n in sizes), sizes
+
+
+def test_the_high_half_of_a_pair_is_rounded_one_way(tmp_path):
+    """A number's high half is stored and taken off to form the low one: two
+    uses that must see one rounding. An instruction that rounds an exact
+    product straight to fp16 next to conversions of its fp32 value makes them
+    two."""
+    if not os.path.exists(build.HIPCC):
+        pytest.skip("no hipcc")
+    out = tmp_path / "ns.s"
+    cmd = [build.HIPCC, *build.CFLAGS, "--cuda-device-only", "-S",
+           os.path.join(build.CSRC, "zds_newton_schulz.hip"), "-o", str(out)]
+    subprocess.run(cmd, check=True, capture_output=True, text=True)
+    kernels = re.findall(r"^(_ZN3zds\d+ns_\w+):\s.*?\n(.*?)^\.Lfunc_end", out.read_text(), re.M | re.S)
+    assert len(kernels) >= 50
+    assert [name for name, body in kernels if "v_fma_mix" in body] == []
