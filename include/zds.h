@@ -577,13 +577,12 @@ size_t zds_newton_schulz_workspace_bytes(const zds_matrix_plan *plan, zds_dtype 
  *             captured graphs that may be replayed at the same time)
  * BF16: the products take their operands in fp16 (11 bits, scaled by powers of
  * two into its range) and sum in fp32; X is carried with 22 bits, and with up
- * to 64 rows so are A and B (unless the plan also holds larger matrices and
- * does all of them in one sequence of launches). The result is rounded once to
- * bf16; the whole error (2-norm) is 1.1 to 1.4 times that rounding's, up to
- * about 1.7 times for the exception. FP32: operands are two fp16 numbers (22 bits) and
- * three products replace one; over many matrices the error is at most twice
- * that of an fp32 evaluation (2 x 2: 1.6 times, 16 x 17: 1.03, 24 x 3000: 1.3),
- * and with more rows less than that (128 x 128: half of it, 1500 x 2000: a third).
+ * to 64 rows so are A and B. The result is rounded once to bf16; the whole
+ * error (2-norm) is 1.0 to 1.35 times that rounding's.
+ * FP32: operands are two fp16 numbers (22 bits) and three products replace one.
+ * Over many matrices the error is at most twice that of an fp32 evaluation
+ * (2 x 2: 1.6 times, 16 x 17: 1.03, 24 x 3000: 1.3), and with more rows less
+ * than that (128 x 128: half of it, 1500 x 2000: a third).
  * A matrix with an infinity or NaN becomes NaN; the others are not affected. A
  * zero matrix stays zero. Entries of the result below 2^-24 may become zero. */
 zds_status zds_newton_schulz(const zds_matrix_plan *plan, const void *src, void *dst, zds_dtype dtype,

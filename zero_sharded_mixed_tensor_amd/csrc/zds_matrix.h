@@ -25,7 +25,7 @@ struct NsMatrix {
   int32_t part0, nparts;  // this matrix's partial sums of squares in the group's
   int32_t chunk;          // elements of one
   int64_t x[2];     // X of even and odd steps, mp x np
-  int64_t lo;       // what X's fp16 values leave of X, mp x np
+  int64_t lo;       // what X's fp16 values leave of X, mp x np (pair: of even and odd steps)
   int64_t a, b;     // A and B, mp x mp
 };
 
@@ -49,6 +49,7 @@ struct NsList {
 // conversion's 64 x 64 tiles over the padded matrices and the norm's chunks.
 struct NsGroup {
   int32_t mat0, nmat;           // matrices in the plan's device array
+  int32_t pair;                 // of a BF16 plan: some of them are NsMatrix::pair
   int32_t conv0, nconv, chunk0, nchunk;
   NsList gram, poly, full;
 };

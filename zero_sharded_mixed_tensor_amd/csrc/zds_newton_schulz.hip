@@ -19,7 +19,8 @@
 // low*high + high*low + high*high, into the same fp32 accumulators. So do A A
 // and B X of a BF16 result with up to 64 rows, where little averages out
 // (NsMatrix::pair; the error over that of the last rounding alone: 16 x 32
-// 1.60 -> 1.10, 32 x 1000 1.96 -> 1.03; 64 small matrices 92 -> 97 us).
+// 1.47 -> 1.09, 32 x 1000 1.66 -> 1.03; next to larger matrices, 1 x 513 among
+// 1000 x 4096 and others, 474 -> 483 us).
 #include <algorithm>
 #include <new>
 #include <type_traits>
@@ -43,6 +44,7 @@ constexpr int64_t kNormChunk = 32768;
 constexpr int kMaxParts = 1024;
 constexpr int kUnits = 256;  // compute units
 constexpr int kConvTile = 64;
+constexpr int kPairRows = 64;  // rows up to which A and B of a BF16 result are pairs
 
 // A matrix's first X as stored and true: X_true = alpha * X_stored.
 struct NsScale {
@@ -261,7 +263,6 @@ struct NsShape {
   static constexpr int LOADS = T / 8 / WAVES;      // 1 KiB loads of a wave per operand and depth step
   static constexpr int STAGE = T * 128;            // bytes of an operand's tile in LDS
   static constexpr int STAGES = STAGES_;
-  static constexpr bool PAIRS = T == 64;           // matrices whose A and B are pairs, too (NsMatrix::pair)
   // tiles of 192 may hang over the padded sizes
   static constexpr bool OVER = T == 192;
   // the epilogue's strip: MT rows of the wave's part, 16 bits an element, in
@@ -338,7 +339,9 @@ __device__ __forceinline__ void block_barrier() {
   asm volatile("" ::: "memory");
 }
 
-template <int T, int SEG, int WHAT, int STAGES = NsShape<T>::STAGES>
+// PAIR: matrices whose A and B are pairs may be among a BF16 launch's
+// (NsMatrix::pair).
+template <int T, int SEG, int WHAT, int STAGES, bool PAIR>
 __global__ void __launch_bounds__(256, T >= 192 || STAGES > 2 ? 1 : 2) ns_product_kernel(const NsArgs q) {
   typedef NsShape<T, STAGES> S;
   constexpr bool CUT = WHAT == kGramPiece || WHAT == kPolyPiece;
@@ -362,7 +365,10 @@ __global__ void __launch_bounds__(256, T >= 192 || STAGES > 2 ? 1 : 2) ns_produc
   const int64_t pld = KIND == kPoly ? mp : np, qld = KIND == kGram ? np : mp;
   const int64_t pplane = KIND == kPoly ? aplane : xplane, qplane = KIND == kGram ? xplane : aplane;
   const int steps = (KIND == kGram ? mt.np : mt.mp) / kNsDepth;
-  const bool pair = S::PAIRS && SEG == 1 && mt.pair;
+  const bool pair = PAIR && mt.pair;
+  // X's remainder; as an operand's low half it is read while others write theirs
+  half_t *const lo_in = q.ws + mt.lo + (pair && q.odd ? xplane : 0);
+  half_t *const lo_out = q.ws + mt.lo + (pair && !q.odd ? xplane : 0);
   const int all = steps * (!pair || KIND == kGram ? SEG : TURN && q.first ? 2 : 3);
   const int from = CUT ? t.part * all / t.parts : 0;  // depth steps of this piece
   const int total = CUT ? (t.part + 1) * all / t.parts : all;
@@ -403,7 +409,7 @@ __global__ void __launch_bounds__(256, T >= 192 || STAGES > 2 ? 1 : 2) ns_produc
   const auto load_at = [&](int r, uint32_t step) { return S::OVER ? 0u : static_cast<uint32_t>(r * step); };
   const half_t *const p0 = P + (TURN ? static_cast<int64_t>(t.ti) * T : static_cast<int64_t>(t.ti) * T * pld);
   const half_t *const q0 = Q + static_cast<int64_t>(t.tj) * T * qld;
-  const int64_t plow = pair && TURN ? q.ws + mt.lo - P : pplane;  // P's low half
+  const int64_t plow = pair && TURN ? lo_in - P : pplane;  // P's low half
   // the operands of depth step k; behind the last step nothing is loaded
   u32x4 pk, qk;
   auto aim = [&](int k) {
@@ -587,7 +593,7 @@ __global__ void __launch_bounds__(256, T >= 192 || STAGES > 2 ? 1 : 2) ns_produc
   const int64_t old = TURN ? np : mp;
   const int64_t here = qrow * old + prow;
   const half_t *in_h = TURN ? xin : q.ws + mt.a;
-  const half_t *in_l = SEG == 3 || (pair && !TURN) ? in_h + (TURN ? xplane : aplane) : q.ws + mt.lo;
+  const half_t *in_l = SEG == 3 || (pair && !TURN) ? in_h + (TURN ? xplane : aplane) : lo_in;
   const bool low_in = SEG == 3 || (TURN ? !q.first : pair);
   constexpr int RPI = 64 / S::CHUNKS;  // rows of a 1 KiB access
   constexpr int GR = S::MT / 8;        // groups of 8 rows in a strip
@@ -731,7 +737,7 @@ __global__ void __launch_bounds__(256, T >= 192 || STAGES > 2 ? 1 : 2) ns_produc
       }
     } else if constexpr (KIND == kUpdate) {
       put_rows(at, xout, s);
-      put_rows(at + S::STRIP, SEG == 3 ? xout + xplane : q.ws + mt.lo, s);
+      put_rows(at + S::STRIP, SEG == 3 ? xout + xplane : lo_out, s);
     } else if constexpr (SEG == 1) {
       // the result, in its own orientation and inside its bounds
       uint16_t *dst = static_cast<uint16_t *>(q.dst) + mt.offset;
@@ -786,6 +792,7 @@ __global__ void __launch_bounds__(256) ns_join_kernel(const NsArgs q, int parts)
 #pragma unroll
     for (int i = 0; i < S::MI; ++i) v[i] += o[(i * S::MI + j) * 256];
   }
+  const bool low = SEG == 3 || mt.pair;
   const float alpha = q.first ? q.scales[t.mat].alpha : 1.0f / q.sx;
   const float f1 = POLY ? q.c * (q.sb / (q.sa * q.sa)) : alpha * alpha * q.sa;
   half_t *const out = q.ws + (POLY ? mt.b : mt.a);
@@ -796,7 +803,7 @@ __global__ void __launch_bounds__(256) ns_join_kernel(const NsArgs q, int parts)
     const half_t *a = q.ws + mt.a + row * mp + col;
     f16x4 ah = {}, al = {}, h, l;
     if (POLY) ah = *reinterpret_cast<const f16x4 *>(a);
-    if (POLY && SEG == 3) al = *reinterpret_cast<const f16x4 *>(a + aplane);
+    if (POLY && low) al = *reinterpret_cast<const f16x4 *>(a + aplane);
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
       float x = f1 * v[i][r];
@@ -807,12 +814,12 @@ __global__ void __launch_bounds__(256) ns_join_kernel(const NsArgs q, int parts)
       l[r] = y.low;
     }
     *reinterpret_cast<f16x4 *>(out + row * mp + col) = h;
-    if (SEG == 3) *reinterpret_cast<f16x4 *>(out + aplane + row * mp + col) = l;
+    if (low) *reinterpret_cast<f16x4 *>(out + aplane + row * mp + col) = l;
     if (t.ti != t.tj) {
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
         out[(col + r) * mp + row] = h[r];
-        if (SEG == 3) out[aplane + (col + r) * mp + row] = l[r];
+        if (low) out[aplane + (col + r) * mp + row] = l[r];
       }
     }
   }
@@ -861,15 +868,30 @@ static float pow2_under(double limit, double value) {  // largest power of two w
 // leave room for both (16 of 1100 x 1100: 42 us against 45).
 constexpr int kAlone = 4;
 
-template <int T, int SEG>
-static void launch_products(const NsList &l, const NsTile *tiles, NsArgs q, int kind, hipStream_t s) {
-  const dim3 block(NsShape<T>::WAVES * 64), grid(static_cast<uint32_t>(l.count));
+template <int T, int SEG, int STAGES, bool PAIR>
+static void launch_tiles(dim3 grid, const NsArgs &q, int kind, hipStream_t s) {
+  const dim3 block(NsShape<T>::WAVES * 64);
+  if (kind == kGram) {
+    hipLaunchKernelGGL((ns_product_kernel<T, SEG, kGram, STAGES, PAIR>), grid, block, 0, s, q);
+  } else if (kind == kPoly) {
+    hipLaunchKernelGGL((ns_product_kernel<T, SEG, kPoly, STAGES, PAIR>), grid, block, 0, s, q);
+  } else if constexpr (T != 192) {
+    if (kind == kUpdate) hipLaunchKernelGGL((ns_product_kernel<T, SEG, kUpdate, STAGES, PAIR>), grid, block, 0, s, q);
+    else hipLaunchKernelGGL((ns_product_kernel<T, SEG, kLast, STAGES, PAIR>), grid, block, 0, s, q);
+  }
+}
+
+template <int T, int SEG, bool PAIR>
+static void launch_list(const NsList &l, const NsTile *tiles, NsArgs q, int kind, hipStream_t s) {
+  constexpr int STAGES = NsShape<T>::STAGES;
   if constexpr (T == 256 || T == 128) {
     if (l.cut) {
+      const dim3 block(NsShape<T>::WAVES * 64);
       const dim3 pgrid(static_cast<uint32_t>(l.cut * l.parts)), jgrid(static_cast<uint32_t>(l.cut), NsShape<T>::MI);
       q.tiles = tiles + l.pieces;
-      if (kind == kGram) hipLaunchKernelGGL((ns_product_kernel<T, SEG, kGramPiece>), pgrid, block, 0, s, q);
-      else hipLaunchKernelGGL((ns_product_kernel<T, SEG, kPolyPiece>), pgrid, block, 0, s, q);
+      // (X X^T takes X's high halves only and leaves its sums to the join)
+      if (kind == kGram) hipLaunchKernelGGL((ns_product_kernel<T, SEG, kGramPiece, STAGES, false>), pgrid, block, 0, s, q);
+      else hipLaunchKernelGGL((ns_product_kernel<T, SEG, kPolyPiece, STAGES, PAIR>), pgrid, block, 0, s, q);
       q.tiles = tiles + l.join;
       if (kind == kGram) hipLaunchKernelGGL((ns_join_kernel<T, SEG, false>), jgrid, dim3(256), 0, s, q, l.parts);
       else hipLaunchKernelGGL((ns_join_kernel<T, SEG, true>), jgrid, dim3(256), 0, s, q, l.parts);
@@ -877,33 +899,22 @@ static void launch_products(const NsList &l, const NsTile *tiles, NsArgs q, int 
     }
   }
   q.tiles = tiles + l.first;
+  const dim3 grid(static_cast<uint32_t>(l.count));
   if constexpr (T == 128) {
-    if (l.count <= kUnits) {
-      switch (kind) {
-        case kGram: hipLaunchKernelGGL((ns_product_kernel<T, SEG, kGram, kAlone>), grid, block, 0, s, q); return;
-        case kPoly: hipLaunchKernelGGL((ns_product_kernel<T, SEG, kPoly, kAlone>), grid, block, 0, s, q); return;
-        case kUpdate: hipLaunchKernelGGL((ns_product_kernel<T, SEG, kUpdate, kAlone>), grid, block, 0, s, q); return;
-        default: hipLaunchKernelGGL((ns_product_kernel<T, SEG, kLast, kAlone>), grid, block, 0, s, q); return;
-      }
-    }
+    if (l.count <= kUnits) return launch_tiles<T, SEG, kAlone, PAIR>(grid, q, kind, s);
   }
-  if (kind == kGram) {
-    hipLaunchKernelGGL((ns_product_kernel<T, SEG, kGram>), grid, block, 0, s, q);
-  } else if (kind == kPoly) {
-    hipLaunchKernelGGL((ns_product_kernel<T, SEG, kPoly>), grid, block, 0, s, q);
-  } else if constexpr (T != 192) {
-    if (kind == kUpdate) hipLaunchKernelGGL((ns_product_kernel<T, SEG, kUpdate>), grid, block, 0, s, q);
-    else hipLaunchKernelGGL((ns_product_kernel<T, SEG, kLast>), grid, block, 0, s, q);
-  }
+  launch_tiles<T, SEG, STAGES, PAIR>(grid, q, kind, s);
 }
 
 template <int SEG>
 static void launch_products(const NsGroup &g, const NsTile *tiles, const NsArgs &q, int kind, hipStream_t s) {
   const NsList &l = kind == kGram ? g.gram : kind == kPoly ? g.poly : g.full;
-  if (l.tile == 256) launch_products<256, SEG>(l, tiles, q, kind, s);
-  else if (l.tile == 192) launch_products<192, SEG>(l, tiles, q, kind, s);
-  else if (l.tile == 128) launch_products<128, SEG>(l, tiles, q, kind, s);
-  else launch_products<64, SEG>(l, tiles, q, kind, s);
+  constexpr bool P = SEG == 1;
+  // (the larger tiles' kernels without pairs are a little shorter)
+  if (l.tile == 64) launch_list<64, SEG, P>(l, tiles, q, kind, s);
+  else if (l.tile == 256) P && g.pair ? launch_list<256, SEG, P>(l, tiles, q, kind, s) : launch_list<256, SEG, false>(l, tiles, q, kind, s);
+  else if (l.tile == 192) P && g.pair ? launch_list<192, SEG, P>(l, tiles, q, kind, s) : launch_list<192, SEG, false>(l, tiles, q, kind, s);
+  else P && g.pair ? launch_list<128, SEG, P>(l, tiles, q, kind, s) : launch_list<128, SEG, false>(l, tiles, q, kind, s);
 }
 
 // Rounds `n` tiles (already in an order whose neighbours share operands) so
@@ -1096,7 +1107,7 @@ zds_status build_newton_schulz(zds_matrix_plan *p, const int64_t *offset, const 
     };
     std::vector<Draft> drafts;
     double least = -1.0;
-    // (matrices of up to 64 rows alone keep the padding that carries pairs)
+    // (a larger padding of matrices of up to 64 rows alone is work for nothing)
     const bool small = std::all_of(order.begin(), order.end(), [&](int32_t i) { return std::min(rows[i], cols[i]) <= 64; });
     for (int only : {64, 0, 256, 128}) {
       if (small && only != 64) break;
@@ -1114,7 +1125,7 @@ zds_status build_newton_schulz(zds_matrix_plan *p, const int64_t *offset, const 
           if ((only ? only : padding_of(m.m, m.n)) != padding) continue;
           m.mp = static_cast<int32_t>(round_up(m.m, padding));
           m.np = static_cast<int32_t>(round_up(m.n, padding));
-          m.pair = f == 0 && padding == 64 && m.m <= 64;
+          m.pair = f == 0 && m.m <= kPairRows;  // whatever the padding, and so whatever else the plan holds
           if (elems >= kGroupElements) {
             d.push_back(Draft{padding, {}});
             elems = 0;
@@ -1154,7 +1165,8 @@ zds_status build_newton_schulz(zds_matrix_plan *p, const int64_t *offset, const 
         };
         m.x[0] = take(xe * planes);
         m.x[1] = take(xe * planes);
-        m.lo = f ? 0 : take(xe);
+        m.lo = f ? 0 : take(m.pair ? xe * 2 : xe);
+        g.pair |= m.pair;
         m.a = take(m.pair ? ae * 2 : ae * planes);
         m.b = take(m.pair ? ae * 2 : ae * planes);
         mats[f].push_back(m);
