@@ -22,6 +22,7 @@
 // 1.47 -> 1.09, 32 x 1000 1.66 -> 1.03; next to larger matrices, 1 x 513 among
 // 1000 x 4096 and others, 474 -> 483 us).
 #include <algorithm>
+#include <cmath>
 #include <new>
 #include <type_traits>
 
@@ -829,18 +830,25 @@ __global__ void __launch_bounds__(256) ns_join_kernel(const NsArgs q, int parts)
 // Host side
 // ---------------------------------------------------------------------------
 
-// Largest |a s + b s^3 + c s^5| over [0, top], and largest |b s^2 + c s^4|.
+// Largest |a s + b s^3 + c s^5| and |b s^2 + c s^4| over [0, top]: at the ends
+// or where a slope is zero, a root of a quadratic in l = s^2. (Once for every
+// step of every call: on 4097 samples a call of five steps took 60 us longer.)
 static void poly_bound(const float *k, double top, double *x, double *bx) {
-  double mx = 0.0, mb = 0.0;
-  for (int i = 0; i <= 4096; ++i) {
-    const double s = top * i / 4096, l = s * s;
-    const double b = l * (static_cast<double>(k[1]) + static_cast<double>(k[2]) * l);
-    const double v = fabs(s * (static_cast<double>(k[0]) + b));
-    if (!(v <= mx)) mx = v;
-    if (!(fabs(b) <= mb)) mb = fabs(b);
+  const double a = k[0], b = k[1], c = k[2], end = top * top;
+  *x = *bx = HUGE_VAL;
+  if (!std::isfinite(a) || !std::isfinite(b) || !std::isfinite(c)) return;
+  const auto low = [&](double l) { return b * l + c * l * l; };
+  *x = fabs(top * (a + low(end)));
+  *bx = fabs(low(end));
+  // 5 c l^2 + 3 b l + a = 0; the roots' products and sums in the order that cancels nothing
+  const double d = 9.0 * b * b - 20.0 * a * c;
+  if (d >= 0.0) {
+    const double q = -0.5 * (3.0 * b + (b < 0.0 ? -sqrt(d) : sqrt(d)));
+    for (double l : {q / (5.0 * c), a / q})
+      if (l > 0.0 && l < end) *x = std::max(*x, fabs(sqrt(l) * (a + low(l))));
   }
-  *x = mx;
-  *bx = mb;
+  const double l = -b / (2.0 * c);
+  if (l > 0.0 && l < end) *bx = std::max(*bx, fabs(low(l)));
 }
 
 // What is subtracted from B's diagonal as it is stored, and given back to X as
