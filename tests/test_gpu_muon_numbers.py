@@ -104,3 +104,17 @@ def test_bf16_results_of_a_mixed_set_are_about_one_rounding(shapes):
     for shape, (err, rounding) in orthogonalise(shapes, torch.bfloat16).items():
         before = 1 / 3 if min(shape) <= 64 else 1
         assert err <= (1 + before) * 1.05 ** 2 * rounding, (shape, (err / rounding) ** 0.5)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("coef", [(1.0, 1e-39, 0.0), (1.0, 0.0, -1e-36), (2.0, 1e-30, 1e-30), (1.0, 0.0, 0.0)])
+def test_coefficients_next_to_zero(dtype, coef):
+    """B next to nothing: the result is a X. The norm is off by an fp32 rounding
+    or two, and a BF16 result is rounded once."""
+    x = torch.randn(40 * 70, generator=torch.Generator().manual_seed(3)).to(dtype).cuda()
+    plan = zds.zds_matrix_plan_create([(0, 40, 70)])
+    y = torch.full_like(x, 9.0)
+    zds.zds_newton_schulz(plan, x, y, zds.new_newton_schulz_workspace(plan, dtype), steps=1, coef=[coef])
+    want = coef[0] * x.double() / x.double().norm()
+    assert ((y.double() - want).abs() <= want.abs() * (torch.finfo(dtype).eps / 2 + 2.0 ** -21) + 2.0 ** -24).all()
+    plan.close()

@@ -1233,7 +1233,8 @@ static zds_status run_newton_schulz(const zds_matrix_plan &p, const void *src, v
   // fp16 holds up to 65504: X up to xb, A up to xb^2, B up to bb stay below half of that
   q.sx = pow2_under(32768.0, xb);
   q.sa = pow2_under(32768.0, xb * xb);
-  q.sb = pow2_under(32768.0, bb > 0.0 ? bb : 1.0);
+  // (a B below 2^-24 changes nothing that a result shows; its power would pass fp32's range)
+  q.sb = pow2_under(32768.0, std::max(bb, 0x1p-24));
   for (const NsGroup &g : p.groups[SEG == 3]) {
     q.mats = p.d_mats[SEG == 3] + g.mat0;
     hipLaunchKernelGGL((ns_norm_kernel<D>), dim3(g.nchunk), dim3(256), 0, s, q.mats, p.d_tiles + g.chunk0, src, w.partials, sc);
