@@ -118,3 +118,24 @@ def test_coefficients_next_to_zero(dtype, coef):
     want = coef[0] * x.double() / x.double().norm()
     assert ((y.double() - want).abs() <= want.abs() * (torch.finfo(dtype).eps / 2 + 2.0 ** -21) + 2.0 ** -24).all()
     plan.close()
+
+
+# Steps that start steep and flatten; every value stays below 2.
+STEEP = [(8.2052, -22.9018, 16.4607), (4.0664, -2.8612, 0.5184), (3.9096, -2.8234, 0.5250), (3.2856, -2.4153, 0.4853),
+         (2.2779, -1.6199, 0.3985), (1.8726, -1.2307, 0.3585), (1.875, -1.25, 0.375)]
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("shape", [(1, 1), (40, 70), (96, 160), (600, 512), (2000, 2040)])
+@pytest.mark.parametrize("steps", [1, 2, 3, 7])
+def test_steep_steps_do_not_diverge(dtype, shape, steps):
+    """A matrix of equal elements has the singular value 1, where the first
+    step is steepest, and its roundings all point one way. No
+    step takes a value of up to 1 + 2^-8 past 1.992; 5 % for the roundings."""
+    r, c = shape
+    x = torch.full((r * c,), 0.7, device="cuda").to(dtype)
+    plan = zds.zds_matrix_plan_create([(0, r, c)])
+    y = torch.zeros_like(x)
+    zds.zds_newton_schulz(plan, x, y, zds.new_newton_schulz_workspace(plan, dtype), steps=steps, coef=STEEP[:steps])
+    assert torch.isfinite(y).all() and y.double().norm().item() < 2.1
+    plan.close()

@@ -22,10 +22,10 @@ def refused(coef):
 
 def largest(coef):
     """The largest value of any step by sampling (values of up to 1 to begin
-    with, 2 % over for rounding in each step), and of b s^2 + c s^4."""
+    with, 2^-8 over for rounding in each step), and of b s^2 + c s^4."""
     top, most, mb = 1.0, 0.0, 0.0
     for a, b, c in np.float32(coef).astype(np.float64):
-        s = np.linspace(0.0, 1.02 * top, 200_001)
+        s = np.linspace(0.0, (1 + 2.0 ** -8) * top, 200_001)
         mb = max(mb, np.abs(b * s ** 2 + c * s ** 4).max())
         top = np.abs(a * s + b * s ** 3 + c * s ** 5).max()
         most = max(most, top)
@@ -67,3 +67,16 @@ def test_bound_takes_no_time():
         zds.lib.zds_newton_schulz(None, None, None, zds.ZDS_BF16, arr, 16, None, None, 0, None)
         least = min(least, time.perf_counter() - t)
     assert least < 40e-6, least
+
+
+# Steps that start steep and flatten (8.2 times the smallest singular values in the
+# first, 1.9 in the last): their values stay below 2, but 2 % more in
+# front of every step would take them past 8 in the third.
+STEEP = [(8.2052, -22.9018, 16.4607), (4.0664, -2.8612, 0.5184), (3.9096, -2.8234, 0.5250), (3.2856, -2.4153, 0.4853),
+         (2.2779, -1.6199, 0.3985), (1.8726, -1.2307, 0.3585), (1.875, -1.25, 0.375)]
+
+
+def test_steep_coefficients_that_stay_bounded():
+    assert largest(STEEP)[0] < 2.1
+    for steps in range(1, 8):
+        assert not refused(STEEP[:steps])

@@ -1282,12 +1282,14 @@ extern "C" zds_status zds_newton_schulz(const zds_matrix_plan *plan, const void 
     static const float quintic[3] = {3.4445f, -4.7750f, 2.0315f};
     for (int j = 0; j < 3; ++j) k[3 * i + j] = coef ? coef[3 * i + j] : quintic[j];
   }
-  // the largest singular value any step can leave (2 % over for rounding)
+  // The largest singular value any step can leave. Rounding X, A and B to 11 bits
+  // moves one by at most about 2^-10 of itself in a step even where all roundings
+  // point one way (a matrix of equal elements); 2^-8 over.
   double x = 1.0, xb = 1.0, bb = 0.0;
   float shift[kMaxSteps];
   for (int i = 0; i < steps; ++i) {
     double nx = 0.0, nb = 0.0;
-    poly_bound(k + 3 * i, x * 1.02, &nx, &nb);
+    poly_bound(k + 3 * i, x * (1.0 + 0x1p-8), &nx, &nb);
     if (!(nx <= 8.0) || !(nb <= 1e4))
       return fail(ZDS_EINVAL, "%s: step %d's coefficients can take a singular value past 8", fn, i);
     // (a value at s = 1 that B does not reach is no use)
