@@ -576,9 +576,11 @@ size_t zds_newton_schulz_workspace_bytes(const zds_matrix_plan *plan, zds_dtype 
  *             calls that may run at the same time need one each (so do two
  *             captured graphs that may be replayed at the same time)
  * BF16: the products take their operands in fp16 (11 bits, scaled by powers of
- * two into its range) and sum in fp32; X is carried with 22 bits, and with up
- * to 64 rows so are A and B. The result is rounded once to bf16; the whole
- * error (2-norm) is 1.0 to 1.35 times that rounding's.
+ * two into its range) and sum in fp32; X is carried with 22 bits
+ * (the lower 11 count a + B_ii / 2 times in row i, not a + B), and with up to
+ * 64 rows so are A and B. The result is rounded once to bf16; the whole error
+ * (2-norm) of the default five steps is 1.0 to 1.35 times that rounding's. Steps
+ * that start steeper or go on longer can double it (eight default ones).
  * FP32: operands are two fp16 numbers (22 bits) and three products replace one.
  * Over many matrices the error is at most twice that of an fp32 evaluation
  * (2 x 2: 1.6 times, 16 x 17: 1.03, 24 x 3000: 1.3), and with more rows less

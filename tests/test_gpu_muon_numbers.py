@@ -139,3 +139,14 @@ def test_steep_steps_do_not_diverge(dtype, shape, steps):
     zds.zds_newton_schulz(plan, x, y, zds.new_newton_schulz_workspace(plan, dtype), steps=steps, coef=STEEP[:steps])
     assert torch.isfinite(y).all() and y.double().norm().item() < 2.1
     plan.close()
+
+
+@pytest.mark.parametrize("coef", [STEEP, [(1.875, -1.25, 0.375)] * 16, [(1.5, -0.5, 0.0)] * 12, [QUINTIC] * 3],
+                         ids=["steep", "quintic16", "cubic12", "default3"])
+def test_bf16_results_of_other_steps_are_about_one_rounding(coef):
+    """As for the default steps: one rounding and as much again of everything
+    before it, 5 % for the draw. What the product leaves out of X (its
+    remainder behind 11 bits) must then follow the coefficients that are given."""
+    shapes = [(65, 65)] * 4 + [(96, 160)] * 3 + [(256, 128)] * 3 + [(400, 1500)] * 2 + [(1500, 2000)]
+    for shape, (err, rounding) in orthogonalise(shapes, torch.bfloat16, coef).items():
+        assert err <= 2 * 1.05 ** 2 * rounding, (shape, (err / rounding) ** 0.5)

@@ -33,6 +33,7 @@ namespace zds {
 
 typedef _Float16 half_t;
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
 typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) void lds_void;
 typedef __attribute__((address_space(1))) const void global_cvoid;
@@ -245,7 +246,7 @@ struct NsArgs {
   const zds_step_scalars *sc;
   float *pieces;       // of cut tiles: accumulators as the threads hold them
   float a, b, c;       // the step's coefficients (a: with B's shift)
-  float al;            // factor of X's remainder in a X, where B X leaves it out
+  float al, alb;       // X's remainder in row i counts al + alb B_ii (as stored) times, where B X leaves it out
   float shift;         // subtracted from B's diagonal, as stored
   float sa, sb, sx;    // powers of two: A, B and X (but the first) as stored
   int32_t first;       // the first step: X is scaled by its own alpha
@@ -306,7 +307,11 @@ __device__ __forceinline__ f16x4 read_turned(const char *p) {
 __device__ __forceinline__ void to_lds(const void *global, uint32_t lds) {
   asm volatile("s_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(global), "{m0}"(lds) : "memory");
 }
-// The same in the form that costs the wave no address arithmetic: a buffer
+// 4 bytes a lane, 256 from `lds` on.
+__device__ __forceinline__ void diag_to_lds(const void *global, uint32_t lds) {
+  asm volatile("s_nop 0\n\tglobal_load_lds_dword %0, off" ::"v"(global), "{m0}"(lds) : "memory");
+}
+// The same as to_lds in the form that costs the wave no address arithmetic: a buffer
 // descriptor (base, size in bytes: an access behind it loads nothing), a
 // lane's offset and the load's.
 __device__ __forceinline__ u32x4 buffer_at(const void *p, uint32_t bytes) {
@@ -348,7 +353,9 @@ __global__ void __launch_bounds__(256, T >= 192 || STAGES > 2 ? 1 : 2) ns_produc
   constexpr bool CUT = WHAT == kGramPiece || WHAT == kPolyPiece;
   constexpr int KIND = WHAT == kGramPiece ? kGram : WHAT == kPolyPiece ? kPoly : WHAT;
   constexpr bool TURN = KIND == kUpdate || KIND == kLast;  // P is X, read down its rows
+  constexpr bool REST = SEG == 1 && TURN;  // X's remainder stands beside the product
   __shared__ __align__(1024) char smem[S::STAGES][2][S::STAGE];
+  __shared__ __align__(256) uint32_t diag[REST ? T : 64];  // B's diagonal in the tile's rows, in one half each
   if (q.sc && q.sc->overflow) return;
   const NsTile t = q.tiles[blockIdx.x];
   const NsMatrix mt = q.mats[t.mat];  // all of it now: the waits below count every access
@@ -535,6 +542,10 @@ __global__ void __launch_bounds__(256, T >= 192 || STAGES > 2 ? 1 : 2) ns_produc
       __builtin_amdgcn_sched_barrier(0);
     }
   };
+  if (REST && w * 64 < T) {  // (older than all that the waits below count)
+    const int64_t row = static_cast<int64_t>(t.tj) * T + w * 64 + lane;
+    diag_to_lds(Q + row * mp + (row & ~1), lds_address(diag) + w * 256);
+  }
 #pragma unroll
   for (int d = 0; d < S::STAGES; ++d) {
     aim(from + d);
@@ -685,7 +696,11 @@ __global__ void __launch_bounds__(256, T >= 192 || STAGES > 2 ? 1 : 2) ns_produc
     } else {
       const float os = KIND == kLast ? 1.0f : q.sx;
       f0 = q.a * alpha * os;
-      f2 = SEG == 3 || pair ? f0 : q.al * alpha * os;
+      f2 = f0;
+      if (REST && !pair) {
+        const uint32_t both = diag[wj * S::TW + s * S::MT + fr];
+        f2 = (q.al + q.alb * __builtin_bit_cast(f16x2, both)[fr & 1]) * alpha * os;
+      }
       f1 = alpha / q.sb * os;
     }
 #pragma unroll
@@ -854,11 +869,13 @@ static void poly_bound(const float *k, double top, double *x, double *bx) {
 // What is subtracted from B's diagonal as it is stored, and given back to X as
 // (a + shift) X, which takes no rounding. In the last steps most singular
 // values are near 1 and B near (b + c) I, so the rounding of its diagonal to
-// fp16 would be the largest of all. The remainder of X that B X leaves out
-// counts in a X only; its factors in the last two steps stand for (a + B) X.
-// The error of a BF16 result over that of rounding the exact one: 96 x 160
-// 1.43 -> 1.26, 512 x 1024 1.29 -> 1.18; of an FP32 one: 0.9e-6 -> 0.7e-6 and
-// 1.5e-6 -> 1.4e-6.
+// fp16 would be the largest of all. The error of a BF16 result over that of
+// rounding the exact one: 96 x 160 1.43 -> 1.26, 512 x 1024 1.29 -> 1.18; of an
+// FP32 one: 0.9e-6 -> 0.7e-6 and 1.5e-6 -> 1.4e-6.
+//
+// The remainder of X that B X leaves out would count a + B times: a where
+// singular values are small, and in the mean of a row's directions a + B_ii.
+// It counts halfway between the two, whatever the coefficients.
 static float shift_of(const float *coef, int step, int steps) {
   if (step + 3 < steps) return 0.0f;
   const float d = coef[3 * step + 1] + coef[3 * step + 2];
@@ -1249,7 +1266,8 @@ static zds_status run_newton_schulz(const zds_matrix_plan &p, const void *src, v
       q.first = k == 0;
       q.odd = k & 1;
       q.a += shift[k];
-      q.al = coef[3 * k] * (k + 2 < steps ? 1.0f : k + 1 < steps ? 0.75f : 0.25f);
+      q.al = coef[3 * k] + 0.5f * shift[k];
+      q.alb = 0.5f / q.sb;
       q.shift = shift[k] * q.sb;
       launch_products<SEG>(g, p.d_tiles, q, kGram, s);
       launch_products<SEG>(g, p.d_tiles, q, kPoly, s);
