@@ -1,0 +1,24 @@
+"""MuonStep and the Muon configuration: what is refused, and before what.
+Nothing here reaches a device."""
+
+import pytest
+import torch
+
+from zero_sharded_mixed_tensor_amd.config import ConfigError, from_ds_config
+
+zds = pytest.importorskip("zero_sharded_mixed_tensor_amd.zds", reason="libzds.so not built")
+from zero_sharded_mixed_tensor_amd.step import MuonStep, ShardStep  # noqa: E402
+
+
+def muon_config(**params):
+    return from_ds_config({"optimizer": {"type": "Muon", "params": params}})
+
+
+def test_a_muon_configuration_is_no_adamw_step():
+    """Its hparams() are those of the tensors that AdamW updates next to the
+    matrices: a step of them alone would update the matrices by AdamW, too."""
+    with pytest.raises(zds.ZdsError) as e:
+        ShardStep.from_config(64, muon_config(lr=1e-2))
+    assert "MuonStep" in str(e.value)
+    with pytest.raises(ConfigError):
+        MuonStep.from_config(64, 64, [(0, 8, 8)], from_ds_config({}))

@@ -31,6 +31,8 @@ class ShardStep:
     def from_config(cls, n, cfg, t0=0, beta1_pow0=1.0, beta2_pow0=1.0, device="cuda", stream=None):
         """A step with the settings of a config.StepConfig (hyperparameters,
         loss scaler, clip threshold, micro-batches per step)."""
+        if cfg.muon is not None:
+            raise zds.ZdsError(zds.ZDS_EINVAL, "the configuration's optimizer is Muon: its step is MuonStep")
         return cls(n, cfg.hparams(), cfg.scaler_config(), cfg.max_norm, cfg.accum_steps, t0, beta1_pow0,
                    beta2_pow0, device, stream)
 
