@@ -22,3 +22,13 @@ def test_a_muon_configuration_is_no_adamw_step():
     assert "MuonStep" in str(e.value)
     with pytest.raises(ConfigError):
         MuonStep.from_config(64, 64, [(0, 8, 8)], from_ds_config({}))
+
+
+def test_auto_takes_the_default():
+    auto = muon_config(lr="auto", muon_lr="auto", adam_lr="auto", momentum="auto", nesterov="auto", ns_steps="auto",
+                       scale="auto", weight_decay="auto")
+    assert auto == muon_config()
+    assert muon_config(nesterov=None, scale=None) == muon_config()
+    for bad in ({"nesterov": "yes"}, {"nesterov": 0}, {"scale": "automatic"}, {"scale": 1}):
+        with pytest.raises(ConfigError):
+            muon_config(**bad)

@@ -149,13 +149,17 @@ def _muon(p, lr):
     momentum = _num(p, "momentum", MUON_DEFAULTS["momentum"])
     if not 0.0 <= momentum < 1.0:
         raise ConfigError("momentum must lie in [0, 1)")
-    nesterov = p.get("nesterov", MUON_DEFAULTS["nesterov"])
+    nesterov = p.get("nesterov")
+    if _is_auto(nesterov):
+        nesterov = MUON_DEFAULTS["nesterov"]
     if not isinstance(nesterov, bool):
         raise ConfigError("nesterov: expected true or false, got %r" % (nesterov,))
     steps = _num(p, "ns_steps", MUON_DEFAULTS["ns_steps"], int)
     if not 1 <= steps <= 16:
         raise ConfigError("ns_steps must lie in [1, 16]")
-    scale = p.get("scale", MUON_DEFAULTS["scale"])
+    scale = p.get("scale")
+    if _is_auto(scale):
+        scale = MUON_DEFAULTS["scale"]
     if scale not in ("none", "aspect", "rms"):
         raise ConfigError("scale must be none, aspect or rms, got %r" % (scale,))
     return MuonConfig(_num(p, "muon_lr", lr), momentum, nesterov, steps, scale)
