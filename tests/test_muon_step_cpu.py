@@ -32,3 +32,13 @@ def test_auto_takes_the_default():
     for bad in ({"nesterov": "yes"}, {"nesterov": 0}, {"scale": "automatic"}, {"scale": 1}):
         with pytest.raises(ConfigError):
             muon_config(**bad)
+
+
+def test_one_set_of_defaults():
+    """A recipe that names no value is the same step from the configuration and
+    from the library."""
+    for want, got in ((zds.muon_hparams(), muon_config().muon_hparams()), (zds.hparams(), muon_config().hparams())):
+        assert bytes(want) == bytes(got)
+    from inspect import signature
+    assert muon_config().muon.ns_steps == signature(MuonStep).parameters["ns_steps"].default
+    assert muon_config().muon.ns_steps == signature(zds.zds_newton_schulz).parameters["steps"].default

@@ -541,8 +541,9 @@ def _here(t, what):
 _MUON_SCALES = {"none": ZDS_MUON_SCALE_NONE, "aspect": ZDS_MUON_SCALE_ASPECT, "rms": ZDS_MUON_SCALE_RMS}
 
 
-def muon_hparams(lr=2e-3, momentum=0.95, weight_decay=0.1, nesterov=True, scale="rms"):
-    """scale: "none", "aspect" or "rms" (see zds_muon_scale in include/zds.h)."""
+def muon_hparams(lr=1e-3, momentum=0.95, weight_decay=0.01, nesterov=True, scale="aspect"):
+    """scale: "none", "aspect" or "rms" (see zds_muon_scale in include/zds.h).
+    The defaults are a configuration's; lr and weight_decay are hparams()'s."""
     if scale not in _MUON_SCALES:
         raise ZdsError(ZDS_EINVAL, "scale must be one of %s" % ", ".join(sorted(_MUON_SCALES)))
     return MuonHparams(lr, momentum, weight_decay, int(bool(nesterov)), _MUON_SCALES[scale])
