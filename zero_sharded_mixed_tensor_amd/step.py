@@ -126,16 +126,49 @@ class MuonStep:
         return cls(n, split, matrices, cfg.hparams(), cfg.muon_hparams(), cfg.scaler_config(), cfg.max_norm,
                    cfg.accum_steps, cfg.muon.ns_steps, t0, beta1_pow0, beta2_pow0, None, device, stream)
 
+    def _check(self, grads, master, momentum, exp_avg, exp_avg_sq, params_out):
+        """Refuses what any of the step's calls would, before the first of them
+        has changed anything: a step that ends halfway cannot be repeated."""
+        n, k = self.n, self.split
+        spans = [("update", self.update.data_ptr(), k * self.update.element_size())]
+        for name, t, need, kinds in (("grads", grads, n, None), ("master", master, n, ("float32",)),
+                                     ("momentum", momentum, k, ("float32",)), ("exp_avg", exp_avg, n - k, ("float32",)),
+                                     ("exp_avg_sq", exp_avg_sq, n - k, ("float32",)),
+                                     ("params_out", params_out, n, ("float16", "bfloat16"))):
+            if t is None:
+                if name != "params_out":
+                    raise zds.ZdsError(zds.ZDS_EINVAL, "%s is missing" % name)
+                continue
+            zds._need(t, need, name)
+            zds.dtype_code(t)
+            if kinds is not None and str(t.dtype)[6:] not in kinds:
+                raise zds.ZdsError(zds.ZDS_EINVAL, "%s must be %s" % (name, " or ".join(kinds)))
+            if not t.is_contiguous():
+                raise zds.ZdsError(zds.ZDS_EINVAL, "%s must be contiguous" % name)
+            at, size = zds._here(t, name), need * t.element_size()
+            for other, there, length in spans:
+                # (params_out may lie on the grads: an element is read before it is written;
+                # the first call itself sees to grads and update)
+                if (at < there + length and there < at + size
+                        and {name, other} not in ({"params_out", "grads"}, {"update", "grads"})):
+                    raise zds.ZdsError(zds.ZDS_EINVAL, "%s and %s overlap" % (other, name))
+            spans.append((name, at, size))
+        if not 1 <= self.ns_steps <= 16:
+            raise zds.ZdsError(zds.ZDS_EINVAL, "ns_steps must lie in [1, 16]")
+        zds.check_hparams(self.base.hp)
+
     def apply(self, grads, master, momentum, exp_avg, exp_avg_sq, params_out, stream=None):
         """The update under the step scalars that a norm pass has left.
         grads, master, params_out (or None): n elements; momentum: split;
         exp_avg, exp_avg_sq: n - split."""
+        self._check(grads, master, momentum, exp_avg, exp_avg_sq, params_out)
         b, k = self.base, self.split
         zds.zds_muon_momentum(self.muon, grads, momentum, self.update, b.scalars, stream, n=k)
         zds.zds_newton_schulz(self.plan, self.update, self.update, self.ws, self.ns_steps, None, b.scalars, stream)
         zds.zds_muon_apply(self.muon, self.plan, self.update, master, params_out, b.scalars, stream)
-        zds.zds_adam_step(b.hp, grads[k:], master[k:], exp_avg, exp_avg_sq,
-                          None if params_out is None else params_out[k:], b.scalars, b.state, stream, n=self.n - k)
+        rest = lambda t: None if t is None else t.view(-1)[k:]  # noqa: E731
+        zds.zds_adam_step(b.hp, rest(grads), rest(master), exp_avg, exp_avg_sq, rest(params_out), b.scalars, b.state,
+                          stream, n=self.n - k)
 
     def step(self, grads, master, momentum, exp_avg, exp_avg_sq, params_out, stream=None):
         """The whole step; kernels only, so it can be captured into a graph."""

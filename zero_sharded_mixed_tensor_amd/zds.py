@@ -444,6 +444,11 @@ def zds_adam_step(hp, grads, master, exp_avg, exp_avg_sq, params_out, scalars, s
                              _stream(stream)))
 
 
+def check_hparams(hp):
+    """Refuses what zds_adam_step refuses of hp (a call of no elements)."""
+    _check(lib.zds_adam_step(ctypes.byref(hp), None, ZDS_FP32, None, None, None, None, ZDS_FP16, 0, None, None, None))
+
+
 def _host_ptr(x, what):
     """Host buffer address: a CPU torch tensor or a C-contiguous numpy array."""
     if x is None:
