@@ -32,3 +32,37 @@ def test_a_refused_step_changes_nothing():
     assert st.read_state().t == t0 + 1
     for k in ("master", "momentum", "exp_avg", "exp_avg_sq", "params_out"):
         assert not torch.equal(a[k], before[k]), k
+
+
+@pytest.mark.parametrize("dtype,tol", [(torch.bfloat16, 2.0 ** -7), (torch.float32, 3e-5)])
+def test_a_set_of_two_groups(dtype, tol):
+    """Matrices of more than 2^28 elements together go through the launches in
+    groups, one after another in one workspace; the second here also with sums
+    in pieces. Tolerances as for the other sets of these sizes (2-norm): a BF16
+    rounding and as much again; for FP32 22-bit operands and fp32 sums."""
+    mats, pos = [], 0
+    for r, c in [(4096, 4096)] * 16 + [(2000, 2040)] * 8:
+        mats.append((pos, r, c))
+        pos += r * c + 8
+    x = torch.empty(pos, device="cuda", dtype=dtype).normal_(generator=torch.Generator("cuda").manual_seed(4))
+    plan = zds.zds_matrix_plan_create(mats)
+    ws = zds.new_newton_schulz_workspace(plan, dtype)
+    one = zds.zds_matrix_plan_create(mats[:1])
+    assert ws.numel() < 17 * zds.zds_newton_schulz_workspace_bytes(one, dtype)      # one group's, not all's
+    one.close()
+    ws.fill_(0xFF)
+    y = torch.full_like(x, 9.0)
+    zds.zds_newton_schulz(plan, x, y, ws)
+    for k in (0, 15, 16, 23):
+        o, r, c = mats[k]
+        g = x[o:o + r * c].view(r, c).double()
+        g = g / (g.norm() + 1e-7)
+        for _ in range(5):
+            a = g @ g.T.contiguous()
+            g = 3.4445 * g + (-4.7750 * a + 2.0315 * (a @ a)) @ g
+        assert ((y[o:o + r * c].view(r, c).double() - g).norm() / g.norm()).item() <= tol, k
+        assert (y[o + r * c:o + r * c + 8] == 9).all()
+    again = torch.full_like(x, 9.0)
+    zds.zds_newton_schulz(plan, x, again, ws)
+    assert torch.equal(again, y)
+    plan.close()
