@@ -66,3 +66,47 @@ def test_a_set_of_two_groups(dtype, tol):
     zds.zds_newton_schulz(plan, x, again, ws)
     assert torch.equal(again, y)
     plan.close()
+
+
+def test_a_muon_rank_is_saved_and_resumed(tmp_path):
+    """Three steps, a save, a load into fresh buffers and two more end on the
+    bits of five straight; the merged file holds every tensor."""
+    shapes = [(96, 160), (200, 72), (64, 64), (777,), (5000,)]
+    numels = [torch.Size(s).numel() for s in shapes]
+    offs, n = zds.zds_flat_layout(numels, 64)
+    offs, split = list(offs), offs[3]
+    mats = [(o, *s) for o, s in zip(offs, shapes[:3])]
+    g = torch.Generator("cuda").manual_seed(6)
+    grads = [torch.empty(n, device="cuda").normal_(0, 1e-2, generator=g).bfloat16() for _ in range(5)]
+    start = torch.empty(n, device="cuda").normal_(0, 0.02, generator=g)
+    for x in grads + [start]:                            # the layout's padding is zero
+        for o, k, e in zip(offs, numels, offs[1:] + [n]):
+            x[o + k:e] = 0
+
+    def fresh():
+        st = MuonStep(n, split, mats, muon=zds.muon_hparams(lr=1e-2, scale="rms"))
+        p, m, v = start.clone(), torch.zeros(n, device="cuda"), torch.zeros(n, device="cuda")
+        return st, p, m, v, torch.zeros(n, dtype=torch.bfloat16, device="cuda")
+
+    def run(st, p, m, v, out, some):
+        for x in some:
+            st.step(x, p, m[:split], m[split:], v[split:], out)
+
+    straight = fresh()
+    run(*straight, grads)
+    first = fresh()
+    run(*first, grads[:3])
+    meta, path = zds.checkpoint_meta(numels, 1, 0, 64), str(tmp_path / "rank0.zckpt")
+    zds.zds_checkpoint_save(path, meta, numels, first[1], first[2], first[3], first[0].base.state)
+    second = fresh()
+    zds.zds_checkpoint_load(path, meta, numels, second[1], second[2], second[3], second[0].base.state)
+    assert second[0].read_state().t == 3
+    run(*second, grads[3:])
+    torch.cuda.synchronize()
+    for a, b in zip(straight[1:], second[1:]):
+        assert torch.equal(a, b)
+    assert second[0].read_state().t == straight[0].read_state().t == 5
+    for section, whole in ((0, first[1]), (1, first[2])):
+        parts = zds.split_consolidated(zds.zds_consolidate_fp32([path], section), numels)
+        for o, k, part in zip(offs, numels, parts):
+            assert torch.equal(torch.from_numpy(part), whole[o:o + k].cpu())

@@ -102,7 +102,12 @@ class MuonStep:
 
     matrices: [(flat offset, rows, cols)], all inside [0, split); elements of
     that range outside them (padding) are not updated. A split at a multiple
-    of 64 keeps every slice aligned."""
+    of 64 keeps every slice aligned.
+
+    Checkpoints take three sections of n elements: give the momentum and
+    exp_avg one buffer m (m[:split], m[split:]) and exp_avg_sq the end of
+    another (v[split:], zeros in front), and save and load master, m, v and
+    base.state, as of a world of one, since the rank's tensors are whole."""
 
     def __init__(self, n, split, matrices, hp=None, muon=None, scaler=None, max_norm=1.0, accum_steps=1, ns_steps=5,
                  t0=0, beta1_pow0=1.0, beta2_pow0=1.0, update_dtype=None, device="cuda", stream=None):
