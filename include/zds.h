@@ -550,7 +550,7 @@ int64_t zds_matrix_plan_span(const zds_matrix_plan *plan);
  *             is refused: a momentum below its range would be lost.
  * The arrays must not overlap, but update may be grads if both have one dtype
  * size.
- * 6 B read + 4 B written per element and the update's size. */
+ * Per element the grad's size + 4 B read, 4 B + the update's size written. */
 zds_status zds_muon_momentum(const zds_muon_hparams *hp, const void *grads, zds_dtype grad_dtype, float *momentum,
                              void *update, zds_dtype update_dtype, int64_t n,
                              const zds_step_scalars *scalars_dev, void *stream);

@@ -11,6 +11,8 @@ The fields that decide one rank's optimizer step are read here; the others
                             ("aspect", "rms" or "none") -> zds_muon_hparams for
                             the matrices; betas, eps, weight_decay for the other
                             tensors' AdamW; lr for both, or muon_lr and adam_lr
+                            (with any ZeRO stage the matrices are dealt out whole:
+                            MuonStep; the updates are bf16)
   fp16.enabled + loss_scale 0 -> dynamic scaler with loss_scale_window,
                             initial_scale_power, hysteresis, min_loss_scale;
                             > 0 -> that static scale; fp16 params
