@@ -110,3 +110,32 @@ def test_a_muon_rank_is_saved_and_resumed(tmp_path):
         parts = zds.split_consolidated(zds.zds_consolidate_fp32([path], section), numels)
         for o, k, part in zip(offs, numels, parts):
             assert torch.equal(torch.from_numpy(part), whole[o:o + k].cpu())
+
+
+def test_a_step_on_another_stream_than_the_current_one():
+    """Built while the current stream is busy and run on one of the caller's at
+    once: nothing that the construction left on the current stream comes later."""
+    n, split = 200 * 72 + 3000, 200 * 72
+    g = torch.randn(n, generator=torch.Generator().manual_seed(9)).bfloat16().cuda()
+    start = torch.randn(n, generator=torch.Generator().manual_seed(10)).cuda()
+
+    def run(stream, busy):
+        a = [g, start.clone(), torch.zeros(split, device="cuda"), torch.zeros(n - split, device="cuda"),
+             torch.zeros(n - split, device="cuda"), torch.zeros(n, dtype=torch.bfloat16, device="cuda")]
+        torch.cuda.synchronize()
+        if busy:
+            x = torch.ones(4096, 4096, device="cuda")
+            for _ in range(20):
+                x = x @ x * 1e-4
+        st = MuonStep(n, split, [(0, 200, 72)], stream=stream)
+        for _ in range(2):
+            st.step(*a, stream=stream)
+        torch.cuda.synchronize()
+        return st, a
+
+    want, a = run(None, False)
+    got, b = run(torch.cuda.Stream(), True)
+    for x, y in zip(a, b):
+        assert torch.equal(x, y)
+    assert torch.equal(got.update, want.update) and got.update.abs().max() > 0
+    assert got.read_state().t == want.read_state().t == 2

@@ -25,6 +25,9 @@ class ShardStep:
         self.state = zds.new_state(device)
         self.scalars = zds.new_scalars(device)
         self.ws = zds.new_workspace(n, device)
+        if stream is not None:  # the buffers were cleared on the current stream
+            import torch
+            torch.cuda.current_stream(device).synchronize()
         zds.zds_step_state_init(self.state, self.cfg, t0, beta1_pow0, beta2_pow0, stream)
 
     @classmethod
@@ -121,7 +124,7 @@ class MuonStep:
         self.muon = muon if muon is not None else zds.muon_hparams()
         self.base = ShardStep(n, hp, scaler, max_norm, accum_steps, t0, beta1_pow0, beta2_pow0, device, stream)
         dtype = torch.bfloat16 if update_dtype is None else update_dtype
-        self.update = torch.zeros(split, dtype=dtype, device=device)
+        self.update = torch.empty(split, dtype=dtype, device=device)  # every step writes all of it first
         self.ws = zds.new_newton_schulz_workspace(self.plan, dtype, device)
 
     @classmethod
