@@ -582,9 +582,11 @@ size_t zds_newton_schulz_workspace_bytes(const zds_matrix_plan *plan, zds_dtype 
  * (2-norm) of the default five steps is 1.0 to 1.35 times that rounding's. Steps
  * that start steeper or go on longer can double it (eight default ones).
  * FP32: operands are two fp16 numbers (22 bits) and three products replace one.
- * Over many matrices the error is at most twice that of an fp32 evaluation
- * (2 x 2: 1.6 times, 16 x 17: 1.03, 24 x 3000: 1.3), and with more rows less
- * than that (128 x 128: half of it, 1500 x 2000: a third).
+ * With up to 64 rows the error over many matrices is at most twice that of an
+ * fp32 evaluation (2 x 2: 1.6 times, 16 x 17: 1.03, 24 x 3000: 1.3), with long
+ * rows more, as the matrix instructions lose a little in each of n / 32
+ * additions (32 x 30000: 2.5 times, 32 x 130000: 3.6). With more rows it is less
+ * than an fp32 evaluation's (128 x 128: half of it, 1500 x 2000: a third).
  * A matrix with an infinity or NaN becomes NaN; the others are not affected. A
  * zero matrix stays zero. Entries of the result below 2^-24 may become zero. */
 zds_status zds_newton_schulz(const zds_matrix_plan *plan, const void *src, void *dst, zds_dtype dtype,
