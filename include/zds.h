@@ -605,6 +605,172 @@ zds_status zds_muon_apply(const zds_muon_hparams *hp, const zds_matrix_plan *pla
                           zds_dtype update_dtype, float *master, void *params_out, zds_dtype param_dtype,
                           const zds_step_scalars *scalars_dev, void *stream);
 
+/* ---------------------------------------------------------------------------
+ * Random numbers from a counter: nothing random is stored or sent. One call
+ * of the generator is Philox4x32-10 (Salmon, Moraes, Dror, Shaw: "Parallel
+ * random numbers: as easy as 1, 2, 3", 2011): four 32-bit words that are a
+ * function of
+ *   key      the caller's 64-bit seed
+ *   counter  (call index, low and high 32 bits; steps_seen of the step state;
+ *            stream: 1 for rounding, 2 for dropout)
+ * steps_seen is read on the device and advances with every
+ * zds_loss_scaler_update, so a captured step draws new numbers on each replay,
+ * a resumed run those the uninterrupted run would have drawn, and every rank
+ * the same. `first` is the flat index of a call's element 0 (the shard's lo):
+ * numbers follow the flat element, not the partition.
+ * ------------------------------------------------------------------------- */
+
+/* The four words of one call, computed on the host (out4: 4 entries). */
+zds_status zds_random_words_host(uint64_t seed, uint64_t call, uint32_t steps_seen, uint32_t stream, uint32_t *out4);
+
+/* ---------------------------------------------------------------------------
+ * Moments in fewer bits: the state that AdamW keeps between steps, quantised
+ * as a step writes it and read back by the next one. A first moment takes
+ * 1 + 1/32 B in E4M3 and a second moment as much in UE5M3 (2 B in BF16), where
+ * fp32 takes 4.
+ *
+ * E4M3 and UE5M3: blocks of 32 consecutive elements (the last may be shorter)
+ * share one exponent byte s, an element has an 8-bit code: E4M3 a sign, 4
+ * exponent and 3 mantissa bits; UE5M3, for values >= 0, 5 exponent and 3
+ * mantissa bits. With F = 15 (E4M3) or 31 (UE5M3) a code's magnitude bits,
+ * taken as the top exponent and mantissa bits of an fp32 number z (code << 20),
+ * stand for z * 2^(s - F). The exponent field of 0 is the linear range below.
+ *   s       of the block's largest magnitude A: the fp32 exponent field of A,
+ *           plus one if A's mantissa is over 1.75 (the codes' largest value is
+ *           1.75 * 2^(s - 127)); at most 255; UE5M3: at least 11
+ *   code    of a value x: z = |x| * 2^(F - s) in fp32 (exact, but for what is
+ *           2^-20 of a code's least step), then the bits of z rounded to their
+ *           top 12: to nearest even, or at random: (bits + 16 r + 8) >> 20
+ *   top code (0x7f with either sign, 0xff): an infinity, a NaN, or for UE5M3 a
+ *           negative value; it reads back as NaN. Its block's s is 255 for an
+ *           infinity or NaN, which leaves little of the other values
+ *   UE5M3   a value > 0 never gets code 0: a second moment that is not 0 does
+ *           not read back as 0, which would divide by eps alone
+ * What was read back and is quantised again (to nearest or at random) reads
+ * back as the same values. Magnitudes above 1.875 * 2^127 may read back
+ * as infinity.
+ * BF16: the value's top 16 bits, rounded to nearest even or at random:
+ * (bits + r) >> 16; a value other than 0 does not become 0. Infinities and
+ * NaN stay what they are.
+ * r is the element's 16 random bits: with f = first + i, half f % 2 (0: the
+ * low one) of word (f / 2) % 4 of call f / 8 of stream 1. E4M3 takes them as
+ * they are, UE5M3 and BF16 with the two bytes exchanged, so that both moments
+ * of an element are rounded on (all but) independent bits. A random rounding
+ * is right on average to 2^-17 of a code's step (BF16: exactly).
+ *
+ * Why at random, and what it costs: an exponential average with factor beta
+ * changes by about 1 - beta of its value in a step; to nearest, a code whose
+ * half step is larger than that never moves. At random it moves on average by
+ * the right amount, and the roundings add noise of a relative variance of
+ * about 2^-9.5 / (2 (1 - beta)) for 8 bits, 2^-17.5 / (2 (1 - beta)) for BF16:
+ *   beta   0.9: 0.7 %, 0.95: 1.4 % (a deviation of 12 % of v, 6 % of its root),
+ *          0.98: 3.5 %, 0.999: 70 % (8 bits), 0.3 % (BF16)
+ * so a second moment in 8 bits is for beta2 up to about 0.98, BF16 beyond.
+ * ------------------------------------------------------------------------- */
+
+typedef enum zds_state_format {
+  ZDS_STATE_E4M3 = 0,
+  ZDS_STATE_UE5M3 = 1,
+  ZDS_STATE_BF16 = 2,
+  ZDS_STATE_RANGE_MIN_ = -2147483647 - 1,
+  ZDS_STATE_RANGE_MAX_ = 2147483647
+} zds_state_format;
+
+typedef enum zds_rounding {
+  ZDS_ROUND_NEAREST = 0,
+  ZDS_ROUND_RANDOM = 1,
+  ZDS_ROUND_RANGE_MIN_ = -2147483647 - 1,
+  ZDS_ROUND_RANGE_MAX_ = 2147483647
+} zds_rounding;
+
+/* Quantises n fp32 values (a running state that is to be kept in fewer bits,
+ * or one read from a checkpoint).
+ *   src    device fp32, n elements (n below 2^40)
+ *   codes  device, n bytes (n 16-bit elements for BF16), written
+ *   exps   device, ceil(n / 32) bytes, written; NULL for BF16
+ *   seed, first, state_dev  used by ZDS_ROUND_RANDOM only (state_dev may be
+ *          NULL otherwise); first >= 0, a multiple of 32
+ * The arrays must not overlap. Per element 4 B read, a code written. */
+zds_status zds_state_quantise(const float *src, int64_t n, zds_state_format format, zds_rounding rounding,
+                              uint64_t seed, int64_t first, const zds_step_state *state_dev, void *codes,
+                              uint8_t *exps, void *stream);
+
+/* Reads n values back: dst (device, FP32 or BF16) receives what the codes
+ * stand for, exactly in FP32, rounded to nearest even in BF16 (exact there too
+ * for 8-bit codes of magnitudes from 2^-126). The arrays must not overlap. */
+zds_status zds_state_dequantise(const void *codes, const uint8_t *exps, int64_t n, zds_state_format format, void *dst,
+                                zds_dtype dst_dtype, void *stream);
+
+/* zds_adam_step on moments in fewer bits: reads both back, applies the same
+ * update, and quantises what it writes at random: master and params_out are
+ * those of zds_adam_step on the state that zds_state_dequantise gives, and the
+ * codes those of zds_state_quantise (ZDS_ROUND_RANDOM, the same seed and
+ * first) on the moments it leaves, bit for bit.
+ *   exp_avg       device, n codes of E4M3, with exp_avg_exps
+ *   exp_avg_sq    device, n codes of sq_format (UE5M3 with exp_avg_sq_exps, or
+ *                 BF16 with NULL)
+ *   seed, first   as for zds_state_quantise (first >= 0, a multiple of 32)
+ * Other arguments, and the skip on overflow, as for zds_adam_step. No two of
+ * the arrays may overlap, but params_out may be the grads if both are 16 bits.
+ * 16.1 B per element (16-bit grads, UE5M3), where zds_adam_step moves 28. */
+zds_status zds_adam_step_q8(const zds_adamw_hparams *hp, const void *grads, zds_dtype grad_dtype, float *master,
+                            void *exp_avg, uint8_t *exp_avg_exps, void *exp_avg_sq, zds_state_format sq_format,
+                            uint8_t *exp_avg_sq_exps, void *params_out, zds_dtype param_dtype, int64_t n,
+                            uint64_t seed, int64_t first, zds_step_scalars *scalars_dev,
+                            const zds_step_state *state_dev, void *stream);
+
+/* ---------------------------------------------------------------------------
+ * Gradient dropout: the two ends of an exchange in which every group of
+ * `ratio` consecutive elements sends one, chosen at random by the counter
+ * above, so that neither a mask nor places are stored or sent: all ranks
+ * choose the same elements (same seed, first and steps_seen), and messages of
+ * ceil(n / ratio) values can be summed by a plain all-reduce or
+ * reduce-scatter. What a rank does not send it keeps in an fp32 error buffer
+ * and adds to its next gradient.
+ * ratio is a power of two from 2 to 256. With j = first / ratio + g, the kept
+ * place of local group g is the top log2(ratio) bits of byte j % 16 (byte b is
+ * bits 8 (b % 4) and up of word b / 4) of call j / 16 of stream 2. A last
+ * group that is not whole keeps nothing where its place lies past the end: it
+ * sends 0.
+ * ------------------------------------------------------------------------- */
+
+/*   x        device, n elements of x_dtype: the rank's gradient under the loss
+ *            scale S (state_dev->scale)
+ *   error    device fp32, n elements, updated, in units without the loss scale
+ *            (so that it outlives a change of S); or NULL
+ *   values   device, ceil(n / ratio) elements of value_dtype, written
+ *   scalars_dev  may be NULL; else nothing is taken from x when its overflow
+ *            flag is set: error stays as it is and every value is NaN, so that
+ *            the sum of the messages overflows on every rank and all of them
+ *            skip the step
+ * With error: c = x + S * error (fp32, one rounding per operation);
+ *   kept:     value = round_nearest_even(c), error = (c - value) * (1 / S); a
+ *             value that is not finite (fp16) leaves error = c * (1 / S)
+ *   not kept: error = c * (1 / S)
+ * Without: value = round_nearest_even(ratio * x) of the kept element, which is
+ * right on average.
+ * A step that is skipped after the exchange loses what it sent. No two arrays
+ * may overlap. first >= 0, a multiple of ratio; n below 2^40. */
+zds_status zds_dropout_compress(const void *x, zds_dtype x_dtype, float *error, int64_t n, int32_t ratio,
+                                uint64_t seed, int64_t first, const zds_step_scalars *scalars_dev,
+                                const zds_step_state *state_dev, void *values, zds_dtype value_dtype, void *stream);
+
+/* Writes num_peers (1..16) messages into a gradient of n elements: with t the
+ * fp32 sum of the peers' values of a group, in peer order, its kept element
+ * becomes t and the others 0 (ZDS_OVERWRITE), or t is added to it, last, and
+ * the others are left alone (ZDS_ACCUMULATE; only kept elements are read and
+ * written). dst: device, FP32 or the values' type, rounded once. No mean is
+ * taken: to average over peers, give the step accum_steps = K * N. A message
+ * that was all-reduced is one peer; the overflow flag and norm of an
+ * overwritten gradient are those of the summed message, so
+ * zds_overflow_and_norm over the ceil(n / ratio) values (or
+ * zds_reduce_peer_slices_norm of the messages) saves a pass over the gradient.
+ * Must be called before the zds_loss_scaler_update that ends the step whose
+ * zds_dropout_compress made the values. dst must not overlap a message. */
+zds_status zds_dropout_decompress(const void *const *peer_values, int32_t num_peers, zds_dtype value_dtype, int64_t n,
+                                  int32_t ratio, uint64_t seed, int64_t first, const zds_step_state *state_dev,
+                                  void *dst, zds_dtype dst_dtype, zds_accum_mode mode, void *stream);
+
 /* Row a3. Initialise the device step state from cfg with Adam step count t0
  * and powers beta1^t0, beta2^t0 (1, 1 for a fresh optimizer). */
 zds_status zds_step_state_init(zds_step_state *state_dev, const zds_scaler_config *cfg, int64_t t0,

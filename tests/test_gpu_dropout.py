@@ -1,0 +1,254 @@
+"""Gradient dropout on the GPU against the plain definitions, bit for bit: a
+message and an error are one or two fp32 operations from the inputs."""
+
+import numpy as np
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+if not torch.cuda.is_available():
+    pytest.skip("no GPU", allow_module_level=True)
+
+from oracle import quantised as Q  # noqa: E402
+from oracle.zero_step import narrow, widen  # noqa: E402
+from tests.test_gpu_quantised import scalars, state  # noqa: E402
+from tests.util import to_dev, to_host  # noqa: E402
+from zero_sharded_mixed_tensor_amd import zds  # noqa: E402
+from zero_sharded_mixed_tensor_amd.step import DropoutExchange, QuantisedStep, ShardStep  # noqa: E402
+
+TDT = {"fp16": torch.float16, "bf16": torch.bfloat16, "fp32": torch.float32}
+SEED = 0xC0FFEE1234567
+
+
+def host(x32, dtype):
+    return x32.astype(np.float32) if dtype == "fp32" else narrow(x32.astype(np.float32), dtype)
+
+
+def same(got, want, dtype):
+    """Bit for bit; NaN is NaN."""
+    nan = np.isnan(widen(want, dtype))
+    assert np.array_equal(np.isnan(widen(got, dtype)), nan)
+    view = (lambda a: a.view(np.uint32)) if dtype == "fp32" else (lambda a: a)
+    assert np.array_equal(view(got)[~nan], view(want)[~nan])
+
+
+def shifted(a, dtype, pad, room=0):
+    return to_dev(np.concatenate([a[:1].repeat(pad), a, a[:1].repeat(room)]), dtype)[pad:]
+
+
+@pytest.mark.parametrize("ratio", [2, 4, 8, 64, 256])
+@pytest.mark.parametrize("xdt,vdt", [("fp16", "fp16"), ("bf16", "bf16"), ("bf16", "fp32"), ("fp32", "fp32"),
+                                     ("fp32", "fp16")])
+@pytest.mark.parametrize("n,pad", [(1, 0), (5, 0), (257, 0), (4096, 0), (4097, 1), (50003, 0), (50003, 3)])
+def test_compress_bit_exact(ratio, xdt, vdt, n, pad):
+    rng = np.random.default_rng(n + ratio)
+    x = host(rng.standard_normal(n) * 64, xdt)
+    e = (rng.standard_normal(n) * 0.3).astype(np.float32)
+    if n > 1000:
+        e[rng.integers(0, n, 40)] *= np.float32(1e5)         # past fp16's range
+    first, steps, scale = ratio * (16 * 999 + n % 16), 5, 128.0
+    for feedback in (True, False):
+        err = e if feedback else None
+        want, werr = Q.dropout_compress(x, xdt, err, ratio, SEED, first, steps, scale, vdt)
+        dx = shifted(x, xdt, pad)
+        de = shifted(e, "fp32", pad, 8) if feedback else None
+        dv = torch.full((want.size + 8,), 7.0, dtype=TDT[vdt], device="cuda")
+        zds.zds_dropout_compress(dx, de, ratio, dv, SEED, first, state(steps, scale), scalars(), n=n)
+        same(to_host(dv)[:want.size], want, vdt)
+        assert (dv[want.size:] == 7.0).all()
+        if feedback:
+            same(to_host(de)[:n], werr, "fp32")
+            assert (to_host(de)[n:] == e[0]).all()
+
+
+@pytest.mark.parametrize("ratio", [2, 4, 16, 256])
+@pytest.mark.parametrize("vdt,odt", [("bf16", "fp32"), ("bf16", "bf16"), ("fp16", "fp16"), ("fp32", "fp32")])
+@pytest.mark.parametrize("n,pad,peers", [(1, 0, 1), (5, 0, 3), (4096, 0, 2), (4099, 1, 16), (50003, 0, 8), (50003, 2, 1)])
+def test_decompress_bit_exact(ratio, vdt, odt, n, pad, peers):
+    rng = np.random.default_rng(n + ratio)
+    groups = -(-n // ratio)
+    msgs = [host(rng.standard_normal(groups), vdt) for _ in range(peers)]
+    dst = host(rng.standard_normal(n), odt)
+    first, steps = ratio * (77 + n % 16), 9
+    dev = [to_dev(m, vdt) for m in msgs]
+    for mode in (zds.ZDS_OVERWRITE, zds.ZDS_ACCUMULATE):
+        want = Q.dropout_decompress(msgs, vdt, n, ratio, SEED, first, steps, dst, odt, mode == zds.ZDS_ACCUMULATE)
+        dd = shifted(dst, odt, pad, 8)
+        zds.zds_dropout_decompress(dev, ratio, dd, SEED, first, state(steps), mode, n=n)
+        got = to_host(dd)
+        same(got[:n], want, odt)
+        same(got[n:], dst[:1].repeat(8), odt)
+
+
+def test_infinities_and_nan():
+    """Where the caller does not look first, they stay where they are: a kept
+    one is sent, another one is kept in the error."""
+    n, ratio = 64, 8
+    x = np.ones(n, np.float32)
+    x[::3], x[1] = np.inf, np.nan
+    e = np.zeros(n, np.float32)
+    want, werr = Q.dropout_compress(x, "fp32", e, ratio, 1, 0, 0, 1.0, "fp32")
+    de, dv = to_dev(e, "fp32"), torch.zeros(8, device="cuda")
+    zds.zds_dropout_compress(to_dev(x, "fp32"), de, ratio, dv, 1, 0, state())
+    same(to_host(dv), want, "fp32")
+    same(to_host(de), werr, "fp32")
+
+
+@pytest.mark.parametrize("vdt", ["fp16", "bf16", "fp32"])
+def test_overflow_poisons_the_message(vdt):
+    n, ratio = 10007, 4
+    e = np.random.default_rng(0).standard_normal(n).astype(np.float32)
+    x = torch.ones(n, dtype=torch.float16, device="cuda")
+    for feedback in (True, False):
+        de = to_dev(e, "fp32") if feedback else None
+        dv = torch.zeros(2502 + 3, dtype=TDT[vdt], device="cuda")
+        zds.zds_dropout_compress(x, de, ratio, dv, 1, 0, state(), scalars(overflow=1))
+        assert torch.isnan(dv[:2502]).all() and (dv[2502:] == 0).all()
+        assert not feedback or np.array_equal(to_host(de), e)
+
+
+def test_nothing_is_lost():
+    """Every element is either sent or still in the error, exactly: over the
+    steps the decoded messages and the last error add up to the inputs. Whole
+    numbers below 2^24 in all, so fp32 sums are exact."""
+    n, ratio = 3000, 8
+    rng = np.random.default_rng(4)
+    err, total, sent = torch.zeros(n, device="cuda"), torch.zeros(n, device="cuda"), torch.zeros(n, device="cuda")
+    values = torch.empty(375, device="cuda")
+    seen = torch.zeros(n, device="cuda")
+    for k in range(64):
+        x = to_dev(rng.integers(-100, 101, n).astype(np.float32), "fp32")
+        total += x
+        zds.zds_dropout_compress(x, err, ratio, values, 3, 0, state(k))
+        zds.zds_dropout_decompress([values], ratio, sent, 3, 0, state(k), zds.ZDS_ACCUMULATE)
+        one = torch.empty(n, device="cuda")
+        zds.zds_dropout_decompress([torch.ones_like(values)], ratio, one, 3, 0, state(k))
+        seen += one
+        assert (one.view(-1, ratio).sum(1) == 1).all()
+    assert torch.equal(total, sent + err)
+    # an element is kept in 64 of 8 * 64 draws: 8 on average, a deviation of 2.6
+    assert seen.sum() == 375 * 64 and seen.max() <= 8 + 6 * 2.7
+
+
+def test_offsets_past_32_bits():
+    n, ratio = (1 << 32) + 4133, 16
+    a = n - n % 4096 - 8192
+    x = torch.empty(n, dtype=torch.bfloat16, device="cuda").normal_()
+    err = torch.zeros(n, device="cuda")
+    v, v2 = torch.empty(-(-n // ratio), device="cuda"), torch.empty(-(-(n - a) // ratio), device="cuda")
+    zds.zds_dropout_compress(x, err, ratio, v, 3, 0, state(2))
+    e2 = torch.zeros(n - a, device="cuda")
+    zds.zds_dropout_compress(x[a:].clone(), e2, ratio, v2, 3, a, state(2))
+    assert torch.equal(v[a // ratio:], v2) and torch.equal(err[a:], e2)
+    zds.zds_dropout_decompress([v], ratio, err, 3, 0, state(2))
+    zds.zds_dropout_decompress([v2], ratio, e2, 3, a, state(2))
+    assert torch.equal(err[a:], e2) and int((e2 != 0).sum()) <= v2.numel()
+    zds.zds_dropout_decompress([v], ratio, err, 3, 0, state(2), zds.ZDS_ACCUMULATE)
+    zds.zds_dropout_decompress([v2], ratio, e2, 3, a, state(2), zds.ZDS_ACCUMULATE)
+    assert torch.equal(err[a:], e2)
+    # without feedback
+    zds.zds_dropout_compress(x, None, ratio, v, 3, 0, state(2))
+    zds.zds_dropout_compress(x[a:].clone(), None, ratio, v2, 3, a, state(2))
+    assert torch.equal(v[a // ratio:], v2)
+
+
+def test_exchange_of_two_ranks_with_quantised_moments():
+    """Two ranks' whole steps as they would run: each compresses its own grads,
+    the messages are summed, both decode, step and update their loss scale;
+    one rank's overflow at step 3 is skipped by both and costs no rank its
+    error; eager, and one rank's step replayed from a graph."""
+    n, ratio, world = 70003, 4, 2
+
+    def rank():
+        st = QuantisedStep(n, zds.hparams(lr=1e-3, beta2=0.95), zds.scaler_config(initial_scale_power=8), max_norm=1.0,
+                           accum_steps=world, seed=9, first=0)
+        return dict(st=st, ex=DropoutExchange(n, ratio, torch.bfloat16, seed=21, first=0),
+                    master=torch.full((n,), 0.01, device="cuda"), mv=st.new_moments(),
+                    params=torch.zeros(n, dtype=torch.float16, device="cuda"), g=torch.empty(n, device="cuda"),
+                    x=torch.zeros(n, dtype=torch.float16, device="cuda"))
+
+    def grads(k, r):
+        g = torch.Generator(device="cuda").manual_seed(1000 * k + r)
+        x = torch.randn(n, device="cuda", generator=g).mul_(0.3).half()
+        if k == 3 and r == 1:
+            x[123] = float("inf")
+        return x
+
+    def send(q):
+        q["st"].norm(q["x"])
+        q["ex"].compress(q["x"], q["st"])
+
+    def take(q, total):
+        q["ex"].norm(total, q["st"])
+        q["ex"].decompress([total], q["g"], q["st"])
+        q["st"].adam(q["g"], q["master"], *q["mv"], q["params"])
+        q["st"].scaler()
+
+    total = torch.empty(-(-n // ratio), device="cuda")
+    ranks = [rank(), rank()]
+    scales, log = [], []
+    for k in range(8):
+        scales.append(ranks[0]["st"].read_state().scale)
+        for r, q in enumerate(ranks):
+            q["x"].copy_(grads(k, r))
+            send(q)
+        total.copy_(ranks[0]["ex"].values.float() + ranks[1]["ex"].values.float())
+        errors = [q["ex"].error.clone() for q in ranks]
+        for q in ranks:
+            take(q, total)
+        log.append((ranks[0]["master"].clone(), ranks[0]["ex"].values.clone(), ranks[1]["ex"].values.clone()))
+        # the norm of the message is the gradient's
+        sc = zds.new_scalars()
+        zds.zds_overflow_and_norm(ranks[0]["g"], world, 1.0, ranks[0]["st"].state, sc, ranks[0]["st"].ws)
+        a, b = zds.read_scalars(sc), ranks[0]["st"].read_scalars()
+        assert a.overflow == b.overflow == (1 if k == 3 else 0)
+        if k != 3:
+            assert abs(a.sumsq - b.sumsq) <= 1e-12 * a.sumsq
+        for q, before in zip(ranks, errors):
+            assert torch.equal(q["ex"].error, before) and torch.isfinite(q["ex"].error).all()
+    for name in ("master", "params"):
+        assert torch.equal(ranks[0][name], ranks[1][name])
+    assert bytes(ranks[0]["st"].read_state()) == bytes(ranks[1]["st"].read_state())
+    assert ranks[0]["st"].read_state().steps_skipped == 1 and scales[4] == scales[3] / 2
+    assert torch.equal(log[3][0], log[2][0]) and not torch.equal(log[4][0], log[3][0])
+
+    # rank 0 from a graph: its two halves around the exchange
+    q = rank()
+    peer = torch.empty_like(ranks[1]["ex"].values)
+    other = torch.empty(-(-n // ratio), device="cuda")
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        send(q)
+        other.copy_(q["ex"].values.float() + peer.float())
+        take(q, other)
+    for k in range(8):
+        q["x"].copy_(grads(k, 0))
+        peer.copy_(log[k][2])
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(q["master"], log[k][0]), k
+
+
+def test_dense_step_after_an_exchange():
+    """The decoded gradient feeds the fp32 step, too; without feedback the
+    message is right on average: over 2048 steps of one gradient the mean of
+    the decoded ones is the gradient, to five deviations of the mean (an
+    element is x * ratio in one of ratio steps: x^2 (ratio - 1) a step)."""
+    n, ratio, steps = 1000, 4, 2048
+    x = torch.linspace(-1, 1, n, device="cuda")
+    ex = DropoutExchange(n, ratio, torch.float32, seed=4, feedback=False)
+    mean = torch.zeros(n, dtype=torch.float64, device="cuda")
+    g = torch.empty(n, device="cuda")
+    st = ShardStep(n, zds.hparams(lr=0.0), zds.scaler_config(dynamic=False), max_norm=0.0)
+    p, m, v = (torch.zeros(n, device="cuda") for _ in range(3))
+    for _ in range(steps):
+        ex.compress(x, st)
+        ex.norm(ex.values, st)
+        ex.decompress([ex.values], g, st)
+        st.adam(g, p, m, v, None)
+        st.scaler()
+        mean += g
+    off = (mean / steps - x).abs()
+    assert (off <= 5 * x.abs() * ((ratio - 1) / steps) ** 0.5 + 1e-6).all()

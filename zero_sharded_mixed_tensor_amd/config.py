@@ -13,6 +13,9 @@ The fields that decide one rank's optimizer step are read here; the others
                             tensors' AdamW; lr for both, or muon_lr and adam_lr
                             (with any ZeRO stage the matrices are dealt out whole:
                             MuonStep; the updates are bf16)
+  optimizer.type AdamW8bit (or Adam8bit)  AdamW's parameters; the moments are
+                            kept in fewer bits (QuantisedStep). second_moment:
+                            "8bit", "bf16", or "auto": 8 bits up to beta2 0.98
   fp16.enabled + loss_scale 0 -> dynamic scaler with loss_scale_window,
                             initial_scale_power, hysteresis, min_loss_scale;
                             > 0 -> that static scale; fp16 params
@@ -84,6 +87,7 @@ class StepConfig:
     stage: int
     offload: bool
     muon: Optional[MuonConfig] = None  # optimizer.type Muon: the matrices' settings
+    second_moment: Optional[str] = None  # optimizer.type AdamW8bit: "8bit" or "bf16"
 
     def muon_hparams(self):
         from . import zds
@@ -177,9 +181,9 @@ def from_ds_config(cfg, world=1):
     opt = cfg.get("optimizer") or {"type": "AdamW", "params": {}}
     typ = str(opt.get("type", "AdamW"))
     p = opt.get("params") or {}
-    if typ.lower() == "adam" and p.get("adam_w_mode", True) is False and p.get("weight_decay", 0) not in (0, 0.0):
+    if typ.lower() in ("adam", "adam8bit") and p.get("adam_w_mode", True) is False and p.get("weight_decay", 0) not in (0, 0.0):
         raise ConfigError("Adam with L2-coupled weight decay is not this step's update (AdamW)")
-    if typ.lower() not in ("adamw", "adam", "muon"):
+    if typ.lower() not in ("adamw", "adam", "adamw8bit", "adam8bit", "muon"):
         raise ConfigError("optimizer %r: the step implements AdamW and Muon" % typ)
     betas = p.get("betas", ADAMW_DEFAULTS["betas"])
     if _is_auto(betas):
@@ -196,6 +200,13 @@ def from_ds_config(cfg, world=1):
     if typ.lower() == "muon":
         muon = _muon(p, lr)
         lr = _num(p, "adam_lr", lr)
+    second = None
+    if typ.lower() in ("adamw8bit", "adam8bit"):
+        second = p.get("second_moment")
+        if _is_auto(second):  # the roundings' noise in v grows with 1 / (1 - beta2)
+            second = "8bit" if b2 <= 0.98 else "bf16"
+        if second not in ("8bit", "bf16"):
+            raise ConfigError("second_moment must be 8bit or bf16, got %r" % (second,))
     # precision and loss scaling
     fp16, f = _enabled(cfg, "fp16")
     bf16, _ = _enabled(cfg, "bf16")
@@ -231,10 +242,12 @@ def from_ds_config(cfg, world=1):
     offload = str(off.get("device", "none")).lower() == "cpu"
     if offload and muon is not None:
         raise ConfigError("Muon's matrices are updated on the device: offload_optimizer is for AdamW")
+    if offload and second is not None:
+        raise ConfigError("moments in 8 bits are updated on the device: offload_optimizer is for fp32 moments")
     return StepConfig(lr=lr, beta1=b1, beta2=b2, eps=eps, weight_decay=wd, dynamic=dynamic,
                       initial_scale_power=power, window=window, hysteresis=hyst, min_scale=floor,
                       static_scale=static, max_norm=max_norm, accum_steps=k, param_dtype=pdt, stage=stage,
-                      offload=offload, muon=muon)
+                      offload=offload, muon=muon, second_moment=second)
 
 
 def load_ds_config(path, world=1):

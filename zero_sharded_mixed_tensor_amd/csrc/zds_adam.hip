@@ -64,8 +64,7 @@
 // single-wave prep kernel into the caller's step-scalars struct, so the
 // update kernel only loads them. (Deriving them in every block instead, by
 // one wave while its loads are in flight, measured 0.4 % slower.)
-#include "zds_device.h"
-#include "zds_internal.h"
+#include "zds_adam.h"
 
 namespace {
 // Threads per block of the element-wise kernel.
@@ -92,52 +91,6 @@ struct AdamArgs {
   void *out;
   int64_t n;
 };
-
-struct ElemConsts {
-  float b1, b2, omb1, omb2, eps, step_size, decay, gs;
-  double inv_bc2;
-};
-
-// 1 - beta is formed here in fp32, as the step's definition does (one fp32
-// subtraction; exact for beta in [0.5, 1]).
-__device__ __forceinline__ ElemConsts load_consts(const zds_step_scalars *sc) {
-  ElemConsts c;
-  c.b1 = sc->beta1;
-  c.b2 = sc->beta2;
-  c.eps = sc->eps;
-  c.omb1 = 1.0f - c.b1;
-  c.omb2 = 1.0f - c.b2;
-  c.step_size = sc->step_size;
-  c.inv_bc2 = sc->inv_bc2_sqrt;
-  c.decay = sc->decay;
-  c.gs = sc->grad_scale;
-  return c;
-}
-
-// One element, fp32, one rounding per operation, in this order.
-//
-// sqrt(v) / bc2 (bc2 = sqrt(1 - beta2^t) in fp32) is formed as
-// fp32(float64(sqrt(v)) * r) with r = 1 / float64(bc2) correctly rounded.
-// That is the correctly rounded fp32 quotient: r carries a relative error of
-// at most 2^-53 and the float64 product another 2^-53, so the product is
-// within 2^-52 (relatively) of the exact quotient; the exact quotient a/b of
-// two fp32 numbers is never a point halfway between two fp32 numbers (a
-// halfway point times b would need more than 24 significant bits), and lies at
-// least 2^-49 (relatively) away from every such point, because
-// |a - b*M| is a non-zero multiple of the coarser of a's and b*M's
-// granularities. So no rounding boundary separates the product from the
-// exact quotient. Here a = sqrt(v) is 0, NaN, inf or at least 2^-74.5, and
-// the quotient stays in the normal range; bc2 = 0 (beta2 = 1) gives
-// r = inf and the same inf / NaN as the division.
-__device__ __forceinline__ void adam_elem(float x, const ElemConsts &c, float &p, float &m, float &v) {
-  const float g = x * c.gs;
-  m = c.b1 * m + c.omb1 * g;
-  v = c.b2 * v + c.omb2 * (g * g);
-  const float q = static_cast<float>(static_cast<double>(sqrtf(v)) * c.inv_bc2);
-  const float denom = q + c.eps;
-  p = p * c.decay;
-  p = p - c.step_size * (m / denom);
-}
 
 // Scheduling priority of a wave: raised while it issues its loads and stores,
 // lowered for the update.
@@ -455,11 +408,16 @@ static void launch_gd(zds_dtype pdt, bool wo, bool vec, bool vec16, hipStream_t 
   }
 }
 
+zds_status launch_adam_constants(const zds_adamw_hparams &hp, const zds_step_state *state, zds_step_scalars *scalars,
+                                 hipStream_t stream) {
+  hipLaunchKernelGGL(adam_prep_kernel, dim3(1), dim3(64), 0, stream, hp, state, scalars);
+  return check_launch("adam_step constants kernel");
+}
+
 zds_status launch_adam(const zds_adamw_hparams &hp, const void *grads, zds_dtype gdt, float *master,
                        float *m, float *v, void *out, zds_dtype pdt, int64_t n, zds_step_scalars *scalars,
                        const zds_step_state *state, hipStream_t stream) {
-  hipLaunchKernelGGL(adam_prep_kernel, dim3(1), dim3(64), 0, stream, hp, state, scalars);
-  zds_status st = check_launch("adam_step constants kernel");
+  const zds_status st = launch_adam_constants(hp, state, scalars, stream);
   if (st != ZDS_OK) return st;
   const AdamArgs a{scalars, grads, master, m, v, out, n};
   const bool vec = aligned(grads, gdt == ZDS_FP32 ? 16 : 8) && aligned(master, 16) && aligned(m, 16) &&

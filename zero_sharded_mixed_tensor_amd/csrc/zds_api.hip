@@ -498,6 +498,15 @@ extern "C" zds_status zds_overflow_and_norm(const void *grads, zds_dtype dtype, 
                      static_cast<double *>(ws), static_cast<hipStream_t>(stream));
 }
 
+zds_status zds::check_adamw(const char *fn, const zds_adamw_hparams *hp) {
+  if (!hp) return fail(ZDS_EINVAL, "%s: null hparams", fn);
+  if (!(hp->beta1 >= 0.5f && hp->beta1 < 1.0f && hp->beta2 >= 0.5f && hp->beta2 < 1.0f))
+    return fail(ZDS_EINVAL, "%s: betas must lie in [0.5, 1)", fn);
+  if (!(hp->eps > 0.0f) || !(hp->lr >= 0.0f) || !(hp->weight_decay >= 0.0f))
+    return fail(ZDS_EINVAL, "%s: need eps > 0, lr >= 0, weight_decay >= 0", fn);
+  return ZDS_OK;
+}
+
 extern "C" zds_status zds_adam_step(const zds_adamw_hparams *hp, const void *grads, zds_dtype grad_dtype,
                                     float *master, float *exp_avg, float *exp_avg_sq, void *params_out,
                                     zds_dtype param_dtype, int64_t n, zds_step_scalars *scalars_dev,
@@ -509,11 +518,8 @@ extern "C" zds_status zds_adam_step(const zds_adamw_hparams *hp, const void *gra
     return fail(ZDS_EINVAL, "zds_adam_step: param dtype must be fp16 or bf16");
   if (n < 0) return fail(ZDS_EINVAL, "zds_adam_step: n < 0");
   if (n >= (int64_t(1) << 40)) return fail(ZDS_EINVAL, "zds_adam_step: n must be below 2^40");
-  if (!(hp->beta1 >= 0.5f && hp->beta1 < 1.0f && hp->beta2 >= 0.5f && hp->beta2 < 1.0f))
-    return fail(ZDS_EINVAL, "zds_adam_step: betas must lie in [0.5, 1)");
-  if (!(hp->eps > 0.0f) || !(hp->lr >= 0.0f) || !(hp->weight_decay >= 0.0f))
-    return fail(ZDS_EINVAL, "zds_adam_step: need eps > 0, lr >= 0, weight_decay >= 0");
-  if (n == 0) return ZDS_OK;
+  const zds_status st = zds::check_adamw("zds_adam_step", hp);
+  if (st != ZDS_OK || n == 0) return st;
   if (!grads || !master || !exp_avg || !exp_avg_sq || !scalars_dev || !state_dev)
     return fail(ZDS_EINVAL, "zds_adam_step: null pointer");
   if (!aligned(grads, static_cast<uintptr_t>(dtype_size(grad_dtype))) || !aligned(master, 4) ||

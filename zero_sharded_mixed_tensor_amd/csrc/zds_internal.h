@@ -75,9 +75,22 @@ zds_status launch_adam(const zds_adamw_hparams &hp, const void *grads, zds_dtype
                        float *m, float *v, void *out, zds_dtype pdt, int64_t n, zds_step_scalars *scalars,
                        const zds_step_state *state, hipStream_t stream);
 
+// The step's fp32 constants into the scalars struct (one wave).
+zds_status launch_adam_constants(const zds_adamw_hparams &hp, const zds_step_state *state, zds_step_scalars *scalars,
+                                 hipStream_t stream);
+
 zds_status launch_scaler(zds_step_state *state, const zds_step_scalars *scalars, float beta1,
                          float beta2, hipStream_t stream);
 zds_status launch_state_init(zds_step_state *state, const zds_step_state &init, hipStream_t stream);
+
+// Refuses hyperparameters outside AdamW's ranges, for entry point `fn`.
+zds_status check_adamw(const char *fn, const zds_adamw_hparams *hp);
+
+// Whether [a, a + na) and [b, b + nb) share a byte.
+inline bool ranges_meet(const void *a, int64_t na, const void *b, int64_t nb) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return na > 0 && nb > 0 && (x < y ? y - x < static_cast<uintptr_t>(na) : x - y < static_cast<uintptr_t>(nb));
+}
 
 // A dispatch packet counts work-items in 32 bits: a launch must stay below
 // 2^32 of them. Grids are capped here and the kernels loop over the rest.

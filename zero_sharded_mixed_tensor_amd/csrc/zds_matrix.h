@@ -84,12 +84,6 @@ struct zds_matrix_plan {
 };
 
 namespace zds {
-// Whether [a, a + na) and [b, b + nb) share a byte.
-inline bool ranges_meet(const void *a, int64_t na, const void *b, int64_t nb) {
-  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-  return na > 0 && nb > 0 && (x < y ? y - x < static_cast<uintptr_t>(na) : x - y < static_cast<uintptr_t>(nb));
-}
-
 // Tables of the Newton-Schulz groups into the plan (sizes already checked).
 zds_status build_newton_schulz(zds_matrix_plan *p, const int64_t *offset, const int32_t *rows, const int32_t *cols,
                                int32_t num);

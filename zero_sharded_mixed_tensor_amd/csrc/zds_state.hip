@@ -1,0 +1,211 @@
+// Moments in fewer bits: quantising fp32 arrays and reading them back
+// (include/zds.h describes the formats; zds_quantised.h has the arithmetic).
+//
+// Both are HBM-bound streams: 4 B read and a code (1 + 1/32 or 2 B) written
+// per element, and the other way round. A wave takes units of 512 elements,
+// each lane a quad of each half, so that a block of 32 lies in 8 neighbouring
+// lanes and its largest magnitude takes three cross-lane moves.
+#include "zds_internal.h"
+#include "zds_quantised.h"
+
+namespace zds {
+
+struct ConvertArgs {
+  const void *src;
+  void *dst;
+  uint8_t *exps;
+  const uint8_t *exps_in;
+  int64_t n;
+  uint64_t seed;
+  int64_t first;
+  const zds_step_state *state;
+};
+
+// Unaligned or cut quads: element by element.
+template <typename T>
+__device__ __forceinline__ void load_elements(const T *p, int64_t e, int64_t n, T (&x)[4]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) x[i] = e + i < n ? p[e + i] : T(0);
+}
+
+template <int F, bool RANDOM, bool VEC>
+__global__ void __launch_bounds__(256) quantise_kernel(ConvertArgs a) {
+  const int lane = threadIdx.x & 63;
+  const int64_t units = (a.n + kStateUnit - 1) / kStateUnit;
+  const float *src = static_cast<const float *>(a.src);
+  const uint32_t steps = RANDOM ? a.state->steps_seen : 0u;
+  for (int64_t u = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 6); u < units;
+       u += static_cast<int64_t>(gridDim.x) * 4) {
+    QuadBits rb{};
+    if (RANDOM) rb = unit_random_bits(a.seed, static_cast<uint64_t>((a.first + u * kStateUnit) >> 3), steps, lane);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int64_t e = u * kStateUnit + 256 * h + 4 * lane;
+      const bool whole = e + 4 <= a.n;
+      float x[4];
+      if (VEC && whole) load_quad<ZDS_FP32>(src, e >> 2, x);
+      else load_elements(src, e, a.n, x);
+      const uint32_t (&w)[2] = h ? rb.r1 : rb.r0;
+      if constexpr (F == ZDS_STATE_BF16) {
+        const u32x2 c = encode_quad_bf16<RANDOM>(x, w);
+        if (VEC && whole) {
+          st_stream(static_cast<u32x2 *>(a.dst) + (e >> 2), c);
+        } else {
+          uint16_t *d = static_cast<uint16_t *>(a.dst);
+          for (int i = 0; i < 4; ++i)
+            if (e + i < a.n) d[e + i] = static_cast<uint16_t>((i < 2 ? c.x : c.y) >> (16 * (i & 1)));
+        }
+      } else {
+        uint32_t m = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) m = magnitude(x[i]) > m ? magnitude(x[i]) : m;
+        const uint32_t s = exponent_byte<F>(block_max(m));
+        const uint32_t c = encode_quad<F, RANDOM>(x, s, w);
+        uint8_t *d = static_cast<uint8_t *>(a.dst);
+        if (VEC && whole) {
+          st_stream(reinterpret_cast<uint32_t *>(d + e), c);
+        } else {
+          for (int i = 0; i < 4; ++i)
+            if (e + i < a.n) d[e + i] = static_cast<uint8_t>(c >> (8 * i));
+        }
+        if ((lane & 7) == 0 && e < a.n) a.exps[e >> 5] = static_cast<uint8_t>(s);
+      }
+    }
+  }
+}
+
+template <int F, int D, bool VEC>
+__global__ void __launch_bounds__(256) dequantise_kernel(ConvertArgs a) {
+  const int64_t quads = (a.n + 3) / 4;
+  for (int64_t q = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; q < quads;
+       q += static_cast<int64_t>(gridDim.x) * 256) {
+    const int64_t e = 4 * q;
+    const bool whole = e + 4 <= a.n;
+    float x[4];
+    if constexpr (F == ZDS_STATE_BF16) {
+      if (VEC && whole) {
+        load_quad<ZDS_BF16>(a.src, q, x);
+      } else {
+        uint16_t c[4];
+        load_elements(static_cast<const uint16_t *>(a.src), e, a.n, c);
+        for (int i = 0; i < 4; ++i) x[i] = __uint_as_float(static_cast<uint32_t>(c[i]) << 16);
+      }
+    } else {
+      const uint32_t s = a.exps_in[e >> 5];
+      uint32_t w;
+      if (VEC && whole) {
+        w = ld_stream(static_cast<const uint32_t *>(a.src) + q);
+      } else {
+        uint8_t c[4];
+        load_elements(static_cast<const uint8_t *>(a.src), e, a.n, c);
+        w = c[0] | (c[1] << 8) | (c[2] << 16) | (static_cast<uint32_t>(c[3]) << 24);
+      }
+      decode_quad<F>(w, s, x);
+    }
+    if (VEC && whole) {
+      if (D == ZDS_FP32) store_quad(static_cast<float *>(a.dst), q, x);
+      else store_quad16<ZDS_BF16>(a.dst, q, x);
+    } else {
+      for (int i = 0; i < 4; ++i) {
+        if (e + i >= a.n) break;
+        if (D == ZDS_FP32) static_cast<float *>(a.dst)[e + i] = x[i];
+        else static_cast<uint16_t *>(a.dst)[e + i] = narrow1<ZDS_BF16>(x[i]);
+      }
+    }
+  }
+}
+
+template <int F, bool RANDOM>
+static void quantise_go(bool vec, const ConvertArgs &a, hipStream_t s) {
+  int64_t g = (a.n + 4 * kStateUnit - 1) / (4 * kStateUnit);
+  if (g > max_blocks(256)) g = max_blocks(256);
+  if (vec) hipLaunchKernelGGL((quantise_kernel<F, RANDOM, true>), dim3(static_cast<uint32_t>(g)), dim3(256), 0, s, a);
+  else hipLaunchKernelGGL((quantise_kernel<F, RANDOM, false>), dim3(static_cast<uint32_t>(g)), dim3(256), 0, s, a);
+}
+
+template <int F, int D>
+static void dequantise_go(bool vec, const ConvertArgs &a, hipStream_t s) {
+  int64_t g = (a.n + 1023) / 1024;
+  if (g > max_blocks(256)) g = max_blocks(256);
+  if (vec) hipLaunchKernelGGL((dequantise_kernel<F, D, true>), dim3(static_cast<uint32_t>(g)), dim3(256), 0, s, a);
+  else hipLaunchKernelGGL((dequantise_kernel<F, D, false>), dim3(static_cast<uint32_t>(g)), dim3(256), 0, s, a);
+}
+
+static bool valid_format(int f) { return f == ZDS_STATE_E4M3 || f == ZDS_STATE_UE5M3 || f == ZDS_STATE_BF16; }
+static int64_t code_size(zds_state_format f) { return f == ZDS_STATE_BF16 ? 2 : 1; }
+
+// What both conversions check: dst_size and src_size are bytes per element.
+static zds_status check_convert(const char *fn, const void *codes, const void *exps, int64_t n, zds_state_format f,
+                                const void *plain, int64_t plain_size) {
+  if (!codes || !plain) return fail(ZDS_EINVAL, "%s: null pointer", fn);
+  if ((f == ZDS_STATE_BF16) != (exps == nullptr))
+    return fail(ZDS_EINVAL, f == ZDS_STATE_BF16 ? "%s: BF16 takes no exps" : "%s: null exps", fn);
+  if (!aligned(plain, static_cast<uintptr_t>(plain_size)) || !aligned(codes, static_cast<uintptr_t>(code_size(f))))
+    return fail(ZDS_EALIGN, "%s: pointer not aligned to its element size", fn);
+  const int64_t nb = (n + 31) / 32, cb = n * code_size(f), pb = n * plain_size;
+  if (ranges_meet(codes, cb, plain, pb) ||
+      (exps && (ranges_meet(exps, nb, codes, cb) || ranges_meet(exps, nb, plain, pb))))
+    return fail(ZDS_EINVAL, "%s: the arrays overlap", fn);
+  return ZDS_OK;
+}
+
+}  // namespace zds
+
+using namespace zds;
+
+extern "C" zds_status zds_random_words_host(uint64_t seed, uint64_t call, uint32_t steps_seen, uint32_t stream,
+                                            uint32_t *out4) {
+  clear_error();
+  if (!out4) return fail(ZDS_EINVAL, "zds_random_words_host: null output");
+  const RandomWords q = random_words(seed, call, steps_seen, stream);
+  for (int i = 0; i < 4; ++i) out4[i] = q.w[i];
+  return ZDS_OK;
+}
+
+extern "C" zds_status zds_state_quantise(const float *src, int64_t n, zds_state_format format, zds_rounding rounding,
+                                         uint64_t seed, int64_t first, const zds_step_state *state_dev, void *codes,
+                                         uint8_t *exps, void *stream) {
+  clear_error();
+  const char *fn = "zds_state_quantise";
+  if (!valid_format(format)) return fail(ZDS_EINVAL, "%s: bad format", fn);
+  if (rounding != ZDS_ROUND_NEAREST && rounding != ZDS_ROUND_RANDOM) return fail(ZDS_EINVAL, "%s: bad rounding", fn);
+  if (n < 0 || n >= kStateMost) return fail(ZDS_EINVAL, "%s: n must lie in [0, 2^40)", fn);
+  const bool random = rounding == ZDS_ROUND_RANDOM;
+  if (random && (first < 0 || first % 32 != 0)) return fail(ZDS_EINVAL, "%s: first must be a multiple of 32, >= 0", fn);
+  if (n == 0) return ZDS_OK;
+  if (random && !state_dev) return fail(ZDS_EINVAL, "%s: null state", fn);
+  if (random && !aligned(state_dev, 8)) return fail(ZDS_EALIGN, "%s: state not 8-byte aligned", fn);
+  const zds_status st = check_convert(fn, codes, exps, n, format, src, 4);
+  if (st != ZDS_OK) return st;
+  const ConvertArgs a{src, codes, exps, nullptr, n, seed, random ? first : 0, state_dev};
+  const bool vec = aligned(src, 16) && aligned(codes, format == ZDS_STATE_BF16 ? 8 : 4);
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  switch (format) {
+    case ZDS_STATE_E4M3: random ? quantise_go<ZDS_STATE_E4M3, true>(vec, a, s) : quantise_go<ZDS_STATE_E4M3, false>(vec, a, s); break;
+    case ZDS_STATE_UE5M3: random ? quantise_go<ZDS_STATE_UE5M3, true>(vec, a, s) : quantise_go<ZDS_STATE_UE5M3, false>(vec, a, s); break;
+    default: random ? quantise_go<ZDS_STATE_BF16, true>(vec, a, s) : quantise_go<ZDS_STATE_BF16, false>(vec, a, s); break;
+  }
+  return check_launch("state_quantise kernel");
+}
+
+extern "C" zds_status zds_state_dequantise(const void *codes, const uint8_t *exps, int64_t n, zds_state_format format,
+                                           void *dst, zds_dtype dst_dtype, void *stream) {
+  clear_error();
+  const char *fn = "zds_state_dequantise";
+  if (!valid_format(format)) return fail(ZDS_EINVAL, "%s: bad format", fn);
+  if (dst_dtype != ZDS_FP32 && dst_dtype != ZDS_BF16) return fail(ZDS_EINVAL, "%s: dst dtype must be bf16 or fp32", fn);
+  if (n < 0 || n >= kStateMost) return fail(ZDS_EINVAL, "%s: n must lie in [0, 2^40)", fn);
+  if (n == 0) return ZDS_OK;
+  const zds_status st = check_convert(fn, codes, exps, n, format, dst, dtype_size(dst_dtype));
+  if (st != ZDS_OK) return st;
+  const ConvertArgs a{codes, dst, nullptr, exps, n, 0, 0, nullptr};
+  const bool f = dst_dtype == ZDS_FP32;
+  const bool vec = aligned(dst, f ? 16 : 8) && aligned(codes, format == ZDS_STATE_BF16 ? 8 : 4);
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  switch (format) {
+    case ZDS_STATE_E4M3: f ? dequantise_go<ZDS_STATE_E4M3, ZDS_FP32>(vec, a, s) : dequantise_go<ZDS_STATE_E4M3, ZDS_BF16>(vec, a, s); break;
+    case ZDS_STATE_UE5M3: f ? dequantise_go<ZDS_STATE_UE5M3, ZDS_FP32>(vec, a, s) : dequantise_go<ZDS_STATE_UE5M3, ZDS_BF16>(vec, a, s); break;
+    default: f ? dequantise_go<ZDS_STATE_BF16, ZDS_FP32>(vec, a, s) : dequantise_go<ZDS_STATE_BF16, ZDS_BF16>(vec, a, s); break;
+  }
+  return check_launch("state_dequantise kernel");
+}

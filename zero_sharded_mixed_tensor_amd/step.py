@@ -2,8 +2,8 @@
 
 engine.backward's gradient handling -> zds_grad_accumulate per micro-batch;
 engine.step -> zds_overflow_and_norm, zds_adam_step (MuonStep: Muon's three
-calls for the matrices and zds_adam_step for the rest), zds_loss_scaler_update,
-all on one stream with no host synchronisation (devpress.csdn.net DeepSpeed
+calls for the matrices and zds_adam_step for the rest; QuantisedStep:
+zds_adam_step_q8), zds_loss_scaler_update, all on one stream with no host synchronisation (devpress.csdn.net DeepSpeed
 tutorial §3.3: the engine's backward and step replace the plain ones).
 """
 
@@ -36,6 +36,8 @@ class ShardStep:
         loss scaler, clip threshold, micro-batches per step)."""
         if cfg.muon is not None:
             raise zds.ZdsError(zds.ZDS_EINVAL, "the configuration's optimizer is Muon: its step is MuonStep")
+        if cfg.second_moment is not None:
+            raise zds.ZdsError(zds.ZDS_EINVAL, "the configuration keeps its moments in 8 bits: its step is QuantisedStep")
         return cls(n, cfg.hparams(), cfg.scaler_config(), cfg.max_norm, cfg.accum_steps, t0, beta1_pow0,
                    beta2_pow0, device, stream)
 
@@ -189,6 +191,100 @@ class MuonStep:
 
     def read_scalars(self):
         return self.base.read_scalars()
+
+
+class QuantisedStep(ShardStep):
+    """A rank whose moments are kept in fewer bits: E4M3 for the first and, as
+    `second` says, UE5M3 (8 bits; beta2 up to about 0.98) or BF16 for the
+    second. The calls are ShardStep's, with QuantisedStates for exp_avg and
+    exp_avg_sq.
+
+    seed: of the random roundings; first: the flat index of element 0 (the
+    shard's lo), so that an element's roundings do not depend on the
+    partition."""
+
+    def __init__(self, n, hp=None, scaler=None, max_norm=1.0, accum_steps=1, t0=0, beta1_pow0=1.0, beta2_pow0=1.0,
+                 second=zds.ZDS_STATE_UE5M3, seed=0, first=0, device="cuda", stream=None):
+        if second not in (zds.ZDS_STATE_UE5M3, zds.ZDS_STATE_BF16):
+            raise zds.ZdsError(zds.ZDS_EINVAL, "the second moment's format must be UE5M3 or BF16")
+        if first < 0 or first % 32:
+            raise zds.ZdsError(zds.ZDS_EINVAL, "first must be a multiple of 32, >= 0")
+        super().__init__(n, hp, scaler, max_norm, accum_steps, t0, beta1_pow0, beta2_pow0, device, stream)
+        self.second, self.seed, self.first = second, zds._seed(seed), first
+
+    @classmethod
+    def from_config(cls, n, cfg, t0=0, beta1_pow0=1.0, beta2_pow0=1.0, seed=0, first=0, device="cuda", stream=None):
+        """A step with the settings of a config.StepConfig whose optimizer is
+        AdamW8bit."""
+        if cfg.second_moment is None:
+            raise zds.ZdsError(zds.ZDS_EINVAL, "the configuration's moments are fp32: its step is ShardStep")
+        second = zds.ZDS_STATE_BF16 if cfg.second_moment == "bf16" else zds.ZDS_STATE_UE5M3
+        return cls(n, cfg.hparams(), cfg.scaler_config(), cfg.max_norm, cfg.accum_steps, t0, beta1_pow0, beta2_pow0,
+                   second, seed, first, device, stream)
+
+    def new_moments(self):
+        """(exp_avg, exp_avg_sq) of zeros, on the state's device."""
+        return (zds.new_quantised_state(self.n, zds.ZDS_STATE_E4M3, self.state.device),
+                zds.new_quantised_state(self.n, self.second, self.state.device))
+
+    def adam(self, grads, master, exp_avg, exp_avg_sq, params_out, stream=None):
+        if isinstance(exp_avg_sq, zds.QuantisedState) and exp_avg_sq.fmt != self.second:
+            raise zds.ZdsError(zds.ZDS_EINVAL, "exp_avg_sq is not of the step's format")
+        zds.zds_adam_step_q8(self.hp, grads, master, exp_avg, exp_avg_sq, params_out, self.seed, self.first,
+                             self.scalars, self.state, stream, n=self.n)
+
+    def quantise(self, exp_avg32, exp_avg_sq32, exp_avg, exp_avg_sq, stream=None):
+        """Takes over fp32 moments, to the nearest codes."""
+        zds.zds_state_quantise(exp_avg32, exp_avg, stream=stream, n=self.n)
+        zds.zds_state_quantise(exp_avg_sq32, exp_avg_sq, stream=stream, n=self.n)
+
+    def read_back(self, exp_avg, exp_avg_sq, exp_avg32, exp_avg_sq32, stream=None):
+        """The moments in fp32, exactly: quantise() of these reads back as the
+        same values, so a checkpoint of them (zds_checkpoint_save) resumes the
+        run bit for bit, and one of a ShardStep can go on in fewer bits."""
+        zds.zds_state_dequantise(exp_avg, exp_avg32, stream, n=self.n)
+        zds.zds_state_dequantise(exp_avg_sq, exp_avg_sq32, stream, n=self.n)
+
+
+class DropoutExchange:
+    """One rank's end of an exchange that sends one element of each group of
+    `ratio`: the message's buffer and the fp32 feedback buffer (feedback False:
+    none; what is sent is then scaled by ratio). Every rank uses the same seed
+    and first. A step over N ranks (accum_steps = K * N):
+
+        step.norm(grads)                     # the rank's own overflow flag
+        ex.compress(grads, step)
+        all_reduce(ex.values)
+        ex.norm(ex.values, step)             # flag, norm and clip of the sum
+        ex.decompress([ex.values], grads, step)
+        step.adam(grads, ...); step.scaler()"""
+
+    def __init__(self, n, ratio, dtype=None, seed=0, first=0, feedback=True, device="cuda"):
+        import torch
+        if ratio not in (2, 4, 8, 16, 32, 64, 128, 256):
+            raise zds.ZdsError(zds.ZDS_EINVAL, "ratio must be a power of two in [2, 256]")
+        if first < 0 or first % ratio:
+            raise zds.ZdsError(zds.ZDS_EINVAL, "first must be a multiple of ratio, >= 0")
+        self.n, self.ratio, self.seed, self.first = n, ratio, zds._seed(seed), first
+        self.groups = zds.dropout_groups(n, ratio)
+        self.values = torch.zeros(self.groups, dtype=torch.bfloat16 if dtype is None else dtype, device=device)
+        self.error = torch.zeros(n, dtype=torch.float32, device=device) if feedback else None
+
+    def compress(self, grads, step, stream=None):
+        """The message of this rank's grads. step.scalars' overflow flag, left
+        by a norm pass over them, poisons it."""
+        zds.zds_dropout_compress(grads, self.error, self.ratio, self.values, self.seed, self.first, step.state,
+                                 step.scalars, stream, n=self.n)
+
+    def norm(self, total, step, stream=None):
+        """Overflow flag, norm and clip of the gradient that an all-reduced
+        message (or zds_reduce_peer_slices' sum of several) makes: those of the
+        message, as the other elements are 0."""
+        zds.zds_overflow_and_norm(total, step.accum_steps, step.max_norm, step.state, step.scalars, step.ws, stream,
+                                  n=self.groups)
+
+    def decompress(self, peers, dst, step, mode=zds.ZDS_OVERWRITE, stream=None):
+        zds.zds_dropout_decompress(peers, self.ratio, dst, self.seed, self.first, step.state, mode, stream, n=self.n)
 
 
 class OffloadStep:

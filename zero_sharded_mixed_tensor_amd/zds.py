@@ -23,6 +23,8 @@ ZDS_FP16, ZDS_BF16, ZDS_FP32 = 0, 1, 2
 ZDS_COPY, ZDS_OVERWRITE, ZDS_ACCUMULATE = 0, 1, 2
 ZDS_ON_DEVICE, ZDS_ON_HOST = 0, 1
 ZDS_MUON_SCALE_NONE, ZDS_MUON_SCALE_ASPECT, ZDS_MUON_SCALE_RMS = 0, 1, 2
+ZDS_STATE_E4M3, ZDS_STATE_UE5M3, ZDS_STATE_BF16 = 0, 1, 2
+ZDS_ROUND_NEAREST, ZDS_ROUND_RANDOM = 0, 1
 
 STATE_BYTES = 64
 SCALARS_BYTES = 64
@@ -82,7 +84,7 @@ assert ctypes.sizeof(StepState) == STATE_BYTES and ctypes.sizeof(StepScalars) ==
 assert ctypes.sizeof(CheckpointMeta) == 48 and ctypes.sizeof(MuonHparams) == 20
 
 _P = ctypes.c_void_p
-_I32, _I64, _U32 = ctypes.c_int32, ctypes.c_int64, ctypes.c_uint32
+_I32, _I64, _U32, _U64 = ctypes.c_int32, ctypes.c_int64, ctypes.c_uint32, ctypes.c_uint64
 _PI64 = ctypes.POINTER(ctypes.c_int64)
 _SIGS = {
     "zds_flat_layout": (_I32, [_PI64, _I32, _I32, _PI64, _PI64]),
@@ -126,6 +128,13 @@ _SIGS = {
     "zds_newton_schulz_workspace_bytes": (ctypes.c_size_t, [_P, _I32]),
     "zds_newton_schulz": (_I32, [_P, _P, _P, _I32, ctypes.POINTER(ctypes.c_float), _I32, _P, _P, ctypes.c_size_t, _P]),
     "zds_muon_apply": (_I32, [ctypes.POINTER(MuonHparams), _P, _P, _I32, _P, _P, _I32, _P, _P]),
+    "zds_random_words_host": (_I32, [_U64, _U64, _U32, _U32, ctypes.POINTER(_U32)]),
+    "zds_state_quantise": (_I32, [_P, _I64, _I32, _I32, _U64, _I64, _P, _P, _P, _P]),
+    "zds_state_dequantise": (_I32, [_P, _P, _I64, _I32, _P, _I32, _P]),
+    "zds_adam_step_q8": (_I32, [ctypes.POINTER(AdamWHparams), _P, _I32, _P, _P, _P, _P, _I32, _P, _P, _I32, _I64,
+                                _U64, _I64, _P, _P, _P]),
+    "zds_dropout_compress": (_I32, [_P, _I32, _P, _I64, _I32, _U64, _I64, _P, _P, _P, _I32, _P]),
+    "zds_dropout_decompress": (_I32, [ctypes.POINTER(_P), _I32, _I32, _I64, _I32, _U64, _I64, _P, _P, _I32, _I32, _P]),
     "zds_step_state_init": (_I32, [_P, ctypes.POINTER(ScalerConfig), _I64, ctypes.c_double,
                                    ctypes.c_double, _P]),
     "zds_loss_scaler_update": (_I32, [_P, _P, ctypes.POINTER(AdamWHparams), _P]),
@@ -642,6 +651,155 @@ def zds_muon_apply(hp, plan, update, master, params_out, scalars, stream=None):
     _check(lib.zds_muon_apply(ctypes.byref(hp), plan.handle, _here(update, "update"), dtype_code(update),
                               _here(master, "master"), _here(params_out, "params_out"), pdt,
                               _here(scalars, "scalars"), _stream(stream)))
+
+
+# ------------------------------------------------------------------ moments in fewer bits
+
+def _seed(seed):
+    seed = int(seed)
+    if not 0 <= seed < 1 << 64:
+        raise ZdsError(ZDS_EINVAL, "seed %d is not a 64-bit number" % seed)
+    return seed
+
+
+def _size(n, what):
+    """ctypes cuts a number that is too large for its type instead of refusing it."""
+    n = int(n)
+    if not -(1 << 63) <= n < 1 << 63:
+        raise ZdsError(ZDS_EINVAL, "%s %d is out of range" % (what, n))
+    return n
+
+
+def zds_random_words_host(seed, call, steps_seen, stream):
+    """The four 32-bit words of one call of the counter-based generator."""
+    out = (_U32 * 4)()
+    _check(lib.zds_random_words_host(_seed(seed), _seed(call), int(steps_seen) & 0xFFFFFFFF, int(stream), out))
+    return list(out)
+
+
+class QuantisedState:
+    """One moment in fewer bits: its format, the codes (uint8, or bfloat16 for
+    ZDS_STATE_BF16) and the exponent bytes of its blocks of 32 (None for
+    BF16). The device tensors are the caller's."""
+
+    def __init__(self, fmt, codes, exps=None):
+        self.fmt, self.codes, self.exps = fmt, codes, exps
+
+    def numel(self):
+        return self.codes.numel()
+
+
+def new_quantised_state(n, fmt, device="cuda"):
+    """A moment of n zeros."""
+    if fmt == ZDS_STATE_BF16:
+        return QuantisedState(fmt, torch.zeros(n, dtype=torch.bfloat16, device=device))
+    if fmt not in (ZDS_STATE_E4M3, ZDS_STATE_UE5M3):
+        raise ZdsError(ZDS_EINVAL, "bad state format %r" % (fmt,))
+    return QuantisedState(fmt, torch.zeros(n, dtype=torch.uint8, device=device),
+                          torch.zeros((n + 31) // 32, dtype=torch.uint8, device=device))
+
+
+def _quantised(q, n, what):
+    """Addresses (codes, exps) of a QuantisedState of at least n elements."""
+    if not isinstance(q, QuantisedState):
+        raise ZdsError(ZDS_EINVAL, "%s must be a QuantisedState" % what)
+    wide = q.fmt == ZDS_STATE_BF16
+    if q.codes.dtype != (torch.bfloat16 if wide else torch.uint8):
+        raise ZdsError(ZDS_EINVAL, "%s: codes must be %s" % (what, "bf16" if wide else "uint8"))
+    _need(q.codes, n, what + " codes")
+    if wide != (q.exps is None):
+        raise ZdsError(ZDS_EINVAL, "%s: %s" % (what, "a BF16 moment has no exps" if wide else "exps is missing"))
+    if q.exps is not None:
+        if q.exps.dtype != torch.uint8:
+            raise ZdsError(ZDS_EINVAL, "%s: exps must be uint8" % what)
+        _need(q.exps, (n + 31) // 32, what + " exps")
+    return _here(q.codes, what + " codes"), _here(q.exps, what + " exps")
+
+
+def zds_state_quantise(src, q, rounding=ZDS_ROUND_NEAREST, seed=0, first=0, state=None, stream=None, n=None):
+    """src: fp32; q: the QuantisedState that is written. seed, first (the flat
+    index of element 0) and state (the step state) are ZDS_ROUND_RANDOM's."""
+    n = src.numel() if n is None else n
+    if src.dtype != torch.float32:
+        raise ZdsError(ZDS_EINVAL, "src must be fp32")
+    _need(src, n, "src")
+    _need_bytes(state, STATE_BYTES, "state")
+    codes, exps = _quantised(q, n, "state")
+    _check(lib.zds_state_quantise(_here(src, "src"), n, q.fmt, rounding, _seed(seed), _size(first, "first"),
+                                  _here(state, "state"), codes, exps, _stream(stream)))
+
+
+def zds_state_dequantise(q, dst, stream=None, n=None):
+    """dst: fp32 or bf16, receives what q's codes stand for."""
+    n = dst.numel() if n is None else n
+    _need(dst, n, "dst")
+    codes, exps = _quantised(q, n, "state")
+    _check(lib.zds_state_dequantise(codes, exps, n, q.fmt, _here(dst, "dst"), dtype_code(dst), _stream(stream)))
+
+
+def zds_adam_step_q8(hp, grads, master, exp_avg, exp_avg_sq, params_out, seed, first, scalars, state, stream=None,
+                     n=None):
+    """zds_adam_step on two QuantisedStates (exp_avg: E4M3; exp_avg_sq: UE5M3
+    or BF16), read back, and quantised at random from seed, first (the flat
+    index of element 0) and the step state."""
+    n = master.numel() if n is None else n
+    if master.dtype != torch.float32:
+        raise ZdsError(ZDS_EINVAL, "master must be fp32")
+    for name, t in (("master", master), ("grads", grads), ("params_out", params_out)):
+        _need(t, n, name)
+    _need_bytes(scalars, SCALARS_BYTES, "scalars")
+    _need_bytes(state, STATE_BYTES, "state")
+    m, v = _quantised(exp_avg, n, "exp_avg"), _quantised(exp_avg_sq, n, "exp_avg_sq")
+    if exp_avg.fmt != ZDS_STATE_E4M3:
+        raise ZdsError(ZDS_EINVAL, "exp_avg's format must be E4M3")
+    pdt = dtype_code(params_out) if params_out is not None else ZDS_FP16
+    _check(lib.zds_adam_step_q8(ctypes.byref(hp), _here(grads, "grads"), dtype_code(grads), _here(master, "master"),
+                                m[0], m[1], v[0], exp_avg_sq.fmt, v[1], _here(params_out, "params_out"), pdt, n,
+                                _seed(seed), _size(first, "first"), _here(scalars, "scalars"), _here(state, "state"),
+                                _stream(stream)))
+
+
+# ------------------------------------------------------------------ gradient dropout
+
+def dropout_groups(n, ratio):
+    """Values in a message of n elements."""
+    if ratio < 1:
+        raise ZdsError(ZDS_EINVAL, "ratio must be positive")
+    return -(-n // ratio)
+
+
+def zds_dropout_compress(x, error, ratio, values, seed, first, state, scalars=None, stream=None, n=None):
+    """x: the rank's gradient; error: fp32 feedback buffer, updated, or None;
+    values: the message, dropout_groups(n, ratio) elements, written; scalars:
+    the step scalars whose overflow flag poisons the message, or None."""
+    n = x.numel() if n is None else n
+    if error is not None and error.dtype != torch.float32:
+        raise ZdsError(ZDS_EINVAL, "error must be fp32")
+    _need(x, n, "x")
+    _need(error, n, "error")
+    _need(values, dropout_groups(n, ratio), "values")
+    _need_bytes(state, STATE_BYTES, "state")
+    _need_bytes(scalars, SCALARS_BYTES, "scalars")
+    _check(lib.zds_dropout_compress(_here(x, "x"), dtype_code(x), _here(error, "error"), n, ratio, _seed(seed),
+                                    _size(first, "first"), _here(scalars, "scalars"), _here(state, "state"),
+                                    _here(values, "values"), dtype_code(values), _stream(stream)))
+
+
+def zds_dropout_decompress(peers, ratio, dst, seed, first, state, mode=ZDS_OVERWRITE, stream=None, n=None):
+    """peers: the messages (device tensors of one type), in sum order; dst:
+    the gradient, fp32 or of the messages' type."""
+    n = dst.numel() if n is None else n
+    _need(dst, n, "dst")
+    _need_bytes(state, STATE_BYTES, "state")
+    for k, t in enumerate(peers):
+        if t.dtype != peers[0].dtype:
+            raise ZdsError(ZDS_EINVAL, "the messages must share one dtype")
+        _need(t, dropout_groups(n, ratio), "peer %d" % k)
+    arr = (_P * max(1, len(peers)))(*[_here(t, "peer %d" % k) for k, t in enumerate(peers)])
+    vdt = dtype_code(peers[0]) if len(peers) else ZDS_FP32
+    _check(lib.zds_dropout_decompress(arr, len(peers), vdt, n, ratio, _seed(seed), _size(first, "first"),
+                                      _here(state, "state"), _here(dst, "dst"), dtype_code(dst), mode,
+                                      _stream(stream)))
 
 
 # ------------------------------------------------------------------ checkpoints
