@@ -22,107 +22,98 @@ struct AdamQ8Args {
   int64_t first;
 };
 
-// Element e + i of a quad that is cut or not aligned.
-template <typename T>
-__device__ __forceinline__ T element_or_zero(const void *p, int64_t e, int64_t n) {
-  return e < n ? static_cast<const T *>(p)[e] : T(0);
+// One unit of 512 elements by a wave: each lane a quad of either half. FULL:
+// the unit lies inside the arrays, and they are aligned.
+template <int GD, int PD, int VF, bool FULL>
+__device__ __forceinline__ void q8_unit(const AdamQ8Args &a, const ElemConsts &c, int64_t u, uint32_t steps, int lane) {
+  const QuadBits rb = unit_random_bits(a.seed, static_cast<uint64_t>((a.first + u * kStateUnit) >> 3), steps, lane);
+  uint8_t *mc = static_cast<uint8_t *>(a.m);
+  uint8_t *vc = static_cast<uint8_t *>(a.v);
+  uint16_t *v16 = static_cast<uint16_t *>(a.v);
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int64_t e = u * kStateUnit + 256 * h + 4 * lane;
+    const bool any = FULL || e < a.n;
+    float g[4], p[4], m[4], v[4];
+    uint32_t mw = 0, vw = 0;
+    const uint32_t ms = any ? a.me[e >> 5] : 0u;
+    const uint32_t vs = VF != ZDS_STATE_BF16 && any ? a.ve[e >> 5] : 0u;
+    if (FULL) {
+      load_quad<GD>(a.g, e >> 2, g);
+      load_quad<ZDS_FP32>(a.p, e >> 2, p);
+      mw = ld_stream(reinterpret_cast<const uint32_t *>(mc + e));
+      if constexpr (VF == ZDS_STATE_BF16) load_quad<ZDS_BF16>(a.v, e >> 2, v);
+      else vw = ld_stream(reinterpret_cast<const uint32_t *>(vc + e));
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const bool in = e + i < a.n;
+        g[i] = in ? widen1<GD>(a.g, e + i) : 0.0f;
+        p[i] = in ? a.p[e + i] : 0.0f;
+        mw |= (in ? static_cast<uint32_t>(mc[e + i]) : 0u) << (8 * i);
+        if constexpr (VF == ZDS_STATE_BF16) v[i] = in ? widen1<ZDS_BF16>(a.v, e + i) : 0.0f;
+        else vw |= (in ? static_cast<uint32_t>(vc[e + i]) : 0u) << (8 * i);
+      }
+    }
+    decode_quad<ZDS_STATE_E4M3>(mw, ms, m);
+    if constexpr (VF != ZDS_STATE_BF16) decode_quad<VF>(vw, vs, v);
+    uint32_t mm = 0, vm = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      adam_elem(g[i], c, p[i], m[i], v[i]);
+      if (!FULL && e + i >= a.n) m[i] = v[i] = 0.0f;
+      mm = magnitude(m[i]) > mm ? magnitude(m[i]) : mm;
+      vm = magnitude(v[i]) > vm ? magnitude(v[i]) : vm;
+    }
+    const uint32_t (&w)[2] = h ? rb.r1 : rb.r0;
+    mm = block_max(mm);
+    const uint32_t ms1 = exponent_byte<ZDS_STATE_E4M3>(mm);
+    mw = encode_quad<ZDS_STATE_E4M3, true>(m, ms1, mm, w);
+    u32x2 v2{};
+    uint32_t vs1 = 0;
+    if constexpr (VF == ZDS_STATE_BF16) {
+      v2 = encode_quad_bf16<true>(v, w);
+    } else {
+      vm = block_max(vm);
+      vs1 = exponent_byte<VF>(vm);
+      vw = encode_quad<VF, true, true>(v, vs1, vm, w);
+    }
+    if (FULL) {
+      store_quad(a.p, e >> 2, p);
+      if constexpr (PD >= 0) store_quad16<PD>(a.out, e >> 2, p);
+      st_stream(reinterpret_cast<uint32_t *>(mc + e), mw);
+      if constexpr (VF == ZDS_STATE_BF16) st_stream(reinterpret_cast<u32x2 *>(v16 + e), v2);
+      else st_stream(reinterpret_cast<uint32_t *>(vc + e), vw);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (e + i >= a.n) break;
+        a.p[e + i] = p[i];
+        if constexpr (PD >= 0) static_cast<uint16_t *>(a.out)[e + i] = narrow1<PD>(p[i]);
+        mc[e + i] = static_cast<uint8_t>(mw >> (8 * i));
+        if constexpr (VF == ZDS_STATE_BF16) v16[e + i] = static_cast<uint16_t>((i < 2 ? v2.x : v2.y) >> (16 * (i & 1)));
+        else vc[e + i] = static_cast<uint8_t>(vw >> (8 * i));
+      }
+    }
+    if ((lane & 7) == 0 && any) {
+      a.me[e >> 5] = static_cast<uint8_t>(ms1);
+      if constexpr (VF != ZDS_STATE_BF16) a.ve[e >> 5] = static_cast<uint8_t>(vs1);
+    }
+  }
 }
 
-// The kernel that a wave runs: units of 512 elements, each lane a quad of
-// either half. PD: the params' type, -1 for none.
+// PD: the params' type, -1 for none.
 template <int GD, int PD, int VF, bool VEC>
 __global__ void __launch_bounds__(256) adam_q8_kernel(AdamQ8Args a) {
   if (a.sc->overflow) return;  // the step is skipped: uniform, nothing is touched
   const ElemConsts c = load_consts(a.sc);
   const uint32_t steps = a.state->steps_seen;
   const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int64_t units = (a.n + kStateUnit - 1) / kStateUnit;
-  for (int64_t u = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 6); u < units;
-       u += static_cast<int64_t>(gridDim.x) * 4) {
-    const QuadBits rb = unit_random_bits(a.seed, static_cast<uint64_t>((a.first + u * kStateUnit) >> 3), steps, lane);
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int64_t e = u * kStateUnit + 256 * h + 4 * lane;
-      const bool whole = VEC && e + 4 <= a.n;
-      const bool any = e < a.n;
-      float g[4], p[4], m[4], v[4];
-      const uint32_t ms = any ? a.me[e >> 5] : 0u;
-      uint32_t mw = 0;
-      if (whole) {
-        load_quad<GD>(a.g, e >> 2, g);
-        load_quad<ZDS_FP32>(a.p, e >> 2, p);
-        mw = ld_stream(reinterpret_cast<const uint32_t *>(static_cast<const uint8_t *>(a.m) + e));
-      } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          g[i] = e + i < a.n ? widen1<GD>(a.g, e + i) : 0.0f;
-          p[i] = element_or_zero<float>(a.p, e + i, a.n);
-          mw |= static_cast<uint32_t>(element_or_zero<uint8_t>(a.m, e + i, a.n)) << (8 * i);
-        }
-      }
-      decode_quad<ZDS_STATE_E4M3>(mw, ms, m);
-      if constexpr (VF == ZDS_STATE_BF16) {
-        if (whole) {
-          load_quad<ZDS_BF16>(a.v, e >> 2, v);
-        } else {
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            v[i] = __uint_as_float(static_cast<uint32_t>(element_or_zero<uint16_t>(a.v, e + i, a.n)) << 16);
-        }
-      } else {
-        const uint32_t vs = any ? a.ve[e >> 5] : 0u;
-        uint32_t vw = 0;
-        if (whole) {
-          vw = ld_stream(reinterpret_cast<const uint32_t *>(static_cast<const uint8_t *>(a.v) + e));
-        } else {
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            vw |= static_cast<uint32_t>(element_or_zero<uint8_t>(a.v, e + i, a.n)) << (8 * i);
-        }
-        decode_quad<VF>(vw, vs, v);
-      }
-      uint32_t mm = 0, vm = 0;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        adam_elem(g[i], c, p[i], m[i], v[i]);
-        if (!whole && e + i >= a.n) m[i] = v[i] = 0.0f;
-        mm = magnitude(m[i]) > mm ? magnitude(m[i]) : mm;
-        vm = magnitude(v[i]) > vm ? magnitude(v[i]) : vm;
-      }
-      const uint32_t (&w)[2] = h ? rb.r1 : rb.r0;
-      const uint32_t ms1 = exponent_byte<ZDS_STATE_E4M3>(block_max(mm));
-      const uint32_t mc = encode_quad<ZDS_STATE_E4M3, true>(m, ms1, w);
-      u32x2 vc{};
-      uint32_t vs1 = 0;
-      if constexpr (VF == ZDS_STATE_BF16) {
-        vc = encode_quad_bf16<true>(v, w);
-      } else {
-        vs1 = exponent_byte<VF>(block_max(vm));
-        vc.x = encode_quad<VF, true>(v, vs1, w);
-      }
-      if (whole) {
-        store_quad(a.p, e >> 2, p);
-        if constexpr (PD >= 0) store_quad16<PD>(a.out, e >> 2, p);
-        st_stream(reinterpret_cast<uint32_t *>(static_cast<uint8_t *>(a.m) + e), mc);
-        if constexpr (VF == ZDS_STATE_BF16) st_stream(static_cast<u32x2 *>(a.v) + (e >> 2), vc);
-        else st_stream(reinterpret_cast<uint32_t *>(static_cast<uint8_t *>(a.v) + e), vc.x);
-      } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          if (e + i >= a.n) break;
-          a.p[e + i] = p[i];
-          if constexpr (PD >= 0) static_cast<uint16_t *>(a.out)[e + i] = narrow1<PD>(p[i]);
-          static_cast<uint8_t *>(a.m)[e + i] = static_cast<uint8_t>(mc >> (8 * i));
-          if constexpr (VF == ZDS_STATE_BF16)
-            static_cast<uint16_t *>(a.v)[e + i] = static_cast<uint16_t>((i < 2 ? vc.x : vc.y) >> (16 * (i & 1)));
-          else static_cast<uint8_t *>(a.v)[e + i] = static_cast<uint8_t>(vc.x >> (8 * i));
-        }
-      }
-      if ((lane & 7) == 0 && any) {
-        a.me[e >> 5] = static_cast<uint8_t>(ms1);
-        if constexpr (VF != ZDS_STATE_BF16) a.ve[e >> 5] = static_cast<uint8_t>(vs1);
-      }
-    }
+  for (int64_t u = static_cast<int64_t>(blockIdx.x) * 4 + wave; u < units; u += static_cast<int64_t>(gridDim.x) * 4) {
+    if (VEC && (u + 1) * kStateUnit <= a.n) q8_unit<GD, PD, VF, VEC>(a, c, u, steps, lane);
+    else q8_unit<GD, PD, VF, false>(a, c, u, steps, lane);
   }
 }
 

@@ -52,7 +52,7 @@ __device__ __forceinline__ uint32_t exponent_byte(uint32_t amax) {
   return t > StateFormat<F>::least ? t : StateFormat<F>::least;
 }
 
-// One code. r: 16 random bits, used as they come (RANDOM only).
+// One code of any value. r: 16 random bits, used as they come (RANDOM only).
 template <int F, bool RANDOM>
 __device__ __forceinline__ uint32_t encode1(float x, uint32_t s, uint32_t r) {
   const uint32_t bits = __float_as_uint(x), mag = bits & 0x7fffffffu;
@@ -66,14 +66,6 @@ __device__ __forceinline__ uint32_t encode1(float x, uint32_t s, uint32_t r) {
   }
   c = mag >= 0x7f800000u ? 0x7fu : c;
   return c | ((bits >> 24) & 0x80u);
-}
-
-template <int F>
-__device__ __forceinline__ float decode1(uint32_t code, uint32_t s) {
-  const uint32_t mag = code & StateFormat<F>::mask;
-  float x = ldexpf(__uint_as_float(mag << 20), static_cast<int>(s) - StateFormat<F>::top);
-  x = mag == StateFormat<F>::mask ? __uint_as_float(0x7fc00000u) : x;
-  return F == ZDS_STATE_E4M3 && code > 0x7fu ? -x : x;
 }
 
 // The 16-bit format: the value's top bits.
@@ -109,12 +101,50 @@ __device__ __forceinline__ QuadBits unit_random_bits(uint64_t seed, uint64_t cal
   return odd ? QuadBits{{t0, t1}, {q.w[2], q.w[3]}} : QuadBits{{q.w[0], q.w[1]}, {t0, t1}};
 }
 
-// Four codes of a quad in a word. w: its 8 random bytes.
-template <int F, bool RANDOM>
-__device__ __forceinline__ uint32_t encode_quad(const float (&x)[4], uint32_t s, const uint32_t (&w)[2]) {
+// Four codes of a quad in a word. amax: the block's largest magnitude; w: the
+// quad's 8 random bytes. The rounding is added to the bits of the scaled values
+// (the sign stays at the top: a magnitude's sum never reaches it), the upper
+// halves of two of them make a word, and the code's bits move to that word's
+// bytes 0 and 2. What the formats say of special values is left to a branch
+// that a wave takes only where it holds one: infinities and NaN are known from
+// amax, and a UE5M3 code 0 from the least sum. A UE5M3 value must not be
+// negative here (NONNEGATIVE: none is; else it is looked at).
+template <int F, bool RANDOM, bool NONNEGATIVE = false>
+__device__ __forceinline__ uint32_t encode_quad(const float (&x)[4], uint32_t s, uint32_t amax, const uint32_t (&w)[2]) {
   const uint32_t a = F == ZDS_STATE_E4M3 ? w[0] : swap_bytes(w[0]), b = F == ZDS_STATE_E4M3 ? w[1] : swap_bytes(w[1]);
-  return encode1<F, RANDOM>(x[0], s, a & 0xffffu) | (encode1<F, RANDOM>(x[1], s, a >> 16) << 8) |
-         (encode1<F, RANDOM>(x[2], s, b & 0xffffu) << 16) | (encode1<F, RANDOM>(x[3], s, b >> 16) << 24);
+  const uint32_t r[4] = {a & 0xffffu, a >> 16, b & 0xffffu, b >> 16};
+  const int k = StateFormat<F>::top - static_cast<int>(s);
+  uint32_t t[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t z = __float_as_uint(ldexpf(x[i], k));
+    t[i] = RANDOM ? z + (r[i] << 4) + 8u : z + 0x7ffffu + ((z >> 20) & 1u);
+  }
+  // (selectors 0-3 name bytes of the second operand, 4-7 of the first)
+  uint32_t p = __builtin_amdgcn_perm(t[1], t[0], 0x07060302u), q = __builtin_amdgcn_perm(t[3], t[2], 0x07060302u);
+  if (F == ZDS_STATE_E4M3) {
+    p = (0x00800080u & (p >> 8)) | (0xff7fff7fu & (p >> 4));
+    q = (0x00800080u & (q >> 8)) | (0xff7fff7fu & (q >> 4));
+  } else {
+    p >>= 4;
+    q >>= 4;
+  }
+  uint32_t c = __builtin_amdgcn_perm(q, p, 0x06040200u);
+  bool special = amax >= 0x7f800000u;
+  if (F == ZDS_STATE_UE5M3) {
+    uint32_t least = t[0];
+    uint32_t most = t[0];
+#pragma unroll
+    for (int i = 1; i < 4; ++i) {
+      least = t[i] < least ? t[i] : least;
+      most = t[i] > most ? t[i] : most;
+    }
+    special = special || least < 0x100000u || (!NONNEGATIVE && most >= 0x80000000u);
+  }
+  if (special)
+    c = encode1<F, RANDOM>(x[0], s, r[0]) | (encode1<F, RANDOM>(x[1], s, r[1]) << 8) |
+        (encode1<F, RANDOM>(x[2], s, r[2]) << 16) | (encode1<F, RANDOM>(x[3], s, r[3]) << 24);
+  return c;
 }
 template <bool RANDOM>
 __device__ __forceinline__ u32x2 encode_quad_bf16(const float (&x)[4], const uint32_t (&w)[2]) {
@@ -122,10 +152,31 @@ __device__ __forceinline__ u32x2 encode_quad_bf16(const float (&x)[4], const uin
   return u32x2{encode_bf16<RANDOM>(x[0], a & 0xffffu) | (encode_bf16<RANDOM>(x[1], a >> 16) << 16),
                encode_bf16<RANDOM>(x[2], b & 0xffffu) | (encode_bf16<RANDOM>(x[3], b >> 16) << 16)};
 }
+// E4M3 codes are the 8-bit floats that the hardware converts (two at a time,
+// NaN included); of UE5M3 codes the top one is looked for in the whole word
+// (a zero byte of its complement).
 template <int F>
 __device__ __forceinline__ void decode_quad(uint32_t w, uint32_t s, float (&x)[4]) {
+  if constexpr (F == ZDS_STATE_E4M3) {
+    const int k = static_cast<int>(s) - 127 - 8;  // 448 = 1.75 * 2^8 is the largest code's value
+    const auto lo = __builtin_amdgcn_cvt_pk_f32_fp8(static_cast<int>(w), false);
+    const auto hi = __builtin_amdgcn_cvt_pk_f32_fp8(static_cast<int>(w), true);
+    x[0] = ldexpf(lo[0], k);
+    x[1] = ldexpf(lo[1], k);
+    x[2] = ldexpf(hi[0], k);
+    x[3] = ldexpf(hi[1], k);
+  } else {
+    const int k = static_cast<int>(s) - StateFormat<F>::top;
+    x[0] = ldexpf(__uint_as_float((w << 20) & 0x0ff00000u), k);
+    x[1] = ldexpf(__uint_as_float((w << 12) & 0x0ff00000u), k);
+    x[2] = ldexpf(__uint_as_float((w << 4) & 0x0ff00000u), k);
+    x[3] = ldexpf(__uint_as_float((w >> 4) & 0x0ff00000u), k);
+    if ((~w - 0x01010101u) & w & 0x80808080u) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) x[i] = decode1<F>((w >> (8 * i)) & 0xffu, s);
+      for (int i = 0; i < 4; ++i)
+        if (((w >> (8 * i)) & 0xffu) == 0xffu) x[i] = __uint_as_float(0x7fc00000u);
+    }
+  }
 }
 
 // Elements a wave takes at once, and the largest n of a call.

@@ -59,8 +59,9 @@ __global__ void __launch_bounds__(256) quantise_kernel(ConvertArgs a) {
         uint32_t m = 0;
 #pragma unroll
         for (int i = 0; i < 4; ++i) m = magnitude(x[i]) > m ? magnitude(x[i]) : m;
-        const uint32_t s = exponent_byte<F>(block_max(m));
-        const uint32_t c = encode_quad<F, RANDOM>(x, s, w);
+        m = block_max(m);
+        const uint32_t s = exponent_byte<F>(m);
+        const uint32_t c = encode_quad<F, RANDOM>(x, s, m, w);
         uint8_t *d = static_cast<uint8_t *>(a.dst);
         if (VEC && whole) {
           st_stream(reinterpret_cast<uint32_t *>(d + e), c);
