@@ -52,4 +52,9 @@ __device__ __forceinline__ void adam_elem(float x, const ElemConsts &c, float &p
   p = p - c.step_size * (m / denom);
 }
 
+// Scheduling priority of a wave: raised while it issues its loads and stores,
+// lowered for the update.
+__device__ __forceinline__ void memory_phase() { __builtin_amdgcn_s_setprio(3); }
+__device__ __forceinline__ void update_phase() { __builtin_amdgcn_s_setprio(0); }
+
 }  // namespace zds

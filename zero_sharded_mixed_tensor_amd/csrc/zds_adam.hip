@@ -92,11 +92,6 @@ struct AdamArgs {
   int64_t n;
 };
 
-// Scheduling priority of a wave: raised while it issues its loads and stores,
-// lowered for the update.
-__device__ __forceinline__ void memory_phase() { __builtin_amdgcn_s_setprio(3); }
-__device__ __forceinline__ void update_phase() { __builtin_amdgcn_s_setprio(0); }
-
 // Wide wave-specialised variant: one tile of 1024 elements per 8-wave block,
 // in two halves of 512. Waves 0-1 move the master tile, 2-3 m, 4-5 v: wave w
 // holds quarter (w & 1) of each half, one 1 KiB access per half. 16-bit

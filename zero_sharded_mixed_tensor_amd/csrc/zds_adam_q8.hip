@@ -20,109 +20,190 @@ struct AdamQ8Args {
   int64_t n;
   uint64_t seed;
   int64_t first;
+  int64_t tile0;  // the launch's first tile
 };
 
-// One unit of 512 elements by a wave: each lane a quad of either half. FULL:
-// the unit lies inside the arrays, and they are aligned.
-template <int GD, int PD, int VF, bool FULL>
-__device__ __forceinline__ void q8_unit(const AdamQ8Args &a, const ElemConsts &c, int64_t u, uint32_t steps, int lane) {
-  const QuadBits rb = unit_random_bits(a.seed, static_cast<uint64_t>((a.first + u * kStateUnit) >> 3), steps, lane);
+// One element on each lane, the block of 32 that shares an exponent in half a
+// wave: what is not a whole tile, and arrays without the tiles' alignment. All
+// lanes of a wave call it; e is past the end on some.
+template <int GD, int PD, int VF>
+__device__ __forceinline__ void q8_element(const AdamQ8Args &a, const ElemConsts &c, int64_t e, uint32_t steps) {
+  const bool in = e < a.n;
   uint8_t *mc = static_cast<uint8_t *>(a.m);
   uint8_t *vc = static_cast<uint8_t *>(a.v);
   uint16_t *v16 = static_cast<uint16_t *>(a.v);
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const int64_t e = u * kStateUnit + 256 * h + 4 * lane;
-    const bool any = FULL || e < a.n;
-    float g[4], p[4], m[4], v[4];
-    uint32_t mw = 0, vw = 0;
-    const uint32_t ms = any ? a.me[e >> 5] : 0u;
-    const uint32_t vs = VF != ZDS_STATE_BF16 && any ? a.ve[e >> 5] : 0u;
-    if (FULL) {
-      load_quad<GD>(a.g, e >> 2, g);
-      load_quad<ZDS_FP32>(a.p, e >> 2, p);
-      mw = ld_stream(reinterpret_cast<const uint32_t *>(mc + e));
-      if constexpr (VF == ZDS_STATE_BF16) load_quad<ZDS_BF16>(a.v, e >> 2, v);
-      else vw = ld_stream(reinterpret_cast<const uint32_t *>(vc + e));
-    } else {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const bool in = e + i < a.n;
-        g[i] = in ? widen1<GD>(a.g, e + i) : 0.0f;
-        p[i] = in ? a.p[e + i] : 0.0f;
-        mw |= (in ? static_cast<uint32_t>(mc[e + i]) : 0u) << (8 * i);
-        if constexpr (VF == ZDS_STATE_BF16) v[i] = in ? widen1<ZDS_BF16>(a.v, e + i) : 0.0f;
-        else vw |= (in ? static_cast<uint32_t>(vc[e + i]) : 0u) << (8 * i);
-      }
-    }
-    decode_quad<ZDS_STATE_E4M3>(mw, ms, m);
-    if constexpr (VF != ZDS_STATE_BF16) decode_quad<VF>(vw, vs, v);
-    uint32_t mm = 0, vm = 0;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      adam_elem(g[i], c, p[i], m[i], v[i]);
-      if (!FULL && e + i >= a.n) m[i] = v[i] = 0.0f;
-      mm = magnitude(m[i]) > mm ? magnitude(m[i]) : mm;
-      vm = magnitude(v[i]) > vm ? magnitude(v[i]) : vm;
-    }
-    const uint32_t (&w)[2] = h ? rb.r1 : rb.r0;
-    mm = block_max(mm);
-    const uint32_t ms1 = exponent_byte<ZDS_STATE_E4M3>(mm);
-    mw = encode_quad<ZDS_STATE_E4M3, true>(m, ms1, mm, w);
-    u32x2 v2{};
-    uint32_t vs1 = 0;
-    if constexpr (VF == ZDS_STATE_BF16) {
-      v2 = encode_quad_bf16<true>(v, w);
-    } else {
-      vm = block_max(vm);
-      vs1 = exponent_byte<VF>(vm);
-      vw = encode_quad<VF, true, true>(v, vs1, vm, w);
-    }
-    if (FULL) {
-      store_quad(a.p, e >> 2, p);
-      if constexpr (PD >= 0) store_quad16<PD>(a.out, e >> 2, p);
-      st_stream(reinterpret_cast<uint32_t *>(mc + e), mw);
-      if constexpr (VF == ZDS_STATE_BF16) st_stream(reinterpret_cast<u32x2 *>(v16 + e), v2);
-      else st_stream(reinterpret_cast<uint32_t *>(vc + e), vw);
-    } else {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if (e + i >= a.n) break;
-        a.p[e + i] = p[i];
-        if constexpr (PD >= 0) static_cast<uint16_t *>(a.out)[e + i] = narrow1<PD>(p[i]);
-        mc[e + i] = static_cast<uint8_t>(mw >> (8 * i));
-        if constexpr (VF == ZDS_STATE_BF16) v16[e + i] = static_cast<uint16_t>((i < 2 ? v2.x : v2.y) >> (16 * (i & 1)));
-        else vc[e + i] = static_cast<uint8_t>(vw >> (8 * i));
-      }
-    }
-    if ((lane & 7) == 0 && any) {
-      a.me[e >> 5] = static_cast<uint8_t>(ms1);
-      if constexpr (VF != ZDS_STATE_BF16) a.ve[e >> 5] = static_cast<uint8_t>(vs1);
-    }
+  float p = 0.0f, m = 0.0f, v = 0.0f;
+  if (in) {
+    p = a.p[e];
+    m = decode1<ZDS_STATE_E4M3>(mc[e], a.me[e >> 5]);
+    if constexpr (VF == ZDS_STATE_BF16) v = __uint_as_float(static_cast<uint32_t>(v16[e]) << 16);
+    else v = decode1<VF>(vc[e], a.ve[e >> 5]);
+    adam_elem(widen1<GD>(a.g, e), c, p, m, v);
+  }
+  const uint32_t r = element_random_bits(a.seed, static_cast<uint64_t>(a.first + e), steps);
+  const uint32_t rs = swap_bytes(r);
+  const uint32_t ms = exponent_byte<ZDS_STATE_E4M3>(block_max_lanes(magnitude(m)));
+  const uint32_t mcode = encode1<ZDS_STATE_E4M3, true>(m, ms, r);
+  uint32_t vs = 0, vcode;
+  if constexpr (VF == ZDS_STATE_BF16) {
+    vcode = encode_bf16<true>(v, rs);
+  } else {
+    vs = exponent_byte<VF>(block_max_lanes(magnitude(v)));
+    vcode = encode1<VF, true>(v, vs, rs);
+  }
+  if (!in) return;
+  a.p[e] = p;
+  if constexpr (PD >= 0) static_cast<uint16_t *>(a.out)[e] = narrow1<PD>(p);
+  mc[e] = static_cast<uint8_t>(mcode);
+  if constexpr (VF == ZDS_STATE_BF16) v16[e] = static_cast<uint16_t>(vcode);
+  else vc[e] = static_cast<uint8_t>(vcode);
+  if ((threadIdx.x & 31) == 0) {
+    a.me[e >> 5] = static_cast<uint8_t>(ms);
+    if constexpr (VF != ZDS_STATE_BF16) a.ve[e >> 5] = static_cast<uint8_t>(vs);
   }
 }
 
-// PD: the params' type, -1 for none.
-template <int GD, int PD, int VF, bool VEC>
-__global__ void __launch_bounds__(256) adam_q8_kernel(AdamQ8Args a) {
+// Elements of a tile: one quad for each thread of a block.
+constexpr int kQ8Block = 512;
+constexpr int kQ8Tile = 4 * kQ8Block;
+
+// What the waves of a block hand each other: what they move 16 bytes a lane
+// and use a quad a lane, and the generator's calls (one for 8 elements).
+template <int VF>
+struct Q8Tile {
+  u32x4 io[256];  // 16-bit grads in, 16-bit params out
+  u32x4 m[128];   // codes, in and out
+  u32x4 v[VF == ZDS_STATE_BF16 ? 256 : 128];
+  u32x4 random[256];
+  uint8_t me[64], ve[64];
+};
+
+// One tile a block, and a last block for the elements behind the last whole
+// tile. PD: the params' type, -1 for none.
+template <int GD, int PD, int VF>
+__global__ void __launch_bounds__(kQ8Block, 8) adam_q8_tile_kernel(AdamQ8Args a) {
+  __shared__ Q8Tile<VF> sh;
+  constexpr bool WIDE = VF == ZDS_STATE_BF16;
   if (a.sc->overflow) return;  // the step is skipped: uniform, nothing is touched
   const ElemConsts c = load_consts(a.sc);
   const uint32_t steps = a.state->steps_seen;
-  const int lane = threadIdx.x & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int64_t units = (a.n + kStateUnit - 1) / kStateUnit;
-  for (int64_t u = static_cast<int64_t>(blockIdx.x) * 4 + wave; u < units; u += static_cast<int64_t>(gridDim.x) * 4) {
-    if (VEC && (u + 1) * kStateUnit <= a.n) q8_unit<GD, PD, VF, VEC>(a, c, u, steps, lane);
-    else q8_unit<GD, PD, VF, false>(a, c, u, steps, lane);
+  const int t = threadIdx.x, lane = t & 63;
+  const int64_t first = (a.tile0 + blockIdx.x) * kQ8Tile;
+  if (first + kQ8Tile > a.n) {
+    for (int64_t e = first + t; e < ((a.n + 63) & ~int64_t(63)); e += kQ8Block) q8_element<GD, PD, VF>(a, c, e, steps);
+    return;
   }
+  const int w = __builtin_amdgcn_readfirstlane(t >> 6);
+  uint16_t *gp = static_cast<uint16_t *>(const_cast<void *>(a.g)) + first;
+  uint8_t *mp = static_cast<uint8_t *>(a.m) + first;
+  uint8_t *vp = static_cast<uint8_t *>(a.v) + (WIDE ? 2 * first : first);
+  float *pp = a.p + first;
+  // The pieces that this wave moves: 16-bit grads (and params) by waves 0-3;
+  // 8-bit codes of m by waves 4-5 and of v by waves 6-7; a 16-bit v by waves
+  // 4-7, and then m by waves 2-3.
+  const bool has_g = GD != ZDS_FP32 && w < 4, has_o = PD >= 0 && w < 4;
+  const bool has_m = WIDE ? w == 2 || w == 3 : w == 4 || w == 5;
+  const bool has_v = WIDE ? w >= 4 : w >= 6;
+  const uint32_t at_m = 16 * (t - (WIDE ? 128 : 256)), at_v = 16 * (t - (WIDE ? 256 : 384));
+  memory_phase();
+  u32x4 x0{}, x1{};
+  uint32_t eb = 0;
+  if (has_g) x0 = ld_stream_global(reinterpret_cast<const u32x4 *>(gp) + t);
+  if (has_m) x1 = ld_stream_global(reinterpret_cast<const u32x4 *>(mp + at_m));
+  if (has_v) x0 = ld_stream_global(reinterpret_cast<const u32x4 *>(vp + at_v));
+  if (w == 4) eb = a.me[(first >> 5) + lane];
+  if (!WIDE && w == 6) eb = a.ve[(first >> 5) + lane];
+  const f32x4 p4 = ld_stream_global(reinterpret_cast<const f32x4 *>(pp) + t);
+  f32x4 g4{};
+  if (GD == ZDS_FP32) g4 = ld_stream_global(reinterpret_cast<const f32x4 *>(static_cast<const float *>(a.g) + first) + t);
+  update_phase();
+  if (w < 4) {
+    const RandomWords q = random_words(a.seed, static_cast<uint64_t>((a.first + first) >> 3) + t, steps, kStreamRounding);
+    sh.random[t] = u32x4{q.w[0], q.w[1], q.w[2], q.w[3]};
+  }
+  uint8_t *sm = reinterpret_cast<uint8_t *>(sh.m), *sv = reinterpret_cast<uint8_t *>(sh.v);
+  if (has_g) sh.io[t] = x0;
+  if (has_m) *reinterpret_cast<u32x4 *>(sm + at_m) = x1;
+  if (has_v) *reinterpret_cast<u32x4 *>(sv + at_v) = x0;
+  if (w == 4) sh.me[lane] = static_cast<uint8_t>(eb);
+  if (!WIDE && w == 6) sh.ve[lane] = static_cast<uint8_t>(eb);
+  __syncthreads();
+  float g[4], p[4] = {p4.x, p4.y, p4.z, p4.w}, m[4], v[4];
+  u32x2 *io2 = reinterpret_cast<u32x2 *>(sh.io);
+  if constexpr (GD == ZDS_FP32) {
+    g[0] = g4.x; g[1] = g4.y; g[2] = g4.z; g[3] = g4.w;
+  } else {
+    const u32x2 q = io2[t];
+    g[0] = lo_of<GD>(q.x); g[1] = hi_of<GD>(q.x); g[2] = lo_of<GD>(q.y); g[3] = hi_of<GD>(q.y);
+  }
+  uint32_t *sm1 = reinterpret_cast<uint32_t *>(sh.m), *sv1 = reinterpret_cast<uint32_t *>(sh.v);
+  u32x2 *sv2 = reinterpret_cast<u32x2 *>(sh.v);
+  decode_quad<ZDS_STATE_E4M3>(sm1[t], sh.me[t >> 3], m);
+  if constexpr (WIDE) {
+    const u32x2 q = sv2[t];
+    v[0] = bf16_lo(q.x); v[1] = bf16_hi(q.x); v[2] = bf16_lo(q.y); v[3] = bf16_hi(q.y);
+  } else {
+    decode_quad<VF>(sv1[t], sh.ve[t >> 3], v);
+  }
+  uint32_t mm = 0, vm = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    adam_elem(g[i], c, p[i], m[i], v[i]);
+    mm = magnitude(m[i]) > mm ? magnitude(m[i]) : mm;
+    vm = magnitude(v[i]) > vm ? magnitude(v[i]) : vm;
+  }
+  st_stream_at(pp, 16 * t, f32x4{p[0], p[1], p[2], p[3]});
+  const u32x2 rr = reinterpret_cast<const u32x2 *>(sh.random)[t];
+  const uint32_t rw[2] = {rr.x, rr.y};
+  mm = block_max(mm);
+  const uint32_t ms = exponent_byte<ZDS_STATE_E4M3>(mm);
+  sm1[t] = encode_quad<ZDS_STATE_E4M3, true>(m, ms, mm, rw);
+  if ((lane & 7) == 0) sh.me[t >> 3] = static_cast<uint8_t>(ms);
+  if constexpr (WIDE) {
+    sv2[t] = encode_quad_bf16<true>(v, rw);
+  } else {
+    vm = block_max(vm);
+    const uint32_t vs = exponent_byte<VF>(vm);
+    sv1[t] = encode_quad<VF, true, true>(v, vs, vm, rw);
+    if ((lane & 7) == 0) sh.ve[t >> 3] = static_cast<uint8_t>(vs);
+  }
+  if constexpr (PD >= 0) io2[t] = u32x2{pack2<PD>(p[0], p[1]), pack2<PD>(p[2], p[3])};
+  __syncthreads();
+  memory_phase();
+  if (has_o) st_stream_at(static_cast<uint16_t *>(a.out) + first, 16 * t, sh.io[t]);
+  if (has_m) st_stream_at(mp, at_m, *reinterpret_cast<u32x4 *>(sm + at_m));
+  if (has_v) st_stream_at(vp, at_v, *reinterpret_cast<u32x4 *>(sv + at_v));
+  if (w == 4) a.me[(first >> 5) + lane] = sh.me[lane];
+  if (!WIDE && w == 6) a.ve[(first >> 5) + lane] = sh.ve[lane];
+}
+
+// Element by element.
+template <int GD, int PD, int VF>
+__global__ void __launch_bounds__(256) adam_q8_element_kernel(AdamQ8Args a) {
+  if (a.sc->overflow) return;
+  const ElemConsts c = load_consts(a.sc);
+  const uint32_t steps = a.state->steps_seen;
+  for (int64_t e = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; e < ((a.n + 63) & ~int64_t(63));
+       e += static_cast<int64_t>(gridDim.x) * 256)
+    q8_element<GD, PD, VF>(a, c, e, steps);
 }
 
 template <int GD, int PD, int VF>
 static void q8_go(bool vec, const AdamQ8Args &a, hipStream_t s) {
-  int64_t g = (a.n + 4 * kStateUnit - 1) / (4 * kStateUnit);
-  if (g > max_blocks(256)) g = max_blocks(256);
-  if (vec) hipLaunchKernelGGL((adam_q8_kernel<GD, PD, VF, true>), dim3(static_cast<uint32_t>(g)), dim3(256), 0, s, a);
-  else hipLaunchKernelGGL((adam_q8_kernel<GD, PD, VF, false>), dim3(static_cast<uint32_t>(g)), dim3(256), 0, s, a);
+  if (!vec) {
+    int64_t g = (a.n + 255) / 256;
+    if (g > max_blocks(256)) g = max_blocks(256);
+    hipLaunchKernelGGL((adam_q8_element_kernel<GD, PD, VF>), dim3(static_cast<uint32_t>(g)), dim3(256), 0, s, a);
+    return;
+  }
+  AdamQ8Args b = a;
+  const int64_t tiles = (a.n + kQ8Tile - 1) / kQ8Tile;
+  for (b.tile0 = 0; b.tile0 < tiles; b.tile0 += max_blocks(kQ8Block)) {  // one launch below 2^34 elements
+    const int64_t left = tiles - b.tile0;
+    hipLaunchKernelGGL((adam_q8_tile_kernel<GD, PD, VF>),
+                       dim3(static_cast<uint32_t>(left < max_blocks(kQ8Block) ? left : max_blocks(kQ8Block))),
+                       dim3(kQ8Block), 0, s, b);
+  }
 }
 template <int GD, int PD>
 static void q8_vf(zds_state_format f, bool vec, const AdamQ8Args &a, hipStream_t s) {
@@ -184,9 +265,9 @@ extern "C" zds_status zds_adam_step_q8(const zds_adamw_hparams *hp, const void *
   st = launch_adam_constants(*hp, state_dev, scalars_dev, s);
   if (st != ZDS_OK) return st;
   const AdamQ8Args a{scalars_dev, state_dev,       grads,      master, exp_avg, exp_avg_exps,
-                     exp_avg_sq,  exp_avg_sq_exps, params_out, n,      seed,    first};
-  const bool vec = aligned(grads, grad_dtype == ZDS_FP32 ? 16 : 8) && aligned(master, 16) && aligned(exp_avg, 4) &&
-                   aligned(exp_avg_sq, wide ? 8 : 4) && (!params_out || aligned(params_out, 8));
+                     exp_avg_sq,  exp_avg_sq_exps, params_out, n,      seed,    first,        0};
+  const bool vec = aligned(grads, 16) && aligned(master, 16) && aligned(exp_avg, 16) && aligned(exp_avg_sq, 16) &&
+                   (!params_out || aligned(params_out, 16));
   switch (grad_dtype) {
     case ZDS_FP16: q8_pd<ZDS_FP16>(param_dtype, sq_format, vec, a, s); break;
     case ZDS_BF16: q8_pd<ZDS_BF16>(param_dtype, sq_format, vec, a, s); break;

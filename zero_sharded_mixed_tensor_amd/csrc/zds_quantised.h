@@ -43,6 +43,14 @@ __device__ __forceinline__ uint32_t block_max(uint32_t a) {
   return a;
 }
 
+// The same over the 32 lanes of a block that has one element on each.
+__device__ __forceinline__ uint32_t block_max_lanes(uint32_t a) {
+  const auto over = [](uint32_t x, uint32_t y) { return x > y ? x : y; };
+  a = block_max(a);
+  a = over(a, static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(a), 0x128, 0xf, 0xf, false)));  // row_ror:8
+  return over(a, static_cast<uint32_t>(__builtin_amdgcn_ds_swizzle(static_cast<int>(a), 0x401f)));  // lane ^ 16
+}
+
 // Exponent byte of a block whose largest magnitude has these bits: its
 // exponent field, one more over 1.75.
 template <int F>
@@ -66,6 +74,15 @@ __device__ __forceinline__ uint32_t encode1(float x, uint32_t s, uint32_t r) {
   }
   c = mag >= 0x7f800000u ? 0x7fu : c;
   return c | ((bits >> 24) & 0x80u);
+}
+
+// The value of one code.
+template <int F>
+__device__ __forceinline__ float decode1(uint32_t code, uint32_t s) {
+  const uint32_t mag = code & StateFormat<F>::mask;
+  const float x = ldexpf(__uint_as_float(mag << 20), static_cast<int>(s) - StateFormat<F>::top);
+  if (mag == StateFormat<F>::mask) return __uint_as_float(0x7fc00000u);
+  return F == ZDS_STATE_E4M3 && code > 0x7fu ? -x : x;
 }
 
 // The 16-bit format: the value's top bits.
@@ -101,14 +118,22 @@ __device__ __forceinline__ QuadBits unit_random_bits(uint64_t seed, uint64_t cal
   return odd ? QuadBits{{t0, t1}, {q.w[2], q.w[3]}} : QuadBits{{q.w[0], q.w[1]}, {t0, t1}};
 }
 
+// The 16 random bits of the element with flat index f.
+__device__ __forceinline__ uint32_t element_random_bits(uint64_t seed, uint64_t f, uint32_t steps_seen) {
+  const RandomWords q = random_words(seed, f >> 3, steps_seen, kStreamRounding);
+  const uint32_t lo = (f & 2) ? q.w[1] : q.w[0], hi = (f & 2) ? q.w[3] : q.w[2];
+  const uint32_t w = (f & 4) ? hi : lo;
+  return (f & 1) ? w >> 16 : w & 0xffffu;
+}
+
 // Four codes of a quad in a word. amax: the block's largest magnitude; w: the
-// quad's 8 random bytes. The rounding is added to the bits of the scaled values
-// (the sign stays at the top: a magnitude's sum never reaches it), the upper
-// halves of two of them make a word, and the code's bits move to that word's
-// bytes 0 and 2. What the formats say of special values is left to a branch
-// that a wave takes only where it holds one: infinities and NaN are known from
-// amax, and a UE5M3 code 0 from the least sum. A UE5M3 value must not be
-// negative here (NONNEGATIVE: none is; else it is looked at).
+// quad's 8 random bytes. (z + 16 r + 8) >> 20 is ((z + 8) >> 4) + r, shifted by
+// 16, so that each random half is added as it lies; the code is then the upper
+// half's low byte (the sign stays four bits above it: a magnitude's sum never
+// reaches it), and byte permutations gather the four. What the formats say of
+// special values is left to a branch that a wave takes only where it holds one:
+// infinities and NaN are known from amax, a UE5M3 code 0 from the least sum, a
+// negative value (where NONNEGATIVE does not rule them out) from the largest.
 template <int F, bool RANDOM, bool NONNEGATIVE = false>
 __device__ __forceinline__ uint32_t encode_quad(const float (&x)[4], uint32_t s, uint32_t amax, const uint32_t (&w)[2]) {
   const uint32_t a = F == ZDS_STATE_E4M3 ? w[0] : swap_bytes(w[0]), b = F == ZDS_STATE_E4M3 ? w[1] : swap_bytes(w[1]);
@@ -118,16 +143,13 @@ __device__ __forceinline__ uint32_t encode_quad(const float (&x)[4], uint32_t s,
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const uint32_t z = __float_as_uint(ldexpf(x[i], k));
-    t[i] = RANDOM ? z + (r[i] << 4) + 8u : z + 0x7ffffu + ((z >> 20) & 1u);
+    t[i] = RANDOM ? ((z + 8u) >> 4) + r[i] : (z + 0x7ffffu + ((z >> 20) & 1u)) >> 4;
   }
   // (selectors 0-3 name bytes of the second operand, 4-7 of the first)
   uint32_t p = __builtin_amdgcn_perm(t[1], t[0], 0x07060302u), q = __builtin_amdgcn_perm(t[3], t[2], 0x07060302u);
   if (F == ZDS_STATE_E4M3) {
-    p = (0x00800080u & (p >> 8)) | (0xff7fff7fu & (p >> 4));
-    q = (0x00800080u & (q >> 8)) | (0xff7fff7fu & (q >> 4));
-  } else {
-    p >>= 4;
-    q >>= 4;
+    p |= (p >> 4) & 0x00800080u;
+    q |= (q >> 4) & 0x00800080u;
   }
   uint32_t c = __builtin_amdgcn_perm(q, p, 0x06040200u);
   bool special = amax >= 0x7f800000u;
@@ -139,7 +161,7 @@ __device__ __forceinline__ uint32_t encode_quad(const float (&x)[4], uint32_t s,
       least = t[i] < least ? t[i] : least;
       most = t[i] > most ? t[i] : most;
     }
-    special = special || least < 0x100000u || (!NONNEGATIVE && most >= 0x80000000u);
+    special = special || least < 0x10000u || (!NONNEGATIVE && most >= 0x8000000u);
   }
   if (special)
     c = encode1<F, RANDOM>(x[0], s, r[0]) | (encode1<F, RANDOM>(x[1], s, r[1]) << 8) |
