@@ -702,10 +702,15 @@ zds_status zds_state_dequantise(const void *codes, const uint8_t *exps, int64_t 
                                 zds_dtype dst_dtype, void *stream);
 
 /* zds_adam_step on moments in fewer bits: reads both back, applies the same
- * update, and quantises what it writes at random: master and params_out are
- * those of zds_adam_step on the state that zds_state_dequantise gives, and the
- * codes those of zds_state_quantise (ZDS_ROUND_RANDOM, the same seed and
- * first) on the moments it leaves, bit for bit.
+ * update, and quantises what it writes at random. The moments are those that
+ * zds_adam_step leaves of the state that zds_state_dequantise gives, and the
+ * codes those that zds_state_quantise makes of them (ZDS_ROUND_RANDOM, the same
+ * seed and first), bit for bit. The update's root and quotient are within 1 ulp
+ * each instead of correctly rounded: with u = lr / (1 - b1^t) * (m / denom),
+ * master differs from zds_adam_step's by at most 2^-20 |u| and one rounding
+ * (where v is below 2^104; from there on it counts as infinite), and params_out
+ * is its cast.
+ *   hp            as for zds_adam_step, but eps >= 2^-100
  *   exp_avg       device, n codes of E4M3, with exp_avg_exps
  *   exp_avg_sq    device, n codes of sq_format (UE5M3 with exp_avg_sq_exps, or
  *                 BF16 with NULL)

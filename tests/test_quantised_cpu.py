@@ -200,7 +200,7 @@ def step_args(**kw):
 def test_step_refusals():
     fn = "zds_adam_step_q8"
     for kw, text in ((dict(hp=None), "hparams"), (dict(hp=zds.hparams(beta1=0.3)), "betas"),
-                     (dict(hp=zds.hparams(eps=0.0)), "eps"), (dict(hp=zds.hparams(lr=float("nan"))), "lr"),
+                     (dict(hp=zds.hparams(eps=0.0)), "eps"), (dict(hp=zds.hparams(eps=1e-31)), "eps"), (dict(hp=zds.hparams(lr=float("nan"))), "lr"),
                      (dict(gdt=5), "grad dtype"), (dict(pdt=2), "param dtype"), (dict(fmt=0), "second moment"),
                      (dict(fmt=3), "second moment"), (dict(n=-1), "n must"), (dict(n=1 << 40), "n must"),
                      (dict(first=33), "first"), (dict(first=-32), "first"),
