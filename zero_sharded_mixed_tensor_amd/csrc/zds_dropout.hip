@@ -2,17 +2,23 @@
 // `ratio` consecutive elements sends one, chosen by the counter-based
 // generator (include/zds.h has the definition, zds_random.h the generator).
 //
-// Every kernel works on tiles: a block first makes the kept places of the
-// tile's groups in LDS (one generator call covers 16 groups), then streams.
+// Four streams, all bound by HBM. With feedback, encoding reads x and the error
+// and writes the error (2 or 4 + 8 B an element) and the values; without, it
+// reads one element of each group. Decoding writes the whole gradient (4 or 2 B
+// an element) or, when it adds, reads and writes one element of each group.
+// A block first makes the kept places of its groups in LDS: one call of the
+// generator covers 16 groups, so its arithmetic does not show.
 #include "zds_internal.h"
 #include "zds_quantised.h"
 
 namespace zds {
 
-// Elements of a tile of the kernels that walk a gradient, and groups of a tile
-// of those that walk a message.
-constexpr int kDropTile = 4096;
-constexpr int kDropGroups = 4096;
+// Elements of a block's tile where a gradient is encoded, and where one is
+// written; groups of a block where single elements are read or added to.
+constexpr int kEncodeBlock = 512;
+constexpr int kEncodeTile = 4 * kEncodeBlock;
+constexpr int kSpreadTile = 16384;
+constexpr int kDropGroups = 1024;
 
 struct DropArgs {
   const void *x;
@@ -25,6 +31,7 @@ struct DropArgs {
   uint64_t seed;
   int32_t shift;     // log2(ratio)
   int32_t npeers;
+  int64_t tile0;     // the launch's first tile
   const zds_step_scalars *sc;
   const zds_step_state *state;
 };
@@ -59,82 +66,103 @@ __device__ __forceinline__ float put(void *base, int64_t i, float x) {
   }
 }
 
-template <int XD, bool VEC>
-__device__ __forceinline__ void load_x(const void *p, int64_t e, int64_t n, bool whole, float (&x)[4]) {
-  if (VEC && whole) {
-    load_quad<XD>(p, e >> 2, x);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) x[i] = e + i < n ? widen1<XD>(p, e + i) : 0.0f;
+// What becomes of element e with c = x + scale * error: sent if it is kept, and
+// the new error. in: its place in its group, place: the kept one; at: where the
+// value goes (value(at) stores it and returns it as stored).
+template <typename Put>
+__device__ __forceinline__ float encode_element(float c, float inv, int in, int place, bool missing, const Put &value) {
+  if (in == place) {
+    const float sent = value(c);
+    if (magnitude(sent) < 0x7f800000u) c = c - sent;
+  } else if (missing && in == 0) {
+    value(0.0f);  // the place of a cut last group lies past the end
+  }
+  return c * inv;
+}
+
+// A tile, or what there is of it, by a block, one element by one.
+template <int XD, int D>
+__device__ __forceinline__ void encode_elements(const DropArgs &a, int64_t first, float scale, float inv, uint8_t *kept) {
+  const int64_t g0 = first >> a.shift;
+  const int mask = (1 << a.shift) - 1;
+  const int off = make_kept(a, g0, kEncodeTile >> a.shift, kept);
+  for (int k = threadIdx.x; k < kEncodeTile && first + k < a.n; k += kEncodeBlock) {
+    const int64_t e = first + k;
+    const int in = k & mask, g = k >> a.shift, place = kept[off + g] >> (8 - a.shift);
+    const float c = widen1<XD>(a.x, e) + scale * a.err[e];
+    a.err[e] = encode_element(c, inv, in, place, e - in + place >= a.n, [&](float v) { return put<D>(a.values, g0 + g, v); });
   }
 }
 
-// With error feedback: reads x and the error, writes the error and the values.
+// With error feedback. A block takes a tile of 2048 elements, each thread a
+// quad; 16-bit x comes in 16 bytes a lane by waves 0-3, and the values go out
+// so, through LDS; a wave has one load in flight. VEC: whole tiles are aligned.
 template <int XD, int D, bool VEC>
-__global__ void __launch_bounds__(256) dropout_encode_kernel(DropArgs a) {
-  __shared__ __align__(16) uint8_t kept[kDropTile / 2 + 32];
-  const int64_t tiles = (a.n + kDropTile - 1) / kDropTile;
-  const int ratio = 1 << a.shift;
-  const bool skip = a.sc && a.sc->overflow;
-  const float scale = a.state->scale, inv = 1.0f / scale;
-  for (int64_t t = blockIdx.x; t < tiles; t += gridDim.x) {
-    const int64_t g0 = (t * kDropTile) >> a.shift;
-    const int off = make_kept(a, g0, kDropTile >> a.shift, kept);
-    for (int q = threadIdx.x; q < kDropTile / 4; q += 256) {
-      const int64_t e = t * kDropTile + 4 * q;
-      if (e >= a.n) break;
-      const bool whole = e + 4 <= a.n;
-      if (skip) {
-        for (int i = 0; i < 4; ++i)
-          if (e + i < a.n && ((4 * q + i) & (ratio - 1)) == 0) put<D>(a.values, (e + i) >> a.shift, __uint_as_float(0x7fc00000u));
-        continue;
-      }
-      float x[4], er[4];
-      load_x<XD, VEC>(a.x, e, a.n, whole, x);
-      load_x<ZDS_FP32, VEC>(a.err, e, a.n, whole, er);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int in = (4 * q + i) & (ratio - 1), k = (4 * q + i) >> a.shift;
-        const int place = kept[off + k] >> (8 - a.shift);
-        float c = x[i] + scale * er[i];
-        if (e + i < a.n) {
-          if (in == place) {
-            const float sent = put<D>(a.values, g0 + k, c);
-            if (magnitude(sent) < 0x7f800000u) c = c - sent;
-          } else if (in == 0 && e + i + place >= a.n) {
-            put<D>(a.values, g0 + k, 0.0f);  // the place of a cut last group lies past the end
-          }
-        }
-        er[i] = c * inv;
-      }
-      if (VEC && whole) {
-        store_quad(a.err, e >> 2, er);
-      } else {
-        for (int i = 0; i < 4; ++i)
-          if (e + i < a.n) a.err[e + i] = er[i];
-      }
-    }
-    __syncthreads();  // the next tile's places
+__global__ void __launch_bounds__(kEncodeBlock) dropout_encode_kernel(DropArgs a) {
+  __shared__ __align__(16) uint8_t kept[kEncodeTile / 2 + 32];
+  __shared__ u32x4 xs[kEncodeTile / 8];
+  __shared__ u32x4 out[kEncodeTile / (D == ZDS_FP32 ? 8 : 16)];
+  const int t = threadIdx.x;
+  const int w = __builtin_amdgcn_readfirstlane(t >> 6);
+  const int64_t first = (a.tile0 + blockIdx.x) * kEncodeTile;
+  const int64_t g0 = first >> a.shift;
+  const int groups = kEncodeTile >> a.shift, mask = (1 << a.shift) - 1;
+  if (a.sc && a.sc->overflow) {  // uniform
+    for (int k = t; k < groups && g0 + k < a.groups; k += kEncodeBlock) put<D>(a.values, g0 + k, __uint_as_float(0x7fc00000u));
+    return;
   }
+  const float scale = a.state->scale, inv = 1.0f / scale;
+  if (!VEC || first + kEncodeTile > a.n) {
+    encode_elements<XD, D>(a, first, scale, inv, kept);
+    return;
+  }
+  float *err = a.err + first;
+  f32x4 xf{};
+  if (XD == ZDS_FP32) {
+    xf = ld_stream_global(reinterpret_cast<const f32x4 *>(static_cast<const float *>(a.x) + first) + t);
+    wait_vmem();
+  } else if (w < 4) {
+    xs[t] = ld_stream_global(reinterpret_cast<const u32x4 *>(static_cast<const uint16_t *>(a.x) + first) + t);
+  }
+  const f32x4 e4 = ld_stream_global(reinterpret_cast<const f32x4 *>(err) + t);
+  const int off = make_kept(a, g0, groups, kept);
+  float x[4], er[4] = {e4.x, e4.y, e4.z, e4.w};
+  if constexpr (XD == ZDS_FP32) {
+    x[0] = xf.x; x[1] = xf.y; x[2] = xf.z; x[3] = xf.w;
+  } else {
+    const u32x2 q = reinterpret_cast<const u32x2 *>(xs)[t];
+    x[0] = lo_of<XD>(q.x); x[1] = hi_of<XD>(q.x); x[2] = lo_of<XD>(q.y); x[3] = hi_of<XD>(q.y);
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int k = 4 * t + i, g = k >> a.shift, place = kept[off + g] >> (8 - a.shift);
+    er[i] = encode_element(x[i] + scale * er[i], inv, k & mask, place, false, [&](float v) { return put<D>(out, g, v); });
+  }
+  st_stream_at(err, 16 * t, f32x4{er[0], er[1], er[2], er[3]});
+  __syncthreads();
+  constexpr int size = D == ZDS_FP32 ? 4 : 2;
+  if (16 * t < groups * size) st_stream_at(static_cast<uint8_t *>(a.values) + g0 * size, 16 * t, out[t]);
 }
 
 // Without feedback: only the kept elements are read.
 template <int XD, int D>
 __global__ void __launch_bounds__(256) dropout_gather_kernel(DropArgs a) {
   __shared__ __align__(16) uint8_t kept[kDropGroups + 32];
-  const int64_t tiles = (a.groups + kDropGroups - 1) / kDropGroups;
   const float ratio = static_cast<float>(1 << a.shift);
   const bool skip = a.sc && a.sc->overflow;
-  for (int64_t t = blockIdx.x; t < tiles; t += gridDim.x) {
-    const int64_t g0 = t * kDropGroups;
-    const int off = make_kept(a, g0, kDropGroups, kept);
-    for (int k = threadIdx.x; k < kDropGroups && g0 + k < a.groups; k += 256) {
-      const int64_t e = ((g0 + k) << a.shift) + (kept[off + k] >> (8 - a.shift));
-      float v = e < a.n ? ratio * widen1<XD>(a.x, e) : 0.0f;
-      if (skip) v = __uint_as_float(0x7fc00000u);
-      put<D>(a.values, g0 + k, v);
-    }
-    __syncthreads();
+  const int64_t g0 = (a.tile0 + blockIdx.x) * kDropGroups;
+  const int off = make_kept(a, g0, kDropGroups, kept);
+  float v[kDropGroups / 256];
+#pragma unroll
+  for (int i = 0; i < kDropGroups / 256; ++i) {
+    const int k = threadIdx.x + 256 * i;
+    const int64_t e = ((g0 + k) << a.shift) + (kept[off + k] >> (8 - a.shift));
+    v[i] = skip ? __uint_as_float(0x7fc00000u) : e < a.n ? ratio * widen1<XD>(a.x, e) : 0.0f;
+  }
+#pragma unroll
+  for (int i = 0; i < kDropGroups / 256; ++i) {
+    const int k = threadIdx.x + 256 * i;
+    if (g0 + k < a.groups) put<D>(a.values, g0 + k, v[i]);
   }
 }
 
@@ -146,36 +174,77 @@ __device__ __forceinline__ float peer_sum(const DropArgs &a, int64_t g) {
   return t;
 }
 
-// Every element of the gradient is written.
-template <int D, int OD, bool VEC>
-__global__ void __launch_bounds__(256) dropout_spread_kernel(DropArgs a) {
-  __shared__ __align__(16) uint8_t kept[kDropTile / 2 + 32];
-  __shared__ float sum[kDropTile / 2];
-  const int64_t tiles = (a.n + kDropTile - 1) / kDropTile;
-  const int ratio = 1 << a.shift;
-  for (int64_t t = blockIdx.x; t < tiles; t += gridDim.x) {
-    const int64_t g0 = (t * kDropTile) >> a.shift;
-    const int count = kDropTile >> a.shift;
-    for (int k = threadIdx.x; k < count && g0 + k < a.groups; k += 256) sum[k] = peer_sum<D>(a, g0 + k);
-    const int off = make_kept(a, g0, count, kept);
-    for (int q = threadIdx.x; q < kDropTile / 4; q += 256) {
-      const int64_t e = t * kDropTile + 4 * q;
-      if (e >= a.n) break;
-      float o[4];
+// Groups that 16 bytes of a message hold.
+template <int D>
+constexpr int per_piece() {
+  return D == ZDS_FP32 ? 4 : 8;
+}
+template <int D>
+__device__ __forceinline__ void unpack_piece(const u32x4 &q, float (&x)[per_piece<D>()]) {
+  const uint32_t w[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int in = (4 * q + i) & (ratio - 1), k = (4 * q + i) >> a.shift;
-        o[i] = in == (kept[off + k] >> (8 - a.shift)) ? sum[k] : 0.0f;
-      }
-      if (VEC && e + 4 <= a.n) {
-        if constexpr (OD == ZDS_FP32) store_quad(static_cast<float *>(a.dst), e >> 2, o);
-        else store_quad16<OD>(a.dst, e >> 2, o);
-      } else {
-        for (int i = 0; i < 4; ++i)
-          if (e + i < a.n) put<OD>(a.dst, e + i, o[i]);
-      }
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (D == ZDS_FP32) {
+      x[i] = __uint_as_float(w[i]);
+    } else {
+      x[2 * i] = lo_of<D>(w[i]);
+      x[2 * i + 1] = hi_of<D>(w[i]);
     }
-    __syncthreads();
+  }
+}
+
+// Every element of the gradient is written: a tile of 16384 elements a block
+// (or what 2048 groups make, if that is less). The tile's sums are formed 16
+// bytes of a message a lane, then written out a quad (16-bit: two) a lane, one
+// store in flight per wave. VEC: whole tiles are aligned.
+template <int D, int OD, bool VEC>
+__global__ void __launch_bounds__(256) dropout_spread_kernel(DropArgs a, int tile) {
+  constexpr int kGroups = 2048;
+  __shared__ __align__(16) uint8_t kept[kGroups + 32];
+  __shared__ f32x4 sums[kGroups / 4];
+  float *sum = reinterpret_cast<float *>(sums);
+  const int t = threadIdx.x;
+  const int64_t first = (a.tile0 + blockIdx.x) * tile;
+  const int64_t g0 = first >> a.shift;
+  const int groups = tile >> a.shift, mask = (1 << a.shift) - 1;
+  if (!VEC || first + tile > a.n) {
+    for (int k = t; k < groups && g0 + k < a.groups; k += 256) sum[k] = peer_sum<D>(a, g0 + k);
+    const int off = make_kept(a, g0, groups, kept);
+    for (int k = t; k < tile && first + k < a.n; k += 256) {
+      const int g = k >> a.shift;
+      put<OD>(a.dst, first + k, (k & mask) == (kept[off + g] >> (8 - a.shift)) ? sum[g] : 0.0f);
+    }
+    return;
+  }
+  constexpr int P = per_piece<D>();
+  for (int k = t; k * P < groups; k += 256) {
+    float s[P], x[P];
+    const int64_t at = g0 / P + k;  // (a whole tile begins at a multiple of P groups)
+    unpack_piece<D>(ld_stream(static_cast<const u32x4 *>(a.peers[0]) + at), s);
+    for (int j = 1; j < a.npeers; ++j) {
+      unpack_piece<D>(ld_stream(static_cast<const u32x4 *>(a.peers[j]) + at), x);
+#pragma unroll
+      for (int i = 0; i < P; ++i) s[i] = s[i] + x[i];
+    }
+#pragma unroll
+    for (int i = 0; i < P; i += 4) sums[(k * P + i) / 4] = f32x4{s[i], s[i + 1], s[i + 2], s[i + 3]};
+  }
+  const int off = make_kept(a, g0, groups, kept);
+  constexpr int E = OD == ZDS_FP32 ? 4 : 8;
+  for (int q = t; q < tile / E; q += 256) {
+    float o[E];
+#pragma unroll
+    for (int i = 0; i < E; ++i) {
+      const int k = E * q + i, g = k >> a.shift;
+      o[i] = (k & mask) == (kept[off + g] >> (8 - a.shift)) ? sum[g] : 0.0f;
+    }
+    wait_vmem();
+    if constexpr (OD == ZDS_FP32) {
+      st_stream_at(static_cast<float *>(a.dst) + first, 16 * q, f32x4{o[0], o[1], o[2], o[3]});
+    } else {
+      st_stream_at(static_cast<uint16_t *>(a.dst) + first, 16 * q,
+                   u32x4{pack2<OD>(o[0], o[1]), pack2<OD>(o[2], o[3]), pack2<OD>(o[4], o[5]), pack2<OD>(o[6], o[7])});
+    }
   }
 }
 
@@ -183,31 +252,50 @@ __global__ void __launch_bounds__(256) dropout_spread_kernel(DropArgs a) {
 template <int D, int OD>
 __global__ void __launch_bounds__(256) dropout_add_kernel(DropArgs a) {
   __shared__ __align__(16) uint8_t kept[kDropGroups + 32];
-  const int64_t tiles = (a.groups + kDropGroups - 1) / kDropGroups;
-  for (int64_t t = blockIdx.x; t < tiles; t += gridDim.x) {
-    const int64_t g0 = t * kDropGroups;
-    const int off = make_kept(a, g0, kDropGroups, kept);
-    for (int k = threadIdx.x; k < kDropGroups && g0 + k < a.groups; k += 256) {
-      const int64_t e = ((g0 + k) << a.shift) + (kept[off + k] >> (8 - a.shift));
-      if (e < a.n) put<OD>(a.dst, e, widen1<OD>(a.dst, e) + peer_sum<D>(a, g0 + k));
-    }
-    __syncthreads();
+  const int64_t g0 = (a.tile0 + blockIdx.x) * kDropGroups;
+  float s[kDropGroups / 256];
+#pragma unroll
+  for (int i = 0; i < kDropGroups / 256; ++i) {
+    const int64_t g = g0 + threadIdx.x + 256 * i;
+    s[i] = g < a.groups ? peer_sum<D>(a, g) : 0.0f;
+  }
+  const int off = make_kept(a, g0, kDropGroups, kept);
+  float o[kDropGroups / 256];
+#pragma unroll
+  for (int i = 0; i < kDropGroups / 256; ++i) {
+    const int k = threadIdx.x + 256 * i;
+    const int64_t e = ((g0 + k) << a.shift) + (kept[off + k] >> (8 - a.shift));
+    o[i] = e < a.n ? widen1<OD>(a.dst, e) : 0.0f;
+  }
+#pragma unroll
+  for (int i = 0; i < kDropGroups / 256; ++i) {
+    const int k = threadIdx.x + 256 * i;
+    const int64_t e = ((g0 + k) << a.shift) + (kept[off + k] >> (8 - a.shift));
+    if (e < a.n) put<OD>(a.dst, e, o[i] + s[i]);
   }
 }
 
-static uint32_t blocks_for(int64_t items, int per_block) {
-  const int64_t g = (items + per_block - 1) / per_block;
-  return static_cast<uint32_t>(g < max_blocks(256) ? g : max_blocks(256));
+// One block for each of `count` tiles, in launches below 2^32 work-items.
+template <typename Launch>
+static void each_tile(DropArgs a, int64_t count, int threads, const Launch &launch) {
+  const int64_t most = max_blocks(threads);
+  for (a.tile0 = 0; a.tile0 < count; a.tile0 += most)
+    launch(a, dim3(static_cast<uint32_t>(count - a.tile0 < most ? count - a.tile0 : most)));
 }
+static int64_t pieces(int64_t items, int64_t of) { return (items + of - 1) / of; }
 
 template <int XD, int D>
 static void compress_go(const DropArgs &a, bool vec, hipStream_t s) {
-  if (!a.err)
-    hipLaunchKernelGGL((dropout_gather_kernel<XD, D>), dim3(blocks_for(a.groups, kDropGroups)), dim3(256), 0, s, a);
-  else if (vec)
-    hipLaunchKernelGGL((dropout_encode_kernel<XD, D, true>), dim3(blocks_for(a.n, kDropTile)), dim3(256), 0, s, a);
-  else
-    hipLaunchKernelGGL((dropout_encode_kernel<XD, D, false>), dim3(blocks_for(a.n, kDropTile)), dim3(256), 0, s, a);
+  if (!a.err) {
+    each_tile(a, pieces(a.groups, kDropGroups), 256, [&](const DropArgs &b, dim3 g) {
+      hipLaunchKernelGGL((dropout_gather_kernel<XD, D>), g, dim3(256), 0, s, b);
+    });
+    return;
+  }
+  each_tile(a, pieces(a.n, kEncodeTile), kEncodeBlock, [&](const DropArgs &b, dim3 g) {
+    if (vec) hipLaunchKernelGGL((dropout_encode_kernel<XD, D, true>), g, dim3(kEncodeBlock), 0, s, b);
+    else hipLaunchKernelGGL((dropout_encode_kernel<XD, D, false>), g, dim3(kEncodeBlock), 0, s, b);
+  });
 }
 template <int XD>
 static void compress_values(zds_dtype d, const DropArgs &a, bool vec, hipStream_t s) {
@@ -218,12 +306,17 @@ static void compress_values(zds_dtype d, const DropArgs &a, bool vec, hipStream_
 
 template <int D, int OD>
 static void decompress_go(const DropArgs &a, bool add, bool vec, hipStream_t s) {
-  if (add)
-    hipLaunchKernelGGL((dropout_add_kernel<D, OD>), dim3(blocks_for(a.groups, kDropGroups)), dim3(256), 0, s, a);
-  else if (vec)
-    hipLaunchKernelGGL((dropout_spread_kernel<D, OD, true>), dim3(blocks_for(a.n, kDropTile)), dim3(256), 0, s, a);
-  else
-    hipLaunchKernelGGL((dropout_spread_kernel<D, OD, false>), dim3(blocks_for(a.n, kDropTile)), dim3(256), 0, s, a);
+  if (add) {
+    each_tile(a, pieces(a.groups, kDropGroups), 256, [&](const DropArgs &b, dim3 g) {
+      hipLaunchKernelGGL((dropout_add_kernel<D, OD>), g, dim3(256), 0, s, b);
+    });
+    return;
+  }
+  const int tile = (2048 << a.shift) < kSpreadTile ? 2048 << a.shift : kSpreadTile;
+  each_tile(a, pieces(a.n, tile), 256, [&](const DropArgs &b, dim3 g) {
+    if (vec) hipLaunchKernelGGL((dropout_spread_kernel<D, OD, true>), g, dim3(256), 0, s, b, tile);
+    else hipLaunchKernelGGL((dropout_spread_kernel<D, OD, false>), g, dim3(256), 0, s, b, tile);
+  });
 }
 template <int D>
 static void decompress_to(zds_dtype od, const DropArgs &a, bool add, bool vec, hipStream_t s) {
@@ -279,7 +372,7 @@ extern "C" zds_status zds_dropout_compress(const void *x, zds_dtype x_dtype, flo
   a.shift = shift;
   a.sc = scalars_dev;
   a.state = state_dev;
-  const bool vec = aligned(x, x_dtype == ZDS_FP32 ? 16 : 8) && aligned(error, 16);
+  const bool vec = aligned(x, 16) && aligned(error, 16) && aligned(values, 16);
   hipStream_t s = static_cast<hipStream_t>(stream);
   switch (x_dtype) {
     case ZDS_FP16: compress_values<ZDS_FP16>(value_dtype, a, vec, s); break;
@@ -324,7 +417,8 @@ extern "C" zds_status zds_dropout_decompress(const void *const *peer_values, int
   a.shift = shift;
   a.npeers = num_peers;
   a.state = state_dev;
-  const bool vec = aligned(dst, dst_dtype == ZDS_FP32 ? 16 : 8);
+  bool vec = aligned(dst, 16);
+  for (int k = 0; k < num_peers; ++k) vec = vec && aligned(peer_values[k], 16);
   hipStream_t s = static_cast<hipStream_t>(stream);
   switch (value_dtype) {
     case ZDS_FP16: decompress_to<ZDS_FP16>(dst_dtype, a, mode == ZDS_ACCUMULATE, vec, s); break;

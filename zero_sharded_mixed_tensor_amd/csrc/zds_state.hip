@@ -75,45 +75,91 @@ __global__ void __launch_bounds__(256) quantise_kernel(ConvertArgs a) {
   }
 }
 
-template <int F, int D, bool VEC>
-__global__ void __launch_bounds__(256) dequantise_kernel(ConvertArgs a) {
-  const int64_t quads = (a.n + 3) / 4;
-  for (int64_t q = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; q < quads;
-       q += static_cast<int64_t>(gridDim.x) * 256) {
-    const int64_t e = 4 * q;
-    const bool whole = e + 4 <= a.n;
-    float x[4];
-    if constexpr (F == ZDS_STATE_BF16) {
-      if (VEC && whole) {
-        load_quad<ZDS_BF16>(a.src, q, x);
+// The value of element e.
+template <int F>
+__device__ __forceinline__ float read_element(const ConvertArgs &a, int64_t e) {
+  if constexpr (F == ZDS_STATE_BF16) return widen1<ZDS_BF16>(a.src, e);
+  else return decode1<F>(static_cast<const uint8_t *>(a.src)[e], a.exps_in[e >> 5]);
+}
+template <int D>
+__device__ __forceinline__ void write_element(void *dst, int64_t e, float x) {
+  if constexpr (D == ZDS_FP32) static_cast<float *>(dst)[e] = x;
+  else static_cast<uint16_t *>(dst)[e] = narrow1<ZDS_BF16>(x);
+}
+
+// Reading back, a unit of 1024 elements a wave: the codes come in 16 bytes a
+// lane and are used as what a lane stores 16 bytes of, through the wave's own
+// LDS, and a wave has one store in flight. 842M elements of 8 bits to fp32 /
+// bf16: 0.68 / 0.39 ms (6.25 / 6.5 TB/s); its stores back to back 0.73 / 0.39;
+// with 4-byte loads of a quad's codes a lane 0.76 / 0.61. The wave that holds
+// the last elements, if they are no whole unit, reads them one by one.
+constexpr int kReadUnit = 1024;
+template <int F, int D>
+__global__ void __launch_bounds__(256) read_back_kernel(ConvertArgs a) {
+  constexpr bool WIDE = F == ZDS_STATE_BF16;
+  __shared__ u32x4 codes[4][WIDE ? 128 : 64];
+  __shared__ uint8_t exps[4][32];
+  const int lane = threadIdx.x & 63;
+  const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t first = (static_cast<int64_t>(blockIdx.x) * 4 + w) * kReadUnit;
+  if (first + kReadUnit > a.n) {
+    for (int64_t e = first + lane; e < a.n; e += 64) write_element<D>(a.dst, e, read_element<F>(a, e));
+    return;
+  }
+  const u32x4 *src = reinterpret_cast<const u32x4 *>(static_cast<const uint8_t *>(a.src) + (WIDE ? 2 * first : first));
+  u32x4 *sc = codes[w];
+  uint8_t *se = exps[w];
+  uint32_t eb = 0;
+  if (!WIDE && lane < 32) eb = a.exps_in[(first >> 5) + lane];
+  const u32x4 c0 = ld_stream_global(src + lane);
+  u32x4 c1{};
+  if (WIDE) c1 = ld_stream_global(src + 64 + lane);
+  sc[lane] = c0;
+  if (WIDE) sc[64 + lane] = c1;
+  else if (lane < 32) se[lane] = static_cast<uint8_t>(eb);
+  __builtin_amdgcn_wave_barrier();
+  if constexpr (D == ZDS_FP32) {
+    float *dst = static_cast<float *>(a.dst) + first;
+#pragma unroll
+    for (int h = 0; h < 4; ++h) {
+      const int k = 64 * h + lane;
+      float x[4];
+      if constexpr (WIDE) {
+        const u32x2 q = reinterpret_cast<const u32x2 *>(sc)[k];
+        x[0] = bf16_lo(q.x); x[1] = bf16_hi(q.x); x[2] = bf16_lo(q.y); x[3] = bf16_hi(q.y);
       } else {
-        uint16_t c[4];
-        load_elements(static_cast<const uint16_t *>(a.src), e, a.n, c);
-        for (int i = 0; i < 4; ++i) x[i] = __uint_as_float(static_cast<uint32_t>(c[i]) << 16);
+        decode_quad<F>(reinterpret_cast<const uint32_t *>(sc)[k], se[k >> 3], x);
       }
-    } else {
-      const uint32_t s = a.exps_in[e >> 5];
-      uint32_t w;
-      if (VEC && whole) {
-        w = ld_stream(static_cast<const uint32_t *>(a.src) + q);
-      } else {
-        uint8_t c[4];
-        load_elements(static_cast<const uint8_t *>(a.src), e, a.n, c);
-        w = c[0] | (c[1] << 8) | (c[2] << 16) | (static_cast<uint32_t>(c[3]) << 24);
-      }
-      decode_quad<F>(w, s, x);
+      if (h > 0) wait_vmem();
+      st_stream_at(dst, 16 * k, f32x4{x[0], x[1], x[2], x[3]});
     }
-    if (VEC && whole) {
-      if (D == ZDS_FP32) store_quad(static_cast<float *>(a.dst), q, x);
-      else store_quad16<ZDS_BF16>(a.dst, q, x);
-    } else {
-      for (int i = 0; i < 4; ++i) {
-        if (e + i >= a.n) break;
-        if (D == ZDS_FP32) static_cast<float *>(a.dst)[e + i] = x[i];
-        else static_cast<uint16_t *>(a.dst)[e + i] = narrow1<ZDS_BF16>(x[i]);
+  } else {
+    uint16_t *dst = static_cast<uint16_t *>(a.dst) + first;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int k = 64 * h + lane;
+      if (h > 0) wait_vmem();
+      if constexpr (WIDE) {
+        st_stream_at(dst, 16 * k, sc[k]);
+      } else {
+        const u32x2 q = reinterpret_cast<const u32x2 *>(sc)[k];
+        const uint32_t s = se[k >> 2];
+        float x[4], y[4];
+        decode_quad<F>(q.x, s, x);
+        decode_quad<F>(q.y, s, y);
+        st_stream_at(dst, 16 * k, u32x4{pack2<ZDS_BF16>(x[0], x[1]), pack2<ZDS_BF16>(x[2], x[3]),
+                                        pack2<ZDS_BF16>(y[0], y[1]), pack2<ZDS_BF16>(y[2], y[3])});
       }
     }
   }
+}
+
+// Arrays without the units' alignment.
+template <int F, int D>
+__global__ void __launch_bounds__(256) read_back_element_kernel(ConvertArgs a) {
+  for (int64_t e = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; e < a.n;
+       e += static_cast<int64_t>(gridDim.x) * 256)
+    write_element<D>(a.dst, e, read_element<F>(a, e));
 }
 
 template <int F, bool RANDOM>
@@ -126,10 +172,23 @@ static void quantise_go(bool vec, const ConvertArgs &a, hipStream_t s) {
 
 template <int F, int D>
 static void dequantise_go(bool vec, const ConvertArgs &a, hipStream_t s) {
-  int64_t g = (a.n + 1023) / 1024;
-  if (g > max_blocks(256)) g = max_blocks(256);
-  if (vec) hipLaunchKernelGGL((dequantise_kernel<F, D, true>), dim3(static_cast<uint32_t>(g)), dim3(256), 0, s, a);
-  else hipLaunchKernelGGL((dequantise_kernel<F, D, false>), dim3(static_cast<uint32_t>(g)), dim3(256), 0, s, a);
+  if (!vec) {
+    int64_t g = (a.n + 255) / 256;
+    if (g > max_blocks(256)) g = max_blocks(256);
+    hipLaunchKernelGGL((read_back_element_kernel<F, D>), dim3(static_cast<uint32_t>(g)), dim3(256), 0, s, a);
+    return;
+  }
+  // units of one launch: a dispatch holds fewer than 2^32 work-items
+  constexpr int64_t most = max_blocks(256) * 4 * kReadUnit;
+  for (int64_t at = 0; at < a.n; at += most) {
+    ConvertArgs b = a;
+    b.src = static_cast<const uint8_t *>(a.src) + (F == ZDS_STATE_BF16 ? 2 * at : at);
+    if (F != ZDS_STATE_BF16) b.exps_in = a.exps_in + (at >> 5);
+    b.dst = static_cast<uint8_t *>(a.dst) + (D == ZDS_FP32 ? 4 : 2) * at;
+    b.n = a.n - at < most ? a.n - at : most;
+    hipLaunchKernelGGL((read_back_kernel<F, D>), dim3(static_cast<uint32_t>((b.n + 4 * kReadUnit - 1) / (4 * kReadUnit))),
+                       dim3(256), 0, s, b);
+  }
 }
 
 static bool valid_format(int f) { return f == ZDS_STATE_E4M3 || f == ZDS_STATE_UE5M3 || f == ZDS_STATE_BF16; }
@@ -201,7 +260,7 @@ extern "C" zds_status zds_state_dequantise(const void *codes, const uint8_t *exp
   if (st != ZDS_OK) return st;
   const ConvertArgs a{codes, dst, nullptr, exps, n, 0, 0, nullptr};
   const bool f = dst_dtype == ZDS_FP32;
-  const bool vec = aligned(dst, f ? 16 : 8) && aligned(codes, format == ZDS_STATE_BF16 ? 8 : 4);
+  const bool vec = aligned(dst, 16) && aligned(codes, 16);
   hipStream_t s = static_cast<hipStream_t>(stream);
   switch (format) {
     case ZDS_STATE_E4M3: f ? dequantise_go<ZDS_STATE_E4M3, ZDS_FP32>(vec, a, s) : dequantise_go<ZDS_STATE_E4M3, ZDS_BF16>(vec, a, s); break;
