@@ -67,22 +67,23 @@ __device__ __forceinline__ float put(void *base, int64_t i, float x) {
   }
 }
 
-// What becomes of element e with c = x + scale * error: sent if it is kept, and
-// the new error. in: its place in its group, place: the kept one; at: where the
-// value goes (value(at) stores it and returns it as stored).
+// What becomes of an element with c = x + scale * error (without feedback: c =
+// ratio * x): sent if it is kept; returns what is left of it. in: its place in
+// its group, place: the kept one; missing: that one lies past the end. value(v)
+// stores a value and returns it as stored.
 template <typename Put>
-__device__ __forceinline__ float encode_element(float c, float inv, int in, int place, bool missing, const Put &value) {
+__device__ __forceinline__ float encode_element(float c, int in, int place, bool missing, const Put &value) {
   if (in == place) {
     const float sent = value(c);
     if (magnitude(sent) < 0x7f800000u) c = c - sent;
   } else if (missing && in == 0) {
-    value(0.0f);  // the place of a cut last group lies past the end
+    value(0.0f);
   }
-  return c * inv;
+  return c;
 }
 
 // A tile, or what there is of it, by a block, one element by one.
-template <int XD, int D>
+template <int XD, int D, bool ERR>
 __device__ __forceinline__ void encode_elements(const DropArgs &a, int64_t first, float scale, float inv, uint8_t *kept) {
   const int64_t g0 = first >> a.shift;
   const int mask = (1 << a.shift) - 1;
@@ -90,18 +91,22 @@ __device__ __forceinline__ void encode_elements(const DropArgs &a, int64_t first
   for (int k = threadIdx.x; k < kEncodeTile && first + k < a.n; k += kEncodeBlock) {
     const int64_t e = first + k;
     const int in = k & mask, g = k >> a.shift, place = kept[off + g] >> (8 - a.shift);
-    const float c = widen1<XD>(a.x, e) + scale * a.err[e];
-    a.err[e] = encode_element(c, inv, in, place, e - in + place >= a.n, [&](float v) { return put<D>(a.values, g0 + g, v); });
+    const float x = widen1<XD>(a.x, e);
+    const float left = encode_element(ERR ? x + scale * a.err[e] : scale * x, in, place, e - in + place >= a.n,
+                                      [&](float v) { return put<D>(a.values, g0 + g, v); });
+    if (ERR) a.err[e] = left * inv;
   }
 }
 
-// With error feedback. A block takes a tile of 2048 elements, each thread a
-// quad; 16-bit x comes in 16 bytes a lane by waves 0-3, and the values go out
-// so, through LDS; a wave has one load in flight. VEC: whole tiles are aligned.
-template <int XD, int D, bool VEC>
+// A block takes a tile of 2048 elements, each thread a quad; 16-bit x comes in
+// 16 bytes a lane by waves 0-3, and the values go out so, through LDS; a wave
+// has one load in flight. ERR: with feedback; VEC: whole tiles are aligned.
+// bf16, ratio 16, feedback, 842M: 1.32 ms (6.5 TB/s); four quads a thread
+// loaded where they are used: 1.43.
+template <int XD, int D, bool ERR, bool VEC>
 __global__ void __launch_bounds__(kEncodeBlock) dropout_encode_kernel(DropArgs a) {
   __shared__ __align__(16) uint8_t kept[kEncodeTile / 2 + 32];
-  __shared__ u32x4 xs[kEncodeTile / 8];
+  __shared__ u32x4 xs[XD == ZDS_FP32 ? 1 : kEncodeTile / 8];
   __shared__ u32x4 out[kEncodeTile / (D == ZDS_FP32 ? 8 : 16)];
   const int t = threadIdx.x;
   const int w = __builtin_amdgcn_readfirstlane(t >> 6);
@@ -112,20 +117,20 @@ __global__ void __launch_bounds__(kEncodeBlock) dropout_encode_kernel(DropArgs a
     for (int k = t; k < groups && g0 + k < a.groups; k += kEncodeBlock) put<D>(a.values, g0 + k, __uint_as_float(0x7fc00000u));
     return;
   }
-  const float scale = a.state->scale, inv = 1.0f / scale;
+  const float scale = ERR ? a.state->scale : static_cast<float>(1 << a.shift), inv = ERR ? 1.0f / scale : 0.0f;
   if (!VEC || first + kEncodeTile > a.n) {
-    encode_elements<XD, D>(a, first, scale, inv, kept);
+    encode_elements<XD, D, ERR>(a, first, scale, inv, kept);
     return;
   }
-  float *err = a.err + first;
-  f32x4 xf{};
+  float *err = ERR ? a.err + first : nullptr;
+  f32x4 xf{}, e4{};
   if (XD == ZDS_FP32) {
     xf = ld_stream_global(reinterpret_cast<const f32x4 *>(static_cast<const float *>(a.x) + first) + t);
-    wait_vmem();
+    if (ERR) wait_vmem();
   } else if (w < 4) {
     xs[t] = ld_stream_global(reinterpret_cast<const u32x4 *>(static_cast<const uint16_t *>(a.x) + first) + t);
   }
-  const f32x4 e4 = ld_stream_global(reinterpret_cast<const f32x4 *>(err) + t);
+  if (ERR) e4 = ld_stream_global(reinterpret_cast<const f32x4 *>(err) + t);
   const int off = make_kept(a, g0, groups, kept);
   float x[4], er[4] = {e4.x, e4.y, e4.z, e4.w};
   if constexpr (XD == ZDS_FP32) {
@@ -137,15 +142,16 @@ __global__ void __launch_bounds__(kEncodeBlock) dropout_encode_kernel(DropArgs a
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int k = 4 * t + i, g = k >> a.shift, place = kept[off + g] >> (8 - a.shift);
-    er[i] = encode_element(x[i] + scale * er[i], inv, k & mask, place, false, [&](float v) { return put<D>(out, g, v); });
+    er[i] = inv * encode_element(ERR ? x[i] + scale * er[i] : scale * x[i], k & mask, place, false,
+                                 [&](float v) { return put<D>(out, g, v); });
   }
-  st_stream_at(err, 16 * t, f32x4{er[0], er[1], er[2], er[3]});
+  if (ERR) st_stream_at(err, 16 * t, f32x4{er[0], er[1], er[2], er[3]});
   __syncthreads();
   constexpr int size = D == ZDS_FP32 ? 4 : 2;
   if (16 * t < groups * size) st_stream_at(static_cast<uint8_t *>(a.values) + g0 * size, 16 * t, out[t]);
 }
 
-// Without feedback: only the kept elements are read.
+// Without feedback: only the kept elements are loaded.
 template <int XD, int D>
 __global__ void __launch_bounds__(256) dropout_gather_kernel(DropArgs a) {
   __shared__ __align__(16) uint8_t kept[kDropGroups + 32];
@@ -292,17 +298,33 @@ static void each_tile(DropArgs a, int64_t count, int threads, const Launch &laun
 }
 static int64_t pieces(int64_t items, int64_t of) { return (items + of - 1) / of; }
 
+template <int XD, int D, bool ERR>
+static void encode_go(const DropArgs &a, bool vec, hipStream_t s) {
+  each_tile(a, pieces(a.n, kEncodeTile), kEncodeBlock, [&](const DropArgs &b, dim3 g) {
+    if (vec) hipLaunchKernelGGL((dropout_encode_kernel<XD, D, ERR, true>), g, dim3(kEncodeBlock), 0, s, b);
+    else hipLaunchKernelGGL((dropout_encode_kernel<XD, D, ERR, false>), g, dim3(kEncodeBlock), 0, s, b);
+  });
+}
+
+// Without feedback fp32 elements in groups of up to 64 bytes are streamed: every
+// 128-byte line of x is read either way, by fewer instructions. 45M elements, us
+// gathered / streamed: fp32 at ratio 2 49 / 44, 16 36 / 33, 32 33 / 33, 64 18 /
+// 34. 16-bit elements are gathered: bf16 at ratio 2 41 / 38, but at 8 19 / 36,
+// as a tile is then too little for a block.
 template <int XD, int D>
 static void compress_go(const DropArgs &a, bool vec, hipStream_t s) {
-  if (!a.err) {
-    each_tile(a, pieces(a.groups, kDropGroups), 256, [&](const DropArgs &b, dim3 g) {
-      hipLaunchKernelGGL((dropout_gather_kernel<XD, D>), g, dim3(256), 0, s, b);
-    });
+  if (a.err) {
+    encode_go<XD, D, true>(a, vec, s);
     return;
   }
-  each_tile(a, pieces(a.n, kEncodeTile), kEncodeBlock, [&](const DropArgs &b, dim3 g) {
-    if (vec) hipLaunchKernelGGL((dropout_encode_kernel<XD, D, true>), g, dim3(kEncodeBlock), 0, s, b);
-    else hipLaunchKernelGGL((dropout_encode_kernel<XD, D, false>), g, dim3(kEncodeBlock), 0, s, b);
+  if constexpr (XD == ZDS_FP32) {
+    if (a.shift <= 4) {
+      encode_go<XD, D, false>(a, vec, s);
+      return;
+    }
+  }
+  each_tile(a, pieces(a.groups, kDropGroups), 256, [&](const DropArgs &b, dim3 g) {
+    hipLaunchKernelGGL((dropout_gather_kernel<XD, D>), g, dim3(256), 0, s, b);
   });
 }
 template <int XD>
