@@ -617,7 +617,8 @@ zds_status zds_muon_apply(const zds_muon_hparams *hp, const zds_matrix_plan *pla
  * zds_loss_scaler_update, so a captured step draws new numbers on each replay,
  * a resumed run those the uninterrupted run would have drawn, and every rank
  * the same. `first` is the flat index of a call's element 0 (the shard's lo):
- * numbers follow the flat element, not the partition.
+ * numbers follow the flat element, not the partition. first + n must not pass
+ * 2^63.
  * ------------------------------------------------------------------------- */
 
 /* The four words of one call, computed on the host (out4: 4 entries). */

@@ -162,7 +162,7 @@ def test_quantise_refusals():
     fn = "zds_state_quantise"
     for kw, text in ((dict(fmt=3), "format"), (dict(fmt=-1), "format"), (dict(rounding=2), "rounding"),
                      (dict(n=-1), "n must"), (dict(n=1 << 40), "n must"), (dict(first=-32), "first"),
-                     (dict(first=16), "first"), (dict(state=None), "state"), (dict(src=None), "null"),
+                     (dict(first=16), "first"), (dict(first=(1 << 63) - 64), "first"), (dict(state=None), "state"), (dict(src=None), "null"),
                      (dict(codes=None), "null"), (dict(exps=None), "exps"), (dict(fmt=2), "no exps"),
                      (dict(codes=FAKE), "overlap"), (dict(exps=FAKE * 3), "overlap"), (dict(exps=FAKE + 396), "overlap")):
         _refused(fn, quantise_args(**kw), text)
@@ -203,7 +203,7 @@ def test_step_refusals():
                      (dict(hp=zds.hparams(eps=0.0)), "eps"), (dict(hp=zds.hparams(eps=1e-31)), "eps"), (dict(hp=zds.hparams(lr=float("nan"))), "lr"),
                      (dict(gdt=5), "grad dtype"), (dict(pdt=2), "param dtype"), (dict(fmt=0), "second moment"),
                      (dict(fmt=3), "second moment"), (dict(n=-1), "n must"), (dict(n=1 << 40), "n must"),
-                     (dict(first=33), "first"), (dict(first=-32), "first"),
+                     (dict(first=33), "first"), (dict(first=-32), "first"), (dict(first=(1 << 63) - 64), "first"),
                      (dict(fmt=2), "no exps"), (dict(fmt=2, ve=None, v=2 * FAKE + 398), "overlap"),
                      (dict(out=2 * FAKE), "overlap"), (dict(m=4 * FAKE + 3), "overlap"), (dict(ve=4 * FAKE), "overlap"),
                      (dict(gdt=2, out=FAKE), "overlap"), (dict(out=FAKE + 2), "overlap")):
@@ -226,7 +226,7 @@ def test_dropout_refusals():
     for kw, text in ((dict(ratio=1), "ratio"), (dict(ratio=3), "ratio"), (dict(ratio=512), "ratio"),
                      (dict(ratio=-4), "ratio"), (dict(ratio=0), "ratio"), (dict(vdt=3), "value dtype"),
                      (dict(xdt=3), "x dtype"), (dict(n=-1), "n must"), (dict(n=1 << 40), "n must"),
-                     (dict(first=2), "first"), (dict(first=-4), "first"), (dict(x=None), "null"),
+                     (dict(first=2), "first"), (dict(first=-4), "first"), (dict(first=(1 << 63) - 64), "first"), (dict(x=None), "null"),
                      (dict(values=None), "null"), (dict(state=None), "null"), (dict(values=FAKE), "overlap"),
                      (dict(error=FAKE + 1996), "overlap"), (dict(values=2 * FAKE), "overlap")):
         _refused(fn, comp(**kw), text)
@@ -244,7 +244,7 @@ def test_dropout_refusals():
     fn = "zds_dropout_decompress"
     for kw, text in ((dict(num=0), "num_peers"), (dict(num=17), "num_peers"), (dict(mode=0), "mode"),
                      (dict(mode=3), "mode"), (dict(ratio=6), "ratio"), (dict(odt=0), "dst"), (dict(vdt=2, odt=1), "dst"),
-                     (dict(first=6), "first"), (dict(peers=None), "null"), (dict(dst=None), "null"),
+                     (dict(first=6), "first"), (dict(first=(1 << 63) - 64), "first"), (dict(peers=None), "null"), (dict(dst=None), "null"),
                      (dict(state=None), "null"), (dict(peers=(FAKE, None)), "peer 1"), (dict(dst=2 * FAKE - 8), "overlaps peer 1")):
         _refused(fn, dec(**kw), text)
     for kw, text in ((dict(dst=4 * FAKE + 2), "aligned"), (dict(peers=(FAKE + 1, 2 * FAKE)), "peer 0")):

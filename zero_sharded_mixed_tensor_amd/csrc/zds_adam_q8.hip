@@ -270,7 +270,8 @@ extern "C" zds_status zds_adam_step_q8(const zds_adamw_hparams *hp, const void *
   if (sq_format != ZDS_STATE_UE5M3 && sq_format != ZDS_STATE_BF16)
     return fail(ZDS_EINVAL, "%s: the second moment's format must be UE5M3 or BF16", fn);
   if (n < 0 || n >= kStateMost) return fail(ZDS_EINVAL, "%s: n must lie in [0, 2^40)", fn);
-  if (first < 0 || first % 32 != 0) return fail(ZDS_EINVAL, "%s: first must be a multiple of 32, >= 0", fn);
+  if (first < 0 || first % 32 != 0 || first > INT64_MAX - n)
+    return fail(ZDS_EINVAL, "%s: first must be a multiple of 32 in [0, 2^63 - n)", fn);
   if (n == 0) return ZDS_OK;
   const bool wide = sq_format == ZDS_STATE_BF16;
   if (!grads || !master || !exp_avg || !exp_avg_exps || !exp_avg_sq || (!wide && !exp_avg_sq_exps) || !scalars_dev ||

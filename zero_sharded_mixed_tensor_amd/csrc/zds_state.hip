@@ -194,7 +194,7 @@ static void dequantise_go(bool vec, const ConvertArgs &a, hipStream_t s) {
 static bool valid_format(int f) { return f == ZDS_STATE_E4M3 || f == ZDS_STATE_UE5M3 || f == ZDS_STATE_BF16; }
 static int64_t code_size(zds_state_format f) { return f == ZDS_STATE_BF16 ? 2 : 1; }
 
-// What both conversions check: dst_size and src_size are bytes per element.
+// What both conversions check; plain_size: bytes per element of the array that is no code.
 static zds_status check_convert(const char *fn, const void *codes, const void *exps, int64_t n, zds_state_format f,
                                 const void *plain, int64_t plain_size) {
   if (!codes || !plain) return fail(ZDS_EINVAL, "%s: null pointer", fn);
@@ -231,7 +231,8 @@ extern "C" zds_status zds_state_quantise(const float *src, int64_t n, zds_state_
   if (rounding != ZDS_ROUND_NEAREST && rounding != ZDS_ROUND_RANDOM) return fail(ZDS_EINVAL, "%s: bad rounding", fn);
   if (n < 0 || n >= kStateMost) return fail(ZDS_EINVAL, "%s: n must lie in [0, 2^40)", fn);
   const bool random = rounding == ZDS_ROUND_RANDOM;
-  if (random && (first < 0 || first % 32 != 0)) return fail(ZDS_EINVAL, "%s: first must be a multiple of 32, >= 0", fn);
+  if (random && (first < 0 || first % 32 != 0 || first > INT64_MAX - n))
+    return fail(ZDS_EINVAL, "%s: first must be a multiple of 32 in [0, 2^63 - n)", fn);
   if (n == 0) return ZDS_OK;
   if (random && !state_dev) return fail(ZDS_EINVAL, "%s: null state", fn);
   if (random && !aligned(state_dev, 8)) return fail(ZDS_EALIGN, "%s: state not 8-byte aligned", fn);
