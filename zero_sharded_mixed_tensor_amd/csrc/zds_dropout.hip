@@ -17,8 +17,8 @@ namespace zds {
 // written; groups of a block where single elements are read or added to.
 constexpr int kEncodeBlock = 512;
 constexpr int kEncodeTile = 4 * kEncodeBlock;
-constexpr int kSpreadBlock = 512;
-constexpr int kSpreadTile = 8 * kSpreadBlock;
+constexpr int kSpreadBlock = 256;
+constexpr int kSpreadTile = 16 * kSpreadBlock;
 constexpr int kDropGroups = 1024;
 
 struct DropArgs {
@@ -185,9 +185,12 @@ __device__ __forceinline__ float peer_sum(const DropArgs &a, int64_t g) {
 // messages come in 16 bytes a lane, dealt out over all waves, into LDS (as many
 // messages at a time as 16 KiB hold), where each thread sums its groups in peer
 // order; then the tile is written 16 bytes a lane. VEC: whole tiles are aligned.
-// 8 bf16 messages, ratio 8, 842M fp32 elements: 0.835 ms (6.05 TB/s); a lane
-// reading all messages of its 8 groups, one after another or together, left most
-// waves without a load: 0.93 to 0.96 ms, tiles of 16384.
+// 8 bf16 messages, ratio 8, 842M fp32 elements: 0.823 ms (6.14 TB/s); blocks
+// of 512 threads 0.835; a lane reading all messages of its 8 groups, one after
+// another or together, left most waves without a load: 0.93 to 0.96 (tiles of
+// 16384). Tiles of 8192 and 16384 are slower wherever messages are read to any
+// amount (202M elements, ratio 2, 8 messages: 411 us, 488), a little faster
+// for many messages of a high ratio, of which a tile reads a few bytes each.
 template <int D, int OD, bool VEC>
 __global__ void __launch_bounds__(kSpreadBlock) dropout_spread_kernel(DropArgs a) {
   constexpr int kGroups = kSpreadTile / 2, kRaw = 16384;
@@ -216,14 +219,22 @@ __global__ void __launch_bounds__(kSpreadBlock) dropout_spread_kernel(DropArgs a
   for (int j0 = 0; j0 < a.npeers; j0 += most) {
     const int peers = a.npeers - j0 < most ? a.npeers - j0 : most;
     if (j0 > 0) __syncthreads();
-    for (int k = t; k < peers << pieces_shift; k += kSpreadBlock)
-      raw[k] = ld_stream(reinterpret_cast<const u32x4 *>(static_cast<const uint8_t *>(a.peers[j0 + (k >> pieces_shift)]) +
-                                                         g0 * size) + (k & ((1 << pieces_shift) - 1)));
+    const auto fetch = [&](const void *from, int k) {
+      raw[k] = ld_stream_global(reinterpret_cast<const u32x4 *>(static_cast<const uint8_t *>(from) + g0 * size) +
+                                (k & ((1 << pieces_shift) - 1)));
+    };
+    if (pieces_shift >= 6) {  // a wave's pieces are of one message: its address comes from the scalar arguments
+      for (int k = t; k < peers << pieces_shift; k += kSpreadBlock)
+        fetch(a.peers[j0 + __builtin_amdgcn_readfirstlane(k >> pieces_shift)], k);
+    } else {
+      for (int k = t; k < peers << pieces_shift; k += kSpreadBlock) fetch(a.peers[j0 + (k >> pieces_shift)], k);
+    }
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < kGroups / kSpreadBlock; ++i) {
       const int g = t + kSpreadBlock * i;
       if (g >= groups) break;
+#pragma unroll 4
       for (int j = 0; j < peers; ++j) {
         const float x = widen1<D>(raw, j * groups + g);
         s[i] = j0 + j == 0 ? x : s[i] + x;
