@@ -768,9 +768,9 @@ zds_status zds_dropout_compress(const void *x, zds_dtype x_dtype, float *error, 
  * written). dst: device, FP32 or the values' type, rounded once. No mean is
  * taken: to average over peers, give the step accum_steps = K * N. A message
  * that was all-reduced is one peer; the overflow flag and norm of an
- * overwritten gradient are those of the summed message, so
- * zds_overflow_and_norm over the ceil(n / ratio) values (or
- * zds_reduce_peer_slices_norm of the messages) saves a pass over the gradient.
+ * overwritten gradient of the message's type are those of that message, so
+ * zds_overflow_and_norm over its ceil(n / ratio) values saves a pass over the
+ * gradient (and so does zds_reduce_peer_slices_norm, which sums several).
  * Must be called before the zds_loss_scaler_update that ends the step whose
  * zds_dropout_compress made the values. dst must not overlap a message. */
 zds_status zds_dropout_decompress(const void *const *peer_values, int32_t num_peers, zds_dtype value_dtype, int64_t n,

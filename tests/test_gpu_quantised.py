@@ -435,6 +435,54 @@ def test_noise_of_the_second_moment():
     assert ratio.var() < 0.04
 
 
+def test_two_steps_at_once():
+    """Two ranks' steps side by side on two streams, each with its own state:
+    what they leave is what they leave one after the other."""
+    n = 1 << 20
+
+    def rank(seed):
+        g = torch.Generator(device="cuda").manual_seed(seed)
+        step = QuantisedStep(n + seed, zds.hparams(lr=1e-3, beta2=0.95), zds.scaler_config(dynamic=False), seed=seed)
+        return dict(step=step, g=torch.randn(n + seed, device="cuda", generator=g).bfloat16(), mv=step.new_moments(),
+                    p=torch.randn(n + seed, device="cuda", generator=g),
+                    o=torch.empty(n + seed, dtype=torch.bfloat16, device="cuda"))
+
+    def go(q, stream):
+        for _ in range(5):
+            q["step"].step(q["g"], q["p"], *q["mv"], q["o"], stream)
+    alone = [rank(3), rank(4)]
+    for q in alone:
+        go(q, None)
+    both = [rank(3), rank(4)]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for q, s in zip(both, streams):
+            q["step"].step(q["g"], q["p"], *q["mv"], q["o"], s)
+    torch.cuda.synchronize()
+    for a, b in zip(alone, both):
+        assert torch.equal(a["p"], b["p"]) and torch.equal(a["o"], b["o"])
+        assert all(torch.equal(x.codes, y.codes) and torch.equal(x.exps, y.exps) for x, y in zip(a["mv"], b["mv"]))
+
+
+def test_refusals_on_the_device():
+    n = 256
+    q = zds.new_quantised_state(n, zds.ZDS_STATE_E4M3)
+    x = torch.zeros(2 * n, device="cuda")
+    for bad in (lambda: zds.zds_state_quantise(x[::2], q), lambda: zds.zds_state_quantise(x[:n].cpu(), q),
+                lambda: zds.zds_state_quantise(x[:n], zds.QuantisedState(0, q.codes.cpu(), q.exps)),
+                lambda: zds.zds_state_dequantise(q, x[::2]), lambda: zds.zds_state_dequantise(q, x[:n].double()),
+                lambda: zds.zds_state_quantise(x[:n], q, zds.ZDS_ROUND_RANDOM),
+                lambda: zds.zds_state_quantise(x[:n], q, zds.ZDS_ROUND_RANDOM, 1, 8, state()),
+                lambda: zds.zds_adam_step_q8(zds.hparams(), x[:n], x[n:], q, q, None, 0, 0, scalars(), state()),
+                lambda: zds.zds_dropout_compress(x[:n], x[n:], 8, x[n:], 0, 0, state()),
+                lambda: zds.zds_dropout_decompress([x[:n]], 8, x[:n], 0, 0, state())):
+        with pytest.raises(zds.ZdsError):
+            bad()
+    torch.cuda.synchronize()
+    assert (x == 0).all() and (q.codes == 0).all()
+
+
 def test_zero_elements_and_fp32_step_mix():
     q = zds.new_quantised_state(0, zds.ZDS_STATE_E4M3)
     zds.zds_state_quantise(torch.empty(0, device="cuda"), q)
