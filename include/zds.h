@@ -711,6 +711,8 @@ zds_status zds_state_dequantise(const void *codes, const uint8_t *exps, int64_t 
  * master differs from zds_adam_step's by at most 2^-20 |u| and one rounding
  * (where v is below 2^104; from there on it counts as infinite), and params_out
  * is its cast.
+ * Calls of few elements form the step's constants in the update's own kernel and
+ * leave those in scalars_dev as they were.
  *   hp            as for zds_adam_step, but eps >= 2^-100
  *   exp_avg       device, n codes of E4M3, with exp_avg_exps
  *   exp_avg_sq    device, n codes of sq_format (UE5M3 with exp_avg_sq_exps, or

@@ -244,9 +244,10 @@ def check_params(got, want, before, consts):
 
 
 @pytest.mark.parametrize("second", [zds.ZDS_STATE_UE5M3, zds.ZDS_STATE_BF16])
-def test_step_is_read_back_adam_quantise(second):
-    """One call against its three parts on the device, at a size of many tiles."""
-    n = 3 * 1024 * 1024 + 777
+@pytest.mark.parametrize("n", [3 * 1024 * 1024 + 777, 5 * 1024 * 1024 + 31])
+def test_step_is_read_back_adam_quantise(second, n):
+    """One call against its three parts on the device, at sizes of many tiles,
+    on either side of where the step's constants get a launch of their own."""
     hp = zds.hparams(lr=1e-3, beta2=0.95, weight_decay=0.1)
     g = torch.Generator(device="cuda").manual_seed(4)
     grads = torch.randn(n, device="cuda", generator=g).mul_(1e-3).bfloat16()
