@@ -2,9 +2,11 @@
 // (include/zds.h describes the formats; zds_quantised.h has the arithmetic).
 //
 // Both are HBM-bound streams: 4 B read and a code (1 + 1/32 or 2 B) written
-// per element, and the other way round. A wave takes units of 512 elements,
-// each lane a quad of each half, so that a block of 32 lies in 8 neighbouring
-// lanes and its largest magnitude takes three cross-lane moves.
+// per element, and the other way round. Quantising, a wave takes units of 512
+// elements, each lane a quad of each half, so that a block of 32 lies in 8
+// neighbouring lanes and its largest magnitude takes three cross-lane moves:
+// 202M elements to 8 bits 155 us to nearest, 157 at random (6.5 TB/s, the rate of
+// a copy), to BF16 183 (6.6).
 #include "zds_internal.h"
 #include "zds_quantised.h"
 
