@@ -67,23 +67,23 @@ __device__ __forceinline__ float put(void *base, int64_t i, float x) {
   }
 }
 
-// What becomes of an element with c = x + scale * error (without feedback: c =
-// ratio * x): sent if it is kept; returns what is left of it. in: its place in
-// its group, place: the kept one; missing: that one lies past the end. value(v)
-// stores a value and returns it as stored.
+// What becomes of an element with c = x + scale * error: sent if it is kept;
+// returns the new error. in: its place in its group, place: the kept one;
+// missing: that one lies past the end. value(v) stores a value and returns it as
+// stored.
 template <typename Put>
-__device__ __forceinline__ float encode_element(float c, int in, int place, bool missing, const Put &value) {
+__device__ __forceinline__ float encode_element(float c, float inv, int in, int place, bool missing, const Put &value) {
   if (in == place) {
     const float sent = value(c);
     if (magnitude(sent) < 0x7f800000u) c = c - sent;
   } else if (missing && in == 0) {
     value(0.0f);
   }
-  return c;
+  return c * inv;
 }
 
 // A tile, or what there is of it, by a block, one element by one.
-template <int XD, int D, bool ERR>
+template <int XD, int D>
 __device__ __forceinline__ void encode_elements(const DropArgs &a, int64_t first, float scale, float inv, uint8_t *kept) {
   const int64_t g0 = first >> a.shift;
   const int mask = (1 << a.shift) - 1;
@@ -91,19 +91,17 @@ __device__ __forceinline__ void encode_elements(const DropArgs &a, int64_t first
   for (int k = threadIdx.x; k < kEncodeTile && first + k < a.n; k += kEncodeBlock) {
     const int64_t e = first + k;
     const int in = k & mask, g = k >> a.shift, place = kept[off + g] >> (8 - a.shift);
-    const float x = widen1<XD>(a.x, e);
-    const float left = encode_element(ERR ? x + scale * a.err[e] : scale * x, in, place, e - in + place >= a.n,
-                                      [&](float v) { return put<D>(a.values, g0 + g, v); });
-    if (ERR) a.err[e] = left * inv;
+    const float c = widen1<XD>(a.x, e) + scale * a.err[e];
+    a.err[e] = encode_element(c, inv, in, place, e - in + place >= a.n, [&](float v) { return put<D>(a.values, g0 + g, v); });
   }
 }
 
-// A block takes a tile of 2048 elements, each thread a quad; 16-bit x comes in
-// 16 bytes a lane by waves 0-3, and the values go out so, through LDS; a wave
-// has one load in flight. ERR: with feedback; VEC: whole tiles are aligned.
-// bf16, ratio 16, feedback, 842M: 1.32 ms (6.5 TB/s); four quads a thread
-// loaded where they are used: 1.43.
-template <int XD, int D, bool ERR, bool VEC>
+// With feedback. A block takes a tile of 2048 elements, each thread a quad;
+// 16-bit x comes in 16 bytes a lane by waves 0-3, and the values go out so,
+// through LDS; a wave has one load in flight. VEC: whole tiles are aligned.
+// bf16, ratio 16, 842M elements: 1.32 ms (6.5 TB/s); four quads a thread loaded
+// where they are used: 1.43.
+template <int XD, int D, bool VEC>
 __global__ void __launch_bounds__(kEncodeBlock) dropout_encode_kernel(DropArgs a) {
   __shared__ __align__(16) uint8_t kept[kEncodeTile / 2 + 32];
   __shared__ u32x4 xs[XD == ZDS_FP32 ? 1 : kEncodeTile / 8];
@@ -117,20 +115,20 @@ __global__ void __launch_bounds__(kEncodeBlock) dropout_encode_kernel(DropArgs a
     for (int k = t; k < groups && g0 + k < a.groups; k += kEncodeBlock) put<D>(a.values, g0 + k, __uint_as_float(0x7fc00000u));
     return;
   }
-  const float scale = ERR ? a.state->scale : static_cast<float>(1 << a.shift), inv = ERR ? 1.0f / scale : 0.0f;
+  const float scale = a.state->scale, inv = 1.0f / scale;
   if (!VEC || first + kEncodeTile > a.n) {
-    encode_elements<XD, D, ERR>(a, first, scale, inv, kept);
+    encode_elements<XD, D>(a, first, scale, inv, kept);
     return;
   }
-  float *err = ERR ? a.err + first : nullptr;
-  f32x4 xf{}, e4{};
+  float *err = a.err + first;
+  f32x4 xf{};
   if (XD == ZDS_FP32) {
     xf = ld_stream_global(reinterpret_cast<const f32x4 *>(static_cast<const float *>(a.x) + first) + t);
-    if (ERR) wait_vmem();
+    wait_vmem();
   } else if (w < 4) {
     xs[t] = ld_stream_global(reinterpret_cast<const u32x4 *>(static_cast<const uint16_t *>(a.x) + first) + t);
   }
-  if (ERR) e4 = ld_stream_global(reinterpret_cast<const f32x4 *>(err) + t);
+  const f32x4 e4 = ld_stream_global(reinterpret_cast<const f32x4 *>(err) + t);
   const int off = make_kept(a, g0, groups, kept);
   float x[4], er[4] = {e4.x, e4.y, e4.z, e4.w};
   if constexpr (XD == ZDS_FP32) {
@@ -142,13 +140,67 @@ __global__ void __launch_bounds__(kEncodeBlock) dropout_encode_kernel(DropArgs a
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int k = 4 * t + i, g = k >> a.shift, place = kept[off + g] >> (8 - a.shift);
-    er[i] = inv * encode_element(ERR ? x[i] + scale * er[i] : scale * x[i], k & mask, place, false,
-                                 [&](float v) { return put<D>(out, g, v); });
+    er[i] = encode_element(x[i] + scale * er[i], inv, k & mask, place, false, [&](float v) { return put<D>(out, g, v); });
   }
-  if (ERR) st_stream_at(err, 16 * t, f32x4{er[0], er[1], er[2], er[3]});
+  st_stream_at(err, 16 * t, f32x4{er[0], er[1], er[2], er[3]});
   __syncthreads();
   constexpr int size = D == ZDS_FP32 ? 4 : 2;
   if (16 * t < groups * size) st_stream_at(static_cast<uint8_t *>(a.values) + g0 * size, 16 * t, out[t]);
+}
+
+// Without feedback and with short groups, aligned: x is streamed, four 16-byte
+// pieces a thread (4096 fp32 or 8192 16-bit elements a block), and the values go
+// out 16 bytes a lane.
+template <int XD>
+constexpr int kPickTile = 256 * 4 * (XD == ZDS_FP32 ? 4 : 8);
+template <int XD, int D>
+__global__ void __launch_bounds__(256) dropout_pick_kernel(DropArgs a) {
+  constexpr int E = XD == ZDS_FP32 ? 4 : 8, tile = kPickTile<XD>, size = D == ZDS_FP32 ? 4 : 2;
+  __shared__ __align__(16) uint8_t kept[tile / 2 + 32];
+  __shared__ u32x4 out[tile / 2 * size / 16];
+  const int t = threadIdx.x;
+  const int64_t first = (a.tile0 + blockIdx.x) * tile;
+  const int64_t g0 = first >> a.shift;
+  const int groups = tile >> a.shift, mask = (1 << a.shift) - 1;
+  const float ratio = static_cast<float>(1 << a.shift);
+  const bool skip = a.sc && a.sc->overflow;
+  if (skip || first + tile > a.n) {
+    const int off = make_kept(a, g0, groups, kept);
+    for (int k = t; k < groups && g0 + k < a.groups; k += 256) {
+      const int64_t e = ((g0 + k) << a.shift) + (kept[off + k] >> (8 - a.shift));
+      put<D>(a.values, g0 + k, skip ? __uint_as_float(0x7fc00000u) : e < a.n ? ratio * widen1<XD>(a.x, e) : 0.0f);
+    }
+    return;
+  }
+  const u32x4 *src = reinterpret_cast<const u32x4 *>(static_cast<const uint8_t *>(a.x) + first * (XD == ZDS_FP32 ? 4 : 2));
+  u32x4 q[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) q[i] = ld_stream_global(src + 256 * i + t);
+  const int off = make_kept(a, g0, groups, kept);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t w[4] = {q[i].x, q[i].y, q[i].z, q[i].w};
+#pragma unroll
+    for (int l = 0; l < E; l += 4) {
+      const int k = E * (256 * i + t) + l, g = k >> a.shift;
+      float x[4];
+      if constexpr (XD == ZDS_FP32) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) x[j] = __uint_as_float(w[j]);
+      } else {
+        x[0] = lo_of<XD>(w[l / 2]); x[1] = hi_of<XD>(w[l / 2]); x[2] = lo_of<XD>(w[l / 2 + 1]); x[3] = hi_of<XD>(w[l / 2 + 1]);
+      }
+      if (a.shift > 1) {  // a quad lies in one group
+        const int at = (kept[off + g] >> (8 - a.shift)) - (k & mask);
+        if (at >= 0 && at < 4) put<D>(out, g, ratio * (at < 2 ? (at == 0 ? x[0] : x[1]) : (at == 2 ? x[2] : x[3])));
+      } else {
+        put<D>(out, g, ratio * (kept[off + g] >> 7 ? x[1] : x[0]));
+        put<D>(out, g + 1, ratio * (kept[off + g + 1] >> 7 ? x[3] : x[2]));
+      }
+    }
+  }
+  __syncthreads();
+  for (int k = t; 16 * k < groups * size; k += 256) st_stream_at(static_cast<uint8_t *>(a.values) + g0 * size, 16 * k, out[k]);
 }
 
 // Without feedback: only the kept elements are loaded.
@@ -315,34 +367,27 @@ static void each_tile(DropArgs a, int64_t count, int threads, const Launch &laun
 }
 static int64_t pieces(int64_t items, int64_t of) { return (items + of - 1) / of; }
 
-template <int XD, int D, bool ERR>
-static void encode_go(const DropArgs &a, bool vec, hipStream_t s) {
-  each_tile(a, pieces(a.n, kEncodeTile), kEncodeBlock, [&](const DropArgs &b, dim3 g) {
-    if (vec) hipLaunchKernelGGL((dropout_encode_kernel<XD, D, ERR, true>), g, dim3(kEncodeBlock), 0, s, b);
-    else hipLaunchKernelGGL((dropout_encode_kernel<XD, D, ERR, false>), g, dim3(kEncodeBlock), 0, s, b);
-  });
-}
-
-// Without feedback fp32 elements in groups of up to 64 bytes are streamed: every
-// 128-byte line of x is read either way, by fewer instructions. 45M elements, us
-// gathered / streamed: fp32 at ratio 2 49 / 44, 16 36 / 33, 32 33 / 33, 64 18 /
-// 34. 16-bit elements are gathered: bf16 at ratio 2 41 / 38, but at 8 19 / 36,
-// as a tile is then too little for a block.
+// Without feedback groups of up to a 128-byte line are streamed, since every line
+// of x is read either way; of longer ones only the kept elements are loaded. 45M
+// elements, us gathered / streamed: fp32 at ratio 2 49 / 43, 16 36 / 31, 32 (128
+// bytes) 33 / 29; bf16 at 2 41 / 23, 16 20 / 17, 64 (128 bytes) 19 / 15. At twice
+// the line a gather reads half of them: fp32 at 64 17.
 template <int XD, int D>
 static void compress_go(const DropArgs &a, bool vec, hipStream_t s) {
   if (a.err) {
-    encode_go<XD, D, true>(a, vec, s);
-    return;
+    each_tile(a, pieces(a.n, kEncodeTile), kEncodeBlock, [&](const DropArgs &b, dim3 g) {
+      if (vec) hipLaunchKernelGGL((dropout_encode_kernel<XD, D, true>), g, dim3(kEncodeBlock), 0, s, b);
+      else hipLaunchKernelGGL((dropout_encode_kernel<XD, D, false>), g, dim3(kEncodeBlock), 0, s, b);
+    });
+  } else if (vec && ((XD == ZDS_FP32 ? 4 : 2) << a.shift) <= 128) {
+    each_tile(a, pieces(a.n, kPickTile<XD>), 256, [&](const DropArgs &b, dim3 g) {
+      hipLaunchKernelGGL((dropout_pick_kernel<XD, D>), g, dim3(256), 0, s, b);
+    });
+  } else {
+    each_tile(a, pieces(a.groups, kDropGroups), 256, [&](const DropArgs &b, dim3 g) {
+      hipLaunchKernelGGL((dropout_gather_kernel<XD, D>), g, dim3(256), 0, s, b);
+    });
   }
-  if constexpr (XD == ZDS_FP32) {
-    if (a.shift <= 4) {
-      encode_go<XD, D, false>(a, vec, s);
-      return;
-    }
-  }
-  each_tile(a, pieces(a.groups, kDropGroups), 256, [&](const DropArgs &b, dim3 g) {
-    hipLaunchKernelGGL((dropout_gather_kernel<XD, D>), g, dim3(256), 0, s, b);
-  });
 }
 template <int XD>
 static void compress_values(zds_dtype d, const DropArgs &a, bool vec, hipStream_t s) {
