@@ -766,8 +766,8 @@ zds_status zds_dropout_compress(const void *x, zds_dtype x_dtype, float *error, 
 /* Writes num_peers (1..16) messages into a gradient of n elements: with t the
  * fp32 sum of the peers' values of a group, in peer order, its kept element
  * becomes t and the others 0 (ZDS_OVERWRITE), or t is added to it, last, and
- * the others are left alone (ZDS_ACCUMULATE; only kept elements are read and
- * written). dst: device, FP32 or the values' type, rounded once. No mean is
+ * the others keep their bits (ZDS_ACCUMULATE; in short groups they are written
+ * back, so nothing else may write to dst meanwhile). dst: device, FP32 or the values' type, rounded once. No mean is
  * taken: to average over peers, give the step accum_steps = K * N. A message
  * that was all-reduced is one peer; the overflow flag and norm of an
  * overwritten gradient of the message's type are those of that message, so

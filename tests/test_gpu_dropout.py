@@ -81,6 +81,25 @@ def test_decompress_bit_exact(ratio, vdt, odt, n, pad, peers):
         same(got[n:], dst[:1].repeat(8), odt)
 
 
+@pytest.mark.parametrize("odt", ["fp32", "bf16", "fp16"])
+@pytest.mark.parametrize("ratio", [2, 4, 8, 32, 64, 128])
+def test_adding_keeps_the_other_bits(ratio, odt):
+    """Any bits: NaN payloads, subnormal numbers, signed zeros."""
+    n, first, steps = 3 * 4096 + 17, ratio * 3, 4
+    rng = np.random.default_rng(ratio)
+    dst = rng.integers(0, 2 ** 32, n, np.uint32).view(np.float32) if odt == "fp32" else \
+        rng.integers(0, 2 ** 16, n, np.uint16)
+    msg = host(rng.standard_normal(-(-n // ratio)), odt)
+    kept = np.isin(np.arange(n), Q.kept_places(n, ratio, SEED, first, steps))
+    want = Q.dropout_decompress([msg], odt, n, ratio, SEED, first, steps, dst, odt, True)
+    dd = to_dev(dst, odt)
+    zds.zds_dropout_decompress([to_dev(msg, odt)], ratio, dd, SEED, first, state(steps), zds.ZDS_ACCUMULATE, n=n)
+    got = to_host(dd)
+    bits = (lambda a: a.view(np.uint32)) if odt == "fp32" else (lambda a: a)
+    assert np.array_equal(bits(got)[~kept], bits(dst)[~kept])
+    same(got, want, odt)
+
+
 def test_infinities_and_nan():
     """Where the caller does not look first, they stay where they are: a kept
     one is sent, another one is kept in the error."""

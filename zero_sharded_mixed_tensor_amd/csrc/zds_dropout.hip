@@ -233,7 +233,8 @@ __device__ __forceinline__ float peer_sum(const DropArgs &a, int64_t g) {
   return t;
 }
 
-// Every element of the gradient is written, a tile of 4096 a block. The
+// Every element of the gradient is written (ADD: read, and all but the kept ones
+// written back as they are), a tile of 4096 a block. The
 // messages come in 16 bytes a lane, dealt out over all waves, into LDS (as many
 // messages at a time as 16 KiB hold), where each thread sums its groups in peer
 // order; then the tile is written 16 bytes a lane. VEC: whole tiles are aligned.
@@ -243,7 +244,7 @@ __device__ __forceinline__ float peer_sum(const DropArgs &a, int64_t g) {
 // 16384). Tiles of 8192 and 16384 are slower wherever messages are read to any
 // amount (202M elements, ratio 2, 8 messages: 411 us, 488), a little faster
 // for many messages of a high ratio, of which a tile reads a few bytes each.
-template <int D, int OD, bool VEC>
+template <int D, int OD, bool VEC, bool ADD>
 __global__ void __launch_bounds__(kSpreadBlock) dropout_spread_kernel(DropArgs a) {
   constexpr int kGroups = kSpreadTile / 2, kRaw = 16384;
   __shared__ __align__(16) uint8_t kept[kGroups + 32];
@@ -258,6 +259,10 @@ __global__ void __launch_bounds__(kSpreadBlock) dropout_spread_kernel(DropArgs a
     const int off = make_kept(a, g0, groups, kept);
     for (int k = t; k < kSpreadTile && first + k < a.n; k += kSpreadBlock) {
       const int g = k >> a.shift;
+      if (ADD) {
+        if ((k & mask) == (kept[off + g] >> (8 - a.shift))) put<OD>(a.dst, first + k, widen1<OD>(a.dst, first + k) + sum[g]);
+        continue;
+      }
       put<OD>(a.dst, first + k, (k & mask) == (kept[off + g] >> (8 - a.shift)) ? sum[g] : 0.0f);
     }
     return;
@@ -266,6 +271,14 @@ __global__ void __launch_bounds__(kSpreadBlock) dropout_spread_kernel(DropArgs a
   const int bytes = groups * size;                          // of one message's part of the tile
   const int pieces_shift = 31 - __builtin_clz(bytes >> 4);  // (32 bytes at least: 16 groups at a ratio of 256)
   const int most = kRaw / bytes;
+  constexpr int E = OD == ZDS_FP32 ? 4 : 8, W = kSpreadTile / E / kSpreadBlock;
+  u32x4 old[W];
+  if (ADD) {
+#pragma unroll
+    for (int i = 0; i < W; ++i)
+      old[i] = ld_stream_global(reinterpret_cast<const u32x4 *>(static_cast<const uint8_t *>(a.dst) + first * (16 / E)) +
+                                t + kSpreadBlock * i);
+  }
   const int off = make_kept(a, g0, groups, kept);
   float s[kGroups / kSpreadBlock];
   for (int j0 = 0; j0 < a.npeers; j0 += most) {
@@ -298,34 +311,40 @@ __global__ void __launch_bounds__(kSpreadBlock) dropout_spread_kernel(DropArgs a
   for (int i = 0; i < kGroups / kSpreadBlock; ++i)
     if (t + kSpreadBlock * i < groups) sum[t + kSpreadBlock * i] = s[i];
   __syncthreads();
-  constexpr int E = OD == ZDS_FP32 ? 4 : 8;
 #pragma unroll
-  for (int i = 0; i < kSpreadTile / E / kSpreadBlock; ++i) {
+  for (int i = 0; i < W; ++i) {
     const int q = t + kSpreadBlock * i;
-    float o[E];
+    uint32_t w[4] = {0u, 0u, 0u, 0u};
+    if (ADD) {
+      w[0] = old[i].x; w[1] = old[i].y; w[2] = old[i].z; w[3] = old[i].w;
+    }
 #pragma unroll
     for (int l = 0; l < E; l += 4) {
       const int k = E * q + l, g = k >> a.shift;
-      if (a.shift > 1) {  // a quad lies in one group
-        const int at = (kept[off + g] >> (8 - a.shift)) - (k & mask);
-        const float x = sum[g];
+      const bool one = a.shift > 1;  // a quad lies in one group, or is two
+      const int at = one ? (kept[off + g] >> (8 - a.shift)) - (k & mask) : kept[off + g] >> 7;
+      const int at2 = one ? at : 2 + (kept[off + g + 1] >> 7);
+      const float x = sum[g], x2 = one ? x : sum[g + 1];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) o[l + i] = at == i ? x : 0.0f;
-      } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) o[l + i] = (i & 1) == kept[off + g + (i >> 1)] >> 7 ? sum[g + (i >> 1)] : 0.0f;
+      for (int j = 0; j < 4; ++j) {
+        const bool is = at == j || at2 == j;
+        const float y = j < 2 ? x : x2;
+        if constexpr (OD == ZDS_FP32) {
+          w[j] = is ? __float_as_uint(ADD ? __uint_as_float(w[j]) + y : y) : w[j];
+        } else {
+          const int u = (l + j) / 2;
+          const float before = (j & 1) ? hi_of<OD>(w[u]) : lo_of<OD>(w[u]);
+          const uint32_t h = narrow1<OD>(ADD ? before + y : y);
+          w[u] = !is ? w[u] : (j & 1) ? (w[u] & 0xffffu) | (h << 16) : (w[u] & 0xffff0000u) | h;
+        }
       }
     }
-    if constexpr (OD == ZDS_FP32) {
-      st_stream_at(static_cast<float *>(a.dst) + first, 16 * q, f32x4{o[0], o[1], o[2], o[3]});
-    } else {
-      st_stream_at(static_cast<uint16_t *>(a.dst) + first, 16 * q,
-                   u32x4{pack2<OD>(o[0], o[1]), pack2<OD>(o[2], o[3]), pack2<OD>(o[4], o[5]), pack2<OD>(o[6], o[7])});
-    }
+    st_stream_at(static_cast<uint8_t *>(a.dst) + first * (16 / E), 16 * q, u32x4{w[0], w[1], w[2], w[3]});
   }
 }
 
-// Only the kept elements are read and written: of a gradient of 45M fp32
+// Adding to the kept elements of long groups, or to a dst that is not aligned;
+// only they are read and written: of a gradient of 45M fp32
 // elements at ratio 64, 705K lines of 128 bytes are read for 4 bytes each and
 // written back in part (counters: 96 MB read, 22.5 MB written), 30 us. Fewer
 // groups a block (29 us), the messages' loads before or after the gradient's (31)
@@ -396,17 +415,24 @@ static void compress_values(zds_dtype d, const DropArgs &a, bool vec, hipStream_
   else compress_go<XD, ZDS_FP32>(a, vec, s);
 }
 
+// Adding: a group of up to a 128-byte line is streamed like an overwrite, since
+// every line of dst is read and written either way; of longer ones only the kept
+// elements are. 202M elements, bf16 messages, us by element / streamed: fp32 dst,
+// one message, ratio 2 357 / 294, 8 336 / 270, 32 (128 bytes) 356 / 267, 64 146 /
+// 266; bf16 dst, 2 311 / 157, 8 169 / 135, 64 (128 bytes) 138 / 126, 128 54 / 126;
+// 16 messages at ratio 2 1,771 / 830 and 1,728 / 704.
 template <int D, int OD>
 static void decompress_go(const DropArgs &a, bool add, bool vec, hipStream_t s) {
-  if (add) {
+  if (add && !(vec && ((OD == ZDS_FP32 ? 4 : 2) << a.shift) <= 128)) {
     each_tile(a, pieces(a.groups, kDropGroups), 256, [&](const DropArgs &b, dim3 g) {
       hipLaunchKernelGGL((dropout_add_kernel<D, OD>), g, dim3(256), 0, s, b);
     });
     return;
   }
   each_tile(a, pieces(a.n, kSpreadTile), kSpreadBlock, [&](const DropArgs &b, dim3 g) {
-    if (vec) hipLaunchKernelGGL((dropout_spread_kernel<D, OD, true>), g, dim3(kSpreadBlock), 0, s, b);
-    else hipLaunchKernelGGL((dropout_spread_kernel<D, OD, false>), g, dim3(kSpreadBlock), 0, s, b);
+    if (add) hipLaunchKernelGGL((dropout_spread_kernel<D, OD, true, true>), g, dim3(kSpreadBlock), 0, s, b);
+    else if (vec) hipLaunchKernelGGL((dropout_spread_kernel<D, OD, true, false>), g, dim3(kSpreadBlock), 0, s, b);
+    else hipLaunchKernelGGL((dropout_spread_kernel<D, OD, false, false>), g, dim3(kSpreadBlock), 0, s, b);
   });
 }
 template <int D>
