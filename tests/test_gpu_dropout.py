@@ -81,6 +81,22 @@ def test_decompress_bit_exact(ratio, vdt, odt, n, pad, peers):
         same(got[n:], dst[:1].repeat(8), odt)
 
 
+@pytest.mark.parametrize("vdt,odt", [("bf16", "bf16"), ("fp16", "fp32"), ("fp32", "fp32")])
+@pytest.mark.parametrize("ratio", [64, 128, 256])
+@pytest.mark.parametrize("n", [128 * 4096, 259 * 4096 + 5])
+def test_decompress_tiles_in_runs(ratio, vdt, odt, n):
+    """Long enough for the order of tiles that shares lines between them."""
+    rng = np.random.default_rng(ratio)
+    msgs = [host(rng.standard_normal(-(-n // ratio)), vdt) for _ in range(3)]
+    dst = host(rng.standard_normal(n), odt)
+    want = Q.dropout_decompress(msgs, vdt, n, ratio, SEED, ratio, 5, dst, odt, False)
+    dd = shifted(dst, odt, 0, 8)
+    zds.zds_dropout_decompress([to_dev(m, vdt) for m in msgs], ratio, dd, SEED, ratio, state(5), n=n)
+    got = to_host(dd)
+    same(got[:n], want, odt)
+    same(got[n:], dst[:1].repeat(8), odt)
+
+
 @pytest.mark.parametrize("odt", ["fp32", "bf16", "fp16"])
 @pytest.mark.parametrize("ratio", [2, 4, 8, 32, 64, 128])
 def test_adding_keeps_the_other_bits(ratio, odt):
