@@ -308,6 +308,15 @@ def test_binding_lengths():
     assert zds.dropout_groups(100, 8) == 13 and zds.dropout_groups(0, 8) == 0
 
 
+@pytest.mark.parametrize("ratio", [2 ** 32 + 2, 2 ** 32 + 4, -2 ** 32 + 8, 2 ** 64 + 256, 512, 1])
+def test_binding_refuses_a_ratio_that_ctypes_would_cut(ratio):
+    """The messages' lengths are checked with the whole number: cut to 32 bits,
+    a ratio of 2^32 + 4 would be one of 4, whose message is not of one value."""
+    st = torch.zeros(64, dtype=torch.uint8)
+    _raises(lambda: zds.zds_dropout_compress(_f32(1000), None, ratio, _f32(1000), 0, 0, st), "ratio")
+    _raises(lambda: zds.zds_dropout_decompress([_f32(1000)], ratio, _f32(1000), 0, 0, st), "ratio")
+
+
 # ------------------------------------------------------------------ configuration and step classes
 
 def config(kind="AdamW8bit", **params):

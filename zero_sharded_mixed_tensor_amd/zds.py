@@ -778,6 +778,13 @@ def dropout_groups(n, ratio):
     return -(-n // ratio)
 
 
+def _ratio(ratio):
+    """ctypes cuts a ratio to 32 bits, and the messages are sized by the whole number."""
+    if not 2 <= ratio <= 256:
+        raise ZdsError(ZDS_EINVAL, "ratio %d is not a power of two in [2, 256]" % ratio)
+    return ratio
+
+
 def zds_dropout_compress(x, error, ratio, values, seed, first, state, scalars=None, stream=None, n=None):
     """x: the rank's gradient; error: fp32 feedback buffer, updated, or None;
     values: the message, dropout_groups(n, ratio) elements, written; scalars:
@@ -787,7 +794,7 @@ def zds_dropout_compress(x, error, ratio, values, seed, first, state, scalars=No
         raise ZdsError(ZDS_EINVAL, "error must be fp32")
     _need(x, n, "x")
     _need(error, n, "error")
-    _need(values, dropout_groups(n, ratio), "values")
+    _need(values, dropout_groups(n, _ratio(ratio)), "values")
     _need_bytes(state, STATE_BYTES, "state")
     _need_bytes(scalars, SCALARS_BYTES, "scalars")
     _check(lib.zds_dropout_compress(_here(x, "x"), dtype_code(x), _here(error, "error"), n, ratio, _seed(seed),
@@ -799,12 +806,13 @@ def zds_dropout_decompress(peers, ratio, dst, seed, first, state, mode=ZDS_OVERW
     """peers: the messages (device tensors of one type), in sum order; dst:
     the gradient, fp32 or of the messages' type."""
     n = dst.numel() if n is None else n
+    groups = dropout_groups(n, _ratio(ratio))
     _need(dst, n, "dst")
     _need_bytes(state, STATE_BYTES, "state")
     for k, t in enumerate(peers):
         if t.dtype != peers[0].dtype:
             raise ZdsError(ZDS_EINVAL, "the messages must share one dtype")
-        _need(t, dropout_groups(n, ratio), "peer %d" % k)
+        _need(t, groups, "peer %d" % k)
     arr = (_P * max(1, len(peers)))(*[_here(t, "peer %d" % k) for k, t in enumerate(peers)])
     vdt = dtype_code(peers[0]) if len(peers) else ZDS_FP32
     _check(lib.zds_dropout_decompress(arr, len(peers), vdt, n, ratio, _seed(seed), _size(first, "first"),
