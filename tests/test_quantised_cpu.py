@@ -317,6 +317,25 @@ def test_binding_refuses_a_ratio_that_ctypes_would_cut(ratio):
     _raises(lambda: zds.zds_dropout_decompress([_f32(1000)], ratio, _f32(1000), 0, 0, st), "ratio")
 
 
+def test_binding_refuses_a_length_that_ctypes_would_cut():
+    """n = 1000 - 2^64 is no longer than any buffer, and is 1000 in 64 bits."""
+    n, st, sc = 1000 - 2 ** 64, torch.zeros(64, dtype=torch.uint8), torch.zeros(64, dtype=torch.uint8)
+    m, v = (zds.new_quantised_state(32, f, "cpu") for f in (zds.ZDS_STATE_E4M3, zds.ZDS_STATE_UE5M3))
+    x = _f32(32)
+    for call in (lambda: zds.zds_state_quantise(x, m, n=n), lambda: zds.zds_state_dequantise(m, x, n=n),
+                 lambda: zds.zds_adam_step_q8(zds.hparams(), x, x, m, v, None, 0, 0, sc, st, n=n),
+                 lambda: zds.zds_dropout_compress(x, None, 4, x, 0, 0, st, n=n),
+                 lambda: zds.zds_dropout_decompress([x], 4, x, 0, 0, st, n=n),
+                 lambda: zds.zds_adam_step(zds.hparams(), x, x, x, x, None, sc, st, n=n),
+                 lambda: zds.zds_overflow_and_norm(x, 1, 0.0, st, sc, x, n=n),
+                 lambda: zds.zds_muon_momentum(zds.muon_hparams(), x, x, x, sc, n=n),
+                 lambda: zds.zds_reduce_peer_slices([x.half()], x, zds.ZDS_OVERWRITE, n=n),
+                 lambda: zds.zds_onebit_compress(x, None, 64, x, x, n=n)):
+        _raises(call, "out of range")
+    for n in (2 ** 64 + 4, 2 ** 63):
+        _raises(lambda: zds.zds_state_quantise(x, m, n=n), "src holds 32")
+
+
 # ------------------------------------------------------------------ configuration and step classes
 
 def config(kind="AdamW8bit", **params):

@@ -192,7 +192,11 @@ def _numel(x):
 
 def _need(x, n, what):
     """The library takes plain pointers and sizes: a buffer shorter than the
-    call's n would be read or written past its end, so the binding refuses it."""
+    call's n would be read or written past its end, so the binding refuses it.
+    (ctypes cuts a number to the low bits of its type: an n that is no int64
+    would pass here as a negative one and be another number there.)"""
+    if n < -(1 << 63):
+        raise ZdsError(ZDS_EINVAL, "%s: a length of %d is out of range" % (what, n))
     if x is not None and _numel(x) < n:
         raise ZdsError(ZDS_EINVAL, "%s holds %d elements, the call needs %d" % (what, _numel(x), n))
 
