@@ -121,6 +121,16 @@ def test_checkpoint_lengths(tmp_path):
         assert np.array_equal(a, b)
 
 
+def test_onebit_chunk_that_ctypes_would_cut():
+    """The scales are counted with the whole number: of a chunk of 2^32 + 1024
+    one scale for 5000 elements, of 1024 five."""
+    words, scales = zds.onebit_payload(5000, 8192, device="cpu")
+    x = _f32(5000)
+    for chunk in (2 ** 32 + 1024, 2 ** 31):
+        _raises(lambda: zds.zds_onebit_compress(x, None, chunk, words, scales), "chunk must")
+        _raises(lambda: zds.zds_onebit_decompress([(words, scales)], chunk, x), "chunk must")
+
+
 def test_cpu_adam_lengths():
     hp = zds.hparams()
     n = 64

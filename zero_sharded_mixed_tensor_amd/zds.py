@@ -515,8 +515,8 @@ def onebit_payload(n, chunk, device="cuda"):
 
 
 def _need_payload(words, scales, n, chunk):
-    if chunk < 1:
-        raise ZdsError(ZDS_EINVAL, "chunk must be positive")
+    if not 1 <= chunk < 1 << 31:  # (the library takes a C int, which ctypes would cut it to)
+        raise ZdsError(ZDS_EINVAL, "chunk must be positive and below 2^31")
     _need_bytes(words, 256 * ((n + 2047) // 2048), "words")
     _need_bytes(scales, 4 * ((n + chunk - 1) // chunk), "scales")
 
