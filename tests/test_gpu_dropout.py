@@ -287,3 +287,35 @@ def test_dense_step_after_an_exchange():
         mean += g
     off = (mean / steps - x).abs()
     assert (off <= 5 * x.abs() * ((ratio - 1) / steps) ** 0.5 + 1e-6).all()
+
+
+def test_first_calls_on_another_stream_than_the_current_one():
+    """Built while the current stream is busy and used on one of the caller's at
+    once: nothing that the constructions left on the current stream comes later."""
+    n, ratio = 300007, 8
+    x = torch.randn(n, generator=torch.Generator().manual_seed(3)).bfloat16().cuda()
+    start = torch.randn(n, generator=torch.Generator().manual_seed(4)).cuda()
+
+    def run(stream, busy):
+        p, g, out = start.clone(), torch.empty(n, device="cuda"), torch.empty(n, dtype=torch.bfloat16, device="cuda")
+        torch.cuda.synchronize()
+        if busy:
+            y = torch.ones(4096, 4096, device="cuda")
+            for _ in range(20):
+                y = y @ y * 1e-4
+        st = QuantisedStep(n, zds.hparams(lr=1e-3, beta2=0.95), zds.scaler_config(dynamic=False), seed=2, stream=stream)
+        ex = DropoutExchange(n, ratio, torch.float32, seed=6)
+        m, v = st.new_moments()
+        for _ in range(2):
+            ex.compress(x, st, stream)
+            ex.norm(ex.values, st, stream)
+            ex.decompress([ex.values], g, st, stream=stream)
+            st.adam(g, p, m, v, out, stream)
+            st.scaler(stream)
+        torch.cuda.synchronize()
+        return p, g, out, m.codes, m.exps, v.codes, v.exps, ex.values, ex.error
+
+    want = run(None, False)
+    for a, b in zip(run(torch.cuda.Stream(), True), want):
+        assert torch.equal(a, b)
+    assert want[8].abs().max() > 0

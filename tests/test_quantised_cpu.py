@@ -380,3 +380,26 @@ def test_step_classes_refuse():
     assert ex.groups == 13 and ex.values.numel() == 13 and ex.error is None
     with pytest.raises(zds.ZdsError):
         ex.compress(_f32(100), type("S", (), dict(state=torch.zeros(64, dtype=torch.uint8), scalars=None)))
+
+
+def test_buffers_are_cleared_before_they_are_handed_out(monkeypatch):
+    """Each construction that clears memory waits for the stream that does it,
+    after the last of its buffers is made: the calls may come on another one."""
+    log = []
+    zeros = torch.zeros
+    monkeypatch.setattr(torch, "zeros", lambda *a, **k: log.append("clear") or zeros(*a, **dict(k, device="cpu")))
+    monkeypatch.setattr(torch.cuda, "current_stream",
+                        lambda device=None: type("S", (), dict(synchronize=lambda self: log.append("wait")))())
+    DropoutExchange(64, 8, device="cuda")
+    assert log == ["clear", "clear", "wait"]
+    log.clear()
+    DropoutExchange(64, 8, feedback=False, device=torch.device("cuda", 0))
+    assert log == ["clear", "wait"]
+    log.clear()
+    step = object.__new__(QuantisedStep)
+    step.n, step.second, step.state = 64, zds.ZDS_STATE_UE5M3, type("T", (), dict(device=torch.device("cuda", 0)))
+    step.new_moments()
+    assert log == ["clear"] * 4 + ["wait"]
+    log.clear()
+    DropoutExchange(64, 8, device="cpu")
+    assert log == ["clear", "clear"]

@@ -10,6 +10,14 @@ tutorial §3.3: the engine's backward and step replace the plain ones).
 from . import zds
 
 
+def _wait_cleared(device):
+    """Waits for the current stream, on which a step's buffers were cleared: the
+    first call on them may come on another one."""
+    import torch
+    if torch.device(device).type == "cuda":
+        torch.cuda.current_stream(device).synchronize()
+
+
 class ShardStep:
     """Device buffers of one rank's step: the 64-byte step state, the 64-byte
     per-step scalars and the norm workspace, plus the step's settings."""
@@ -25,9 +33,8 @@ class ShardStep:
         self.state = zds.new_state(device)
         self.scalars = zds.new_scalars(device)
         self.ws = zds.new_workspace(n, device)
-        if stream is not None:  # the buffers were cleared on the current stream
-            import torch
-            torch.cuda.current_stream(device).synchronize()
+        if stream is not None:
+            _wait_cleared(device)
         zds.zds_step_state_init(self.state, self.cfg, t0, beta1_pow0, beta2_pow0, stream)
 
     @classmethod
@@ -223,9 +230,12 @@ class QuantisedStep(ShardStep):
                    second, seed, first, device, stream)
 
     def new_moments(self):
-        """(exp_avg, exp_avg_sq) of zeros, on the state's device."""
-        return (zds.new_quantised_state(self.n, zds.ZDS_STATE_E4M3, self.state.device),
-                zds.new_quantised_state(self.n, self.second, self.state.device))
+        """(exp_avg, exp_avg_sq) of zeros, on the state's device, ready for a
+        call on any stream."""
+        moments = (zds.new_quantised_state(self.n, zds.ZDS_STATE_E4M3, self.state.device),
+                   zds.new_quantised_state(self.n, self.second, self.state.device))
+        _wait_cleared(self.state.device)
+        return moments
 
     def adam(self, grads, master, exp_avg, exp_avg_sq, params_out, stream=None):
         if isinstance(exp_avg_sq, zds.QuantisedState) and exp_avg_sq.fmt != self.second:
@@ -269,6 +279,7 @@ class DropoutExchange:
         self.groups = zds.dropout_groups(n, ratio)
         self.values = torch.zeros(self.groups, dtype=torch.bfloat16 if dtype is None else dtype, device=device)
         self.error = torch.zeros(n, dtype=torch.float32, device=device) if feedback else None
+        _wait_cleared(device)  # (the calls take any stream)
 
     def compress(self, grads, step, stream=None):
         """The message of this rank's grads. step.scalars' overflow flag, left
