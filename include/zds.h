@@ -731,8 +731,9 @@ zds_status zds_adam_step_q8(const zds_adamw_hparams *hp, const void *grads, zds_
  * Gradient dropout: the two ends of an exchange in which every group of
  * `ratio` consecutive elements sends one, chosen at random by the counter
  * above, so that neither a mask nor places are stored or sent: all ranks
- * choose the same elements (same seed, first and steps_seen), and messages of
- * ceil(n / ratio) values can be summed by a plain all-reduce or
+ * choose the same elements (same seed, first, n and steps_seen: every rank
+ * sends its gradient of the same elements), and messages of ceil(n / ratio)
+ * values can be summed by a plain all-reduce or
  * reduce-scatter. What a rank does not send it keeps in an fp32 error buffer
  * and adds to its next gradient.
  * ratio is a power of two from 2 to 256. With j = first / ratio + g, the kept
@@ -774,7 +775,10 @@ zds_status zds_dropout_compress(const void *x, zds_dtype x_dtype, float *error, 
  * zds_overflow_and_norm over its ceil(n / ratio) values saves a pass over the
  * gradient (and so does zds_reduce_peer_slices_norm, which sums several).
  * Must be called before the zds_loss_scaler_update that ends the step whose
- * zds_dropout_compress made the values. dst must not overlap a message. */
+ * zds_dropout_compress made the values. dst must not overlap a message.
+ * A rank that needs the elements [lo, hi) only (its shard; lo a multiple of
+ * ratio) passes the messages from value lo / ratio on, n = hi - lo and
+ * first + lo. */
 zds_status zds_dropout_decompress(const void *const *peer_values, int32_t num_peers, zds_dtype value_dtype, int64_t n,
                                   int32_t ratio, uint64_t seed, int64_t first, const zds_step_state *state_dev,
                                   void *dst, zds_dtype dst_dtype, zds_accum_mode mode, void *stream);

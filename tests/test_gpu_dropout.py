@@ -319,3 +319,55 @@ def test_first_calls_on_another_stream_than_the_current_one():
     for a, b in zip(run(torch.cuda.Stream(), True), want):
         assert torch.equal(a, b)
     assert want[8].abs().max() > 0
+
+
+@pytest.mark.parametrize("ratio,world", [(16, 2), (4, 3), (64, 4)])
+def test_ranks_that_each_update_their_shard(ratio, world):
+    """Every rank sends its gradient of all elements and decodes its own shard:
+    what the ranks' shards become, put together, is what one rank that updates
+    everything makes of the same messages, bit for bit, the 8-bit moments'
+    roundings included, as they follow the flat element."""
+    numels = [50003, 777, 20000]
+    align = max(64, ratio)
+    total = zds.zds_shard_range(zds.zds_flat_layout(numels, align)[1], world, world - 1, align)[1]
+    hp, cfg = zds.hparams(lr=1e-3, beta2=0.95), zds.scaler_config(initial_scale_power=8)
+    start = torch.randn(total, device="cuda", generator=torch.Generator(device="cuda").manual_seed(1)) * 0.02
+
+    def rank(lo, hi):
+        st = QuantisedStep(hi - lo, hp, cfg, max_norm=1.0, accum_steps=world, seed=9, first=lo)
+        return dict(st=st, ex=DropoutExchange(total, ratio, torch.bfloat16, seed=21), lo=lo, hi=hi, mv=st.new_moments(),
+                    p=start[lo:hi].clone(), g=torch.empty(hi - lo, device="cuda"),
+                    o=torch.empty(hi - lo, dtype=torch.bfloat16, device="cuda"))
+
+    def take(q, message, span):
+        q["ex"].norm(message, q["st"])
+        q["ex"].decompress([message], q["g"], q["st"], span=span)
+        q["st"].adam(q["g"], q["p"], *q["mv"], q["o"])
+        q["st"].scaler()
+
+    ranks = [rank(*zds.zds_shard_range(total, world, r, align)) for r in range(world)]
+    assert len({q["lo"] for q in ranks}) == world
+    whole = rank(0, total)
+    for k in range(5):
+        for r, q in enumerate(ranks):
+            x = torch.randn(total, device="cuda", generator=torch.Generator(device="cuda").manual_seed(10 * k + r)).half()
+            if k == 2 and r == 1:
+                x[-5] = float("inf")                       # outside the shards of most ranks
+            q["ex"].flag(x, q["st"])
+            assert q["st"].read_scalars().overflow == (1 if k == 2 and r == 1 else 0)
+            q["ex"].compress(x, q["st"])
+        message = sum(q["ex"].values.float() for q in ranks).bfloat16()
+        for q in ranks:
+            take(q, message, (q["lo"], q["hi"]))
+        take(whole, message, None)
+        scalars = whole["st"].read_scalars()
+        assert scalars.overflow == (1 if k == 2 else 0) and (k == 2 or scalars.norm > 0)
+        for q in ranks:
+            assert bytes(q["st"].read_state()) == bytes(whole["st"].read_state())
+            assert bytes(q["st"].read_scalars())[:32] == bytes(scalars)[:32]
+        for name in ("g", "p", "o"):
+            got = torch.cat([q[name] for q in ranks])
+            assert torch.equal(got.view(torch.uint8), whole[name].view(torch.uint8)), (k, name)
+        assert torch.equal(torch.cat([q["mv"][0].codes for q in ranks]), whole["mv"][0].codes)
+        assert torch.equal(torch.cat([q["mv"][1].codes for q in ranks]), whole["mv"][1].codes)
+    assert not torch.equal(whole["p"], start)

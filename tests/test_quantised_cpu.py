@@ -390,6 +390,7 @@ def test_buffers_are_cleared_before_they_are_handed_out(monkeypatch):
     monkeypatch.setattr(torch, "zeros", lambda *a, **k: log.append("clear") or zeros(*a, **dict(k, device="cpu")))
     monkeypatch.setattr(torch.cuda, "current_stream",
                         lambda device=None: type("S", (), dict(synchronize=lambda self: log.append("wait")))())
+    monkeypatch.setattr(zds, "new_workspace", lambda n, device: None)      # (nothing in it is read first)
     DropoutExchange(64, 8, device="cuda")
     assert log == ["clear", "clear", "wait"]
     log.clear()
@@ -403,3 +404,27 @@ def test_buffers_are_cleared_before_they_are_handed_out(monkeypatch):
     log.clear()
     DropoutExchange(64, 8, device="cpu")
     assert log == ["clear", "clear"]
+
+
+def test_a_span_of_an_exchange():
+    """A shard begins and ends with whole groups (or at the end), and its values
+    are those of its groups in a whole message."""
+    ex = DropoutExchange(1000, 16, torch.float32, first=32, device="cpu")
+    values, dst = torch.arange(63, dtype=torch.float32), _f32(1000)
+    step = type("S", (), dict(state=torch.zeros(64, dtype=torch.uint8)))
+    for span in ((-16, 16), (8, 32), (0, 1001), (0, 24), (32, 16), (1008, 1008), (0, 1008)):
+        _raises(lambda: ex.decompress([values], dst, step, span=span), "span")
+    _raises(lambda: ex.decompress([values[:62]], dst, step, span=(0, 16)), "peer 0 holds 62")
+    _raises(lambda: ex.decompress([values], dst[:15], step, span=(16, 32)), "dst holds 15")
+
+
+def test_what_a_span_passes_on(monkeypatch):
+    ex = DropoutExchange(1000, 16, torch.float32, seed=5, first=32, device="cpu")
+    values, step, got = torch.arange(63, dtype=torch.float32), type("S", (), dict(state=None)), []
+    monkeypatch.setattr(zds, "zds_dropout_decompress",
+                        lambda peers, ratio, dst, seed, first, state, mode, stream, n: got.append(
+                            (peers[0].tolist(), ratio, seed, first, n)))
+    for span in ((0, 1000), (16, 48), (992, 1000), (64, 64), None):
+        ex.decompress([values], None, step, span=span)
+    assert got == [(list(range(63)), 16, 5, 32, 1000), ([1, 2], 16, 5, 48, 32), ([62], 16, 5, 32 + 992, 8),
+                   ([], 16, 5, 96, 0), (list(range(63)), 16, 5, 32, 1000)]

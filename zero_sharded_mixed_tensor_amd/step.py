@@ -259,15 +259,21 @@ class QuantisedStep(ShardStep):
 class DropoutExchange:
     """One rank's end of an exchange that sends one element of each group of
     `ratio`: the message's buffer and the fp32 feedback buffer (feedback False:
-    none; what is sent is then scaled by ratio). Every rank uses the same seed
-    and first. A step over N ranks (accum_steps = K * N):
+    none; what is sent is then scaled by ratio).
 
-        step.norm(grads)                     # the rank's own overflow flag
+    Every rank uses the same seed, n and first, since all of them have to send
+    the same elements: a message is of the rank's gradient over all n elements,
+    whatever part of it the rank then updates. A step over N ranks
+    (accum_steps = K * N), each with the shard [lo, hi):
+
+        ex.flag(grads, step)                 # the rank's own overflow flag
         ex.compress(grads, step)
         all_reduce(ex.values)
         ex.norm(ex.values, step)             # flag, norm and clip of the sum
-        ex.decompress([ex.values], grads, step)
-        step.adam(grads, ...); step.scaler()"""
+        ex.decompress([ex.values], shard, step, span=(lo, hi))
+        step.adam(shard, ...); step.scaler()
+
+    span is left out where every rank updates everything."""
 
     def __init__(self, n, ratio, dtype=None, seed=0, first=0, feedback=True, device="cuda"):
         import torch
@@ -279,10 +285,16 @@ class DropoutExchange:
         self.groups = zds.dropout_groups(n, ratio)
         self.values = torch.zeros(self.groups, dtype=torch.bfloat16 if dtype is None else dtype, device=device)
         self.error = torch.zeros(n, dtype=torch.float32, device=device) if feedback else None
+        self.ws = zds.new_workspace(n, device)  # (a step's own is that of its shard)
         _wait_cleared(device)  # (the calls take any stream)
 
+    def flag(self, grads, step, stream=None):
+        """Leaves the overflow flag of this rank's n grads in step.scalars,
+        where compress() looks for it."""
+        self._norm(grads, step, stream, self.n)
+
     def compress(self, grads, step, stream=None):
-        """The message of this rank's grads. step.scalars' overflow flag, left
+        """The message of this rank's n grads. step.scalars' overflow flag, left
         by a norm pass over them, poisons it."""
         zds.zds_dropout_compress(grads, self.error, self.ratio, self.values, self.seed, self.first, step.state,
                                  step.scalars, stream, n=self.n)
@@ -290,12 +302,27 @@ class DropoutExchange:
     def norm(self, total, step, stream=None):
         """Overflow flag, norm and clip of the gradient that an all-reduced
         message (or zds_reduce_peer_slices' sum of several) makes: those of the
-        message, as the other elements are 0."""
-        zds.zds_overflow_and_norm(total, step.accum_steps, step.max_norm, step.state, step.scalars, step.ws, stream,
-                                  n=self.groups)
+        message, as the other elements are 0. They are of all n elements, and so
+        the same on every rank."""
+        self._norm(total, step, stream, self.groups)
 
-    def decompress(self, peers, dst, step, mode=zds.ZDS_OVERWRITE, stream=None):
-        zds.zds_dropout_decompress(peers, self.ratio, dst, self.seed, self.first, step.state, mode, stream, n=self.n)
+    def decompress(self, peers, dst, step, mode=zds.ZDS_OVERWRITE, stream=None, span=None):
+        """The gradient of the whole messages in peers, or of its elements
+        [lo, hi) = span, into dst (hi - lo elements). lo is a multiple of ratio,
+        and so is hi if it is not n. (Shards at multiples of 16 bytes of a message,
+        8 * ratio elements for 16-bit values, decode faster.)"""
+        lo, hi = (0, self.n) if span is None else span
+        r = self.ratio
+        if not 0 <= lo <= hi <= self.n or lo % r or (hi % r and hi != self.n):
+            raise zds.ZdsError(zds.ZDS_EINVAL, "the span [%d, %d) must lie in [0, %d) at multiples of %d" % (lo, hi, self.n, r))
+        for k, t in enumerate(peers):
+            zds._need(t, self.groups, "peer %d" % k)
+        if span is not None:
+            peers = [t.view(-1)[lo // r:zds.dropout_groups(hi, r)] for t in peers]
+        zds.zds_dropout_decompress(peers, r, dst, self.seed, self.first + lo, step.state, mode, stream, n=hi - lo)
+
+    def _norm(self, x, step, stream, n):
+        zds.zds_overflow_and_norm(x, step.accum_steps, step.max_norm, step.state, step.scalars, self.ws, stream, n=n)
 
 
 class OffloadStep:
