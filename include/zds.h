@@ -758,7 +758,10 @@ zds_status zds_adam_step_q8(const zds_adamw_hparams *hp, const void *grads, zds_
  *   not kept: error = c * (1 / S)
  * Without: value = round_nearest_even(ratio * x) of the kept element, which is
  * right on average.
- * A step that is skipped after the exchange loses what it sent. No two arrays
+ * A step that is skipped after the exchange loses what it sent: a rank whose
+ * own flag is clear has taken that out of its error, earlier feedback included.
+ * Ranks that combine their flags first (the maximum, into scalars_dev) all keep
+ * their errors. No two arrays
  * may overlap. first >= 0, a multiple of ratio; n below 2^40. */
 zds_status zds_dropout_compress(const void *x, zds_dtype x_dtype, float *error, int64_t n, int32_t ratio,
                                 uint64_t seed, int64_t first, const zds_step_scalars *scalars_dev,

@@ -371,3 +371,55 @@ def test_ranks_that_each_update_their_shard(ratio, world):
         assert torch.equal(torch.cat([q["mv"][0].codes for q in ranks]), whole["mv"][0].codes)
         assert torch.equal(torch.cat([q["mv"][1].codes for q in ranks]), whole["mv"][1].codes)
     assert not torch.equal(whole["p"], start)
+
+
+@pytest.mark.parametrize("combined", [False, True])
+def test_what_an_overflow_leaves_in_the_errors(combined):
+    """Two ranks, one of which overflows at step 3. Its message is NaN and both
+    skip the step; its error stays as it was. The other rank's error is what
+    its compress made of it, so that what it sent is lost, unless the flags were
+    combined first: then its error stays, too, and over the other steps decoded
+    messages and errors add up to the gradients, exactly (whole numbers)."""
+    n, ratio, world = 20005, 8, 2
+
+    def rank():
+        st = ShardStep(n, zds.hparams(lr=0.0), zds.scaler_config(initial_scale_power=4), max_norm=0.0, accum_steps=world)
+        return dict(st=st, ex=DropoutExchange(n, ratio, torch.float32, seed=21))
+
+    ranks = [rank() for _ in range(world)]
+    given, taken = torch.zeros(n, device="cuda"), torch.zeros(n, device="cuda")
+    for k in range(6):
+        scale = ranks[0]["st"].read_state().scale
+        flags, xs, before = [], [], [q["ex"].error.clone() for q in ranks]
+        for r, q in enumerate(ranks):
+            x = np.random.default_rng(10 * k + r).integers(-100, 101, n).astype(np.float32) * np.float32(scale)
+            if k == 3 and r == 1:
+                x[123] = np.inf
+            xs.append(x)
+            flags.append(q["ex"].flag(to_dev(x, "fp32"), q["st"]))
+        assert [int(f) for f in flags] == ([0, 1] if k == 3 else [0, 0])
+        if combined:
+            top = torch.maximum(*flags)
+            for f in flags:
+                f.copy_(top)
+        for x, q in zip(xs, ranks):
+            q["ex"].compress(to_dev(x, "fp32"), q["st"])
+        total = ranks[0]["ex"].values + ranks[1]["ex"].values
+        for r, (x, q, e) in enumerate(zip(xs, ranks, before)):
+            skipped = k == 3 and (combined or r == 1)
+            assert torch.isnan(q["ex"].values).all() == skipped
+            want = to_host(e) if skipped else Q.dropout_compress(x, "fp32", to_host(e), ratio, 21, 0, k, scale, "fp32")[1]
+            same(to_host(q["ex"].error), want, "fp32")
+        if k == 3:
+            assert torch.equal(ranks[0]["ex"].error, before[0]) == combined
+        g = torch.empty(n, device="cuda")
+        for q in ranks:
+            q["ex"].norm(total, q["st"])
+            q["ex"].decompress([total], g, q["st"])
+            assert q["st"].read_scalars().overflow == (1 if k == 3 else 0)
+            q["st"].scaler()
+        if k != 3:
+            given += sum(to_dev(x, "fp32") for x in xs) / scale
+            taken += g / scale
+    left = ranks[0]["ex"].error + ranks[1]["ex"].error
+    assert torch.equal(given, taken + left) == combined

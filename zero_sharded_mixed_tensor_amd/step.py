@@ -266,14 +266,21 @@ class DropoutExchange:
     whatever part of it the rank then updates. A step over N ranks
     (accum_steps = K * N), each with the shard [lo, hi):
 
-        ex.flag(grads, step)                 # the rank's own overflow flag
+        flag = ex.flag(grads, step)          # the rank's own overflow flag
+        all_reduce(flag, MAX)
         ex.compress(grads, step)
         all_reduce(ex.values)
         ex.norm(ex.values, step)             # flag, norm and clip of the sum
         ex.decompress([ex.values], shard, step, span=(lo, hi))
         step.adam(shard, ...); step.scaler()
 
-    span is left out where every rank updates everything."""
+    span is left out where every rank updates everything. The flags' all-reduce
+    may be left out, too: a message of a rank that overflows is NaN, and all ranks
+    skip the step. But the other ranks have then taken what they sent out of their
+    errors, feedback of earlier steps among it, and it is lost with the step; with
+    the flags combined first no rank sends anything and all errors stay as they
+    are. (A sum of messages that overflows by itself, in fp16, loses what was sent
+    all the same.)"""
 
     def __init__(self, n, ratio, dtype=None, seed=0, first=0, feedback=True, device="cuda"):
         import torch
@@ -290,8 +297,10 @@ class DropoutExchange:
 
     def flag(self, grads, step, stream=None):
         """Leaves the overflow flag of this rank's n grads in step.scalars,
-        where compress() looks for it."""
+        where compress() looks for it, and returns it: one int32 on the device,
+        0 or 1, whose maximum over the ranks may be written back in place."""
         self._norm(grads, step, stream, self.n)
+        return zds.overflow_flag(step.scalars)
 
     def compress(self, grads, step, stream=None):
         """The message of this rank's n grads. step.scalars' overflow flag, left

@@ -972,6 +972,11 @@ def read_scalars(t):
     return StepScalars.from_buffer_copy(bytes(t.cpu().numpy().tobytes()))
 
 
+def overflow_flag(t):
+    """The overflow flag of step scalars on the device, one int32 in place."""
+    return t.view(torch.int32)[:1]
+
+
 def write_scalars(t, scalars):
     """Host -> device copy of a StepScalars (tests force flags this way)."""
     import numpy as np
