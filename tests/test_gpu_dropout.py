@@ -15,7 +15,7 @@ from oracle.zero_step import narrow, widen  # noqa: E402
 from tests.test_gpu_quantised import scalars, state  # noqa: E402
 from tests.util import to_dev, to_host  # noqa: E402
 from zero_sharded_mixed_tensor_amd import zds  # noqa: E402
-from zero_sharded_mixed_tensor_amd.step import DropoutExchange, QuantisedStep, ShardStep  # noqa: E402
+from zero_sharded_mixed_tensor_amd.step import DropoutExchange, MuonStep, OffloadStep, QuantisedStep, ShardStep  # noqa: E402
 
 TDT = {"fp16": torch.float16, "bf16": torch.bfloat16, "fp32": torch.float32}
 SEED = 0xC0FFEE1234567
@@ -423,3 +423,70 @@ def test_what_an_overflow_leaves_in_the_errors(combined):
             taken += g / scale
     left = ranks[0]["ex"].error + ranks[1]["ex"].error
     assert torch.equal(given, taken + left) == combined
+
+
+def _gradient(ex, k):
+    """What the exchange's message makes in step k, by the plain call, in the message's type."""
+    g = torch.empty(ex.n, dtype=ex.values.dtype, device="cuda")
+    zds.zds_dropout_decompress([ex.values], ex.ratio, g, ex.seed, ex.first, state(k))
+    return g
+
+
+def test_exchange_in_front_of_a_muon_step():
+    """The state and scalars of its base: two steps end where steps on the
+    gradient that the messages make end (no clipping, so that the norm's order
+    of sums does not come in)."""
+    n, split, ratio = 200 * 72 + 3000, 200 * 72, 4
+
+    def fresh():
+        g = torch.Generator(device="cuda").manual_seed(5)
+        return MuonStep(n, split, [(0, 200, 72)], max_norm=0.0, scaler=zds.scaler_config(dynamic=False)), [
+            torch.randn(n, device="cuda", generator=g), torch.zeros(split, device="cuda"),
+            torch.zeros(n - split, device="cuda"), torch.zeros(n - split, device="cuda"),
+            torch.zeros(n, dtype=torch.bfloat16, device="cuda")]
+    (a, sa), (b, sb) = fresh(), fresh()
+    ex, got = DropoutExchange(n, ratio, torch.bfloat16, seed=3), torch.empty(n, dtype=torch.bfloat16, device="cuda")
+    for k in range(2):
+        x = torch.randn(n, generator=torch.Generator().manual_seed(k)).bfloat16().cuda()
+        assert int(ex.flag(x, a)) == 0
+        ex.compress(x, a)
+        ex.norm(ex.values, a)
+        ex.decompress([ex.values], got, a)
+        want = _gradient(ex, k)
+        assert torch.equal(got, want) and (want != 0).any()
+        a.apply(got, *sa)
+        a.base.scaler()
+        b.step(want, *sb)
+    for x, y in zip(sa, sb):
+        assert torch.equal(x, y)
+    assert a.read_state().t == 2 and bytes(a.read_state()) == bytes(b.read_state())
+
+
+def test_exchange_in_front_of_an_offloaded_step():
+    """The state and scalars on the device: two steps, one of them skipped, end
+    where steps on the gradient that the messages make end."""
+    n, ratio = 70001, 8
+
+    def fresh():
+        host = [torch.zeros(n).pin_memory() for _ in range(3)]
+        host[0].copy_(torch.randn(n, generator=torch.Generator().manual_seed(5)))
+        return OffloadStep(n, *host, torch.float16, torch.float16, chunk=1 << 15), host
+    (a, ha), (b, hb) = fresh(), fresh()
+    ex = DropoutExchange(n, ratio, torch.float16, seed=3)
+    pa, pb = (torch.zeros(n, dtype=torch.float16, device="cuda") for _ in range(2))
+    got = torch.empty(n, dtype=torch.float16, device="cuda")
+    for k in range(3):
+        x = torch.randn(n, generator=torch.Generator().manual_seed(k)).half().cuda()
+        if k == 1:
+            x[7] = float("inf")
+        assert int(ex.flag(x, a)) == (1 if k == 1 else 0)
+        ex.compress(x, a)
+        ex.decompress([ex.values], got, a)
+        want = _gradient(ex, k)
+        assert torch.equal(got.view(torch.int16), want.view(torch.int16))
+        for q, g, p in ((a, got, pa), (b, want, pb)):
+            assert q.step(g, p).overflow == (1 if k == 1 else 0)
+    torch.cuda.synchronize()
+    for x, y in zip(ha + [pa], hb + [pb]):
+        assert torch.equal(x, y)
+    assert bytes(a.dev.read_state()) == bytes(b.dev.read_state()) and a.dev.read_state().steps_skipped == 1

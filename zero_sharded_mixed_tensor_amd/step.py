@@ -280,7 +280,12 @@ class DropoutExchange:
     errors, feedback of earlier steps among it, and it is lost with the step; with
     the flags combined first no rank sends anything and all errors stay as they
     are. (A sum of messages that overflows by itself, in fp16, loses what was sent
-    all the same.)"""
+    all the same.)
+
+    step is a ShardStep or QuantisedStep; a MuonStep, which goes on with
+    step.apply(grads, ...) and step.base.scaler(); or an OffloadStep, which goes
+    on with step.step(grads, params): that takes flag and norm of the grads it is
+    given by itself, so they have to be the whole gradient if it clips."""
 
     def __init__(self, n, ratio, dtype=None, seed=0, first=0, feedback=True, device="cuda"):
         import torch
@@ -300,13 +305,14 @@ class DropoutExchange:
         where compress() looks for it, and returns it: one int32 on the device,
         0 or 1, whose maximum over the ranks may be written back in place."""
         self._norm(grads, step, stream, self.n)
-        return zds.overflow_flag(step.scalars)
+        return zds.overflow_flag(_shard_step(step).scalars)
 
     def compress(self, grads, step, stream=None):
         """The message of this rank's n grads. step.scalars' overflow flag, left
         by a norm pass over them, poisons it."""
-        zds.zds_dropout_compress(grads, self.error, self.ratio, self.values, self.seed, self.first, step.state,
-                                 step.scalars, stream, n=self.n)
+        base = _shard_step(step)
+        zds.zds_dropout_compress(grads, self.error, self.ratio, self.values, self.seed, self.first, base.state,
+                                 base.scalars, stream, n=self.n)
 
     def norm(self, total, step, stream=None):
         """Overflow flag, norm and clip of the gradient that an all-reduced
@@ -328,10 +334,17 @@ class DropoutExchange:
             zds._need(t, self.groups, "peer %d" % k)
         if span is not None:
             peers = [t.view(-1)[lo // r:zds.dropout_groups(hi, r)] for t in peers]
-        zds.zds_dropout_decompress(peers, r, dst, self.seed, self.first + lo, step.state, mode, stream, n=hi - lo)
+        zds.zds_dropout_decompress(peers, r, dst, self.seed, self.first + lo, _shard_step(step).state, mode, stream,
+                                   n=hi - lo)
 
     def _norm(self, x, step, stream, n):
-        zds.zds_overflow_and_norm(x, step.accum_steps, step.max_norm, step.state, step.scalars, self.ws, stream, n=n)
+        base = _shard_step(step)
+        zds.zds_overflow_and_norm(x, base.accum_steps, base.max_norm, base.state, base.scalars, self.ws, stream, n=n)
+
+
+def _shard_step(step):
+    """The ShardStep that holds a step's state, scalars and settings."""
+    return step.base if isinstance(step, MuonStep) else step.dev if isinstance(step, OffloadStep) else step
 
 
 class OffloadStep:
