@@ -490,3 +490,38 @@ def test_exchange_in_front_of_an_offloaded_step():
     for x, y in zip(ha + [pa], hb + [pb]):
         assert torch.equal(x, y)
     assert bytes(a.dev.read_state()) == bytes(b.dev.read_state()) and a.dev.read_state().steps_skipped == 1
+
+
+def test_an_exchange_is_resumed():
+    """Steps with a save and a resume between them: the checkpoint's arrays and
+    the exchange's error are all that goes on, bit for bit."""
+    n, ratio = 30011, 16
+
+    def fresh():
+        st = QuantisedStep(n, zds.hparams(lr=1e-3, beta2=0.95), zds.scaler_config(initial_scale_power=6), seed=8)
+        return st, DropoutExchange(n, ratio, torch.bfloat16, seed=9), torch.ones(n, device="cuda"), *st.new_moments()
+
+    def go(st, ex, p, m, v, some):
+        g = torch.empty(n, device="cuda")
+        for k in some:
+            x = torch.randn(n, generator=torch.Generator().manual_seed(k)).half().cuda()
+            ex.flag(x, st)
+            ex.compress(x, st)
+            ex.norm(ex.values, st)
+            ex.decompress([ex.values], g, st)
+            st.adam(g, p, m, v, None)
+            st.scaler()
+
+    straight, first, second = fresh(), fresh(), fresh()
+    go(*straight, range(6))
+    go(*first, range(3))
+    m32, v32 = torch.empty(n, device="cuda"), torch.empty(n, device="cuda")
+    first[0].read_back(first[3], first[4], m32, v32)
+    second[0].state.copy_(first[0].state)
+    second[0].quantise(m32, v32, second[3], second[4])
+    second[2].copy_(first[2])
+    assert first[1].error.abs().max() > 0
+    second[1].error.copy_(first[1].error)
+    go(*second, range(3, 6))
+    assert torch.equal(second[2], straight[2]) and torch.equal(second[1].error, straight[1].error)
+    assert torch.equal(second[1].values, straight[1].values)

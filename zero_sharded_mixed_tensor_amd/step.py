@@ -285,7 +285,10 @@ class DropoutExchange:
     step is a ShardStep or QuantisedStep; a MuonStep, which goes on with
     step.apply(grads, ...) and step.base.scaler(); or an OffloadStep, which goes
     on with step.step(grads, params): that takes flag and norm of the grads it is
-    given by itself, so they have to be the whole gradient if it clips."""
+    given by itself, so they have to be the whole gradient if it clips.
+
+    A run that is to be resumed saves `error` with its checkpoint (n fp32
+    elements, this rank's own) and copies it back."""
 
     def __init__(self, n, ratio, dtype=None, seed=0, first=0, feedback=True, device="cuda"):
         import torch
