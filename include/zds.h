@@ -703,14 +703,10 @@ zds_status zds_state_dequantise(const void *codes, const uint8_t *exps, int64_t 
                                 zds_dtype dst_dtype, void *stream);
 
 /* zds_adam_step on moments in fewer bits: reads both back, applies the same
- * update, and quantises what it writes at random. The moments are those that
- * zds_adam_step leaves of the state that zds_state_dequantise gives, and the
- * codes those that zds_state_quantise makes of them (ZDS_ROUND_RANDOM, the same
- * seed and first), bit for bit. The update's root and quotient are within 1 ulp
- * each instead of correctly rounded: with u = lr / (1 - b1^t) * (m / denom),
- * master differs from zds_adam_step's by at most 2^-20 |u| and one rounding
- * (where v is below 2^104; from there on it counts as infinite), and params_out
- * is its cast.
+ * update, and quantises what it writes at random: master and params_out are
+ * those of zds_adam_step on the state that zds_state_dequantise gives, and the
+ * codes those that zds_state_quantise makes (ZDS_ROUND_RANDOM, the same seed and
+ * first) of the moments it leaves, bit for bit.
  * Calls of few elements form the step's constants in the update's own kernel and
  * leave those in scalars_dev as they were.
  *   hp            as for zds_adam_step, but eps >= 2^-100

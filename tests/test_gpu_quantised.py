@@ -274,6 +274,60 @@ def test_step_is_read_back_adam_quantise(second, n):
     assert torch.equal(o2, p2.bfloat16())
 
 
+@pytest.mark.parametrize("second", [zds.ZDS_STATE_UE5M3, zds.ZDS_STATE_BF16])
+@pytest.mark.parametrize("n,pad", [(700001, 0), (50003, 1), (5 * 1024 * 1024 + 31, 0)])
+@pytest.mark.parametrize("eps", [1e-8, 1e-29])
+def test_step_leaves_the_master_that_adam_leaves(second, n, pad, eps):
+    """master and params are zds_adam_step's on the state that is read back, bit
+    for bit, over all of fp32's range: gradients from 2^-80 to 2^60, whose squares
+    underflow or pass 2^104, elements and blocks of zeros, small parameters."""
+    g = torch.Generator(device="cuda").manual_seed(n + pad)
+
+    def wide(lo, hi, zeros):
+        e = torch.empty((n + pad + 127) // 128, device="cuda").uniform_(lo, hi, generator=g).repeat_interleave(128)[:n + pad]
+        x = torch.randn(n + pad, device="cuda", generator=g) * torch.exp2(e)
+        x[torch.rand(n + pad, device="cuda", generator=g) < zeros] = 0.0
+        x[256:512] = 0.0
+        return x[pad:]
+    grads, master = wide(-80, 60, 0.05), wide(-100, 2, 0.02)
+    m32, v32 = wide(-90, 40, 0.1), wide(-140, 110, 0.1).abs()
+    st, sc = state(3, t=3, b1p=0.7, b2p=0.8), scalars(0.75)
+    hp = zds.hparams(lr=1e-3, beta2=0.95, eps=eps, weight_decay=0.1)
+    m, v = zds.new_quantised_state(n, zds.ZDS_STATE_E4M3), zds.new_quantised_state(n, second)
+    zds.zds_state_quantise(m32, m)
+    zds.zds_state_quantise(v32, v)
+    back = [torch.empty(n, device="cuda") for _ in range(2)]
+    zds.zds_state_dequantise(m, back[0])
+    zds.zds_state_dequantise(v, back[1])
+    p2 = torch.cat([master[:pad], master])[pad:]
+    p1, o1, o2 = master.clone(), torch.empty(n, dtype=torch.float16, device="cuda"), \
+        torch.empty(n, dtype=torch.float16, device="cuda")
+    zds.zds_adam_step(hp, grads.clone(), p1, *back, o1, sc, st)
+    zds.zds_adam_step_q8(hp, grads, p2, m, v, o2, 11, 96, sc, st)
+    nan = torch.isnan(p1)
+    assert (back[1] >= 2.0 ** 104).sum() > n // 1000 and (~nan).sum() > n // 2
+    assert torch.equal(torch.isnan(p2), nan)
+    assert torch.equal(p2.view(torch.int32)[~nan], p1.view(torch.int32)[~nan])
+    assert torch.equal(o2.view(torch.int16)[~nan], o1.view(torch.int16)[~nan])
+
+
+def test_steps_constants_on_either_side_of_their_launch():
+    """Whole tiles of a call that forms the step's constants itself, through 200
+    steps' values of them, against zds_adam_step's bits."""
+    n = 4096
+    g = torch.Generator(device="cuda").manual_seed(1)
+    grads, master = torch.randn(n, device="cuda", generator=g), torch.randn(n, device="cuda", generator=g)
+    for t in range(200):
+        b1, b2 = 0.9 + t % 7 * 0.01, 0.999 - t % 5 * 0.013
+        st, hp = state(t, t=t, b1p=b1 ** t, b2p=b2 ** t), zds.hparams(lr=1e-3 * (1 + t), beta1=b1, beta2=b2)
+        m, v = zds.new_quantised_state(n, zds.ZDS_STATE_E4M3), zds.new_quantised_state(n, zds.ZDS_STATE_UE5M3)
+        back = [torch.zeros(n, device="cuda") for _ in range(2)]
+        p1, p2 = master.clone(), master.clone()
+        zds.zds_adam_step(hp, grads, p1, *back, None, scalars(0.5), st)
+        zds.zds_adam_step_q8(hp, grads, p2, m, v, None, 1, 0, scalars(0.5), st)
+        assert torch.equal(p1, p2), t
+
+
 def test_step_on_the_grads_buffer_and_the_skip():
     n = 4099
     (mc, me), (vc, ve), size = moments(n, 8, Q.UE5M3)

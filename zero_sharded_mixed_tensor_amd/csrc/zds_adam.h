@@ -1,4 +1,5 @@
-// The scalars of AdamW's update kernels and the scheduling of their waves.
+// What AdamW's update kernels share: their scalars, the update of an element and
+// the scheduling of their waves.
 #pragma once
 
 #include "zds_device.h"
@@ -25,6 +26,31 @@ __device__ __forceinline__ ElemConsts load_consts(const zds_step_scalars *sc) {
   c.decay = sc->decay;
   c.gs = sc->grad_scale;
   return c;
+}
+
+// One element, fp32, one rounding per operation, in this order.
+//
+// sqrt(v) / bc2 (bc2 = sqrt(1 - beta2^t) in fp32) is formed as
+// fp32(float64(sqrt(v)) * r) with r = 1 / float64(bc2) correctly rounded.
+// That is the correctly rounded fp32 quotient: r carries a relative error of
+// at most 2^-53 and the float64 product another 2^-53, so the product is
+// within 2^-52 (relatively) of the exact quotient; the exact quotient a/b of
+// two fp32 numbers is never a point halfway between two fp32 numbers (a
+// halfway point times b would need more than 24 significant bits), and lies at
+// least 2^-49 (relatively) away from every such point, because
+// |a - b*M| is a non-zero multiple of the coarser of a's and b*M's
+// granularities. So no rounding boundary separates the product from the
+// exact quotient. Here a = sqrt(v) is 0, NaN, inf or at least 2^-74.5, and
+// the quotient stays in the normal range; bc2 = 0 (beta2 = 1) gives
+// r = inf and the same inf / NaN as the division.
+__device__ __forceinline__ void adam_elem(float x, const ElemConsts &c, float &p, float &m, float &v) {
+  const float g = x * c.gs;
+  m = c.b1 * m + c.omb1 * g;
+  v = c.b2 * v + c.omb2 * (g * g);
+  const float q = static_cast<float>(static_cast<double>(sqrtf(v)) * c.inv_bc2);
+  const float denom = q + c.eps;
+  p = p * c.decay;
+  p = p - c.step_size * (m / denom);
 }
 
 // Scheduling priority of a wave: raised while it issues its loads and stores,

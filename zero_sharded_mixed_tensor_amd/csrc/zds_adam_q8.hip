@@ -3,18 +3,20 @@
 // random (include/zds.h; zds_quantised.h has the formats' arithmetic).
 //
 // A stream of 16.1 B an element (16-bit grads; 18.1 with a BF16 second moment)
-// and about 50 VALU instructions an element, 6 of them the generator's: on 842M
-// elements 2.06 ms of memory at the rate of a copy and 1.4 ms of all SIMDs, so
-// what counts is that the one hides the other. A block of 8 waves takes a tile
-// of 2048 elements; the waves fetch it 16 bytes a lane, one access in flight
-// each, the master's quads straight into the registers of the thread that
-// updates them, grads and codes through LDS; four of the waves make the
-// generator's calls meanwhile; the results go out the same way. 842M elements,
-// bf16: 2.125 ms (6.39 TB/s); before, each lane moving its own quad of every array
-// (4-byte accesses to the codes) 2.36, of which the arithmetic was not the cause
-// (2.48 without it); other layouts that lost: a wave's own 1024 elements through
-// its own LDS, no barriers 2.24; tiles of 4096 in two pipelined halves, as the
-// fp32 step's, 2.28 to 2.39; tiles of 1024 with one access a wave 2.73.
+// and about 75 VALU instructions an element, 6 of them the generator's and 30 the
+// correctly rounded root and quotient: on 842M elements 2.06 ms of memory at the
+// rate of a copy and about as much of all SIMDs, so what counts is that the one
+// hides the other. A block of 8 waves takes a tile of 2048 elements; the waves
+// fetch it 16 bytes a lane, one access in flight each, the master's quads straight
+// into the registers of the thread that updates them, grads and codes through
+// LDS; four of the waves make the generator's calls meanwhile; the results go out
+// the same way. 842M elements, bf16: 2.26 ms (6.01 TB/s). The hardware's root and
+// reciprocal, 26 instructions fewer, took 2.15, but then master is no longer
+// zds_adam_step's. Layouts, timed with those (2.13 then): each lane moving its own
+// quad of every array (4-byte accesses to the codes) 2.36, of which the arithmetic
+// was not the cause (2.48 without it); a wave's own 1024 elements through its own
+// LDS, no barriers 2.24; tiles of 4096 in two pipelined halves, as the fp32
+// step's, 2.28 to 2.39; tiles of 1024 with one access a wave 2.73.
 #include "zds_adam.h"
 #include "zds_quantised.h"
 
@@ -37,48 +39,17 @@ struct AdamQ8Args {
   zds_adamw_hparams hp;
 };
 
-// The update of one element: the moments as zds_adam_step forms them (adam_elem
-// in zds_adam.hip; one rounding per operation, so the codes are those of the
-// separate calls), the parameter with the hardware's square root and
-// reciprocal, which are within 1 ulp, where adam_elem's are correctly rounded:
-// 26 instructions fewer of about 75 an element, and the kernel's time is partly
-// theirs (2.22 against 2.13 ms at 842M elements with bf16 grads).
-// The error of the change u = step_size * (m / denom), in units of 2^-24: root
-// 2, the factor 1 / bc2 rounded 1, the product 1, + eps 1, reciprocal 2, two
-// products 2, together 9, and 5 of adam_elem's own: below 2^-20 |u|, and one
-// rounding of p.
-// The instruction takes a root of subnormals as 0, so v enters times 2^24 and
-// the factor carries 2^-12; from 2^104 on (grads past 2^52) v counts as infinite.
-struct Q8Consts {
-  ElemConsts e;
-  float inv;  // 2^-12 / bc2
-};
-__device__ __forceinline__ Q8Consts load_q8_consts(const zds_step_scalars *sc) {
-  Q8Consts c;
-  c.e = load_consts(sc);
-  c.inv = static_cast<float>(c.e.inv_bc2 * 0x1p-12);
-  return c;
-}
-// The same, formed here from the hyperparameters and the step state.
-__device__ __forceinline__ Q8Consts derive_q8_consts(const AdamQ8Args &a) {
+// The step's constants, formed here from the hyperparameters and the step state.
+__device__ __forceinline__ ElemConsts derive_consts(const AdamQ8Args &a) {
   const AdamConsts k = adam_constants(a.hp, a.state->beta1_pow, a.state->beta2_pow);
-  return Q8Consts{ElemConsts{k.b1, k.b2, k.omb1, k.omb2, k.eps, k.step_size, k.decay, a.sc->grad_scale, k.inv_bc2_sqrt},
-                  static_cast<float>(k.inv_bc2_sqrt * 0x1p-12)};
-}
-__device__ __forceinline__ void q8_elem(float x, const Q8Consts &c, float &p, float &m, float &v) {
-  const float g = x * c.e.gs;
-  m = c.e.b1 * m + c.e.omb1 * g;
-  v = c.e.b2 * v + c.e.omb2 * (g * g);
-  const float denom = __builtin_amdgcn_sqrtf(v * 0x1p24f) * c.inv + c.e.eps;
-  p = p * c.e.decay;
-  p = p - c.e.step_size * (m * __builtin_amdgcn_rcpf(denom));
+  return ElemConsts{k.b1, k.b2, k.omb1, k.omb2, k.eps, k.step_size, k.decay, a.sc->grad_scale, k.inv_bc2_sqrt};
 }
 
 // One element on each lane, the block of 32 that shares an exponent in half a
 // wave: what is not a whole tile, and arrays without the tiles' alignment. All
 // lanes of a wave call it; e is past the end on some.
 template <int GD, int PD, int VF>
-__device__ __forceinline__ void q8_element(const AdamQ8Args &a, const Q8Consts &c, int64_t e, uint32_t steps) {
+__device__ __forceinline__ void q8_element(const AdamQ8Args &a, const ElemConsts &c, int64_t e, uint32_t steps) {
   const bool in = e < a.n;
   uint8_t *mc = static_cast<uint8_t *>(a.m);
   uint8_t *vc = static_cast<uint8_t *>(a.v);
@@ -89,7 +60,7 @@ __device__ __forceinline__ void q8_element(const AdamQ8Args &a, const Q8Consts &
     m = decode1<ZDS_STATE_E4M3>(mc[e], a.me[e >> 5]);
     if constexpr (VF == ZDS_STATE_BF16) v = __uint_as_float(static_cast<uint32_t>(v16[e]) << 16);
     else v = decode1<VF>(vc[e], a.ve[e >> 5]);
-    q8_elem(widen1<GD>(a.g, e), c, p, m, v);
+    adam_elem(widen1<GD>(a.g, e), c, p, m, v);
   }
   const uint32_t r = element_random_bits(a.seed, static_cast<uint64_t>(a.first + e), steps);
   const uint32_t rs = swap_bytes(r);
@@ -127,15 +98,15 @@ struct Q8Tile {
   u32x4 v[VF == ZDS_STATE_BF16 ? 256 : 128];
   u32x4 random[256];
   uint8_t me[64], ve[64];
-  f32x4 consts[2];
+  ElemConsts consts;
 };
 
 // Up to this many elements the blocks form the step's constants themselves, by
 // one wave while the loads are in flight, instead of a launch in front of them:
-// a call of 1M elements takes 6.6 us in a graph instead of 7.6 and 10 us on the
-// host instead of 13; of 4M 16.1 and 16.6; of 8M 28.5 and 27.5, of 842M 2.27 ms
-// and 2.13, as every block pays for the divisions.
-constexpr int64_t kQ8OwnConsts = int64_t(1) << 22;
+// a call of 1M elements takes 7.0 us in a graph instead of 7.8 (and 10 us on the
+// host instead of 13), of 2M 9.2 and 9.6; of 4M 16.3 and 15.5, of 8M 27.8 and
+// 25.5, as every block pays for the divisions.
+constexpr int64_t kQ8OwnConsts = int64_t(1) << 21;
 
 // One tile a block, and a last block for the elements behind the last whole
 // tile. PD: the params' type, -1 for none. OWN: the constants are formed here.
@@ -144,13 +115,13 @@ __global__ void __launch_bounds__(kQ8Block, 8) adam_q8_tile_kernel(AdamQ8Args a)
   __shared__ Q8Tile<VF> sh;
   constexpr bool WIDE = VF == ZDS_STATE_BF16;
   if (a.sc->overflow) return;  // the step is skipped: uniform, nothing is touched
-  Q8Consts c;
-  if (!OWN) c = load_q8_consts(a.sc);
+  ElemConsts c;
+  if (!OWN) c = load_consts(a.sc);
   const uint32_t steps = a.state->steps_seen;
   const int t = threadIdx.x, lane = t & 63;
   const int64_t first = (a.tile0 + blockIdx.x) * kQ8Tile;
   if (first + kQ8Tile > a.n) {
-    if (OWN) c = derive_q8_consts(a);
+    if (OWN) c = derive_consts(a);
     for (int64_t e = first + t; e < ((a.n + 63) & ~int64_t(63)); e += kQ8Block) q8_element<GD, PD, VF>(a, c, e, steps);
     return;
   }
@@ -184,11 +155,8 @@ __global__ void __launch_bounds__(kQ8Block, 8) adam_q8_tile_kernel(AdamQ8Args a)
     sh.random[t] = u32x4{q.w[0], q.w[1], q.w[2], q.w[3]};
   }
   if (OWN && w == 7) {
-    const Q8Consts d = derive_q8_consts(a);
-    if (lane == 0) {
-      sh.consts[0] = f32x4{d.e.b1, d.e.b2, d.e.omb1, d.e.omb2};
-      sh.consts[1] = f32x4{d.e.eps, d.e.step_size, d.e.decay, d.inv};
-    }
+    const ElemConsts d = derive_consts(a);
+    if (lane == 0) sh.consts = d;
   }
   uint8_t *sm = reinterpret_cast<uint8_t *>(sh.m), *sv = reinterpret_cast<uint8_t *>(sh.v);
   if (has_g) sh.io[t] = x0;
@@ -199,10 +167,12 @@ __global__ void __launch_bounds__(kQ8Block, 8) adam_q8_tile_kernel(AdamQ8Args a)
   __syncthreads();
   if (OWN) {
     const auto uniform = [](float x) { return __uint_as_float(__builtin_amdgcn_readfirstlane(__float_as_uint(x))); };
-    const f32x4 k0 = sh.consts[0], k1 = sh.consts[1];
-    c.e = ElemConsts{uniform(k0.x), uniform(k0.y), uniform(k0.z), uniform(k0.w), uniform(k1.x), uniform(k1.y),
-                     uniform(k1.z), a.sc->grad_scale,  0.0};
-    c.inv = uniform(k1.w);
+    const ElemConsts d = sh.consts;
+    const int lo = __builtin_amdgcn_readfirstlane(__double2loint(d.inv_bc2)),
+              hi = __builtin_amdgcn_readfirstlane(__double2hiint(d.inv_bc2));
+    c = ElemConsts{uniform(d.b1),  uniform(d.b2),        uniform(d.omb1),  uniform(d.omb2),
+                   uniform(d.eps), uniform(d.step_size), uniform(d.decay), a.sc->grad_scale,
+                   __hiloint2double(hi, lo)};
   }
   float g[4], p[4] = {p4.x, p4.y, p4.z, p4.w}, m[4], v[4];
   u32x2 *io2 = reinterpret_cast<u32x2 *>(sh.io);
@@ -224,7 +194,7 @@ __global__ void __launch_bounds__(kQ8Block, 8) adam_q8_tile_kernel(AdamQ8Args a)
   uint32_t mm = 0, vm = 0;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    q8_elem(g[i], c, p[i], m[i], v[i]);
+    adam_elem(g[i], c, p[i], m[i], v[i]);
     mm = magnitude(m[i]) > mm ? magnitude(m[i]) : mm;
     vm = magnitude(v[i]) > vm ? magnitude(v[i]) : vm;
   }
@@ -258,7 +228,7 @@ __global__ void __launch_bounds__(kQ8Block, 8) adam_q8_tile_kernel(AdamQ8Args a)
 template <int GD, int PD, int VF>
 __global__ void __launch_bounds__(256) adam_q8_element_kernel(AdamQ8Args a) {
   if (a.sc->overflow) return;
-  const Q8Consts c = load_q8_consts(a.sc);
+  const ElemConsts c = load_consts(a.sc);
   const uint32_t steps = a.state->steps_seen;
   for (int64_t e = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; e < ((a.n + 63) & ~int64_t(63));
        e += static_cast<int64_t>(gridDim.x) * 256)
