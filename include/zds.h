@@ -707,8 +707,6 @@ zds_status zds_state_dequantise(const void *codes, const uint8_t *exps, int64_t 
  * those of zds_adam_step on the state that zds_state_dequantise gives, and the
  * codes those that zds_state_quantise makes (ZDS_ROUND_RANDOM, the same seed and
  * first) of the moments it leaves, bit for bit.
- * Calls of few elements form the step's constants in the update's own kernel and
- * leave those in scalars_dev as they were.
  *   hp            as for zds_adam_step, but eps >= 2^-100
  *   exp_avg       device, n codes of E4M3, with exp_avg_exps
  *   exp_avg_sq    device, n codes of sq_format (UE5M3 with exp_avg_sq_exps, or

@@ -328,6 +328,20 @@ def test_steps_constants_on_either_side_of_their_launch():
         assert torch.equal(p1, p2), t
 
 
+@pytest.mark.parametrize("n,pad", [(5, 0), (2048, 0), (50003, 0), (50003, 1), (3 * 1024 * 1024, 0)])
+@pytest.mark.parametrize("overflow", [0, 1])
+def test_step_leaves_the_scalars_that_adam_leaves(n, pad, overflow):
+    """The step's constants stand in the scalars after every call, whichever
+    kernel formed them, the flag and the factors as they were."""
+    hp, st = zds.hparams(lr=3e-4, beta2=0.95, weight_decay=0.1), state(5, t=5, b1p=0.9 ** 5, b2p=0.95 ** 5)
+    a, b = scalars(0.25, overflow), scalars(0.25, overflow)
+    x = torch.zeros(n + pad, device="cuda")[pad:]
+    zds.zds_adam_step(hp, x, x.clone(), x.clone(), x.clone(), None, a, st)
+    m, v = zds.new_quantised_state(n, zds.ZDS_STATE_E4M3), zds.new_quantised_state(n, zds.ZDS_STATE_UE5M3)
+    zds.zds_adam_step_q8(hp, x, x.clone(), m, v, None, 1, 0, b, st)
+    assert bytes(zds.read_scalars(a)) == bytes(zds.read_scalars(b)) and zds.read_scalars(b).step_size > 0
+
+
 def test_step_on_the_grads_buffer_and_the_skip():
     n = 4099
     (mc, me), (vc, ve), size = moments(n, 8, Q.UE5M3)

@@ -28,6 +28,17 @@ __device__ __forceinline__ ElemConsts load_consts(const zds_step_scalars *sc) {
   return c;
 }
 
+// The step's constants into the scalars struct.
+__device__ __forceinline__ void store_consts(const AdamConsts &c, zds_step_scalars *sc) {
+  sc->inv_bc2_sqrt = c.inv_bc2_sqrt;
+  sc->step_size = c.step_size;
+  sc->bc2_sqrt = c.bc2_sqrt;
+  sc->decay = c.decay;
+  sc->beta1 = c.b1;
+  sc->beta2 = c.b2;
+  sc->eps = c.eps;
+}
+
 // One element, fp32, one rounding per operation, in this order.
 //
 // sqrt(v) / bc2 (bc2 = sqrt(1 - beta2^t) in fp32) is formed as

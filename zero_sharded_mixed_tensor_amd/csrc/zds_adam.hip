@@ -338,14 +338,7 @@ __global__ void __launch_bounds__(kScalarBlock) adam_scalar_kernel(const zds_ste
 __global__ void __launch_bounds__(64) adam_prep_kernel(zds_adamw_hparams hp, const zds_step_state *state,
                                                        zds_step_scalars *sc) {
   if (threadIdx.x != 0) return;
-  const AdamConsts c = adam_constants(hp, state->beta1_pow, state->beta2_pow);
-  sc->inv_bc2_sqrt = c.inv_bc2_sqrt;
-  sc->step_size = c.step_size;
-  sc->bc2_sqrt = c.bc2_sqrt;
-  sc->decay = c.decay;
-  sc->beta1 = c.b1;
-  sc->beta2 = c.b2;
-  sc->eps = c.eps;
+  store_consts(adam_constants(hp, state->beta1_pow, state->beta2_pow), sc);
 }
 
 // Blocks of the element-wise kernel that fit on one CU at once (queried once

@@ -23,7 +23,7 @@
 namespace zds {
 
 struct AdamQ8Args {
-  const zds_step_scalars *sc;
+  zds_step_scalars *sc;
   const zds_step_state *state;
   const void *g;
   float *p;
@@ -39,9 +39,12 @@ struct AdamQ8Args {
   zds_adamw_hparams hp;
 };
 
-// The step's constants, formed here from the hyperparameters and the step state.
-__device__ __forceinline__ ElemConsts derive_consts(const AdamQ8Args &a) {
+// The step's constants, formed here from the hyperparameters and the step state,
+// and by one thread written where a launch in front would have left them. (No
+// block of this kernel reads those fields.)
+__device__ __forceinline__ ElemConsts derive_consts(const AdamQ8Args &a, bool store) {
   const AdamConsts k = adam_constants(a.hp, a.state->beta1_pow, a.state->beta2_pow);
+  if (store) store_consts(k, a.sc);
   return ElemConsts{k.b1, k.b2, k.omb1, k.omb2, k.eps, k.step_size, k.decay, a.sc->grad_scale, k.inv_bc2_sqrt};
 }
 
@@ -114,14 +117,17 @@ template <int GD, int PD, int VF, bool OWN>
 __global__ void __launch_bounds__(kQ8Block, 8) adam_q8_tile_kernel(AdamQ8Args a) {
   __shared__ Q8Tile<VF> sh;
   constexpr bool WIDE = VF == ZDS_STATE_BF16;
-  if (a.sc->overflow) return;  // the step is skipped: uniform, nothing is touched
+  if (a.sc->overflow) {  // the step is skipped: uniform, nothing else is touched
+    if (OWN && blockIdx.x == 0 && threadIdx.x == 0) derive_consts(a, true);
+    return;
+  }
   ElemConsts c;
   if (!OWN) c = load_consts(a.sc);
   const uint32_t steps = a.state->steps_seen;
   const int t = threadIdx.x, lane = t & 63;
   const int64_t first = (a.tile0 + blockIdx.x) * kQ8Tile;
   if (first + kQ8Tile > a.n) {
-    if (OWN) c = derive_consts(a);
+    if (OWN) c = derive_consts(a, blockIdx.x == 0 && t == 0);
     for (int64_t e = first + t; e < ((a.n + 63) & ~int64_t(63)); e += kQ8Block) q8_element<GD, PD, VF>(a, c, e, steps);
     return;
   }
@@ -155,7 +161,7 @@ __global__ void __launch_bounds__(kQ8Block, 8) adam_q8_tile_kernel(AdamQ8Args a)
     sh.random[t] = u32x4{q.w[0], q.w[1], q.w[2], q.w[3]};
   }
   if (OWN && w == 7) {
-    const ElemConsts d = derive_consts(a);
+    const ElemConsts d = derive_consts(a, blockIdx.x == 0 && lane == 0);
     if (lane == 0) sh.consts = d;
   }
   uint8_t *sm = reinterpret_cast<uint8_t *>(sh.m), *sv = reinterpret_cast<uint8_t *>(sh.v);
