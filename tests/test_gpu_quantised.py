@@ -378,6 +378,54 @@ def test_moments_that_are_not_finite():
     assert torch.isnan(back[3]) and torch.isfinite(torch.cat([back[:3], back[4:]])).all()
 
 
+@pytest.mark.parametrize("second", [Q.UE5M3, Q.BF16])
+@pytest.mark.parametrize("n,pad", [(2048 * 5 + 700, 0), (2048 * 5 + 700, 1), (2 * 1024 * 1024 + 3 * 2048 + 777, 0)])
+def test_step_on_what_is_not_finite(second, n, pad):
+    """NaN and infinities in grads and in either moment, squares that overflow
+    and second moments past 2^104, in whole tiles and behind the last one: codes
+    and exponents are the definition's bit for bit, and so is master (NaN is
+    NaN). In a block of 32 of its own each, and in one block together."""
+    rng = np.random.default_rng(n)
+    m32 = (rng.standard_normal(n) * 1e-3).astype(np.float32)
+    v32 = (rng.random(n) * 1e-6).astype(np.float32)
+    g = (rng.standard_normal(n) * 1e-3).astype(np.float32)
+    tail = n - n % 2048
+    for at in (0, 2048 + 96, 3 * 2048, tail - 2048, tail):        # 0, tails: the first and last of a tile's blocks
+        g[at + 3], g[at + 40], g[at + 75] = np.nan, np.inf, -np.inf
+        g[at + 100], g[at + 135], g[at + 170] = 2.0 ** 53, 2.0 ** 60, 2.0 ** 66     # v past 2^104, 2^116, overflow
+        m32[at + 200], m32[at + 235], m32[at + 236] = np.nan, np.inf, -np.inf
+        v32[at + 265], v32[at + 300], v32[at + 335], v32[at + 370] = np.nan, np.inf, 2.0 ** 105, 2.0 ** 120
+        g[at + 400], g[at + 401], m32[at + 402], v32[at + 403], g[at + 404] = np.nan, 2.0 ** 65, np.nan, np.inf, 0.0
+        v32[at + 432:at + 464], m32[at + 432:at + 464], g[at + 432:at + 464] = 0.0, 0.0, 0.0
+        g[at + 440] = 2.0 ** -90                                  # its square is no fp32 number
+    with np.errstate(over="ignore"):
+        m, v = Q.quantise(m32, Q.E4M3), Q.quantise(v32, second)
+    p = (rng.standard_normal(n) * 0.02).astype(np.float32)
+    hp, t = zds.hparams(lr=1e-3, beta1=0.9, beta2=0.95, weight_decay=0.1), 7
+    b1p, b2p = float(np.float32(0.9)) ** t, float(np.float32(0.95)) ** t
+    consts = O.adamw_constants(O.AdamW(1e-3, 0.9, 0.95, 1e-8, 0.1), b1p, b2p)
+    with np.errstate(over="ignore", invalid="ignore"):
+        wp, wm, wv, _ = Q.adam_step_q8(g, "fp32", np.float32(1.0), p, m, v, second, consts, SEED, 0, 3, "bf16")
+    dm, dv = q_of(*m, Q.E4M3, pad), q_of(*v, second, pad)
+    dg, dp = (to_dev(np.concatenate([a[:1].repeat(pad), a]), "fp32")[pad:] for a in (g, p))
+    zds.zds_adam_step_q8(hp, dg, dp, dm, dv, None, SEED, 0, scalars(), state(3, t=t, b1p=b1p, b2p=b2p), n=n)
+    gm, gme = q_host(dm, n)
+    gv, gve = q_host(dv, n)
+    nan = wm[0] & 0x7F == 0x7F                                    # (a NaN's sign is left open)
+    assert np.array_equal(gm & 0x7F, wm[0] & 0x7F) and np.array_equal(gm[~nan], wm[0][~nan])
+    assert np.array_equal(gme, wm[1])
+    if second == Q.BF16:
+        nan = np.isnan((wv[0].astype(np.uint32) << 16).view(np.float32))    # (and a BF16 NaN's bits)
+        assert np.array_equal(np.isnan((gv.astype(np.uint32) << 16).view(np.float32)), nan)
+        assert np.array_equal(gv[~nan], wv[0][~nan])
+    else:
+        assert np.array_equal(gv, wv[0]) and np.array_equal(gve, wv[1])
+    same(to_host(dp)[:n], wp)
+    bad = np.isnan(wp)
+    assert 5 * 8 <= bad.sum() <= n // 100 and not bad[tail + 100]
+    assert (gme == 255).sum() >= 5 * 5
+
+
 def test_offsets_past_32_bits():
     """2^32 + 4133 elements: the last ones against a call of their own."""
     n, tail = (1 << 32) + 4133, 4133 + 32 * 5
