@@ -773,6 +773,10 @@ zds_status zds_dropout_compress(const void *x, zds_dtype x_dtype, float *error, 
  * gradient (and so does zds_reduce_peer_slices_norm, which sums several).
  * Must be called before the zds_loss_scaler_update that ends the step whose
  * zds_dropout_compress made the values. dst must not overlap a message.
+ * Messages and dst may lie at any multiple of their element size; a call goes
+ * element by element, about three times slower, if one of them is not at a
+ * multiple of 16 bytes. (Rows of a gathered buffer are if a row is: pad its
+ * length to one.)
  * A rank that needs the elements [lo, hi) only (its shard; lo a multiple of
  * ratio) passes the messages from value lo / ratio on, n = hi - lo and
  * first + lo. */

@@ -81,6 +81,31 @@ def test_decompress_bit_exact(ratio, vdt, odt, n, pad, peers):
         same(got[n:], dst[:1].repeat(8), odt)
 
 
+@pytest.mark.parametrize("ratio", [2, 4, 16, 256])
+@pytest.mark.parametrize("vdt,odt", [("bf16", "fp32"), ("bf16", "bf16"), ("fp32", "fp32")])
+@pytest.mark.parametrize("n,peers", [(257, 2), (50003, 8), (16 * 4096 + 40, 16)])
+def test_messages_at_any_address(ratio, vdt, odt, n, peers):
+    """Rows of one gathered buffer, of a length that is no multiple of 16 bytes,
+    and one odd message among aligned ones, under an aligned dst: what separate
+    allocations give."""
+    rng = np.random.default_rng(n + ratio)
+    groups = -(-n // ratio)
+    msgs = [host(rng.standard_normal(groups), vdt) for _ in range(peers)]
+    dst = host(rng.standard_normal(n), odt)
+    rows = torch.zeros(peers, groups, dtype=TDT[vdt], device="cuda")
+    for row, m in zip(rows, msgs):
+        row.copy_(to_dev(m, vdt))
+    one = [to_dev(m, vdt) for m in msgs]
+    one[peers // 2] = shifted(msgs[peers // 2], vdt, 1)
+    for mode in (zds.ZDS_OVERWRITE, zds.ZDS_ACCUMULATE):
+        want = Q.dropout_decompress(msgs, vdt, n, ratio, SEED, 0, 9, dst, odt, mode == zds.ZDS_ACCUMULATE)
+        for messages in (list(rows), one):
+            dd = shifted(dst, odt, 0, 8)
+            zds.zds_dropout_decompress(messages, ratio, dd, SEED, 0, state(9), mode, n=n)
+            same(to_host(dd)[:n], want, odt)
+            same(to_host(dd)[n:], dst[:1].repeat(8), odt)
+
+
 @pytest.mark.parametrize("vdt,odt", [("bf16", "bf16"), ("fp16", "fp32"), ("fp32", "fp32")])
 @pytest.mark.parametrize("ratio", [64, 128, 256])
 @pytest.mark.parametrize("n", [128 * 4096, 259 * 4096 + 5])
