@@ -2,10 +2,13 @@
 // `ratio` consecutive elements sends one, chosen by the counter-based
 // generator (include/zds.h has the definition, zds_random.h the generator).
 //
-// Four streams, all bound by HBM. With feedback, encoding reads x and the error
-// and writes the error (2 or 4 + 8 B an element) and the values; without, it
-// reads one element of each group. Decoding writes the whole gradient (4 or 2 B
-// an element) or, when it adds, reads and writes one element of each group.
+// Streams, all bound by HBM. With feedback, encoding reads x and the error and
+// writes the error (2 or 4 + 8 B an element) and the values. Decoding writes the
+// whole gradient (4 or 2 B an element). Encoding without feedback and adding need
+// one element of each group, and memory gives whole lines of 128 bytes: in groups
+// of up to a line (32 fp32 or 64 16-bit elements) every line is touched, so all
+// of x is streamed, or all of dst read and written back; in longer groups only the
+// kept elements are read, or read and written.
 // A block first makes the kept places of its groups in LDS: one call of the
 // generator covers 16 groups, so its arithmetic does not show.
 #include "zds_internal.h"
@@ -13,13 +16,15 @@
 
 namespace zds {
 
-// Elements of a block's tile where a gradient is encoded, and where one is
-// written; groups of a block where single elements are read or added to.
+// Elements of a block's tile where a gradient is encoded with feedback.
 constexpr int kEncodeBlock = 512;
 constexpr int kEncodeTile = 4 * kEncodeBlock;
+// Elements of a block's tile where a whole gradient is written.
 constexpr int kSpreadBlock = 256;
 constexpr int kSpreadTile = 16 * kSpreadBlock;
+// Consecutive tiles that one XCD gets where tiles share lines of a message.
 constexpr int kXcdRun = 16;
+// Groups of a block where only the kept elements are read or added to.
 constexpr int kDropGroups = 1024;
 
 struct DropArgs {
