@@ -415,6 +415,7 @@ def test_a_span_of_an_exchange():
     for span in ((-16, 16), (8, 32), (0, 1001), (0, 24), (32, 16), (1008, 1008), (0, 1008)):
         _raises(lambda: ex.decompress([values], dst, step, span=span), "span")
     _raises(lambda: ex.decompress([values[:62]], dst, step, span=(0, 16)), "peer 0 holds 62")
+    _raises(lambda: ex.decompress([torch.zeros(63, 2)[:, 0]], dst, step, span=(0, 16)), "contiguous")
     _raises(lambda: ex.decompress([values], dst[:15], step, span=(16, 32)), "dst holds 15")
 
 

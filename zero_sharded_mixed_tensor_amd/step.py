@@ -335,6 +335,8 @@ class DropoutExchange:
             raise zds.ZdsError(zds.ZDS_EINVAL, "the span [%d, %d) must lie in [0, %d) at multiples of %d" % (lo, hi, self.n, r))
         for k, t in enumerate(peers):
             zds._need(t, self.groups, "peer %d" % k)
+            if not t.is_contiguous():
+                raise zds.ZdsError(zds.ZDS_EINVAL, "peer %d must be contiguous" % k)
         if span is not None:
             peers = [t.view(-1)[lo // r:zds.dropout_groups(hi, r)] for t in peers]
         zds.zds_dropout_decompress(peers, r, dst, self.seed, self.first + lo, _shard_step(step).state, mode, stream,
