@@ -311,6 +311,20 @@ def test_step_leaves_the_master_that_adam_leaves(second, n, pad, eps):
     assert torch.equal(o2.view(torch.int16)[~nan], o1.view(torch.int16)[~nan])
 
 
+@pytest.mark.parametrize("exponent", [0, -63, 30])
+def test_step_with_every_mantissa(exponent):
+    """The change itself (master starts at 0) for gradients of all 2^23
+    mantissas, their squares over two binades: zds_adam_step's bits."""
+    n = 1 << 23
+    g = ((127 + exponent << 23) + torch.arange(n, dtype=torch.int32, device="cuda")).view(torch.float32)
+    hp, st = zds.hparams(lr=1.0, beta1=0.5, beta2=0.5, eps=1e-29, weight_decay=0.0), state(2, t=2, b1p=0.25, b2p=0.25)
+    m, v = zds.new_quantised_state(n, zds.ZDS_STATE_E4M3), zds.new_quantised_state(n, zds.ZDS_STATE_UE5M3)
+    p, z = torch.zeros(n, device="cuda"), [torch.zeros(n, device="cuda") for _ in range(3)]
+    zds.zds_adam_step(hp, g, *z, None, scalars(), st)
+    zds.zds_adam_step_q8(hp, g, p, m, v, None, 1, 0, scalars(), st)
+    assert torch.equal(p, z[0]) and (p < 0).all()
+
+
 def test_steps_constants_on_either_side_of_their_launch():
     """Whole tiles of a call that forms the step's constants itself, through 200
     steps' values of them, against zds_adam_step's bits."""

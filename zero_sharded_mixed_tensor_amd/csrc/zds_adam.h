@@ -54,14 +54,22 @@ __device__ __forceinline__ void store_consts(const AdamConsts &c, zds_step_scala
 // exact quotient. Here a = sqrt(v) is 0, NaN, inf or at least 2^-74.5, and
 // the quotient stays in the normal range; bc2 = 0 (beta2 = 1) gives
 // r = inf and the same inf / NaN as the division.
-__device__ __forceinline__ void adam_elem(float x, const ElemConsts &c, float &p, float &m, float &v) {
+__device__ __forceinline__ void adam_moments(float x, const ElemConsts &c, float &m, float &v) {
   const float g = x * c.gs;
   m = c.b1 * m + c.omb1 * g;
   v = c.b2 * v + c.omb2 * (g * g);
+}
+__device__ __forceinline__ float adam_denom(float v, const ElemConsts &c) {
   const float q = static_cast<float>(static_cast<double>(sqrtf(v)) * c.inv_bc2);
-  const float denom = q + c.eps;
+  return q + c.eps;
+}
+__device__ __forceinline__ void adam_param(float m, float denom, const ElemConsts &c, float &p) {
   p = p * c.decay;
   p = p - c.step_size * (m / denom);
+}
+__device__ __forceinline__ void adam_elem(float x, const ElemConsts &c, float &p, float &m, float &v) {
+  adam_moments(x, c, m, v);
+  adam_param(m, adam_denom(v, c), c, p);
 }
 
 // Scheduling priority of a wave: raised while it issues its loads and stores,

@@ -3,20 +3,20 @@
 // random (include/zds.h; zds_quantised.h has the formats' arithmetic).
 //
 // A stream of 16.1 B an element (16-bit grads; 18.1 with a BF16 second moment)
-// and about 75 VALU instructions an element, 6 of them the generator's and 30 the
+// and about 65 VALU instructions an element, 6 of them the generator's and 20 the
 // correctly rounded root and quotient: on 842M elements 2.06 ms of memory at the
-// rate of a copy and about as much of all SIMDs, so what counts is that the one
-// hides the other. A block of 8 waves takes a tile of 2048 elements; the waves
-// fetch it 16 bytes a lane, one access in flight each, the master's quads straight
-// into the registers of the thread that updates them, grads and codes through
-// LDS; four of the waves make the generator's calls meanwhile; the results go out
-// the same way. 842M elements, bf16: 2.26 ms (6.01 TB/s). The hardware's root and
-// reciprocal, 26 instructions fewer, took 2.15, but then master is no longer
-// zds_adam_step's. Layouts, timed with those (2.13 then): each lane moving its own
-// quad of every array (4-byte accesses to the codes) 2.36, of which the arithmetic
-// was not the cause (2.48 without it); a wave's own 1024 elements through its own
-// LDS, no barriers 2.24; tiles of 4096 in two pipelined halves, as the fp32
-// step's, 2.28 to 2.39; tiles of 1024 with one access a wave 2.73.
+// rate of a copy and 1.8 of all SIMDs, so what counts is that the one hides the
+// other. A block of 8 waves takes a tile of 2048 elements; the waves fetch it 16
+// bytes a lane, one access in flight each, the master's quads straight into the
+// registers of the thread that updates them, grads and codes through LDS; four of
+// the waves make the generator's calls meanwhile; the results go out the same way.
+// 842M elements, bf16: 2.19 ms (6.2 TB/s). The hardware's root and reciprocal, 16
+// instructions fewer, take 2.15, but then master is no longer zds_adam_step's.
+// Layouts, timed with those (2.13 then): each lane moving its own quad of every
+// array (4-byte accesses to the codes) 2.36, of which the arithmetic was not the
+// cause (2.48 without it); a wave's own 1024 elements through its own LDS, no
+// barriers 2.24; tiles of 4096 in two pipelined halves, as the fp32 step's, 2.28 to
+// 2.39; tiles of 1024 with one access a wave 2.73.
 #include "zds_adam.h"
 #include "zds_quantised.h"
 
@@ -46,6 +46,24 @@ __device__ __forceinline__ ElemConsts derive_consts(const AdamQ8Args &a, bool st
   const AdamConsts k = adam_constants(a.hp, a.state->beta1_pow, a.state->beta2_pow);
   if (store) store_consts(k, a.sc);
   return ElemConsts{k.b1, k.b2, k.omb1, k.omb2, k.eps, k.step_size, k.decay, a.sc->grad_scale, k.inv_bc2_sqrt};
+}
+
+// sqrt(v) / bc2 + eps as adam_denom has it, for v of 0 or from 2^-149 to 2^63, with
+// a shorter root: v enters times 2^64, so that no step of it underflows, and the
+// root's 2^32 leaves in the product with 1 / bc2, in fp64. One Newton step from the
+// hardware's reciprocal root, the residual in one rounding, is correctly rounded
+// for each of the 1.78e9 fp32 numbers from 2^-85 to 2^127 (compared with sqrtf one
+// by one); 0 stays 0, as the reciprocal root is that of 2^-90 then. 6 instructions
+// and a quarter-rate one where sqrtf, which has to serve every number, takes 15 and
+// one: 842M elements 2.24 -> XXX ms.
+constexpr uint32_t kRootMost = 0x5f000000u;  // the bits of 2^63
+__device__ __forceinline__ float adam_denom_in_range(float v, const ElemConsts &c) {
+  const float x = v * 0x1p64f;
+  const float y = __builtin_amdgcn_rsqf(__builtin_fmaxf(x, 0x1p-90f));
+  const float s = x * y;
+  const float root = __builtin_fmaf(__builtin_fmaf(-s, s, x), 0.5f * y, s);
+  const float q = static_cast<float>(static_cast<double>(root) * (c.inv_bc2 * 0x1p-32));
+  return q + c.eps;
 }
 
 // One element on each lane, the block of 32 that shares an exponent in half a
@@ -197,13 +215,26 @@ __global__ void __launch_bounds__(kQ8Block, 8) adam_q8_tile_kernel(AdamQ8Args a)
   } else {
     decode_quad<VF>(sv1[t], sh.ve[t >> 3], v);
   }
-  uint32_t mm = 0, vm = 0;
+  uint32_t mm = 0, vm = 0, vb = 0;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    adam_elem(g[i], c, p[i], m[i], v[i]);
+    adam_moments(g[i], c, m[i], v[i]);
     mm = magnitude(m[i]) > mm ? magnitude(m[i]) : mm;
     vm = magnitude(v[i]) > vm ? magnitude(v[i]) : vm;
+    vb = __float_as_uint(v[i]) > vb ? __float_as_uint(v[i]) : vb;
   }
+  // (a BF16 state may hold negative numbers, whose bits are the larger ones)
+  const bool in_range = (WIDE ? vb : vm) < kRootMost;
+  float denom[4];
+  if (in_range) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) denom[i] = adam_denom_in_range(v[i], c);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) denom[i] = adam_denom(v[i], c);
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) adam_param(m[i], denom[i], c, p[i]);
   st_stream_at(pp, 16 * t, f32x4{p[0], p[1], p[2], p[3]});
   const u32x2 rr = reinterpret_cast<const u32x2 *>(sh.random)[t];
   const uint32_t rw[2] = {rr.x, rr.y};
