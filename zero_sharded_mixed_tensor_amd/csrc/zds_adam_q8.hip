@@ -124,8 +124,8 @@ struct Q8Tile {
 
 // Up to this many elements the blocks form the step's constants themselves, by
 // one wave while the loads are in flight, instead of a launch in front of them:
-// a call of 1M elements takes 7.0 us in a graph instead of 7.8 (and 10 us on the
-// host instead of 13), of 2M 9.2 and 9.6; of 4M 16.3 and 15.5, of 8M 27.8 and
+// a call of 1M elements takes 6.8 us in a graph instead of 7.5 (and 10 us on the
+// host instead of 13), of 2M 9.0 and 9.2; of 4M 16.7 and 15.3, of 8M 28.9 and
 // 25.5, as every block pays for the divisions.
 constexpr int64_t kQ8OwnConsts = int64_t(1) << 21;
 
