@@ -550,3 +550,22 @@ def test_an_exchange_is_resumed():
     go(*second, range(3, 6))
     assert torch.equal(second[2], straight[2]) and torch.equal(second[1].error, straight[1].error)
     assert torch.equal(second[1].values, straight[1].values)
+
+
+@pytest.mark.parametrize("span", [None, (128, 9000)])
+def test_gathered_messages(span):
+    """Four ranks' padded messages as rows of one buffer: decoded from the rows
+    as from the messages themselves, the padding untouched."""
+    n, ratio = 10007, 8
+    st = ShardStep(n, scaler=zds.scaler_config(dynamic=False))
+    exs = [DropoutExchange(n, ratio, torch.bfloat16, seed=4) for _ in range(4)]
+    for r, ex in enumerate(exs):
+        ex.compress(torch.randn(n, device="cuda", generator=torch.Generator(device="cuda").manual_seed(r)).bfloat16(), st)
+        assert not ex.padded[ex.groups:].any()
+    rows = torch.cat([ex.padded for ex in exs]).view(4, -1)
+    assert all(row.data_ptr() % 16 == 0 for row in rows) and rows.shape[1] > exs[0].groups
+    lo, hi = span or (0, n)
+    a, b = torch.empty(hi - lo, device="cuda"), torch.empty(n, device="cuda")
+    exs[0].decompress(list(rows), a, st, span=span)
+    exs[0].decompress([ex.values for ex in exs], b, st)
+    assert torch.equal(a, b[lo:hi]) and (a != 0).any()

@@ -429,3 +429,13 @@ def test_what_a_span_passes_on(monkeypatch):
         ex.decompress([values], None, step, span=span)
     assert got == [(list(range(63)), 16, 5, 32, 1000), ([1, 2], 16, 5, 48, 32), ([62], 16, 5, 32 + 992, 8),
                    ([], 16, 5, 96, 0), (list(range(63)), 16, 5, 32, 1000)]
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("n", [0, 1, 100, 1000, 1024, 733953])
+def test_a_message_with_its_padding(dtype, n):
+    """Rows of this length follow each other at multiples of 16 bytes."""
+    ex = DropoutExchange(n, 8, dtype, device="cpu", feedback=False)
+    assert ex.values.numel() == ex.groups and ex.values.dtype == dtype and ex.values.data_ptr() == ex.padded.data_ptr()
+    size = ex.padded.numel() * ex.padded.element_size()
+    assert size % 16 == 0 and 0 <= size - ex.groups * ex.padded.element_size() < 16 and not ex.padded.any()

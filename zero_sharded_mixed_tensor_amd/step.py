@@ -14,7 +14,7 @@ def _wait_cleared(device):
     """Waits for the current stream, on which a step's buffers were cleared: the
     first call on them may come on another one."""
     import torch
-    if torch.device(device).type == "cuda":
+    if device is not None and torch.device(device).type == "cuda":
         torch.cuda.current_stream(device).synchronize()
 
 
@@ -274,6 +274,11 @@ class DropoutExchange:
         ex.decompress([ex.values], shard, step, span=(lo, hi))
         step.adam(shard, ...); step.scaler()
 
+    Or, to sum in fp32, all_gather(rows, ex.padded), norm() of the rows' sum
+    (zds_reduce_peer_slices) and decompress(list(rows), ...): padded is the message
+    with zeros up to a multiple of 16 bytes, so that every row of the gathered
+    buffer lies where it decodes fast.
+
     span is left out where every rank updates everything. The flags' all-reduce
     may be left out, too: a message of a rank that overflows is NaN, and all ranks
     skip the step. But the other ranks have then taken what they sent out of their
@@ -298,7 +303,10 @@ class DropoutExchange:
             raise zds.ZdsError(zds.ZDS_EINVAL, "first must be a multiple of ratio, >= 0")
         self.n, self.ratio, self.seed, self.first = n, ratio, zds._seed(seed), first
         self.groups = zds.dropout_groups(n, ratio)
-        self.values = torch.zeros(self.groups, dtype=torch.bfloat16 if dtype is None else dtype, device=device)
+        dtype = torch.bfloat16 if dtype is None else dtype
+        line = 16 // dtype.itemsize
+        self.padded = torch.zeros(-(-self.groups // line) * line, dtype=dtype, device=device)
+        self.values = self.padded[:self.groups]
         self.error = torch.zeros(n, dtype=torch.float32, device=device) if feedback else None
         self.ws = zds.new_workspace(n, device)  # (a step's own is that of its shard)
         _wait_cleared(device)  # (the calls take any stream)
