@@ -39,8 +39,13 @@ __device__ __forceinline__ void store_consts(const AdamConsts &c, zds_step_scala
   sc->eps = c.eps;
 }
 
-// One element, fp32, one rounding per operation, in this order.
-//
+// One element, fp32, one rounding per operation, in this order: the moments, the
+// denominator, the parameter (adam_elem does all three).
+__device__ __forceinline__ void adam_moments(float x, const ElemConsts &c, float &m, float &v) {
+  const float g = x * c.gs;
+  m = c.b1 * m + c.omb1 * g;
+  v = c.b2 * v + c.omb2 * (g * g);
+}
 // sqrt(v) / bc2 (bc2 = sqrt(1 - beta2^t) in fp32) is formed as
 // fp32(float64(sqrt(v)) * r) with r = 1 / float64(bc2) correctly rounded.
 // That is the correctly rounded fp32 quotient: r carries a relative error of
@@ -54,11 +59,6 @@ __device__ __forceinline__ void store_consts(const AdamConsts &c, zds_step_scala
 // exact quotient. Here a = sqrt(v) is 0, NaN, inf or at least 2^-74.5, and
 // the quotient stays in the normal range; bc2 = 0 (beta2 = 1) gives
 // r = inf and the same inf / NaN as the division.
-__device__ __forceinline__ void adam_moments(float x, const ElemConsts &c, float &m, float &v) {
-  const float g = x * c.gs;
-  m = c.b1 * m + c.omb1 * g;
-  v = c.b2 * v + c.omb2 * (g * g);
-}
 __device__ __forceinline__ float adam_denom(float v, const ElemConsts &c) {
   const float q = static_cast<float>(static_cast<double>(sqrtf(v)) * c.inv_bc2);
   return q + c.eps;

@@ -51,7 +51,7 @@
 // per-step constant sqrt(1 - beta2^t) is a float64 multiplication by its
 // float64 reciprocal, rounded to fp32 (3 instructions instead of the 11 of a
 // correctly rounded fp32 divide), +2.2 % on the 7B shard then; it gives the
-// correctly rounded quotient for every input, see adam_elem. (2) The waves
+// correctly rounded quotient for every input, see adam_denom. (2) The waves
 // raise their scheduling priority while they issue loads and stores and drop
 // it for the update, so that a block's memory accesses are not queued behind
 // other blocks' arithmetic on the same SIMD: +0.3 to 1 % in four A/B runs

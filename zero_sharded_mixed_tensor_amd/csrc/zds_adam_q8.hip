@@ -54,8 +54,8 @@ __device__ __forceinline__ ElemConsts derive_consts(const AdamQ8Args &a, bool st
 // hardware's reciprocal root, the residual in one rounding, is correctly rounded
 // for each of the 1.78e9 fp32 numbers from 2^-85 to 2^127 (compared with sqrtf one
 // by one); 0 stays 0, as the reciprocal root is that of 2^-90 then. 6 instructions
-// and a quarter-rate one where sqrtf, which has to serve every number, takes 15 and
-// one: 842M elements 2.24 -> XXX ms.
+// and the reciprocal root, where sqrtf, which has to serve every number, takes 15
+// and the root: 842M elements 2.19 ms, with sqrtf 2.27.
 constexpr uint32_t kRootMost = 0x5f000000u;  // the bits of 2^63
 __device__ __forceinline__ float adam_denom_in_range(float v, const ElemConsts &c) {
   const float x = v * 0x1p64f;
