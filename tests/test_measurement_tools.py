@@ -86,6 +86,24 @@ def test_committed_summaries_name_their_commands():
         assert "rocprofv3 " in text and "bench.py --workload" in text, f
 
 
+def test_a_kernels_sources_are_all_that_it_includes():
+    """The hash that says whether a summary is of this build covers every file
+    that the kernel is compiled from."""
+    import re
+    for kernel, files in P.KERNEL_SOURCES.items():
+        seen, todo = set(), [f for f in files if f.endswith(".hip")]
+        assert todo, kernel
+        while todo:
+            f = todo.pop()
+            seen.add(f)
+            for name in re.findall(r'^#include "(\w+\.h)"', open(os.path.join(P.PKG, f)).read(), re.M):
+                path = "csrc/" + name if os.path.exists(os.path.join(P.PKG, "csrc", name)) else "../include/" + name
+                if path not in seen:
+                    todo.append(path)
+        # (the C header declares entry points and the structs that the kernels share with their callers)
+        assert seen - {"../include/zds.h"} <= set(files), (kernel, seen - set(files))
+
+
 def test_bench_refuses_more_than_one_gpu():
     r = subprocess.run([sys.executable, os.path.join(ROOT, "bench.py"), "--gpus", "2"], capture_output=True,
                        text=True, timeout=120)

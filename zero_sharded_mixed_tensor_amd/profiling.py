@@ -27,17 +27,15 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 
 # kernel name prefix -> sources that define it
+_COMMON = ["csrc/zds_device.h", "csrc/zds_internal.h", "csrc/zds_scalar.h", "build.py"]
 KERNEL_SOURCES = {
-    "adam_wide_kernel": ["csrc/zds_adam.hip", "csrc/zds_device.h", "csrc/zds_internal.h", "build.py"],
-    "norm_stage1": ["csrc/zds_norm.hip", "csrc/zds_device.h", "csrc/zds_internal.h", "build.py"],
-    "accumulate_kernel": ["csrc/zds_accumulate.hip", "csrc/zds_device.h", "csrc/zds_internal.h", "build.py"],
-    "reduce_peers_kernel": ["csrc/zds_reduce.hip", "csrc/zds_device.h", "csrc/zds_internal.h", "build.py"],
-    "onebit_encode_kernel": ["csrc/zds_onebit.hip", "csrc/zds_onebit.h", "csrc/zds_device.h", "csrc/zds_internal.h",
-                             "build.py"],
-    "onebit_decode_kernel": ["csrc/zds_onebit.hip", "csrc/zds_onebit.h", "csrc/zds_device.h", "csrc/zds_internal.h",
-                             "build.py"],
-    "onebit_decode_quarter_kernel": ["csrc/zds_onebit.hip", "csrc/zds_onebit.h", "csrc/zds_device.h",
-                                     "csrc/zds_internal.h", "build.py"],
+    "adam_wide_kernel": ["csrc/zds_adam.hip", "csrc/zds_adam.h"] + _COMMON,
+    "norm_stage1": ["csrc/zds_norm.hip"] + _COMMON,
+    "accumulate_kernel": ["csrc/zds_accumulate.hip"] + _COMMON,
+    "reduce_peers_kernel": ["csrc/zds_reduce.hip"] + _COMMON,
+    "onebit_encode_kernel": ["csrc/zds_onebit.hip", "csrc/zds_onebit.h"] + _COMMON,
+    "onebit_decode_kernel": ["csrc/zds_onebit.hip", "csrc/zds_onebit.h"] + _COMMON,
+    "onebit_decode_quarter_kernel": ["csrc/zds_onebit.hip", "csrc/zds_onebit.h"] + _COMMON,
 }
 CALIB_BYTES = 1 << 30
 
